@@ -412,6 +412,119 @@ relation_status_t relation_linear_bwd_gate(const relation_problem_t* p, const vo
                                            size_t workspace_bytes, void* stream);
 
 /*
+ * Paged Relation Cache: serving many requests whose histories live in pages.
+ *
+ * The cache of Sec. 5.3 / Appendix A.5 (the P2 rows and information states I~
+ * of the tokens already processed) is held in pages of page_size tokens, shared
+ * by R requests through a block table; a step appends the new tokens of every
+ * request, packed one request after another, and forms their Relation rows.
+ * Three calls make a step: relation_paged_plan (where each new token goes),
+ * relation_paged_store (the input prologue, and the new tokens' rows into their
+ * pages), relation_paged_fwd (Relation of the new tokens over the pages).
+ *
+ * One problem struct describes all three:
+ *   R requests; N rows of the packed token tensors (the requests' new tokens
+ *   may be fewer: later rows are padding); H Relation heads (P1, Y) and G cache
+ *   heads (P2, I~), H a multiple of G: Relation head h reads cache head
+ *   h / (H / G); pages of page_size tokens; block_table rows of table_width
+ *   entries.
+ * Packed tensors: [N, H, d_h] (X1, P1, Y) and [N, G, d_h] (X2, I), contiguous.
+ * Pages: [pages, G, page_size, row] (RELATION_LAYOUT_BHTD) or
+ *   [pages, page_size, G, row] (RELATION_LAYOUT_BTHD), contiguous, with
+ *   row = d_h except bf16 d_h = 60, whose rows are padded to 64 elements
+ *   (16-byte rows; the padding is never read as data).
+ * block_table: int32 [R, table_width], entry k of row r the page of request r's
+ *   tokens k page_size .. (k+1) page_size - 1; entries past a request's last
+ *   token are never read.  Slots: int64, page * page_size + offset in the page.
+ * Sizes: 1 <= R <= 2^20 (relation_paged_fwd: 8192, else
+ *   RELATION_ERR_UNSUPPORTED); 0 <= N <= 2^31 - 1 (N = 0: plan writes starts and
+ *   used, the other two enqueue nothing); H <= 1024; page_size a power of two
+ *   from 16 to 256 (else RELATION_ERR_UNSUPPORTED); pages <= 2^31 - 1;
+ *   table_width * page_size <= 2^31 - 1; every tensor at most 10^12 elements.
+ *   d_h, dtype, layout, tau_S, lambda as for relation_fwd.
+ * Device-side values out of range (a negative length, a page id outside
+ * [0, pages), packed offsets that do not ascend or pass N) are never followed:
+ * the rows concerned are skipped or read zeros, and
+ * relation_check_device_status() reports RELATION_ERR_INVALID_ARGUMENT.
+ */
+typedef struct {
+    int64_t R, N, H, G, d_h, pages, page_size, table_width;
+    int32_t dtype;  /* relation_dtype_t */
+    float tau_S;    /* as in relation_problem_t */
+    float lambda;   /* as in relation_problem_t */
+    int32_t layout; /* relation_layout_t of the pages */
+} relation_paged_t;
+
+/*
+ * Block tables and slot maps from request lengths, on the device (one kernel;
+ * the host needs no length).  With held_r = ceil(cached_r / page_size) and
+ * need_r = ceil((cached_r + fresh_r) / page_size), each at most table_width:
+ *   starts[r] = sum_{q < r} fresh_q (r = 0..R);
+ *   block_table[r][k] = the next unused entry of free_pages, requests in order,
+ *     for k = held_r .. need_r - 1 (other entries are left as they are);
+ *   for packed token n of request r: positions[n] = cached_r + n - starts[r],
+ *     slots[n] = block_table[r][positions[n] / page_size] * page_size +
+ *     positions[n] % page_size;
+ *   used = sum_r (need_r - held_r).
+ * A used above free_count says that the free list ran out: the entries and slots
+ * it could not serve are -1 (as is the slot of a token past the table's width, or
+ * of one whose page is outside [0, pages)), and the caller frees pages or drops
+ * requests before going on.  Rows starts[R] .. N - 1 get slot -1 and position 0.
+ * cached, fresh: int32 [R].  free_pages: int32 [free_count] (may be NULL when
+ * free_count = 0).  starts: int32 [R + 1].  slots: int64 [N].  positions: int32
+ * [N].  used: int32 [1].  Running it again with the same arguments gives the same
+ * results.  Reads p->R, N, pages, page_size and table_width; the whole struct is
+ * checked.  cached, fresh, free_pages, starts and used need 4-byte alignment only.
+ */
+relation_status_t relation_paged_plan(const relation_paged_t* p, const int32_t* cached, const int32_t* fresh,
+                                      const int32_t* free_pages, size_t free_count, int32_t* block_table,
+                                      int32_t* starts, int64_t* slots, int32_t* positions, int32_t* used,
+                                      void* stream);
+
+/*
+ * The input prologue (RoPE of the relation coordinates, Givens mixing of the
+ * information states, as relation_prologue_fwd) of packed new tokens, with the
+ * rows the cache keeps written straight into their pages (one kernel):
+ *   P1[n] = RoPE(X1[n], positions[n]); page row slots[n] of P2_pages =
+ *   RoPE(X2[n], positions[n]) and of I_pages = the mixed I[n].
+ * theta: float32 [G/2], pairs of cache heads as in relation_prologue_fwd (G even);
+ * NULL stores the states unmixed.  rope_base <= 0: no rotation.  Tokens whose slot
+ * is negative are not cached (their P1 row is still written); a slot past the
+ * last page is reported and skipped.  Two tokens must not share a slot.
+ * P1 must not overlap any input.
+ */
+relation_status_t relation_paged_store(const relation_paged_t* p, const void* X1, const void* X2, const void* I,
+                                       const float* theta, int pairing, float rope_base, const int32_t* positions,
+                                       const int64_t* slots, void* P1, void* P2_pages, void* I_pages, void* stream);
+
+/*
+ * Relation of the new tokens over the paged cache: for token t of request r
+ * (packed row starts[r] + t), at zero-based position i = cached_r + t,
+ *   Y = row i + 1 of the causal relation_fwd over tokens 0..i of the request,
+ * whose P2 and I~ rows (the new tokens' own included) the pages hold.  One new
+ * token per request is a decoding step, cached_r = 0 a whole prompt, anything
+ * between a chunk; one call takes any mix of them.  A request with no new tokens
+ * costs nothing.  Every row sees at least its own token, so no row is empty.
+ * starts: int32 [R + 1] ascending, starts[0] >= 0 and starts[R] <= N; rows
+ * outside the requests' ranges are left unwritten.  cached: int32 [R].
+ * max_fresh: an upper bound of the new tokens of any request, known to the host
+ * (0: none known).  It selects kernels and sizes the workspace; a request with
+ * more new tokens is reported and skipped.
+ * Y: [N, H, d_h].  L: optional float32 [N, H], log sum_j exp(R_ij) in the
+ * paper's convention.
+ * workspace: relation_paged_workspace_bytes(p, max_fresh) bytes (0 = invalid
+ * problem), 16-byte aligned, contents ignored on entry.
+ * The history is split over the whole GPU whatever the requests' lengths; cut rows
+ * are merged from the workspace in a fixed order, so results are the same from run
+ * to run.
+ */
+size_t relation_paged_workspace_bytes(const relation_paged_t* p, int max_fresh);
+relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, const void* P2_pages,
+                                     const void* I_pages, const int32_t* block_table, const int32_t* starts,
+                                     const int32_t* cached, int max_fresh, void* Y, float* L, void* workspace,
+                                     size_t workspace_bytes, void* stream);
+
+/*
  * Reads and clears the device status word of the current device.  Call after
  * synchronising the streams used.  Returns RELATION_OK,
  * RELATION_ERR_DEVICE_TIMEOUT (a bounded wait expired; outputs of the calls

@@ -56,6 +56,25 @@ class Problem(ctypes.Structure):
     ]
 
 
+class Paged(ctypes.Structure):
+    """Mirror of relation_paged_t."""
+
+    _fields_ = [
+        ("R", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("G", ctypes.c_int64),
+        ("d_h", ctypes.c_int64),
+        ("pages", ctypes.c_int64),
+        ("page_size", ctypes.c_int64),
+        ("table_width", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("tau_S", ctypes.c_float),
+        ("lam", ctypes.c_float),
+        ("layout", ctypes.c_int32),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -131,6 +150,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.relation_linear_bwd.argtypes = [ctypes.POINTER(Problem), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                             ctypes.c_int, _VP, ctypes.c_size_t, _VP]
         lib.relation_linear_bwd.restype = ctypes.c_int
+        _PP = ctypes.POINTER(Paged)
+        lib.relation_paged_plan.argtypes = [_PP, _VP, _VP, _VP, ctypes.c_size_t, _VP, _VP, _VP, _VP, _VP, _VP]
+        lib.relation_paged_plan.restype = ctypes.c_int
+        lib.relation_paged_store.argtypes = [_PP, _VP, _VP, _VP, _VP, ctypes.c_int, ctypes.c_float, _VP, _VP, _VP, _VP,
+                                             _VP, _VP]
+        lib.relation_paged_store.restype = ctypes.c_int
+        lib.relation_paged_workspace_bytes.argtypes = [_PP, ctypes.c_int]
+        lib.relation_paged_workspace_bytes.restype = ctypes.c_size_t
+        lib.relation_paged_fwd.argtypes = [_PP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int, _VP, _VP, _VP,
+                                           ctypes.c_size_t, _VP]
+        lib.relation_paged_fwd.restype = ctypes.c_int
         lib.relation_selftest_wait_timeout.argtypes = [ctypes.c_uint32, _VP]
         lib.relation_selftest_wait_timeout.restype = ctypes.c_int
         lib.relation_check_device_status.argtypes = []
@@ -389,6 +419,32 @@ def linear_gate_fwd_bwd(P1, P2, I, R, A_log, dt_bias, dY, tau_S: float, layout: 
     return Y, dP1, dP2, dI, dR, dA, dB
 
 
+def relation_paged_plan(prob: Paged, cached, fresh, free_pages, block_table, starts, slots, positions, used,
+                        stream=None) -> None:
+    _check(load().relation_paged_plan(ctypes.byref(prob), _ptr(cached), _ptr(fresh), _ptr(free_pages),
+                                      0 if free_pages is None else free_pages.numel(), _ptr(block_table),
+                                      _ptr(starts), _ptr(slots), _ptr(positions), _ptr(used), _stream_ptr(stream)),
+           "relation_paged_plan")
+
+
+def relation_paged_store(prob: Paged, X1, X2, I, theta, pairing, rope_base, positions, slots, P1, P2_pages, I_pages,
+                         stream=None) -> None:
+    _check(load().relation_paged_store(ctypes.byref(prob), _ptr(X1), _ptr(X2), _ptr(I), _ptr(theta), pairing,
+                                       rope_base, _ptr(positions), _ptr(slots), _ptr(P1), _ptr(P2_pages),
+                                       _ptr(I_pages), _stream_ptr(stream)), "relation_paged_store")
+
+
+def relation_paged_workspace_bytes(prob: Paged, max_fresh: int) -> int:
+    return int(load().relation_paged_workspace_bytes(ctypes.byref(prob), int(max_fresh)))
+
+
+def relation_paged_fwd(prob: Paged, P1, P2_pages, I_pages, block_table, starts, cached, max_fresh, Y, L, workspace,
+                       stream=None) -> None:
+    _check(load().relation_paged_fwd(ctypes.byref(prob), _ptr(P1), _ptr(P2_pages), _ptr(I_pages), _ptr(block_table),
+                                     _ptr(starts), _ptr(cached), max_fresh, _ptr(Y), _ptr(L), _ptr(workspace),
+                                     workspace.nbytes, _stream_ptr(stream)), "relation_paged_fwd")
+
+
 def relation_check_device_status() -> int:
     return int(load().relation_check_device_status())
 
@@ -506,3 +562,108 @@ def bwd(P1, P2, V, Y, L, dY, tau_S: float, lam: float, causal: bool = True, stre
         workspace = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=P1.device)
     relation_bwd(prob, P1, P2, V, Y, L, dY, dP1, dP2, dV, dlam, workspace, stream)
     return dP1, dP2, dV, dlam
+
+
+# ------------------------------------------------------- paged Relation Cache
+_DTYPE_CODES = {torch.bfloat16: RELATION_BF16, torch.float32: RELATION_F32}
+
+
+def paged_row(d_h: int, dtype) -> int:
+    """Elements from one cached row to the next (rows start on 16 bytes: bf16 d_h = 60 takes 64)."""
+    return -(-d_h // 8) * 8 if dtype == torch.bfloat16 else d_h
+
+
+def paged_pages(pages: int, G: int, page_size: int, d_h: int, dtype, layout: int = RELATION_LAYOUT_BHTD,
+                device="cuda"):
+    """A pair of page pools (P2_pages, I_pages), zeroed."""
+    shape = (pages, G, page_size) if layout == RELATION_LAYOUT_BHTD else (pages, page_size, G)
+    return tuple(torch.zeros(*shape, paged_row(d_h, dtype), dtype=dtype, device=device) for _ in range(2))
+
+
+def _want(t, dtype, name):
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def paged_for(heads, pages, R: int, table_width: int, tau_S: float, lam: float, layout: int) -> Paged:
+    """Problem for packed tensors [N, H, d_h] (heads: the P1 / X1 tensor) over a page pool."""
+    N, H, d = heads.shape
+    if pages.dim() != 4 or pages.dtype is not heads.dtype or heads.dtype not in _DTYPE_CODES:
+        raise ValueError("pages are 4-D and of the packed tensors' dtype (bfloat16 or float32)")
+    if layout == RELATION_LAYOUT_BHTD:
+        P, G, page, row = pages.shape
+    elif layout == RELATION_LAYOUT_BTHD:
+        P, page, G, row = pages.shape
+    else:
+        raise ValueError(f"unknown layout {layout}")
+    if row != paged_row(d, heads.dtype):
+        raise ValueError(f"pages hold rows of {row}, heads of {d} need {paged_row(d, heads.dtype)}")
+    return Paged(R, N, H, G, d, P, page, table_width, _DTYPE_CODES[heads.dtype], tau_S, lam, layout)
+
+
+def paged_plan(cached, fresh, free_pages, block_table, pages: int, page_size: int, starts, slots, positions, used,
+               stream=None) -> None:
+    """Block tables and slot maps of a step: fills block_table (new entries), starts [R + 1], slots [N],
+    positions [N] and used [1] from the requests' lengths (all int32, slots int64)."""
+    for t, name in ((cached, "cached"), (fresh, "fresh"), (block_table, "block_table"), (starts, "starts"),
+                    (positions, "positions"), (used, "used")):
+        _want(t, torch.int32, name)
+    _want(slots, torch.int64, "slots")
+    R, width = block_table.shape
+    N = slots.shape[0]
+    if cached.shape[0] != R or fresh.shape[0] != R or starts.shape[0] != R + 1 or positions.shape[0] != N:
+        raise ValueError("cached and fresh are [R], starts [R + 1], positions and slots [N]")
+    if free_pages is not None:
+        _want(free_pages, torch.int32, "free_pages")
+    # The plan reads sizes only: heads, width and dtype are stand-ins.
+    relation_paged_plan(Paged(R, N, 1, 1, 64, pages, page_size, width, RELATION_BF16, 1.0, 0.0, RELATION_LAYOUT_BHTD),
+                        cached, fresh, free_pages, block_table, starts, slots, positions, used, stream)
+
+
+def paged_store(X1, X2, I, theta, pairing: int, rope_base: float, positions, slots, P1, P2_pages, I_pages,
+                layout: int = RELATION_LAYOUT_BHTD, stream=None) -> None:
+    """RoPE and Givens mixing of packed new tokens, P1 [N, H, d_h] written in place of a copy and the cached rows
+    into their pages; theta None stores the states unmixed."""
+    _want(positions, torch.int32, "positions")
+    _want(slots, torch.int64, "slots")
+    prob = paged_for(X1, P2_pages, 1, 1, 1.0, 0.0, layout)
+    N, G = prob.N, prob.G
+    if X2.shape != I.shape or X2.shape[:2] != (N, G) or X2.shape[2] != prob.d_h or P1.shape != X1.shape or \
+            I_pages.shape != P2_pages.shape or positions.shape[0] != N or slots.shape[0] != N:
+        raise ValueError("X1, P1 are [N, H, d_h], X2, I [N, G, d_h], positions, slots [N], both page pools alike")
+    for t in (X2, I, P1, I_pages):
+        _want(t, X1.dtype, "X2, I, P1 and the pages")
+    relation_paged_store(prob, X1, X2, I, theta, pairing, rope_base, positions, slots, P1, P2_pages, I_pages, stream)
+
+
+def paged_workspace(prob: Paged, max_fresh: int, device="cuda") -> torch.Tensor:
+    """Workspace tensor for relation_paged_fwd."""
+    n = relation_paged_workspace_bytes(prob, max_fresh)
+    if n == 0:
+        raise ValueError("relation_paged_fwd has no workspace for this problem")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_fwd(P1, P2_pages, I_pages, block_table, starts, cached, max_fresh: int, tau_S: float, lam: float, Y=None,
+              L=None, workspace=None, layout: int = RELATION_LAYOUT_BHTD, stream=None):
+    """Relation of packed new tokens P1 [N, H, d_h] over the pages; returns (Y, L).  Y and workspace are allocated
+    when not given; L [N, H] float32 is filled when given."""
+    R, width = block_table.shape
+    prob = paged_for(P1, P2_pages, R, width, tau_S, lam, layout)
+    for t, name in ((block_table, "block_table"), (starts, "starts"), (cached, "cached")):
+        _want(t, torch.int32, name)
+    if starts.shape[0] != R + 1 or cached.shape[0] != R or I_pages.shape != P2_pages.shape or \
+            I_pages.dtype is not P1.dtype:
+        raise ValueError("starts is [R + 1], cached [R], both page pools alike")
+    if Y is None:
+        Y = torch.empty_like(P1)
+    elif Y.shape != P1.shape or Y.dtype is not P1.dtype:
+        raise ValueError("Y is like P1")
+    if L is not None:
+        _want(L, torch.float32, "L")
+        if L.shape != P1.shape[:2]:
+            raise ValueError("L is [N, H]")
+    if workspace is None:
+        workspace = paged_workspace(prob, max_fresh, P1.device)
+    relation_paged_fwd(prob, P1, P2_pages, I_pages, block_table, starts, cached, max_fresh, Y, L, workspace, stream)
+    return Y, L

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/relation.h"
+#include "api_internal.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -45,6 +46,33 @@ relation_status_t device_info(DeviceInfo* out) {
     out->num_sms = g_num_sms[dev];
     return RELATION_OK;
 }
+
+}  // namespace
+
+relation_status_t api_device(unsigned int** status, int* num_sms) {
+    DeviceInfo di;
+    const relation_status_t st = device_info(&di);
+    if (st != RELATION_OK) return st;
+    *status = di.status;
+    *num_sms = di.num_sms;
+    return RELATION_OK;
+}
+
+void api_set_launches(int n) { t_last_launches = n; }
+
+// RoPE frequencies base^(-2c/d) / (2 pi) for c < d/2 as float pairs (computed in double).
+RopeTable rope_table(int d, float base) {
+    RopeTable tab{};
+    tab.enabled = base > 0.f ? 1 : 0;
+    for (int c = 0; c < d / 2 && tab.enabled; ++c) {
+        const double f = pow((double)base, -2.0 * c / d) / (2.0 * 3.14159265358979323846);
+        tab.hi[c] = (float)f;
+        tab.lo[c] = (float)(f - (double)tab.hi[c]);
+    }
+    return tab;
+}
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -576,18 +604,6 @@ relation_status_t relation_check_device_status(void) {
 
 namespace relation {
 namespace {
-// RoPE frequencies base^(-2c/d) / (2 pi) for c < d/2 as float pairs (computed in double).
-RopeTable rope_table(int d, float base) {
-    RopeTable tab{};
-    tab.enabled = base > 0.f ? 1 : 0;
-    for (int c = 0; c < d / 2 && tab.enabled; ++c) {
-        const double f = pow((double)base, -2.0 * c / d) / (2.0 * 3.14159265358979323846);
-        tab.hi[c] = (float)f;
-        tab.lo[c] = (float)(f - (double)tab.hi[c]);
-    }
-    return tab;
-}
-
 relation_status_t check_prologue(const relation_problem_t* p, const void* const* in, int n_in, const void* const* out,
                                  int n_out, const float* theta, int pairing, float rope_base) {
     relation_status_t st = check_problem(p);
