@@ -6,7 +6,7 @@
 // One warp per (token, head): lanes over 32 keys for U, over columns for Y.
 #include <math.h>
 
-#include "paged.h"
+#include "paged_fwd.cuh"
 
 namespace relation {
 namespace {
@@ -22,7 +22,7 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads)
     paged_fwd_rows_kernel(PagedProblem pp, const T* __restrict__ P1, const T* __restrict__ P2, const T* __restrict__ I,
                           const int* __restrict__ table, const int* __restrict__ starts,
-                          const int* __restrict__ cached, int max_fresh, T* __restrict__ Y, float* __restrict__ L,
+                          const int* __restrict__ cached, int max_fresh, int rows_above, T* __restrict__ Y, float* __restrict__ L,
                           unsigned int* status) {
     __shared__ float sq[kThreads / 32][128];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -43,6 +43,7 @@ __global__ void __launch_bounds__(kThreads)
         if (lane == 0) record_status(status, kDevBadPosition);
         return;
     }
+    if ((int64_t)(last - first) * pp.group <= rows_above) return;
     const int i = c + (int)(n - first);
     const T* q = P1 + ((size_t)n * pp.H + h) * pp.d;
     for (int k = lane; k < pp.d; k += 32) sq[warp][k] = load_as_float(q + k) * pp.inv_sqrt_d;
@@ -93,19 +94,26 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-size_t paged_fwd_workspace(const PagedProblem&, bool, int, int) { return 16; }
+size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, int, int num_sms) {
+    return bf16 ? paged_few_workspace(pp, num_sms) : 16;
+}
 
 cudaError_t launch_paged_fwd(const PagedProblem& pp, bool bf16, const PagedFwdArgs& a, int* launches, cudaStream_t s) {
     const unsigned blocks = (unsigned)(((int64_t)pp.N * pp.H + kThreads / 32 - 1) / (kThreads / 32));
-    if (bf16)
+    *launches = 1;
+    if (bf16) {
+        cudaError_t e = launch_paged_few(pp, a, a.workspace, s);
+        *launches = 2;
+        if (e != cudaSuccess || (int64_t)a.max_fresh * pp.group <= kPagedFewRows) return e;
+        *launches = 3;
         paged_fwd_rows_kernel<__nv_bfloat16><<<blocks, kThreads, 0, s>>>(
             pp, (const __nv_bfloat16*)a.P1, (const __nv_bfloat16*)a.P2_pages, (const __nv_bfloat16*)a.I_pages, a.table,
-            a.starts, a.cached, a.max_fresh, (__nv_bfloat16*)a.Y, a.L, a.status);
-    else
+            a.starts, a.cached, a.max_fresh, kPagedFewRows, (__nv_bfloat16*)a.Y, a.L, a.status);
+    } else {
         paged_fwd_rows_kernel<float><<<blocks, kThreads, 0, s>>>(
             pp, (const float*)a.P1, (const float*)a.P2_pages, (const float*)a.I_pages, a.table, a.starts, a.cached,
-            a.max_fresh, (float*)a.Y, a.L, a.status);
-    *launches = 1;
+            a.max_fresh, 0, (float*)a.Y, a.L, a.status);
+    }
     return cudaGetLastError();
 }
 

@@ -1,0 +1,62 @@
+// How the paged forward's work is cut among its workers.
+//
+// Unit: one (request, cache head, row tile): `rows_per_tile` of the request's
+// packed rows (row = token * group + head in the group) against the history its
+// last token sees, in key tiles of `keys`.  All units' key tiles in a fixed order
+// (request, cache head, row tile, key tile) form one line, and worker w of W takes
+// the tiles [w total / W, (w + 1) total / W): every worker has the same number of
+// tiles, within one, whatever the requests' lengths are.  A unit that a boundary
+// cuts is merged from its pieces afterwards.
+//
+// The line's length is known on the device only: every block sums the requests'
+// tiles itself (schedule_build), so the host launches a fixed grid.
+#pragma once
+
+#include <stdint.h>
+
+namespace relation {
+
+// sum_{i < n} floor((a i + b) / m) for n, a, b >= 0, m >= 1, by the Euclidean
+// recursion: whole multiples of m leave a and b, then the lattice points under the
+// line are counted along the other axis.
+__host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, int64_t b) {
+    int64_t sum = 0;
+    while (n > 0) {
+        sum += (a / m) * (n * (n - 1) / 2) + (b / m) * n;
+        a %= m;
+        b %= m;
+        const int64_t top = a * n + b;
+        if (top < m) break;
+        n = top / m;
+        b = top - n * m;
+        const int64_t t = m;
+        m = a;
+        a = t;
+    }
+    return sum;
+}
+
+template <int kRowsPerTile, int kKeys>
+struct Tiling {
+    // Key tiles of row tile q of a request with `rows` packed rows and c cached tokens.
+    __host__ __device__ static int tiles(int c, int rows, int group, int q) {
+        const int last = (rows < (q + 1) * kRowsPerTile ? rows : (q + 1) * kRowsPerTile) - 1;
+        return (int)(((int64_t)c + last / group + kKeys) / kKeys);
+    }
+    __host__ __device__ static int row_tiles(int rows) { return (rows + kRowsPerTile - 1) / kRowsPerTile; }
+    // Key tiles of the first n row tiles.  Full row tiles: ceil((c + ceil(x / g)) / k)
+    // with x = (q + 1) rows_per_tile is ceil((c g + x) / (g k)).
+    __host__ __device__ static int64_t tiles_before(int c, int rows, int group, int n) {
+        const int full = n < rows / kRowsPerTile ? n : rows / kRowsPerTile;
+        int64_t s = 0;
+        if (full <= 2) {
+            for (int q = 0; q < full; ++q) s += tiles(c, rows, group, q);
+        } else {
+            const int64_t m = (int64_t)group * kKeys;
+            s = floor_sum(full, m, kRowsPerTile, (int64_t)c * group + kRowsPerTile + m - 1);
+        }
+        return n > full ? s + tiles(c, rows, group, full) : s;
+    }
+};
+
+}  // namespace relation

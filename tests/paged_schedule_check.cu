@@ -1,0 +1,45 @@
+// Host walk of the paged forward's schedule (csrc/paged_schedule.cuh): prints
+// "ok" when every request's row tiles add up to what tiles_before says, for every
+// prefix, by direct summation.  Built and run on the host by test_paged_schedule.py.
+#include <cstdio>
+
+#include "paged_schedule.cuh"
+
+using namespace relation;
+
+template <int ROWS, int KEYS>
+bool check() {
+    using T = Tiling<ROWS, KEYS>;
+    for (int group : {1, 2, 3, 4, 5, 7, 8, 16, 17, 40, 128, 300})
+        for (int c : {0, 1, 15, 16, 31, 32, 33, 127, 128, 129, 1000, 32767})
+            for (int fresh : {1, 2, 3, 15, 16, 17, 31, 64, 100, 129, 777, 2048}) {
+                const int rows = fresh * group;
+                int64_t sum = 0;
+                for (int q = 0; q <= T::row_tiles(rows); ++q) {
+                    if (T::tiles_before(c, rows, group, q) != sum) {
+                        std::printf("rows/tile %d keys %d group %d cached %d fresh %d: first %d tiles\n", ROWS, KEYS, group,
+                                    c, fresh, q);
+                        return false;
+                    }
+                    if (q == T::row_tiles(rows)) break;
+                    // by definition: the tiles up to the position of the row tile's last token
+                    const int last = (rows < (q + 1) * ROWS ? rows : (q + 1) * ROWS) - 1;
+                    sum += (c + last / group) / KEYS + 1;
+                }
+            }
+    return true;
+}
+
+int main() {
+    for (int64_t n : {0, 1, 2, 5, 17})
+        for (int64_t m : {1, 2, 7, 128})
+            for (int64_t a : {0, 1, 5, 129, 1000})
+                for (int64_t b : {0, 3, 127, 4096}) {
+                    int64_t s = 0;
+                    for (int64_t i = 0; i < n; ++i) s += (a * i + b) / m;
+                    if (s != floor_sum(n, m, a, b)) return std::printf("floor_sum %ld %ld %ld %ld\n", (long)n, (long)m, (long)a, (long)b), 1;
+                }
+    if (!check<16, 32>() || !check<256, 128>() || !check<64, 64>()) return 1;
+    std::printf("ok\n");
+    return 0;
+}
