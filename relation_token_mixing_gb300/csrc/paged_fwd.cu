@@ -6,6 +6,8 @@
 // One warp per (token, head): lanes over 32 keys for U, over columns for Y.
 #include <math.h>
 
+#include <algorithm>
+
 #include "paged_fwd.cuh"
 
 namespace relation {
@@ -94,26 +96,26 @@ __global__ void __launch_bounds__(kThreads)
 
 }  // namespace
 
-size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, int, int num_sms) {
-    return bf16 ? paged_few_workspace(pp, num_sms) : 16;
+size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, int max_fresh, int num_sms) {
+    if (!bf16) return 16;
+    // The two kernels run one after the other on the caller's stream and share the workspace.
+    const size_t few = paged_few_workspace(pp, num_sms);
+    return (int64_t)max_fresh * pp.group <= kPagedFewRows ? few : std::max(few, paged_tc_workspace(pp, num_sms));
 }
 
 cudaError_t launch_paged_fwd(const PagedProblem& pp, bool bf16, const PagedFwdArgs& a, int* launches, cudaStream_t s) {
-    const unsigned blocks = (unsigned)(((int64_t)pp.N * pp.H + kThreads / 32 - 1) / (kThreads / 32));
-    *launches = 1;
     if (bf16) {
-        cudaError_t e = launch_paged_few(pp, a, a.workspace, s);
+        const cudaError_t e = launch_paged_few(pp, a, a.workspace, s);
         *launches = 2;
         if (e != cudaSuccess || (int64_t)a.max_fresh * pp.group <= kPagedFewRows) return e;
-        *launches = 3;
-        paged_fwd_rows_kernel<__nv_bfloat16><<<blocks, kThreads, 0, s>>>(
-            pp, (const __nv_bfloat16*)a.P1, (const __nv_bfloat16*)a.P2_pages, (const __nv_bfloat16*)a.I_pages, a.table,
-            a.starts, a.cached, a.max_fresh, kPagedFewRows, (__nv_bfloat16*)a.Y, a.L, a.status);
-    } else {
-        paged_fwd_rows_kernel<float><<<blocks, kThreads, 0, s>>>(
-            pp, (const float*)a.P1, (const float*)a.P2_pages, (const float*)a.I_pages, a.table, a.starts, a.cached,
-            a.max_fresh, 0, (float*)a.Y, a.L, a.status);
+        *launches = 4;
+        return launch_paged_tc(pp, a, a.workspace, s);
     }
+    const unsigned blocks = (unsigned)(((int64_t)pp.N * pp.H + kThreads / 32 - 1) / (kThreads / 32));
+    *launches = 1;
+    paged_fwd_rows_kernel<float><<<blocks, kThreads, 0, s>>>(
+        pp, (const float*)a.P1, (const float*)a.P2_pages, (const float*)a.I_pages, a.table, a.starts, a.cached,
+        a.max_fresh, 0, (float*)a.Y, a.L, a.status);
     return cudaGetLastError();
 }
 

@@ -154,9 +154,6 @@ struct PieceMeta {
 // this much (a factor 256): exact, numerator and denominator share it.
 constexpr float kRaise = 8.f;
 
-template <typename T>
-__device__ __forceinline__ void store_row_scalar(T* y, int col, float v) { store_from_float(y + col, v); }
-
 }  // namespace paged
 
 // The kernels' launches (paged_few.cu: a request's packed rows fit 32; paged_tc.cu:
@@ -164,6 +161,8 @@ __device__ __forceinline__ void store_row_scalar(T* y, int col, float v) { store
 constexpr int kPagedFewRows = 32;
 size_t paged_few_workspace(const PagedProblem& pp, int num_sms);
 cudaError_t launch_paged_few(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s);
+size_t paged_tc_workspace(const PagedProblem& pp, int num_sms);
+cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s);
 
 // The 4-D map (column, token of a page, cache head, page) of a bf16 page pool, box
 // 64 columns x box_rows tokens, 128-byte swizzle; columns past d read as zero.

@@ -1,0 +1,681 @@
+// Relation of a chunk of new tokens over a paged cache on the tensor cores (bf16
+// in, fp32 accumulate): prompts and prompt chunks ("Ask Self, Ask Others", Sec.
+// 3.1 eq.(1)-(3), Sec. 5.3 eq.(18), Appendix A.5).  Per new token at zero-based
+// position i, U_j = p1 . p2_j / sqrt(d), R_j = SiLU(U_j) for j < i, R_i =
+// sigmoid(U_i / tau_S) + lambda log(i + 1) (the count correction moved to the
+// diagonal: softmax does not see a shift of the whole row), Y = softmax(R) I~.
+//
+// A unit is one request's 256 packed rows (row = token * group + head in the group,
+// so grouped heads share one read of their cache head) of one cache head against
+// the keys up to its last token, in tiles of 128.  The kernel is persistent: the
+// blocks cut all units' key tiles into equal parts (paged_schedule.cuh), so a few
+// long rows fill the GPU as well as many short ones, and a second kernel merges the
+// units that the cuts divide.
+//   warp 0      key producer: the pages of each key tile by TMA, one copy per lane
+//   warp 1      MMA issuer and TMEM owner
+//   warps 2-3   query rows into shared memory; clear the keys past a request's end
+//   warps 4-7   softmax of rows 0-127 (one thread per row)
+//   warps 8-11  softmax of rows 128-255
+// Per key tile, per 128-row half: S = Q K^T (both in shared memory) -> registers:
+// SiLU, mask and Self where the tile reaches the rows' own tokens, online softmax ->
+// P as bf16 in TMEM -> O += P V.  At d <= 64 P has TMEM columns of its own and the
+// next S is issued while the softmax works; at d 80 and 128 P overwrites S and the
+// two halves take turns on the special-function unit.
+//
+// Bound: two special functions per score (tanh, 16 results a cycle and SM; ex2, 32)
+// give 3/32 cycle a score, against 4 d / 8192 = 1/32 cycle (d = 64) or 1/16 (d =
+// 128) of tensor-core time, so the special-function unit, not the tensor core, is
+// the limit at d = 64 and is near it at d = 128.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include "paged_fwd.cuh"
+
+namespace relation {
+namespace paged {
+namespace {
+
+constexpr int kBM = 128, kRows = 256, kKeys = 128;
+constexpr int kThreads = 384;
+// 128 * 56 + 256 * 224 = 64512 = 384 * 168 registers.
+constexpr uint32_t kRegsControl = 56, kRegsSoftmax = 224;
+constexpr int kPanelBytes = 128 * 128;  // 128 rows x 64 bf16
+constexpr int kMinTiles = 2;
+using TcTiling = Tiling<kRows, kKeys>;
+
+template <int D>
+struct TcCfg {
+    static constexpr bool kSepP = D == 64;
+    static constexpr uint32_t kColP = 384;
+    static constexpr int kPanels = D / 64;
+    static constexpr int kTileBytes = kBM * D * 2;
+    static constexpr int kStages = D == 64 ? 4 : 2;
+    static constexpr int kTiles = (2 + 2 * kStages) * kTileBytes;
+    static int smem(int R) { return 1024 + kTiles + 1024 + (R * 4 + 15) / 16 * 16; }
+    static constexpr size_t kSlotFloats = (size_t)kRows * (D + 2);  // o [D/4][256][4], then (m, l) [256]
+};
+
+struct TcBars {
+    uint64_t q_full, q_free;
+    uint64_t k_full[4], v_full[4], kv_empty[4];
+    // In turn: the cleared tile of a piece may be ready before the one of the piece
+    // before has been waited for (never two pieces ahead: q_free holds that back).
+    uint64_t v_clean[2];
+    uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
+    uint64_t turn[2][4];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort_flag;
+    int sums[12];
+};
+static_assert(sizeof(TcBars) <= 1024, "the barriers' region");
+
+__device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
+__device__ __forceinline__ uint32_t as_u(float f) { return __float_as_uint(f); }
+
+// One worker's piece of a unit: key tiles j0 .. j1 - 1, and for each half of the
+// rows how many of them it sees.
+struct Segment {
+    int j0, j1;
+    int rows[2], steps[2], most;
+    int len;    // the request's tokens
+    int tail;   // key tile that the request ends inside (-1: not in this piece)
+};
+__device__ __forceinline__ Segment segment_of(const Cursor& k, int group, int64_t end) {
+    Segment s;
+    s.j0 = k.j;
+    s.j1 = (int)min((int64_t)k.n, k.j + (end - k.f));
+    s.most = 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const int base = k.q * kRows + t * kBM;
+        s.rows[t] = max(0, min(kBM, k.rq.rows - base));
+        const int n = s.rows[t] ? (k.rq.c + (base + s.rows[t] - 1) / group + kKeys) / kKeys : 0;
+        s.steps[t] = max(0, min(s.j1, n) - s.j0);
+        s.most = max(s.most, s.steps[t]);
+    }
+    s.len = k.rq.c + k.rq.rows / group;
+    const int tail = s.len / kKeys;
+    s.tail = (s.len % kKeys != 0 && tail >= s.j0 && tail < s.j0 + s.most) ? tail : -1;
+    return s;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                    const __grid_constant__ FwdView v, const __nv_bfloat16* __restrict__ P1,
+                    __nv_bfloat16* __restrict__ Y, float* __restrict__ L, float* __restrict__ part,
+                    PieceMeta* __restrict__ meta) {
+    using C = TcCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sQ = smem;
+    uint8_t* sK = sQ + 2 * C::kTileBytes;
+    uint8_t* sV = sK + C::kStages * C::kTileBytes;
+    TcBars* bars = reinterpret_cast<TcBars*>(smem + C::kTiles);
+    int* prefix = reinterpret_cast<int*>(smem + C::kTiles + 1024);
+    const PagedProblem& pp = v.pp;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (threadIdx.x == 0) {
+        ptx::mbar_init(&bars->q_full, 2);
+        ptx::mbar_init(&bars->q_free, 1);
+        for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&bars->s_full[t], 1);
+            ptx::mbar_init(&bars->s_free[t], 128);
+            ptx::mbar_init(&bars->p_full[t], 128);
+            ptx::mbar_init(&bars->o_done[t], 1);
+            ptx::mbar_init(&bars->v_clean[t], 2);
+            for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[t][q], 1);
+        }
+        for (int s = 0; s < C::kStages; ++s) {
+            ptx::mbar_init(&bars->k_full[s], 1);
+            ptx::mbar_init(&bars->v_full[s], 1);
+            ptx::mbar_init(&bars->kv_empty[s], 1);
+        }
+        ptx::mbar_init(&bars->drain, 1);
+        bars->abort_flag = 0;
+        ptx::fence_barrier_init();
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
+    }
+    const int64_t total = (int64_t)schedule_build<TcTiling>(v, prefix, bars->sums) * pp.G;
+    const int worker = blockIdx.x;
+    int64_t lo, hi;
+    worker_range(total, (int)gridDim.x, kMinTiles, worker, &lo, &hi);
+    if (lo >= hi) {
+        if (threadIdx.x == 0) meta[worker] = PieceMeta{-1, -1, 0, 0, 0, 0, 0, 0};
+        return;
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc(&bars->tmem_base, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = bars->tmem_base;
+    volatile int* abort_flag = &bars->abort_flag;
+    Cursor k;
+    cursor_seek<TcTiling>(k, v, prefix, lo);
+    bool ok = true;
+    if (warp == 0) {
+        // ------------------------------------------------------------ keys
+        ptx::regs_dec<kRegsControl>();
+        const int box = min(pp.page, kKeys);
+        const int boxes = kKeys / box;
+        int kt = 0, tb0 = -1, tb_r = -1, tb = 0;
+        while (ok && k.f < hi) {
+            const Segment sg = segment_of(k, pp.group, hi);
+            const int need = (sg.len + pp.page_mask) >> pp.page_shift;
+            for (int j = sg.j0; j < sg.j0 + sg.most; ++j, ++kt) {
+                const int s = kt % C::kStages;
+                const int tok = j * kKeys, k0 = tok >> pp.page_shift;
+                if (k.r != tb_r || k0 < tb0 || k0 + boxes > tb0 + 32) {
+                    tb_r = k.r;
+                    tb0 = k0;
+                    tb = 0;
+                    if (tb0 + lane < need) {
+                        tb = v.table[(size_t)k.r * pp.width + tb0 + lane];
+                        // Out of range reads as zeros (the map's bound), and is reported.
+                        if (tb < 0 || tb >= pp.pages) {
+                            record_status(v.status, kDevBadPosition);
+                            tb = pp.pages;
+                        }
+                    }
+                }
+                if (kt >= C::kStages && !ptx::mbar_wait_warp(&bars->kv_empty[s], ((kt / C::kStages) - 1) & 1,
+                                                             abort_flag, v.status, kDevTimeoutEmpty)) {
+                    ok = false;
+                    break;
+                }
+                const int parts = min(boxes, need - k0), copies = C::kPanels * parts;
+                const int p = lane / C::kPanels, panel = lane % C::kPanels;
+                const int page = __shfl_sync(0xffffffffu, tb, (k0 - tb0 + p) & 31);
+                const int off = panel * kPanelBytes + p * box * 128, y = boxes > 1 ? 0 : (tok & pp.page_mask);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->k_full[s], copies * box * 128);
+                __syncwarp();
+                if (lane < copies)
+                    ptx::tma_load_4d(sK + s * C::kTileBytes + off, &tm_k, &bars->k_full[s], panel * 64, y, k.g, page);
+                if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->v_full[s], copies * box * 128);
+                __syncwarp();
+                if (lane < copies)
+                    ptx::tma_load_4d(sV + s * C::kTileBytes + off, &tm_v, &bars->v_full[s], panel * 64, y, k.g, page);
+            }
+            k.f += sg.j1 - sg.j0;
+            cursor_next_unit<TcTiling>(k, v, prefix, hi);
+        }
+        if (*abort_flag) {
+            // Let the copies already issued land before the block exits.
+            for (int x = max(0, kt - C::kStages); x < kt; ++x) {
+                ptx::mbar_drain(&bars->k_full[x % C::kStages], (x / C::kStages) & 1, v.status);
+                ptx::mbar_drain(&bars->v_full[x % C::kStages], (x / C::kStages) & 1, v.status);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        ptx::regs_dec<kRegsControl>();
+        const uint32_t id_s = ptx::idesc_bf16(kBM, kKeys, false, false);
+        const uint32_t id_o = ptx::idesc_bf16(kBM, D, false, true);
+        const uint64_t dq0 = ptx::smem_desc(ptx::smem_u32(sQ), 16, 1024, ptx::kSwizzle128B);
+        const uint64_t dk0 = ptx::smem_desc(ptx::smem_u32(sK), 16, 1024, ptx::kSwizzle128B);
+        const uint64_t dv0 = ptx::smem_desc(ptx::smem_u32(sV), kPanelBytes, 1024, ptx::kSwizzle128B);
+        constexpr uint64_t kTileStep = C::kTileBytes >> 4, kPanelStep = kPanelBytes >> 4;
+        auto issue_s = [&](int t, int s) {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                const uint64_t off = (ks / 4) * kPanelStep + (ks % 4) * 2;  // 32 bytes per K-step
+                ptx::mma_ss_elect(tmem + t * 128, dq0 + t * kTileStep + off, dk0 + s * kTileStep + off, id_s,
+                                  ks > 0 ? 1u : 0u);
+            }
+            ptx::mma_commit_elect(&bars->s_full[t]);
+        };
+        auto issue_pv = [&](int t, int s, bool accumulate) {
+            const uint32_t p_col = C::kSepP ? C::kColP + 64 * t : 128 * t;
+#pragma unroll
+            for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys of V per K-step: 2048 bytes of the MN-major tile
+                ptx::mma_ts_elect(tmem + 256 + t * D, tmem + p_col + ks * 8, dv0 + s * kTileStep + ks * 128, id_o,
+                                  (accumulate || ks > 0) ? 1u : 0u);
+            ptx::mma_commit_elect(&bars->o_done[t]);
+        };
+        auto wait = [&](uint64_t* bar, int phase, unsigned code) {
+            if (ok) ok = ptx::mbar_wait_warp(bar, phase & 1, abort_flag, v.status, code);
+            return ok;
+        };
+        int kt = 0, seg = 0, tails = 0, st[2] = {0, 0};
+        while (ok && k.f < hi) {
+            const Segment sg = segment_of(k, pp.group, hi);
+            if (!wait(&bars->q_full, seg, kDevTimeoutFull)) break;
+            if (!wait(&bars->k_full[kt % C::kStages], kt / C::kStages, kDevTimeoutFull)) break;
+            for (int t = 0; t < 2; ++t) {
+                if (sg.steps[t] == 0) continue;
+                // S of the piece before has been read (d > 64: its P V, issued before, read it).
+                if (C::kSepP && st[t] > 0 && !wait(&bars->s_free[t], st[t] - 1, kDevTimeoutFull)) break;
+                ptx::tc_fence_after();
+                issue_s(t, kt % C::kStages);
+            }
+            if (!ok) break;
+            if (sg.most == 1) ptx::mma_commit_elect(&bars->q_free);
+            for (int j = 0; ok && j < sg.most; ++j) {
+                const int s = (kt + j) % C::kStages, s1 = (kt + j + 1) % C::kStages, next = (kt + j + 1) / C::kStages;
+                bool v_ready = false, k_next = false;
+                auto v_wait = [&]() {
+                    if (v_ready) return true;
+                    v_ready = sg.j0 + j == sg.tail ? wait(&bars->v_clean[tails & 1], tails >> 1, kDevTimeoutFull)
+                                                   : wait(&bars->v_full[s], (kt + j) / C::kStages, kDevTimeoutFull);
+                    return v_ready;
+                };
+                auto k_wait = [&]() {
+                    if (!k_next) k_next = wait(&bars->k_full[s1], next, kDevTimeoutFull);
+                    return k_next;
+                };
+                if constexpr (C::kSepP) {
+                    for (int t = 0; t < 2; ++t) {  // the next S as soon as the softmax holds this one
+                        if (j + 1 >= sg.steps[t]) continue;
+                        if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait()) break;
+                        ptx::tc_fence_after();
+                        issue_s(t, s1);
+                    }
+                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free);
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j >= sg.steps[t]) continue;
+                        if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
+                        ptx::tc_fence_after();
+                        issue_pv(t, s, j > 0);
+                    }
+                } else {
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j >= sg.steps[t]) continue;
+                        if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
+                        ptx::tc_fence_after();
+                        issue_pv(t, s, j > 0);
+                        if (j + 1 < sg.steps[t]) {
+                            if (!k_wait()) break;
+                            ptx::tc_fence_after();
+                            issue_s(t, s1);
+                        }
+                    }
+                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free);
+                }
+                if (ok) ptx::mma_commit_elect(&bars->kv_empty[s]);
+            }
+            kt += sg.most;
+            ++seg;
+            tails += sg.tail >= 0;
+            st[0] += sg.steps[0];
+            st[1] += sg.steps[1];
+            k.f += sg.j1 - sg.j0;
+            cursor_next_unit<TcTiling>(k, v, prefix, hi);
+        }
+        ptx::mma_commit_elect(&bars->drain);
+        ptx::mbar_drain(&bars->drain, 0, v.status);
+    } else if (warp < 4) {
+        // ------------------------------------------------ queries, keys past the end
+        ptx::regs_dec<kRegsControl>();
+        constexpr int kChunks = D / 8, kStep = 64 / kChunks;  // 16-byte chunks of a row; rows at a time
+        const int tr = threadIdx.x - 64, chunk = tr % kChunks;
+        const uint32_t q_u = ptx::smem_u32(sQ) + (chunk / 8) * kPanelBytes;
+        const int cols = max(0, min(8, pp.d - chunk * 8));
+        PieceMeta mine{-1, -1, 0, 0, 0, 0, 0, 0};
+        int kt = 0, seg = 0, tails = 0;
+        while (ok && k.f < hi) {
+            const Segment sg = segment_of(k, pp.group, hi);
+            if (seg > 0 && !ptx::mbar_wait_warp(&bars->q_free, (seg - 1) & 1, abort_flag, v.status, kDevTimeoutEmpty)) {
+                ok = false;
+                break;
+            }
+            // Rows past the unit's are zero.
+            const int row_end = (sg.rows[1] ? 2 : 1) * kBM;
+            for (int r = tr / kChunks; r < row_end; r += kStep) {
+                const int rho = k.q * kRows + r;
+                const bool in = rho < k.rq.rows;
+                const int t = in ? rho / pp.group : 0, hd = k.g * pp.group + (in ? rho - t * pp.group : 0);
+                const __nv_bfloat16* src = P1 + ((size_t)(k.rq.first + t) * pp.H + hd) * pp.d + (cols ? chunk * 8 : 0);
+                const int bytes = in ? cols * 2 : 0, rr = r & 127;
+                const uint32_t dst = q_u + (r >> 7) * C::kTileBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4);
+                if ((pp.d & 7) == 0) {
+                    cp_async16(dst, src, bytes);
+                } else {  // rows of 120 bytes start on 8
+                    cp_async8(dst, src, min(bytes, 8));
+                    cp_async8(dst + 8, bytes > 8 ? src + 4 : src, max(bytes - 8, 0));
+                }
+            }
+            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&bars->q_full);
+            if (sg.tail >= 0) {
+                // Weight 0 times whatever a page holds past the end must be 0.
+                const int x = kt + sg.tail - sg.j0, s = x % C::kStages;
+                if (!ptx::mbar_wait_warp(&bars->v_full[s], (x / C::kStages) & 1, abort_flag, v.status, kDevTimeoutFull)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t* tile = sV + s * C::kTileBytes;
+                for (int r = sg.len - sg.tail * kKeys + tr / 8; r < kKeys; r += 8)
+#pragma unroll
+                    for (int p = 0; p < C::kPanels; ++p)
+                        *reinterpret_cast<uint4*>(tile + p * kPanelBytes + r * 128 + (tr & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bars->v_clean[tails & 1]);
+                ++tails;
+            }
+            if (sg.j0 > 0) {
+                mine.head = k.f - sg.j0;
+            } else if (sg.j1 < k.n) {
+                mine.tail = k.f;
+                mine.first = k.rq.first;
+                mine.c = k.rq.c;
+                mine.g = k.g;
+                mine.q = k.q;
+                mine.rows = k.rq.rows;
+            }
+            kt += sg.most;
+            ++seg;
+            k.f += sg.j1 - sg.j0;
+            cursor_next_unit<TcTiling>(k, v, prefix, hi);
+        }
+        if (threadIdx.x == 64) meta[worker] = ok ? mine : PieceMeta{-1, -1, 0, 0, 0, 0, 0, 0};
+    } else {
+        // ------------------------------------------------------------- softmax
+        ptx::regs_inc<kRegsSoftmax>();
+        const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
+        const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t s_col = t * 128, o_col = 256 + t * D;
+        const float c_half = 0.5f * pp.inv_sqrt_d;                // U/2 per raw dot product
+        const float c_diag = 0.5f * pp.inv_sqrt_d / pp.tau_S;     // U/(2 tau_S)
+        uint64_t* turn_mine = &bars->turn[t][quarter];
+        uint64_t* turn_next = &bars->turn[t ^ 1][quarter];
+        int st = 0, pairs = 0;  // steps of this half, and steps both halves took in turn
+        while (ok && k.f < hi) {
+            const Segment sg = segment_of(k, pp.group, hi);
+            const int steps = sg.steps[t], n_pair = C::kSepP ? 0 : min(sg.steps[0], sg.steps[1]);
+            const int base = k.q * kRows + t * kBM;
+            const int rho = min(base + r, k.rq.rows - 1);
+            const int token = rho / pp.group;
+            const int pos = k.rq.c + token;  // the row's own token: the last key it sees
+            const int first_pos = __shfl_sync(0xffffffffu, pos, 0);  // the warp's least
+            const float corr = pp.lambda * __logf((float)(pos + 1));
+            float m = -INFINITY, l = 0.f;
+            for (int j = 0; ok && j < steps; ++j) {
+                if (!ptx::mbar_wait_warp(&bars->s_full[t], (st + j) & 1, abort_flag, v.status, kDevTimeoutMma)) {
+                    ok = false;
+                    break;
+                }
+                ptx::tc_fence_after();
+                uint32_t sv[128];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    ptx::tmem_ld32(lane_addr + s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
+                ptx::tmem_ld_wait();
+                ptx::pin_regs(sv);
+                if constexpr (C::kSepP) {
+                    ptx::tc_fence_before();
+                    ptx::mbar_arrive(&bars->s_free[t]);  // the next S may overwrite it
+                } else {
+                    const int x = pairs + j;
+                    if (j < n_pair && x + t > 0 &&
+                        !ptx::mbar_wait_warp(turn_mine, (x + t - 1) & 1, abort_flag, v.status, kDevTimeoutMma)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::pin_regs(sv);  // the loops below start after the turn is taken
+                }
+                const int own = pos - (sg.j0 + j) * kKeys;  // the Self entry's column; later ones are masked
+                const bool edge = first_pos < (sg.j0 + j + 1) * kKeys;
+                float self = 0.f;
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) self = c == own ? as_f(sv[c]) : self;
+                    self = fmaf(0.5f, ptx::tanh_approx(self * c_diag), 0.5f) + corr;
+                }
+                const float2 ch2 = make_float2(c_half, c_half);
+#pragma unroll
+                for (int e = 0; e < 64; ++e) {
+                    const float2 h = ptx::mul2(make_float2(as_f(sv[2 * e]), as_f(sv[2 * e + 1])), ch2);
+                    const float2 th = make_float2(ptx::tanh_approx(h.x), ptx::tanh_approx(h.y));
+                    const float2 E = ptx::fma2(h, th, h);  // SiLU(U) = (U/2)(1 + tanh(U/2))
+                    sv[2 * e] = as_u(E.x);
+                    sv[2 * e + 1] = as_u(E.y);
+                }
+                if (edge) {
+#pragma unroll
+                    for (int c = 0; c < 128; ++c) {
+                        const float x = c > own ? -INFINITY : as_f(sv[c]);
+                        sv[c] = as_u(c == own ? self : x);
+                    }
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < 128; c += 8) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mx[q] = ptx::max3(mx[q], as_f(sv[c + 2 * q]), as_f(sv[c + 2 * q + 1]));
+                }
+                const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                const bool rescale = __any_sync(0xffffffffu, m_new > m + kRaise * kLn2);
+                float scale = 1.f;
+                if (rescale) {
+                    // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
+                    scale = m_new == -INFINITY ? 1.f : ptx::ex2_approx((m - m_new) * kLog2e);
+                    l *= scale;
+                    m = m_new;
+                }
+                const float m_ref = m == -INFINITY ? 0.f : m;
+                const float2 l2e2 = make_float2(kLog2e, kLog2e), nm2 = make_float2(-m_ref * kLog2e, -m_ref * kLog2e);
+                float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                make_float2(0.f, 0.f)};
+                uint32_t pk[2][32];
+#pragma unroll
+                for (int c = 0; c < 64; ++c) {
+                    const float2 y = ptx::fma2(make_float2(as_f(sv[2 * c]), as_f(sv[2 * c + 1])), l2e2, nm2);
+                    const float2 p = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+                    ls[c & 3] = ptx::add2(ls[c & 3], p);
+                    pk[c >> 5][c & 31] = ptx::pack_bf16x2(p.x, p.y);
+                }
+                {
+                    const float2 sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
+                    l += sum.x + sum.y;
+                }
+                if constexpr (!C::kSepP) {
+                    ptx::pin_regs(pk[0]);  // and end before it is passed on
+                    ptx::pin_regs(pk[1]);
+                    __syncwarp();
+                    if (j < n_pair && lane == 0) ptx::mbar_arrive(turn_next);
+                }
+                if (j > 0 && (C::kSepP || rescale)) {
+                    // P V of the tile before has read its P, and O is final for a rescale.
+                    if (!ptx::mbar_wait_warp(&bars->o_done[t], (st + j - 1) & 1, abort_flag, v.status, kDevTimeoutMma)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                }
+                const uint32_t p_col = C::kSepP ? C::kColP + 64 * t : s_col;
+                ptx::tmem_st32(lane_addr + p_col, pk[0]);
+                ptx::tmem_st32(lane_addr + p_col + 32, pk[1]);
+                if (rescale && j > 0) {
+#pragma unroll
+                    for (int c0 = 0; c0 < D / 32; ++c0) {
+                        uint32_t ov[32];
+                        ptx::tmem_ld32(lane_addr + o_col + 32 * c0, ov);
+                        ptx::tmem_ld_wait();
+                        ptx::pin_regs(ov);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) ov[e] = as_u(as_f(ov[e]) * scale);
+                        ptx::tmem_st32(lane_addr + o_col + 32 * c0, ov);
+                    }
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+                ptx::mbar_arrive(&bars->p_full[t]);
+            }
+            if (ok && steps > 0) {
+                ok = ptx::mbar_wait_warp(&bars->o_done[t], (st + steps - 1) & 1, abort_flag, v.status, kDevTimeoutMma);
+                ptx::tc_fence_after();
+            }
+            if (ok && sg.rows[t] > 0) {
+                const bool direct = sg.j0 == 0 && sg.j1 == k.n, mine = r < sg.rows[t];
+                const size_t yr = (size_t)(k.rq.first + token) * pp.H + k.g * pp.group + (rho - token * pp.group);
+                float* slot = part + ((size_t)worker * 2 + (sg.j0 == 0 ? 1 : 0)) * C::kSlotFloats;
+                const float inv = direct ? 1.f / l : 1.f;
+#pragma unroll
+                for (int c0 = 0; c0 < D / 32; ++c0) {
+                    if (steps == 0 || 32 * c0 >= pp.d) break;  // columns past the head width are zero padding
+                    uint32_t ov[32];
+                    ptx::tmem_ld32(lane_addr + o_col + 32 * c0, ov);
+                    ptx::tmem_ld_wait();
+                    ptx::pin_regs(ov);
+                    if (direct && mine) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            w[e] = ptx::pack_bf16x2(as_f(ov[2 * e]) * inv, as_f(ov[2 * e + 1]) * inv);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            store_bf16x8(Y + yr * pp.d, 32 * c0 + 8 * e, pp.d, w[4 * e], w[4 * e + 1], w[4 * e + 2],
+                                         w[4 * e + 3]);
+                    } else if (!direct) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<float4*>(slot + ((size_t)(8 * c0 + e) * kRows + t * kBM + r) * 4) =
+                                make_float4(as_f(ov[4 * e]), as_f(ov[4 * e + 1]), as_f(ov[4 * e + 2]),
+                                            as_f(ov[4 * e + 3]));
+                    }
+                }
+                if (!direct)
+                    *reinterpret_cast<float2*>(slot + (size_t)kRows * D + 2 * (t * kBM + r)) = make_float2(m * kLog2e, l);
+                else if (L != nullptr && mine)
+                    L[yr] = m + __log2f(l) * kLn2 - corr;
+            }
+            st += steps;
+            pairs += n_pair;
+            k.f += sg.j1 - sg.j0;
+            cursor_next_unit<TcTiling>(k, v, prefix, hi);
+        }
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Merges the unit that worker blockIdx.x begins and others continue (weights
+// 2^(m_p - max m), pieces in the line's order): a thread per row, 32 columns a block.
+template <int D>
+__global__ void __launch_bounds__(kRows)
+    paged_tc_merge_kernel(const __grid_constant__ FwdView v, const float* __restrict__ part,
+                          const PieceMeta* __restrict__ meta, int workers, __nv_bfloat16* __restrict__ Y,
+                          float* __restrict__ L) {
+    using C = TcCfg<D>;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PagedProblem& pp = v.pp;
+    const int w0 = blockIdx.x, c0 = blockIdx.y * 32, lane = threadIdx.x & 31, r = threadIdx.x;
+    const PieceMeta mt = meta[w0];
+    if (mt.tail < 0) return;
+    int pieces = 1;
+    for (int base = w0 + 1;; base += 32) {
+        const bool more = base + lane < workers && meta[base + lane].head == mt.tail;
+        const unsigned b = __ballot_sync(0xffffffffu, more);
+        pieces += b == 0xffffffffu ? 32 : __ffs(~b) - 1;
+        if (b != 0xffffffffu) break;
+    }
+    const int rho = mt.q * kRows + r;
+    if (rho >= mt.rows) return;
+    auto piece = [&](int p) { return part + ((size_t)(w0 + p) * 2 + (p == 0 ? 1 : 0)) * C::kSlotFloats; };
+    float m = -INFINITY, l = 0.f;
+    for (int p = 0; p < pieces; ++p) m = fmaxf(m, piece(p)[(size_t)kRows * D + 2 * r]);
+    float4 acc[8] = {};
+    for (int p = 0; p < pieces; ++p) {
+        const float* src = piece(p);
+        const float2 ml = *reinterpret_cast<const float2*>(src + (size_t)kRows * D + 2 * r);
+        const float w = ptx::ex2_approx(ml.x - m);
+        if (w == 0.f) continue;  // this piece holds none of the row's keys
+        l = fmaf(w, ml.y, l);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float4 x = *reinterpret_cast<const float4*>(src + ((size_t)(c0 / 4 + e) * kRows + r) * 4);
+            acc[e].x = fmaf(w, x.x, acc[e].x);
+            acc[e].y = fmaf(w, x.y, acc[e].y);
+            acc[e].z = fmaf(w, x.z, acc[e].z);
+            acc[e].w = fmaf(w, x.w, acc[e].w);
+        }
+    }
+    const int token = rho / pp.group;
+    const size_t yr = (size_t)(mt.first + token) * pp.H + mt.g * pp.group + (rho - token * pp.group);
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        store_bf16x8(Y + yr * pp.d, c0 + 8 * e, pp.d, ptx::pack_bf16x2(acc[2 * e].x * inv, acc[2 * e].y * inv),
+                     ptx::pack_bf16x2(acc[2 * e].z * inv, acc[2 * e].w * inv),
+                     ptx::pack_bf16x2(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
+                     ptx::pack_bf16x2(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
+    if (L != nullptr && blockIdx.y == 0)
+        L[yr] = (m + __log2f(l)) * kLn2 - pp.lambda * __logf((float)(mt.c + token + 1));
+}
+
+template <int D>
+size_t tc_bytes(int num_sms) {
+    return num_sms * (sizeof(PieceMeta) + 2 * TcCfg<D>::kSlotFloats * sizeof(float));
+}
+
+template <int D>
+cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, cudaStream_t s) {
+    using C = TcCfg<D>;
+    static_assert(1024 + C::kTiles + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory budget");
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        C::smem(kPagedMaxRequests));
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, kPagedFewRows, INT32_MAX, a.status};
+    const int workers = a.num_sms;
+    PieceMeta* meta = static_cast<PieceMeta*>(ws);
+    float* part = reinterpret_cast<float*>(meta + workers);
+    CUtensorMap mk, mv;
+    cudaError_t e;
+    const int box = std::min(pp.page, kKeys);
+    if ((e = make_page_map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
+    if ((e = make_page_map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
+    paged_tc_kernel<D><<<workers, kThreads, C::smem(pp.R), s>>>(mk, mv, v, (const __nv_bfloat16*)a.P1,
+                                                               (__nv_bfloat16*)a.Y, a.L, part, meta);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)workers, (unsigned)((pp.d + 31) / 32));
+    cfg.blockDim = dim3(kRows);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_tc_merge_kernel<D>, v, (const float*)part, (const PieceMeta*)meta, workers,
+                              (__nv_bfloat16*)a.Y, a.L);
+}
+
+}  // namespace
+}  // namespace paged
+
+size_t paged_tc_workspace(const PagedProblem& pp, int num_sms) {
+    return pp.d <= 64 ? paged::tc_bytes<64>(num_sms) : paged::tc_bytes<128>(num_sms);
+}
+
+cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s) {
+    return pp.d <= 64 ? paged::launch_tc<64>(pp, a, workspace, s) : paged::launch_tc<128>(pp, a, workspace, s);
+}
+
+}  // namespace relation
