@@ -1,0 +1,324 @@
+// Relation of new tokens over a paged cache in float32 on the CUDA cores ("Ask
+// Self, Ask Others", Sec. 3.1 eq.(1)-(3), Sec. 5.3 eq.(18), Appendix A.5), for any
+// number of new tokens: U_j = p1 . p2_j / sqrt(d), R_j = SiLU(U_j) for j < i, R_i =
+// sigmoid(U_i / tau_S) + lambda log(i + 1), Y = softmax(R) I~.
+//
+// A block of 256 threads holds 16 kPer packed rows (row = token * group + head in
+// the group) against 64 keys at a time: thread (ty, tx) of a 16 x 16 grid owns rows
+// ty + 16 i, keys tx + 16 j of the scores and columns 2 tx + 32 j of the output.
+// Both products use the packed fp32 multiply-add (two products an issue slot),
+// scores along the columns' pairs, output along the columns themselves.  P2 of the
+// next tile is copied while the weights are applied, I~ while the scores are
+// formed, so one buffer of each is enough.  Two shapes: kPer = 4 (64 rows), bound by
+// the fp32 pipes with shared memory close behind (12 wavefronts to 16 cycles of
+// multiply-adds per 4 columns and warp), two blocks an SM so that one's copies and
+// exponentials run under the other's products; and kPer = 1 for requests of at most
+// 16 rows, whose time is mostly the copies'.  Measured at 4 requests of 100 to 500
+// new tokens over up to 2048, 16 heads over 8 of 64: 0.249 ms; with 128 rows (kPer =
+// 8, one block an SM by registers) 0.303 ms.  Work is cut as in the bf16 kernels
+// (paged_schedule.cuh).
+//
+// Exponentials use ex2 and the sigmoid's quotient a reciprocal, both within 2^-22;
+// the argument's own rounding (|R| 2^-24) is of that size.
+#include <algorithm>
+#include <mutex>
+
+#include "paged_fwd.cuh"
+
+namespace relation {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 256, kKeys = 64;
+constexpr int kSmallRows = 16;  // requests of at most this many rows take kPer = 1
+constexpr int kMinTiles = 2;
+constexpr int kLong = 4;       // and longer ones this kPer
+constexpr int kPitchP = 80;  // 16 (mod 32): the two rows of a warp's store fall on different banks
+
+template <int kPer>
+using F32Tiling = Tiling<16 * kPer, kKeys>;
+
+// kPairs: pairs of 32 columns of the output (64, 96 or 128 wide).
+template <int kPairs, int kPer>
+struct F32Cfg {
+    static constexpr int kRows = 16 * kPer, kWidth = 32 * kPairs;
+    static constexpr int kPitch = kWidth + 4;  // 4 or 20 (mod 32): eight rows' 16-byte reads cover the banks
+    static constexpr int kFloats = kRows * kPitch + kKeys * kPitch + kKeys * kWidth + kRows * kPitchP;
+    static int smem(int R) { return kFloats * 4 + 64 + (R * 4 + 15) / 16 * 16; }
+    // Blocks an SM holds, by registers and by shared memory (the schedule's summary of R
+    // requests takes little unless R is thousands).
+    static constexpr int kPerSm =
+        std::max(1, std::min(kPer == 1 ? 4 : 2, 220 * 1024 / (kFloats * 4 + 2048)));
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ float sigmoid_f32(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + ptx::ex2_approx(-kLog2e * x)));
+    return y;
+}
+
+template <int kPairs, int kPer>
+__global__ void __launch_bounds__(kThreads, F32Cfg<kPairs, kPer>::kPerSm)
+    paged_f32_kernel(const __grid_constant__ FwdView v, const float* __restrict__ P1, const float* __restrict__ P2,
+                     const float* __restrict__ I, float* __restrict__ Y, float* __restrict__ L,
+                     float* __restrict__ part, PieceMeta* __restrict__ meta) {
+    using C = F32Cfg<kPairs, kPer>;
+    using Tl = F32Tiling<kPer>;
+    constexpr int kRows = C::kRows;
+    extern __shared__ float4 smem4[];
+    float* sQ = reinterpret_cast<float*>(smem4);
+    float* sK = sQ + kRows * C::kPitch;
+    float* sV = sK + kKeys * C::kPitch;
+    float* sP = sV + kKeys * C::kWidth;
+    int* sums = reinterpret_cast<int*>(sP + kRows * kPitchP);
+    int* prefix = sums + 16;
+    const PagedProblem& pp = v.pp;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t total = (int64_t)schedule_build<Tl>(v, prefix, sums) * pp.G;
+    const int worker = blockIdx.x;
+    int64_t lo, hi;
+    worker_range(total, (int)gridDim.x, kMinTiles, worker, &lo, &hi);
+    PieceMeta mine{-1, -1, 0, 0, 0, 0, 0, 0};
+    if (lo >= hi) {
+        if (tid == 0) meta[worker] = mine;
+        return;
+    }
+    Cursor k;
+    cursor_seek<Tl>(k, v, prefix, lo);
+    const int quads = pp.d / 4;
+    const uint32_t k_u = ptx::smem_u32(sK), v_u = ptx::smem_u32(sV);
+    // Key tile j of the unit in hand: four threads a row.  Keys past the end are zero
+    // (whatever their page holds), as are those of a page outside the pool.
+    auto copy = [&](const float* pool, uint32_t dst, int pitch, int j, int len) {
+        const int key = tid >> 2, tok = j * kKeys + key;
+        const uint32_t row = dst + key * pitch * 4;
+        int page = -1;
+        if (tok < len) {
+            page = v.table[(size_t)k.r * pp.width + (tok >> pp.page_shift)];
+            if (page < 0 || page >= pp.pages) {
+                record_status(v.status, kDevBadPosition);
+                page = -1;
+            }
+        }
+        if (page >= 0) {
+            const float* src = pool + page_row_offset(pp, page, tok & pp.page_mask, k.g);
+            for (int c = tid & 3; c < quads; c += 4) cp_async16(row + c * 16, src + c * 4);
+        } else {
+            for (int c = tid & 3; c < quads; c += 4)
+                asm volatile("st.shared.v4.f32 [%0], {%1, %1, %1, %1};" ::"r"(row + c * 16), "f"(0.f) : "memory");
+        }
+        cp_commit();
+    };
+    while (k.f < hi) {
+        const int j0 = k.j, j1 = (int)min((int64_t)k.n, k.j + (hi - k.f));
+        const int len = k.rq.c + k.rq.rows / pp.group;
+        __syncthreads();  // the unit before has been read
+        copy(P2, k_u, C::kPitch, j0, len);
+        copy(I, v_u, C::kWidth, j0, len);
+        int pos[kPer];
+        float corr[kPer], m[kPer], l[kPer];
+        size_t yr[kPer];
+        float2 o[kPer][kPairs];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int rho = min(k.q * kRows + ty + 16 * i, k.rq.rows - 1), t = rho / pp.group;
+            pos[i] = k.rq.c + t;
+            yr[i] = (size_t)(k.rq.first + t) * pp.H + k.g * pp.group + (rho - t * pp.group);
+            corr[i] = pp.lambda * logf((float)(pos[i] + 1));
+            m[i] = -INFINITY;
+            l[i] = 0.f;
+            for (int c = tx; c < quads; c += 16)
+                *reinterpret_cast<float4*>(sQ + (ty + 16 * i) * C::kPitch + 4 * c) =
+                    *reinterpret_cast<const float4*>(P1 + yr[i] * pp.d + 4 * c);
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) o[i][e] = make_float2(0.f, 0.f);
+        }
+        for (int j = j0; j < j1; ++j) {
+            cp_wait<1>();  // P2 of this tile
+            __syncthreads();
+            float2 s2[kPer][4] = {};
+#pragma unroll 2
+            for (int c = 0; c < quads; ++c) {
+                float4 kk[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                    kk[n] = *reinterpret_cast<const float4*>(sK + (tx + 16 * n) * C::kPitch + 4 * c);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const float4 q = *reinterpret_cast<const float4*>(sQ + (ty + 16 * i) * C::kPitch + 4 * c);
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        s2[i][n] = ptx::fma2(make_float2(q.x, q.y), make_float2(kk[n].x, kk[n].y), s2[i][n]);
+                        s2[i][n] = ptx::fma2(make_float2(q.z, q.w), make_float2(kk[n].z, kk[n].w), s2[i][n]);
+                    }
+                }
+            }
+            __syncthreads();
+            if (j + 1 < j1) copy(P2, k_u, C::kPitch, j + 1, len); else cp_commit();
+            const int col = j * kKeys + tx;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                float r[4], mt = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float u = (s2[i][n].x + s2[i][n].y) * pp.inv_sqrt_d;
+                    r[n] = u * sigmoid_f32(u);
+                    if (col + 16 * n == pos[i]) r[n] = sigmoid_f32(u / pp.tau_S) + corr[i];
+                    if (col + 16 * n > pos[i]) r[n] = -INFINITY;
+                    mt = fmaxf(mt, r[n]);
+                }
+#pragma unroll
+                for (int x = 8; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+                const float mn = fmaxf(m[i], mt);
+                // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
+                const float f = mn == -INFINITY ? 1.f : ptx::ex2_approx((m[i] - mn) * kLog2e);
+                const float ref = mn == -INFINITY ? 0.f : mn;
+                m[i] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float p = ptx::ex2_approx((r[n] - ref) * kLog2e);
+                    sum += p;
+                    sP[(ty + 16 * i) * kPitchP + tx + 16 * n] = p;
+                }
+                l[i] = l[i] * f + sum;  // this thread's keys; summed over tx at the end
+#pragma unroll
+                for (int e = 0; e < kPairs; ++e) o[i][e].x *= f, o[i][e].y *= f;
+            }
+            cp_wait<1>();  // I~ of this tile
+            __syncthreads();
+#pragma unroll 2
+            for (int c = 0; c < kKeys / 4; ++c) {
+                float2 vv[4][kPairs];
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e)
+                        vv[n][e] = *reinterpret_cast<const float2*>(sV + (4 * c + n) * C::kWidth + 2 * tx + 32 * e);
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {
+                    const float4 p = *reinterpret_cast<const float4*>(sP + (ty + 16 * i) * kPitchP + 4 * c);
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        o[i][e] = ptx::fma2(make_float2(p.x, p.x), vv[0][e], o[i][e]);
+                        o[i][e] = ptx::fma2(make_float2(p.y, p.y), vv[1][e], o[i][e]);
+                        o[i][e] = ptx::fma2(make_float2(p.z, p.z), vv[2][e], o[i][e]);
+                        o[i][e] = ptx::fma2(make_float2(p.w, p.w), vv[3][e], o[i][e]);
+                    }
+                }
+            }
+            __syncthreads();
+            if (j + 1 < j1) copy(I, v_u, C::kWidth, j + 1, len); else cp_commit();
+        }
+        const bool direct = j0 == 0 && j1 == k.n;
+        float* slot = part + ((size_t)worker * 2 + (j0 == 0 ? 1 : 0)) * slot_floats(kRows, C::kWidth);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            float ls = l[i];
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, x);
+            const int row = ty + 16 * i;
+            if (k.q * kRows + row >= k.rq.rows) continue;
+            const float inv = 1.f / ls;
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+                const int c = 2 * tx + 32 * e;
+                if (direct && c < pp.d) store_pair(Y + yr[i] * pp.d + c, o[i][e].x * inv, o[i][e].y * inv);
+                if (!direct) store_pair(slot + row * C::kWidth + c, o[i][e].x, o[i][e].y);
+            }
+            if (tx == 0) {
+                if (direct) {
+                    if (L != nullptr) L[yr[i]] = m[i] + logf(ls) - corr[i];
+                } else {
+                    store_pair(slot + kRows * C::kWidth + 2 * row, m[i] * kLog2e, ls);
+                }
+            }
+        }
+        if (j0 > 0) {
+            mine.head = k.f - j0;
+        } else if (!direct) {
+            mine.tail = k.f;
+            mine.first = k.rq.first;
+            mine.c = k.rq.c;
+            mine.g = k.g;
+            mine.q = k.q;
+            mine.rows = k.rq.rows;
+        }
+        k.f += j1 - j0;
+        cursor_next_unit<Tl>(k, v, prefix, hi);
+    }
+    if (tid == 0) meta[worker] = mine;
+}
+
+template <int kPairs, int kPer>
+size_t f32_bytes(int num_sms) {
+    using C = F32Cfg<kPairs, kPer>;
+    return (size_t)num_sms * C::kPerSm *
+           (sizeof(PieceMeta) + 2 * slot_floats(C::kRows, C::kWidth) * sizeof(float));
+}
+
+template <int kPairs, int kPer>
+cudaError_t launch_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, cudaStream_t s) {
+    using C = F32Cfg<kPairs, kPer>;
+    static_assert(C::kFloats * 4 + 64 + kPagedMaxRequests * 4 <= 232448, "shared memory budget");
+    auto kern = paged_f32_kernel<kPairs, kPer>;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {
+        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(kPagedMaxRequests));
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, kPer == 1 ? 0 : kSmallRows,
+                    kPer == 1 ? kSmallRows : INT32_MAX, a.status};
+    const int workers = a.num_sms * C::kPerSm;
+    PieceMeta* meta = static_cast<PieceMeta*>(ws);
+    float* part = reinterpret_cast<float*>(meta + workers);
+    kern<<<workers, kThreads, C::smem(pp.R), s>>>(v, (const float*)a.P1, (const float*)a.P2_pages,
+                                                  (const float*)a.I_pages, (float*)a.Y, a.L, part, meta);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_merge_rows<float, C::kRows>(v, C::kWidth, part, meta, workers, a.Y, a.L, s);
+}
+
+template <int kPairs>
+cudaError_t launch_f32_width(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, int* launches, cudaStream_t s) {
+    const cudaError_t e = launch_f32<kPairs, 1>(pp, a, ws, s);
+    *launches = 2;
+    if (e != cudaSuccess || (int64_t)a.max_fresh * pp.group <= kSmallRows) return e;
+    *launches = 4;
+    return launch_f32<kPairs, kLong>(pp, a, ws, s);
+}
+
+template <int kPairs>
+size_t f32_width_bytes(const PagedProblem& pp, int max_fresh, int num_sms) {
+    // The two kernels run one after the other on the caller's stream and share the workspace.
+    const size_t small = f32_bytes<kPairs, 1>(num_sms);
+    return (int64_t)max_fresh * pp.group <= kSmallRows ? small : std::max(small, f32_bytes<kPairs, kLong>(num_sms));
+}
+
+}  // namespace
+}  // namespace paged
+
+size_t paged_f32_workspace(const PagedProblem& pp, int max_fresh, int num_sms) {
+    using namespace paged;
+    if (pp.d <= 64) return f32_width_bytes<2>(pp, max_fresh, num_sms);
+    if (pp.d <= 96) return f32_width_bytes<3>(pp, max_fresh, num_sms);
+    return f32_width_bytes<4>(pp, max_fresh, num_sms);
+}
+
+cudaError_t launch_paged_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, int* launches, cudaStream_t s) {
+    using namespace paged;
+    if (pp.d <= 64) return launch_f32_width<2>(pp, a, ws, launches, s);
+    if (pp.d <= 96) return launch_f32_width<3>(pp, a, ws, launches, s);
+    return launch_f32_width<4>(pp, a, ws, launches, s);
+}
+
+}  // namespace relation

@@ -76,9 +76,6 @@ struct FewBars {
 };
 static_assert(sizeof(FewBars) <= 1024, "the barriers' region");
 
-// Partial rows of a worker: 2 slots x 16 rows x (width values, then m and l).
-__host__ __device__ constexpr size_t few_slot_floats(int width) { return (size_t)kRows * (width + 2); }
-
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -213,7 +210,7 @@ __global__ void __launch_bounds__(FewCfg<DK>::kWarps * 32, 1)
     };
     auto end_unit = [&](int j_end) {
         const bool direct = j_begin == 0 && j_end == k.n;
-        float* slot = part + ((size_t)worker * 2 + (j_begin == 0 ? 1 : 0)) * few_slot_floats(C::kWidth);
+        float* slot = part + ((size_t)worker * 2 + (j_begin == 0 ? 1 : 0)) * slot_floats(kRows, C::kWidth);
         if (!direct) {
             if (j_begin > 0) {
                 mine.head = k.f - j_end;
@@ -385,79 +382,13 @@ __global__ void __launch_bounds__(FewCfg<DK>::kWarps * 32, 1)
     if (lane == 0) meta[worker] = mine;
 }
 
-// Merges the unit that worker blockIdx.x begins and others continue: with the
-// pieces' maxima m_p and sums l_p, weights w_p = 2^(m_p - max m), Y = sum w_p o_p /
-// sum w_p l_p, pieces in the line's order.  One warp per row.
-__global__ void __launch_bounds__(128)
-    paged_few_merge_kernel(const __grid_constant__ FwdView v, int width, const float* __restrict__ part,
-                           const PieceMeta* __restrict__ meta, int workers, __nv_bfloat16* __restrict__ Y,
-                           float* __restrict__ L) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const PagedProblem& pp = v.pp;
-    const int w0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PieceMeta mt = meta[w0];
-    if (mt.tail < 0) return;
-    int pieces = 1;  // worker w0's slot 1, then slots 0 of the workers after it
-    for (int base = w0 + 1;; base += 32) {
-        const bool more = base + lane < workers && meta[base + lane].head == mt.tail;
-        const unsigned b = __ballot_sync(0xffffffffu, more);
-        pieces += b == 0xffffffffu ? 32 : __ffs(~b) - 1;
-        if (b != 0xffffffffu) break;
-    }
-    const size_t slot = few_slot_floats(width);
-    auto piece = [&](int p) { return part + ((size_t)(w0 + p) * 2 + (p == 0 ? 1 : 0)) * slot; };
-    const int rows = min(kRows, mt.rows - mt.q * kRows);
-    for (int row = warp; row < rows; row += 4) {
-        float m = -INFINITY;
-        for (int p = lane; p < pieces; p += 32) m = fmaxf(m, piece(p)[kRows * width + 2 * row]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float l = 0.f;
-        float2 acc[2] = {};
-        for (int p0 = 0; p0 < pieces; p0 += 32) {
-            float wt = 0.f, lp = 0.f;
-            if (p0 + lane < pieces) {
-                const float2 ml = *reinterpret_cast<const float2*>(piece(p0 + lane) + kRows * width + 2 * row);
-                wt = ptx::ex2_approx(ml.x - m);
-                lp = wt * ml.y;
-            }
-            const int n = min(32, pieces - p0);
-#pragma unroll 4
-            for (int p = 0; p < n; ++p) {
-                const float w = __shfl_sync(0xffffffffu, wt, p);
-                l += __shfl_sync(0xffffffffu, lp, p);
-                const float* src = piece(p0 + p) + row * width + 2 * lane;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (64 * e < width) {
-                        const float2 x = *reinterpret_cast<const float2*>(src + 64 * e);
-                        if (w != 0.f) {
-                            acc[e].x = fmaf(w, x.x, acc[e].x);
-                            acc[e].y = fmaf(w, x.y, acc[e].y);
-                        }
-                    }
-            }
-        }
-        const int rho = mt.q * kRows + row, t = rho / pp.group, hd = mt.g * pp.group + (rho - t * pp.group);
-        const size_t yr = (size_t)(mt.first + t) * pp.H + hd;
-        const float inv = 1.f / l;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (64 * e + 2 * lane < pp.d)
-                *reinterpret_cast<uint32_t*>(Y + yr * pp.d + 64 * e + 2 * lane) =
-                    ptx::pack_bf16x2(acc[e].x * inv, acc[e].y * inv);
-        if (L != nullptr && lane == 0)
-            L[yr] = (m + __log2f(l)) * kLn2 - pp.lambda * __logf((float)(mt.c + t + 1));
-    }
-}
-
 template <int DK>
 int few_workers(int num_sms) { return num_sms * FewCfg<DK>::kWarps; }
 
 template <int DK>
 size_t few_bytes(int num_sms) {
     const size_t w = few_workers<DK>(num_sms);
-    return w * sizeof(PieceMeta) + w * 2 * few_slot_floats(FewCfg<DK>::kWidth) * sizeof(float);
+    return w * sizeof(PieceMeta) + w * 2 * slot_floats(kRows, FewCfg<DK>::kWidth) * sizeof(float);
 }
 
 template <int DK, bool kHalf>
@@ -483,18 +414,7 @@ cudaError_t launch_few(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, 
     kern<<<a.num_sms, C::kWarps * 32, C::smem(pp.R), s>>>(mk, mv, v, (const __nv_bfloat16*)a.P1, (__nv_bfloat16*)a.Y,
                                                          a.L, part, meta);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // A programmatic dependent: resident before the pass ends, it waits for its writes in-kernel.
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)workers);
-    cfg.blockDim = dim3(128);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_few_merge_kernel, v, (int)C::kWidth, (const float*)part,
-                              (const PieceMeta*)meta, workers, (__nv_bfloat16*)a.Y, a.L);
+    return launch_merge_rows<__nv_bfloat16, kRows>(v, C::kWidth, part, meta, workers, a.Y, a.L, s);
 }
 
 template <int DK>

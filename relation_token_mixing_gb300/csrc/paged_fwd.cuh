@@ -154,6 +154,99 @@ struct PieceMeta {
 // this much (a factor 256): exact, numerator and denominator share it.
 constexpr float kRaise = 8.f;
 
+// A worker's partial rows: 2 slots of `rows` rows of `width` values, then (m, l) each.
+__host__ __device__ constexpr size_t slot_floats(int rows, int width) { return (size_t)rows * (width + 2); }
+
+__device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
+    *reinterpret_cast<uint32_t*>(p) = ptx::pack_bf16x2(a, b);
+}
+__device__ __forceinline__ void store_pair(float* p, float a, float b) {
+    *reinterpret_cast<float2*>(p) = make_float2(a, b);
+}
+
+// Merges the unit that worker blockIdx.x begins and others continue: with the
+// pieces' maxima m_p and sums l_p, weights w_p = 2^(m_p - max m), Y = sum w_p o_p /
+// sum w_p l_p, pieces in the line's order.  One warp per row.
+template <typename T, int kRows>
+__global__ void __launch_bounds__(128)
+    paged_merge_rows_kernel(const __grid_constant__ FwdView v, int width, const float* __restrict__ part,
+                            const PieceMeta* __restrict__ meta, int workers, T* __restrict__ Y,
+                            float* __restrict__ L) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PagedProblem& pp = v.pp;
+    const int w0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const PieceMeta mt = meta[w0];
+    if (mt.tail < 0) return;
+    int pieces = 1;  // worker w0's slot 1, then slots 0 of the workers after it
+    for (int base = w0 + 1;; base += 32) {
+        const bool more = base + lane < workers && meta[base + lane].head == mt.tail;
+        const unsigned b = __ballot_sync(0xffffffffu, more);
+        pieces += b == 0xffffffffu ? 32 : __ffs(~b) - 1;
+        if (b != 0xffffffffu) break;
+    }
+    const size_t slot = slot_floats(kRows, width);
+    auto piece = [&](int p) { return part + ((size_t)(w0 + p) * 2 + (p == 0 ? 1 : 0)) * slot; };
+    const int rows = min(kRows, mt.rows - mt.q * kRows);
+    for (int row = warp; row < rows; row += 4) {
+        float m = -INFINITY;
+        for (int p = lane; p < pieces; p += 32) m = fmaxf(m, piece(p)[kRows * width + 2 * row]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float l = 0.f;
+        float2 acc[2] = {};
+        for (int p0 = 0; p0 < pieces; p0 += 32) {
+            float wt = 0.f, lp = 0.f;
+            if (p0 + lane < pieces) {
+                const float2 ml = *reinterpret_cast<const float2*>(piece(p0 + lane) + kRows * width + 2 * row);
+                wt = ptx::ex2_approx(ml.x - m);
+                lp = wt * ml.y;
+            }
+            const int n = min(32, pieces - p0);
+#pragma unroll 4
+            for (int p = 0; p < n; ++p) {
+                const float w = __shfl_sync(0xffffffffu, wt, p);
+                l += __shfl_sync(0xffffffffu, lp, p);
+                const float* src = piece(p0 + p) + row * width + 2 * lane;
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (64 * e + 2 * lane < width) {
+                        const float2 x = *reinterpret_cast<const float2*>(src + 64 * e);
+                        if (w != 0.f) {
+                            acc[e].x = fmaf(w, x.x, acc[e].x);
+                            acc[e].y = fmaf(w, x.y, acc[e].y);
+                        }
+                    }
+            }
+        }
+        const int rho = mt.q * kRows + row, t = rho / pp.group, hd = mt.g * pp.group + (rho - t * pp.group);
+        const size_t yr = (size_t)(mt.first + t) * pp.H + hd;
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (64 * e + 2 * lane < pp.d)
+                store_pair(Y + yr * pp.d + 64 * e + 2 * lane, acc[e].x * inv, acc[e].y * inv);
+        if (L != nullptr && lane == 0)
+            L[yr] = (m + __log2f(l)) * kLn2 - pp.lambda * __logf((float)(mt.c + t + 1));
+    }
+}
+
+// Launched as a programmatic dependent of the pass: resident before that ends, it
+// waits for its writes in-kernel.
+template <typename T, int kRows>
+cudaError_t launch_merge_rows(const FwdView& v, int width, const float* part, const PieceMeta* meta, int workers,
+                              void* Y, float* L, cudaStream_t s) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)workers);
+    cfg.blockDim = dim3(128);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, kRows>, v, width, part, meta, workers, (T*)Y, L);
+}
+
 }  // namespace paged
 
 // The kernels' launches (paged_few.cu: a request's packed rows fit 32; paged_tc.cu:
@@ -163,6 +256,9 @@ size_t paged_few_workspace(const PagedProblem& pp, int num_sms);
 cudaError_t launch_paged_few(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s);
 size_t paged_tc_workspace(const PagedProblem& pp, int num_sms);
 cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s);
+size_t paged_f32_workspace(const PagedProblem& pp, int max_fresh, int num_sms);
+cudaError_t launch_paged_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, int* launches,
+                             cudaStream_t s);
 
 // The 4-D map (column, token of a page, cache head, page) of a bf16 page pool, box
 // 64 columns x box_rows tokens, 128-byte swizzle; columns past d read as zero.
