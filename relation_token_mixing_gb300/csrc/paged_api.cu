@@ -73,6 +73,8 @@ PagedProblem paged_problem(const relation_paged_t* p) {
     pp.H = (int)p->H;
     pp.G = (int)p->G;
     pp.group = (int)(p->H / p->G);
+    pp.by_group = FastDiv((uint32_t)pp.group);
+    pp.by_G = FastDiv((uint32_t)pp.G);
     pp.d = (int)p->d_h;
     pp.row = (int)row_elems(p);
     pp.pages = (int)p->pages;

@@ -77,18 +77,25 @@ __global__ void __launch_bounds__(kThreads, F32Cfg<kPairs, kPer>::kPerSm)
     float* sK = sQ + kRows * C::kPitch;
     float* sV = sK + kKeys * C::kPitch;
     float* sP = sV + kKeys * C::kWidth;
-    int* sums = reinterpret_cast<int*>(sP + kRows * kPitchP);
-    int* prefix = sums + 16;
+    int64_t* sums = reinterpret_cast<int64_t*>(sP + kRows * kPitchP);
+    int* prefix = reinterpret_cast<int*>(sums + 8);
     const PagedProblem& pp = v.pp;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t total = (int64_t)schedule_build<Tl>(v, prefix, sums) * pp.G;
+    // The short requests' pass is first and waits for the inputs; the other's end waits for it.
+    if (kPer == 1) dependency_wait();
+    dependency_release();
+    const int total = schedule_build(v, prefix, sums, [&](const Request& q) {
+        return Tl::tiles_before(q.c, q.rows, pp.group, Tl::row_tiles(q.rows));
+    });
     const int worker = blockIdx.x;
-    int64_t lo, hi;
-    worker_range(total, (int)gridDim.x, kMinTiles, worker, &lo, &hi);
-    PieceMeta mine{-1, -1, 0, 0, 0, 0, 0, 0};
+    const Share share(total, (int)gridDim.x, kMinTiles);
+    const int lo = share.begin(worker), hi = share.begin(worker + 1);
+    PieceMeta mine{};
     if (lo >= hi) {
-        if (tid == 0) meta[worker] = mine;
+        if (tid == 0) {
+            meta[worker] = mine;
+            dependency_wait();
+        }
         return;
     }
     Cursor k;
@@ -118,8 +125,8 @@ __global__ void __launch_bounds__(kThreads, F32Cfg<kPairs, kPer>::kPerSm)
         cp_commit();
     };
     while (k.f < hi) {
-        const int j0 = k.j, j1 = (int)min((int64_t)k.n, k.j + (hi - k.f));
-        const int len = k.rq.c + k.rq.rows / pp.group;
+        const int j0 = k.j, j1 = min(k.n, k.j + (hi - k.f));
+        const int len = k.rq.c + pp.by_group.div(k.rq.rows);
         __syncthreads();  // the unit before has been read
         copy(P2, k_u, C::kPitch, j0, len);
         copy(I, v_u, C::kWidth, j0, len);
@@ -129,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, F32Cfg<kPairs, kPer>::kPerSm)
         float2 o[kPer][kPairs];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const int rho = min(k.q * kRows + ty + 16 * i, k.rq.rows - 1), t = rho / pp.group;
+            const int rho = min(k.q * kRows + ty + 16 * i, k.rq.rows - 1), t = pp.by_group.div(rho);
             pos[i] = k.rq.c + t;
             yr[i] = (size_t)(k.rq.first + t) * pp.H + k.g * pp.group + (rho - t * pp.group);
             corr[i] = pp.lambda * logf((float)(pos[i] + 1));
@@ -242,27 +249,22 @@ __global__ void __launch_bounds__(kThreads, F32Cfg<kPairs, kPer>::kPerSm)
                 }
             }
         }
-        if (j0 > 0) {
-            mine.head = k.f - j0;
-        } else if (!direct) {
-            mine.tail = k.f;
-            mine.first = k.rq.first;
-            mine.c = k.rq.c;
-            mine.g = k.g;
-            mine.q = k.q;
-            mine.rows = k.rq.rows;
-        }
+        if (j0 == 0 && !direct) 
+            mine = PieceMeta{share.owner(k.f + k.n - 1) - worker + 1, k.rq.first, k.rq.c, k.rq.rows, k.g, k.q};
         k.f += j1 - j0;
         cursor_next_unit<Tl>(k, v, prefix, hi);
     }
-    if (tid == 0) meta[worker] = mine;
+    if (tid == 0) {
+        meta[worker] = mine;
+        dependency_wait();
+    }
 }
 
 template <int kPairs, int kPer>
 size_t f32_bytes(int num_sms) {
     using C = F32Cfg<kPairs, kPer>;
     return (size_t)num_sms * C::kPerSm *
-           (sizeof(PieceMeta) + 2 * slot_floats(C::kRows, C::kWidth) * sizeof(float));
+           (sizeof(PieceMeta) + 8 + 2 * slot_floats(C::kRows, C::kWidth) * sizeof(float));
 }
 
 template <int kPairs, int kPer>
@@ -279,13 +281,13 @@ cudaError_t launch_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, 
     const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, kPer == 1 ? 0 : kSmallRows,
                     kPer == 1 ? kSmallRows : INT32_MAX, a.status};
     const int workers = a.num_sms * C::kPerSm;
-    PieceMeta* meta = static_cast<PieceMeta*>(ws);
-    float* part = reinterpret_cast<float*>(meta + workers);
-    kern<<<workers, kThreads, C::smem(pp.R), s>>>(v, (const float*)a.P1, (const float*)a.P2_pages,
-                                                  (const float*)a.I_pages, (float*)a.Y, a.L, part, meta);
-    const cudaError_t e = cudaGetLastError();
+    float* part = static_cast<float*>(ws);
+    PieceMeta* meta = reinterpret_cast<PieceMeta*>(part + (size_t)workers * 2 * slot_floats(C::kRows, C::kWidth));
+    const cudaError_t e = launch_chained(kern, dim3((unsigned)workers), kThreads, C::smem(pp.R), s, v,
+                                         (const float*)a.P1, (const float*)a.P2_pages, (const float*)a.I_pages,
+                                         (float*)a.Y, a.L, part, meta);
     if (e != cudaSuccess) return e;
-    return launch_merge_rows<float, C::kRows>(v, C::kWidth, part, meta, workers, a.Y, a.L, s);
+    return launch_merge<float, C::kRows, C::kWidth>(v, part, meta, workers, a.Y, a.L, s);
 }
 
 template <int kPairs>
@@ -294,14 +296,13 @@ cudaError_t launch_f32_width(const PagedProblem& pp, const PagedFwdArgs& a, void
     *launches = 2;
     if (e != cudaSuccess || (int64_t)a.max_fresh * pp.group <= kSmallRows) return e;
     *launches = 4;
-    return launch_f32<kPairs, kLong>(pp, a, ws, s);
+    return launch_f32<kPairs, kLong>(pp, a, static_cast<char*>(ws) + f32_bytes<kPairs, 1>(a.num_sms), s);
 }
 
 template <int kPairs>
 size_t f32_width_bytes(const PagedProblem& pp, int max_fresh, int num_sms) {
-    // The two kernels run one after the other on the caller's stream and share the workspace.
-    const size_t small = f32_bytes<kPairs, 1>(num_sms);
-    return (int64_t)max_fresh * pp.group <= kSmallRows ? small : std::max(small, f32_bytes<kPairs, kLong>(num_sms));
+    const size_t small = f32_bytes<kPairs, 1>(num_sms);  // the two passes overlap: a part each
+    return (int64_t)max_fresh * pp.group <= kSmallRows ? small : small + f32_bytes<kPairs, kLong>(num_sms);
 }
 
 }  // namespace

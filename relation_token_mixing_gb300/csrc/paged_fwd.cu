@@ -6,17 +6,14 @@
 // passes over the other's requests, and the second is launched only where the
 // host's bound on the new tokens lets a request be that long.  float32 has its own
 // pair of kernels on the CUDA cores.
-#include <algorithm>
-
 #include "paged_fwd.cuh"
 
 namespace relation {
 
 size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, int max_fresh, int num_sms) {
     if (!bf16) return paged_f32_workspace(pp, max_fresh, num_sms);
-    // The two kernels run one after the other on the caller's stream and share the workspace.
-    const size_t few = paged_few_workspace(pp, num_sms);
-    return (int64_t)max_fresh * pp.group <= kPagedFewRows ? few : std::max(few, paged_tc_workspace(pp, num_sms));
+    const size_t few = paged_few_workspace(pp, max_fresh, num_sms);  // the two passes overlap: a part each
+    return (int64_t)max_fresh * pp.group <= kPagedFewRows ? few : few + paged_tc_workspace(pp, num_sms);
 }
 
 cudaError_t launch_paged_fwd(const PagedProblem& pp, bool bf16, const PagedFwdArgs& a, int* launches, cudaStream_t s) {
@@ -25,7 +22,7 @@ cudaError_t launch_paged_fwd(const PagedProblem& pp, bool bf16, const PagedFwdAr
     *launches = 2;
     if (e != cudaSuccess || (int64_t)a.max_fresh * pp.group <= kPagedFewRows) return e;
     *launches = 4;
-    return launch_paged_tc(pp, a, a.workspace, s);
+    return launch_paged_tc(pp, a, static_cast<char*>(a.workspace) + paged_few_workspace(pp, a.max_fresh, a.num_sms), s);
 }
 
 }  // namespace relation

@@ -31,8 +31,8 @@ struct Request {
 
 // Lengths that cannot be followed give rows = 0 and are reported.
 __device__ __forceinline__ Request request_of(const FwdView& v, int r) {
-    Request q{v.starts[r], v.cached[r], 0};
-    const int last = v.starts[r + 1];
+    Request q{__ldg(v.starts + r), __ldg(v.cached + r), 0};
+    const int last = __ldg(v.starts + r + 1);
     const int64_t f = (int64_t)last - q.first;
     if (q.first < 0 || f < 0 || last > v.pp.N || q.c < 0 || f > v.max_fresh ||
         q.c + f > ((int64_t)v.pp.width << v.pp.page_shift)) {
@@ -44,24 +44,24 @@ __device__ __forceinline__ Request request_of(const FwdView& v, int r) {
     return q;
 }
 
-// prefix[r] = key tiles of requests 0..r for one cache head.  All threads of the
-// block; sums: one int per warp.  Returns the total (saturated to int).
-template <typename Tl>
-__device__ __forceinline__ int schedule_build(const FwdView& v, int* prefix, int* sums) {
+// prefix[r] = sum over requests 0..r of tiles_of(request), the line's tiles of one
+// cache head.  All threads of the block; sums: one per warp.  Returns the line's
+// length over all cache heads, or 0 (and a report) if it passes 2^31 - 1 tiles.
+template <typename TilesOf>
+__device__ __forceinline__ int schedule_build(const FwdView& v, int* prefix, int64_t* sums, TilesOf tiles_of) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x >> 5;
     int64_t base = 0;
     for (int r0 = 0; r0 < v.pp.R; r0 += (int)blockDim.x) {
         const int r = r0 + tid;
-        int64_t n = 0;
+        int64_t x = 0;
         if (r < v.pp.R) {
             const Request q = request_of(v, r);
-            if (q.rows) n = Tl::tiles_before(q.c, q.rows, v.pp.group, Tl::row_tiles(q.rows));
+            if (q.rows) x = tiles_of(q);
         }
-        int x = (int)min(n, (int64_t)INT32_MAX / 2);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x = (int)min((int64_t)x + y, (int64_t)INT32_MAX / 2);
+            const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
         }
         if (lane == 31) sums[warp] = x;
         __syncthreads();
@@ -74,38 +74,47 @@ __device__ __forceinline__ int schedule_build(const FwdView& v, int* prefix, int
         base += all;
         __syncthreads();
     }
-    return (int)min(base, (int64_t)INT32_MAX);
+    const int64_t total = base * v.pp.G;
+    if (total > (int64_t)INT32_MAX) {
+        record_status(v.status, kDevBadPosition);
+        return 0;
+    }
+    return (int)total;
 }
 
-// A worker's position on the line.
+// The request that has tile f of the line: the first whose sum passes f / G.
+__device__ __forceinline__ int schedule_find(const FwdView& v, const int* prefix, int f) {
+    const int want = v.pp.by_G.div(f);
+    int lo = 0, hi = v.pp.R - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] > want) hi = mid; else lo = mid + 1;
+    }
+    return lo;
+}
+
+// A worker's position on a line of units with many row tiles.
 struct Cursor {
-    int64_t f;  // tile on the line
+    int f;              // tile on the line
     int r, g, q, j, n;  // request, cache head, row tile, key tile, the unit's key tiles
-    int S;      // the request's key tiles of one cache head
     Request rq;
 };
 
-template <typename Tl>
-__device__ __forceinline__ void cursor_request(Cursor& k, const FwdView& v, const int* prefix, int r) {
+__device__ __forceinline__ void cursor_request(Cursor& k, const FwdView& v, int r) {
     k.r = r;
-    k.S = prefix[r] - (r ? prefix[r - 1] : 0);
-    k.rq = Request{v.starts[r], v.cached[r], 0};
-    k.rq.rows = (v.starts[r + 1] - k.rq.first) * v.pp.group;
+    k.rq.first = __ldg(v.starts + r);
+    k.rq.c = __ldg(v.cached + r);
+    k.rq.rows = (__ldg(v.starts + r + 1) - k.rq.first) * v.pp.group;
 }
 
 // Places the cursor on tile f (f below the line's end).
 template <typename Tl>
-__device__ __forceinline__ void cursor_seek(Cursor& k, const FwdView& v, const int* prefix, int64_t f) {
-    const int want = (int)(f / v.pp.G);
-    int lo = 0, hi = v.pp.R - 1;
-    while (lo < hi) {  // first request whose sum passes want
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] > want) hi = mid; else lo = mid + 1;
-    }
-    cursor_request<Tl>(k, v, prefix, lo);
-    const int64_t off = f - (int64_t)(lo ? prefix[lo - 1] : 0) * v.pp.G;
-    k.g = (int)(off / k.S);
-    const int rem = (int)(off - (int64_t)k.g * k.S);
+__device__ __forceinline__ void cursor_seek(Cursor& k, const FwdView& v, const int* prefix, int f) {
+    const int r = schedule_find(v, prefix, f), before = r ? prefix[r - 1] : 0, S = prefix[r] - before;
+    cursor_request(k, v, r);
+    const int off = f - before * v.pp.G;
+    k.g = off / S;
+    const int rem = off - k.g * S;
     int a = 0, b = Tl::row_tiles(k.rq.rows) - 1;
     while (a < b) {  // last row tile that begins at or before rem
         const int mid = (a + b + 1) >> 1;
@@ -119,7 +128,7 @@ __device__ __forceinline__ void cursor_seek(Cursor& k, const FwdView& v, const i
 
 // From a unit's end to the next unit (end: the worker's end of the line).
 template <typename Tl>
-__device__ __forceinline__ void cursor_next_unit(Cursor& k, const FwdView& v, const int* prefix, int64_t end) {
+__device__ __forceinline__ void cursor_next_unit(Cursor& k, const FwdView& v, const int* prefix, int end) {
     k.j = 0;
     if (k.f >= end) return;
     if (++k.q == Tl::row_tiles(k.rq.rows)) {
@@ -128,33 +137,26 @@ __device__ __forceinline__ void cursor_next_unit(Cursor& k, const FwdView& v, co
             k.g = 0;
             int r = k.r + 1;
             while (prefix[r] == prefix[r - 1]) ++r;
-            cursor_request<Tl>(k, v, prefix, r);
+            cursor_request(k, v, r);
         }
     }
     k.n = Tl::tiles(k.rq.c, k.rq.rows, v.pp.group, k.q);
 }
 
-// Worker w's part of the line: at least min_tiles a worker while there are enough.
-__device__ __forceinline__ void worker_range(int64_t total, int workers, int min_tiles, int w, int64_t* lo, int64_t* hi) {
-    const int64_t used = max((int64_t)1, min((int64_t)workers, total / min_tiles));
-    *lo = w < used ? total * w / used : total;
-    *hi = w < used ? total * (w + 1) / used : total;
-}
-
-// What a worker leaves of the units that its ends cut: its first piece when that
-// continues the worker before (slot 0), its last when it begins a unit that the
-// next worker continues (slot 1).  A unit is named by its first tile on the line.
+// A block's partial rows in the workspace: slot 0 of its unit that continues the
+// block before, slot 1 of the one that the next block continues.  Of the latter the
+// block also leaves what the merge needs:
 struct PieceMeta {
-    int64_t head, tail;  // -1: none
-    int first, c, g, q, rows;  // of the tail's unit
-    int pad;
+    int pieces;  // this block's and the following blocks' (0: no such unit)
+    int first, c, rows;  // the unit's request
+    int g, q;            // and its cache head and row tile
 };
 
 // Running maximum of a row in units of log2, raised only when a tile exceeds it by
 // this much (a factor 256): exact, numerator and denominator share it.
 constexpr float kRaise = 8.f;
 
-// A worker's partial rows: 2 slots of `rows` rows of `width` values, then (m, l) each.
+// A slot: `rows` rows of `width` values, then (m, l) each.
 __host__ __device__ constexpr size_t slot_floats(int rows, int width) { return (size_t)rows * (width + 2); }
 
 __device__ __forceinline__ void store_pair(__nv_bfloat16* p, float a, float b) {
@@ -164,95 +166,122 @@ __device__ __forceinline__ void store_pair(float* p, float a, float b) {
     *reinterpret_cast<float2*>(p) = make_float2(a, b);
 }
 
-// Merges the unit that worker blockIdx.x begins and others continue: with the
-// pieces' maxima m_p and sums l_p, weights w_p = 2^(m_p - max m), Y = sum w_p o_p /
-// sum w_p l_p, pieces in the line's order.  One warp per row.
-template <typename T, int kRows>
-__global__ void __launch_bounds__(128)
-    paged_merge_rows_kernel(const __grid_constant__ FwdView v, int width, const float* __restrict__ part,
-                            const PieceMeta* __restrict__ meta, int workers, T* __restrict__ Y,
-                            float* __restrict__ L) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const PagedProblem& pp = v.pp;
-    const int w0 = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const PieceMeta mt = meta[w0];
-    if (mt.tail < 0) return;
-    int pieces = 1;  // worker w0's slot 1, then slots 0 of the workers after it
-    for (int base = w0 + 1;; base += 32) {
-        const bool more = base + lane < workers && meta[base + lane].head == mt.tail;
-        const unsigned b = __ballot_sync(0xffffffffu, more);
-        pieces += b == 0xffffffffu ? 32 : __ffs(~b) - 1;
-        if (b != 0xffffffffu) break;
-    }
-    const size_t slot = slot_floats(kRows, width);
-    auto piece = [&](int p) { return part + ((size_t)(w0 + p) * 2 + (p == 0 ? 1 : 0)) * slot; };
-    const int rows = min(kRows, mt.rows - mt.q * kRows);
-    for (int row = warp; row < rows; row += 4) {
-        float m = -INFINITY;
-        for (int p = lane; p < pieces; p += 32) m = fmaxf(m, piece(p)[kRows * width + 2 * row]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float l = 0.f;
-        float2 acc[2] = {};
-        for (int p0 = 0; p0 < pieces; p0 += 32) {
-            float wt = 0.f, lp = 0.f;
-            if (p0 + lane < pieces) {
-                const float2 ml = *reinterpret_cast<const float2*>(piece(p0 + lane) + kRows * width + 2 * row);
-                wt = ptx::ex2_approx(ml.x - m);
-                lp = wt * ml.y;
-            }
-            const int n = min(32, pieces - p0);
-#pragma unroll 4
-            for (int p = 0; p < n; ++p) {
-                const float w = __shfl_sync(0xffffffffu, wt, p);
-                l += __shfl_sync(0xffffffffu, lp, p);
-                const float* src = piece(p0 + p) + row * width + 2 * lane;
-#pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (64 * e + 2 * lane < width) {
-                        const float2 x = *reinterpret_cast<const float2*>(src + 64 * e);
-                        if (w != 0.f) {
-                            acc[e].x = fmaf(w, x.x, acc[e].x);
-                            acc[e].y = fmaf(w, x.y, acc[e].y);
-                        }
-                    }
-            }
-        }
-        const int rho = mt.q * kRows + row, t = rho / pp.group, hd = mt.g * pp.group + (rho - t * pp.group);
-        const size_t yr = (size_t)(mt.first + t) * pp.H + hd;
-        const float inv = 1.f / l;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-            if (64 * e + 2 * lane < pp.d)
-                store_pair(Y + yr * pp.d + 64 * e + 2 * lane, acc[e].x * inv, acc[e].y * inv);
-        if (L != nullptr && lane == 0)
-            L[yr] = (m + __log2f(l)) * kLn2 - pp.lambda * __logf((float)(mt.c + t + 1));
-    }
+// The kernels of a forward are launched as programmatic dependents, each on the SMs
+// as soon as there is room.  The first one waits for what ran before it and only then
+// releases the next, so whatever starts after that finds its inputs complete; a merge
+// releases the next pass before it waits for its own; and a pass that did not wait at
+// its beginning waits at its end, so that the last kernel's end is that of all.
+__device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dependency_release() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// Launched as a programmatic dependent of the pass: resident before that ends, it
-// waits for its writes in-kernel.
-template <typename T, int kRows>
-cudaError_t launch_merge_rows(const FwdView& v, int width, const float* part, const PieceMeta* meta, int workers,
-                              void* Y, float* L, cudaStream_t s) {
+// A row's merged state: weights 2^(m_p - m) of the pieces so far, m their maximum.
+template <int kQuads>
+struct MergedRow {
+    float m = -INFINITY, l = 0.f;
+    float4 acc[kQuads] = {};
+    __device__ __forceinline__ void add(float pm, float pl, const float4 (&x)[kQuads]) {
+        if (pm == -INFINITY) return;  // none of the row's keys: the piece's values may not be there
+        const float top = fmaxf(m, pm), f = ptx::ex2_approx(m - top), w = ptx::ex2_approx(pm - top);
+        m = top;
+        l = fmaf(w, pl, l * f);
+#pragma unroll
+        for (int e = 0; e < kQuads; ++e) {
+            acc[e].x = fmaf(w, x[e].x, acc[e].x * f);
+            acc[e].y = fmaf(w, x[e].y, acc[e].y * f);
+            acc[e].z = fmaf(w, x[e].z, acc[e].z * f);
+            acc[e].w = fmaf(w, x[e].w, acc[e].w * f);
+        }
+    }
+    // Thread `sub` of the row's eight has columns 32 e + 4 sub and the next three.
+    template <typename T>
+    __device__ __forceinline__ void finish(const PagedProblem& pp, int first, int c, int g, int rho, int sub, T* Y,
+                                           float* L) const {
+        const int t = pp.by_group.div(rho), hd = g * pp.group + (rho - t * pp.group);
+        const size_t yr = (size_t)(first + t) * pp.H + hd;
+        const float inv = 1.f / l;
+#pragma unroll
+        for (int e = 0; e < kQuads; ++e) {
+            const int col = 32 * e + 4 * sub;
+            if (col >= pp.d) continue;
+            store_pair(Y + yr * pp.d + col, acc[e].x * inv, acc[e].y * inv);
+            store_pair(Y + yr * pp.d + col + 2, acc[e].z * inv, acc[e].w * inv);
+        }
+        if (L != nullptr && sub == 0) L[yr] = (m + __log2f(l)) * kLn2 - pp.lambda * __logf((float)(c + t + 1));
+    }
+};
+
+// Merges the units that blocks begin and others continue, pieces in the line's
+// order.  Block (x, y): the unit of the pass's block x, rows 16 y and on, eight threads
+// a row.  The time is that of the dependent loads: the unit, then four pieces' rows
+// at once (a unit seldom has more).
+constexpr int kMergeThreads = 128, kMergeRows = 16;
+
+template <typename T, int kRows, int kWidth>
+__global__ void __launch_bounds__(kMergeThreads)
+    paged_merge_kernel(const __grid_constant__ FwdView v, const float* __restrict__ part,
+                       const PieceMeta* __restrict__ meta, T* __restrict__ Y, float* __restrict__ L) {
+    constexpr int kQuads = kWidth / 32, kBatch = 4;
+    constexpr size_t slot = slot_floats(kRows, kWidth);
+    dependency_release();
+    dependency_wait();
+    const int sub = threadIdx.x & 7, row = blockIdx.y * kMergeRows + (threadIdx.x >> 3);
+    const PieceMeta mt = meta[blockIdx.x];
+    const int rho = mt.q * kRows + row;
+    if (mt.pieces == 0 || row >= kRows || rho >= mt.rows) return;
+    // Piece 0 is this block's slot 1, piece p block (x + p)'s slot 0.
+    const float* base = part + (size_t)blockIdx.x * 2 * slot;
+    MergedRow<kQuads> out;
+    for (int p0 = 0; p0 < mt.pieces; p0 += kBatch) {
+        float2 ml[kBatch];
+        float4 x[kBatch][kQuads];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int p = min(p0 + b, mt.pieces - 1);
+            const float* src = base + (p ? (size_t)p * 2 : (size_t)1) * slot;
+            ml[b] = *reinterpret_cast<const float2*>(src + kRows * kWidth + 2 * row);
+            if (p0 + b >= mt.pieces) ml[b].x = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < kQuads; ++e)
+                x[b][e] = *reinterpret_cast<const float4*>(src + (size_t)row * kWidth + 32 * e + 4 * sub);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) out.add(ml[b].x, ml[b].y, x[b]);
+    }
+    out.finish(v.pp, mt.first, mt.c, mt.g, rho, sub, Y, L);
+}
+
+// One kernel of the chain on stream s, resident before the kernel before it ends.
+template <typename... P, typename... A>
+cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)workers);
-    cfg.blockDim = dim3(128);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_merge_rows_kernel<T, kRows>, v, width, part, meta, workers, (T*)Y, L);
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
+}
+
+template <typename T, int kRows, int kWidth>
+cudaError_t launch_merge(const FwdView& v, const float* part, const PieceMeta* meta, int blocks, void* Y, float* L,
+                         cudaStream_t s) {
+    return launch_chained(paged_merge_kernel<T, kRows, kWidth>,
+                          dim3((unsigned)blocks, (kRows + kMergeRows - 1) / kMergeRows), kMergeThreads, 0, s, v, part,
+                          meta, (T*)Y, L);
 }
 
 }  // namespace paged
 
-// The kernels' launches (paged_few.cu: a request's packed rows fit 32; paged_tc.cu:
+// The kernels' launches (paged_few.cu: a request's packed rows fit 16; paged_tc.cu:
 // more; paged_f32.cu: float32).
-constexpr int kPagedFewRows = 32;
-size_t paged_few_workspace(const PagedProblem& pp, int num_sms);
+constexpr int kPagedFewRows = 16;
+size_t paged_few_workspace(const PagedProblem& pp, int max_fresh, int num_sms);
 cudaError_t launch_paged_few(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s);
 size_t paged_tc_workspace(const PagedProblem& pp, int num_sms);
 cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s);

@@ -3,13 +3,13 @@
 // Unit: one (request, cache head, row tile): `rows_per_tile` of the request's
 // packed rows (row = token * group + head in the group) against the history its
 // last token sees, in key tiles of `keys`.  All units' key tiles in a fixed order
-// (request, cache head, row tile, key tile) form one line, and worker w of W takes
-// the tiles [w total / W, (w + 1) total / W): every worker has the same number of
-// tiles, within one, whatever the requests' lengths are.  A unit that a boundary
-// cuts is merged from its pieces afterwards.
+// (request, cache head, row tile, key tile) form one line, and the workers take
+// consecutive stretches of it that differ by one tile at most, whatever the
+// requests' lengths are.  A unit that a boundary cuts is merged from its pieces
+// afterwards.
 //
 // The line's length is known on the device only: every block sums the requests'
-// tiles itself (schedule_build), so the host launches a fixed grid.
+// tiles itself, so the host launches a fixed grid.
 #pragma once
 
 #include <stdint.h>
@@ -56,6 +56,26 @@ struct Tiling {
             s = floor_sum(full, m, kRowsPerTile, (int64_t)c * group + kRowsPerTile + m - 1);
         }
         return n > full ? s + tiles(c, rows, group, full) : s;
+    }
+};
+
+// A line of `total` tiles cut among `workers`, at least min_tiles each while there
+// are enough: the first `extra` of the `used` workers take one tile more than `each`.
+struct Share {
+    int used, each, extra;
+    __host__ __device__ Share(int total, int workers, int min_tiles) {
+        used = total / min_tiles;
+        used = used < 1 ? 1 : (used > workers ? workers : used);
+        each = total / used;
+        extra = total - each * used;
+    }
+    __host__ __device__ int begin(int w) const {
+        return w >= used ? each * used + extra : w * each + (w < extra ? w : extra);
+    }
+    // The worker that has tile x (x below the line's end).
+    __host__ __device__ int owner(int x) const {
+        const int wide = extra * (each + 1);
+        return x < wide ? x / (each + 1) : extra + (x - wide) / each;
     }
 };
 

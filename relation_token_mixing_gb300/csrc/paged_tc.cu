@@ -54,7 +54,7 @@ struct TcCfg {
     static constexpr int kStages = D == 64 ? 4 : 2;
     static constexpr int kTiles = (2 + 2 * kStages) * kTileBytes;
     static int smem(int R) { return 1024 + kTiles + 1024 + (R * 4 + 15) / 16 * 16; }
-    static constexpr size_t kSlotFloats = (size_t)kRows * (D + 2);  // o [D/4][256][4], then (m, l) [256]
+    static constexpr size_t kSlotFloats = slot_floats(kRows, D);
 };
 
 struct TcBars {
@@ -68,7 +68,7 @@ struct TcBars {
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
-    int sums[12];
+    int64_t sums[12];
 };
 static_assert(sizeof(TcBars) <= 1024, "the barriers' region");
 
@@ -83,10 +83,10 @@ struct Segment {
     int len;    // the request's tokens
     int tail;   // key tile that the request ends inside (-1: not in this piece)
 };
-__device__ __forceinline__ Segment segment_of(const Cursor& k, int group, int64_t end) {
+__device__ __forceinline__ Segment segment_of(const Cursor& k, int group, int end) {
     Segment s;
     s.j0 = k.j;
-    s.j1 = (int)min((int64_t)k.n, k.j + (end - k.f));
+    s.j1 = min(k.n, k.j + (end - k.f));
     s.most = 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* prefix = reinterpret_cast<int*>(smem + C::kTiles + 1024);
     const PagedProblem& pp = v.pp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // The pass before (paged_few.cu) waited for this one's inputs; this one's end waits for it.
+    dependency_release();
     if (threadIdx.x == 0) {
         ptx::mbar_init(&bars->q_full, 2);
         ptx::mbar_init(&bars->q_free, 1);
@@ -148,12 +149,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tma_prefetch_desc(&tm_k);
         ptx::tma_prefetch_desc(&tm_v);
     }
-    const int64_t total = (int64_t)schedule_build<TcTiling>(v, prefix, bars->sums) * pp.G;
+    const int total = schedule_build(v, prefix, bars->sums, [&](const Request& q) {
+        return TcTiling::tiles_before(q.c, q.rows, pp.group, TcTiling::row_tiles(q.rows));
+    });
     const int worker = blockIdx.x;
-    int64_t lo, hi;
-    worker_range(total, (int)gridDim.x, kMinTiles, worker, &lo, &hi);
+    const Share share(total, (int)gridDim.x, kMinTiles);
+    const int lo = share.begin(worker), hi = share.begin(worker + 1);
     if (lo >= hi) {
-        if (threadIdx.x == 0) meta[worker] = PieceMeta{-1, -1, 0, 0, 0, 0, 0, 0};
+        if (threadIdx.x == 0) {
+            meta[worker] = PieceMeta{};
+            dependency_wait();
+        }
         return;
     }
     if (warp == 1) {
@@ -325,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tr = threadIdx.x - 64, chunk = tr % kChunks;
         const uint32_t q_u = ptx::smem_u32(sQ) + (chunk / 8) * kPanelBytes;
         const int cols = max(0, min(8, pp.d - chunk * 8));
-        PieceMeta mine{-1, -1, 0, 0, 0, 0, 0, 0};
+        PieceMeta mine{};
         int kt = 0, seg = 0, tails = 0;
         while (ok && k.f < hi) {
             const Segment sg = segment_of(k, pp.group, hi);
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int r = tr / kChunks; r < row_end; r += kStep) {
                 const int rho = k.q * kRows + r;
                 const bool in = rho < k.rq.rows;
-                const int t = in ? rho / pp.group : 0, hd = k.g * pp.group + (in ? rho - t * pp.group : 0);
+                const int t = in ? pp.by_group.div(rho) : 0, hd = k.g * pp.group + (in ? rho - t * pp.group : 0);
                 const __nv_bfloat16* src = P1 + ((size_t)(k.rq.first + t) * pp.H + hd) * pp.d + (cols ? chunk * 8 : 0);
                 const int bytes = in ? cols * 2 : 0, rr = r & 127;
                 const uint32_t dst = q_u + (r >> 7) * C::kTileBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4);
@@ -371,22 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(&bars->v_clean[tails & 1]);
                 ++tails;
             }
-            if (sg.j0 > 0) {
-                mine.head = k.f - sg.j0;
-            } else if (sg.j1 < k.n) {
-                mine.tail = k.f;
-                mine.first = k.rq.first;
-                mine.c = k.rq.c;
-                mine.g = k.g;
-                mine.q = k.q;
-                mine.rows = k.rq.rows;
-            }
+            if (sg.j0 == 0 && sg.j1 < k.n) 
+                mine = PieceMeta{share.owner(k.f + k.n - 1) - worker + 1, k.rq.first, k.rq.c, k.rq.rows, k.g, k.q};
             kt += sg.most;
             ++seg;
             k.f += sg.j1 - sg.j0;
             cursor_next_unit<TcTiling>(k, v, prefix, hi);
         }
-        if (threadIdx.x == 64) meta[worker] = ok ? mine : PieceMeta{-1, -1, 0, 0, 0, 0, 0, 0};
+        if (threadIdx.x == 64) meta[worker] = ok ? mine : PieceMeta{};
     } else {
         // ------------------------------------------------------------- softmax
         ptx::regs_inc<kRegsSoftmax>();
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int steps = sg.steps[t], n_pair = C::kSepP ? 0 : min(sg.steps[0], sg.steps[1]);
             const int base = k.q * kRows + t * kBM;
             const int rho = min(base + r, k.rq.rows - 1);
-            const int token = rho / pp.group;
+            const int token = pp.by_group.div(rho);
             const int pos = k.rq.c + token;  // the row's own token: the last key it sees
             const int first_pos = __shfl_sync(0xffffffffu, pos, 0);  // the warp's least
             const float corr = pp.lambda * __logf((float)(pos + 1));
@@ -548,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else if (!direct) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<float4*>(slot + ((size_t)(8 * c0 + e) * kRows + t * kBM + r) * 4) =
+                            *reinterpret_cast<float4*>(slot + (size_t)(t * kBM + r) * D + 32 * c0 + 4 * e) =
                                 make_float4(as_f(ov[4 * e]), as_f(ov[4 * e + 1]), as_f(ov[4 * e + 2]),
                                             as_f(ov[4 * e + 3]));
                     }
@@ -570,65 +568,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
     }
-}
-
-// Merges the unit that worker blockIdx.x begins and others continue (weights
-// 2^(m_p - max m), pieces in the line's order): a thread per row, 32 columns a block.
-template <int D>
-__global__ void __launch_bounds__(kRows)
-    paged_tc_merge_kernel(const __grid_constant__ FwdView v, const float* __restrict__ part,
-                          const PieceMeta* __restrict__ meta, int workers, __nv_bfloat16* __restrict__ Y,
-                          float* __restrict__ L) {
-    using C = TcCfg<D>;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const PagedProblem& pp = v.pp;
-    const int w0 = blockIdx.x, c0 = blockIdx.y * 32, lane = threadIdx.x & 31, r = threadIdx.x;
-    const PieceMeta mt = meta[w0];
-    if (mt.tail < 0) return;
-    int pieces = 1;
-    for (int base = w0 + 1;; base += 32) {
-        const bool more = base + lane < workers && meta[base + lane].head == mt.tail;
-        const unsigned b = __ballot_sync(0xffffffffu, more);
-        pieces += b == 0xffffffffu ? 32 : __ffs(~b) - 1;
-        if (b != 0xffffffffu) break;
-    }
-    const int rho = mt.q * kRows + r;
-    if (rho >= mt.rows) return;
-    auto piece = [&](int p) { return part + ((size_t)(w0 + p) * 2 + (p == 0 ? 1 : 0)) * C::kSlotFloats; };
-    float m = -INFINITY, l = 0.f;
-    for (int p = 0; p < pieces; ++p) m = fmaxf(m, piece(p)[(size_t)kRows * D + 2 * r]);
-    float4 acc[8] = {};
-    for (int p = 0; p < pieces; ++p) {
-        const float* src = piece(p);
-        const float2 ml = *reinterpret_cast<const float2*>(src + (size_t)kRows * D + 2 * r);
-        const float w = ptx::ex2_approx(ml.x - m);
-        if (w == 0.f) continue;  // this piece holds none of the row's keys
-        l = fmaf(w, ml.y, l);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float4 x = *reinterpret_cast<const float4*>(src + ((size_t)(c0 / 4 + e) * kRows + r) * 4);
-            acc[e].x = fmaf(w, x.x, acc[e].x);
-            acc[e].y = fmaf(w, x.y, acc[e].y);
-            acc[e].z = fmaf(w, x.z, acc[e].z);
-            acc[e].w = fmaf(w, x.w, acc[e].w);
-        }
-    }
-    const int token = rho / pp.group;
-    const size_t yr = (size_t)(mt.first + token) * pp.H + mt.g * pp.group + (rho - token * pp.group);
-    const float inv = 1.f / l;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-        store_bf16x8(Y + yr * pp.d, c0 + 8 * e, pp.d, ptx::pack_bf16x2(acc[2 * e].x * inv, acc[2 * e].y * inv),
-                     ptx::pack_bf16x2(acc[2 * e].z * inv, acc[2 * e].w * inv),
-                     ptx::pack_bf16x2(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
-                     ptx::pack_bf16x2(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
-    if (L != nullptr && blockIdx.y == 0)
-        L[yr] = (m + __log2f(l)) * kLn2 - pp.lambda * __logf((float)(mt.c + token + 1));
+    if (threadIdx.x == 0) dependency_wait();
 }
 
 template <int D>
 size_t tc_bytes(int num_sms) {
-    return num_sms * (sizeof(PieceMeta) + 2 * TcCfg<D>::kSlotFloats * sizeof(float));
+    return num_sms * (sizeof(PieceMeta) + 8 + 2 * TcCfg<D>::kSlotFloats * sizeof(float));
 }
 
 template <int D>
@@ -644,27 +589,17 @@ cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, c
     if (attr_err != cudaSuccess) return attr_err;
     const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, kPagedFewRows, INT32_MAX, a.status};
     const int workers = a.num_sms;
-    PieceMeta* meta = static_cast<PieceMeta*>(ws);
-    float* part = reinterpret_cast<float*>(meta + workers);
+    float* part = static_cast<float*>(ws);
+    PieceMeta* meta = reinterpret_cast<PieceMeta*>(part + (size_t)workers * 2 * C::kSlotFloats);
     CUtensorMap mk, mv;
     cudaError_t e;
     const int box = std::min(pp.page, kKeys);
     if ((e = make_page_map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
     if ((e = make_page_map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
-    paged_tc_kernel<D><<<workers, kThreads, C::smem(pp.R), s>>>(mk, mv, v, (const __nv_bfloat16*)a.P1,
-                                                               (__nv_bfloat16*)a.Y, a.L, part, meta);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)workers, (unsigned)((pp.d + 31) / 32));
-    cfg.blockDim = dim3(kRows);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_tc_merge_kernel<D>, v, (const float*)part, (const PieceMeta*)meta, workers,
-                              (__nv_bfloat16*)a.Y, a.L);
+    e = launch_chained(paged_tc_kernel<D>, dim3((unsigned)workers), kThreads, C::smem(pp.R), s, mk, mv, v,
+                       (const __nv_bfloat16*)a.P1, (__nv_bfloat16*)a.Y, a.L, part, meta);
+    if (e != cudaSuccess) return e;
+    return launch_merge<__nv_bfloat16, kRows, D>(v, part, meta, workers, a.Y, a.L, s);
 }
 
 }  // namespace

@@ -39,7 +39,23 @@ int main() {
                     for (int64_t i = 0; i < n; ++i) s += (a * i + b) / m;
                     if (s != floor_sum(n, m, a, b)) return std::printf("floor_sum %ld %ld %ld %ld\n", (long)n, (long)m, (long)a, (long)b), 1;
                 }
-    if (!check<16, 32>() || !check<256, 128>() || !check<64, 64>()) return 1;
+    if (!check<256, 128>() || !check<64, 64>()) return 1;
+    // The workers' stretches tile the line, differ by one tile at most, and owner() inverts begin().
+    for (int total : {0, 1, 2, 3, 7, 152, 153, 1000, 4097})
+        for (int workers : {1, 2, 5, 152, 1824})
+            for (int least : {1, 2, 3}) {
+                const Share s(total, workers, least);
+                int at = 0, lo = total, hi = 0;
+                for (int w = 0; w < workers; ++w) {
+                    const int n = s.begin(w + 1) - s.begin(w);
+                    if (s.begin(w) != at || n < 0) return std::printf("share %d %d %d: worker %d\n", total, workers, least, w), 1;
+                    for (int x = at; x < at + n; ++x)
+                        if (s.owner(x) != w) return std::printf("owner %d %d %d: tile %d\n", total, workers, least, x), 1;
+                    at += n;
+                    if (w < s.used) lo = n < lo ? n : lo, hi = n > hi ? n : hi;
+                }
+                if (at != total || hi - lo > 1) return std::printf("share %d %d %d\n", total, workers, least), 1;
+            }
     std::printf("ok\n");
     return 0;
 }
