@@ -36,7 +36,7 @@ constexpr int kLong = 4;       // and longer ones this kPer
 constexpr int kPitchP = 80;  // 16 (mod 32): the two rows of a warp's store fall on different banks
 
 template <int kPer>
-using F32Tiling = Tiling<16 * kPer, kKeys>;
+using F32Tiling = Tiling<16 * kPer, kKeys, 1>;
 
 // kPairs: pairs of 32 columns of the output (64, 96 or 128 wide).
 template <int kPairs, int kPer>
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, F32Cfg<kPairs, kPer>::kPerSm)
     if (kPer == 1) dependency_wait();
     dependency_release();
     const int total = schedule_build(v, prefix, sums, [&](const Request& q) {
-        return Tl::tiles_before(q.c, q.rows, pp.group, Tl::row_tiles(q.rows));
+        return Tl::places(q.c, q.rows, pp.group, Tl::row_tiles(q.rows));
     });
     const int worker = blockIdx.x;
     const Share share(total, (int)gridDim.x, kMinTiles);

@@ -52,7 +52,6 @@ namespace paged {
 namespace {
 
 constexpr int kKeys = 32;     // keys of a stage
-constexpr int kStages = 2;    // of a worker
 constexpr int kMinTiles = 2;  // a worker's least: below that the merge costs more than it spreads
 
 // DK: 16-column steps of the head width (d = 60 reads its last 4 columns as zero).
@@ -60,7 +59,11 @@ constexpr int kMinTiles = 2;  // a worker's least: below that the merge costs mo
 template <int DK, int NT>
 struct FewCfg {
     static constexpr int kPanels = DK > 4 ? 2 : 1;  // 64-column panels
-    static constexpr int kWarps = kPanels == 2 ? 6 : 12;  // workers of a block
+    // Workers of a block and stages of each: 192 KB in all.  128 columns and 8 rows: 4 x 3
+    // (decode 32 x 32k: 268 us, 6 x 2: 278 us); 16 rows, more work a key: 6 x 2 (a mixed step
+    // of 80-wide heads: 95 us, 4 x 3: 101 us).
+    static constexpr int kWarps = kPanels == 1 ? 12 : NT == 1 ? 4 : 6;
+    static constexpr int kStages = kPanels == 2 && NT == 1 ? 3 : 2;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kPanelBytes = kKeys * 128;
     static constexpr int kTensorBytes = kPanels * kPanelBytes;  // P2 or I~ of a stage
@@ -81,7 +84,7 @@ struct FewPiece {
 };
 
 struct FewBars {
-    uint64_t full[12][kStages];
+    uint64_t full[24];  // a worker's stages one after another
     int64_t sums[16];
     FewPiece begun[12], continued;
     int abort_flag;
@@ -151,8 +154,8 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
     int* prefix = reinterpret_cast<int*>(smem + C::kRingBytes + 1024);
     const PagedProblem& pp = v.pp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (threadIdx.x < C::kWarps * kStages) {
-        ptx::mbar_init(&bars->full[0][0] + threadIdx.x, 1);
+    if (threadIdx.x < C::kWarps * C::kStages) {
+        ptx::mbar_init(&bars->full[threadIdx.x], 1);
         ptx::fence_barrier_init();
         if (threadIdx.x == 0) {
             bars->abort_flag = 0;
@@ -174,8 +177,8 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
     if (lane == 0) bars->begun[warp].pieces = 0;
     if (threadIdx.x == 0) bars->continued.pieces = 0;
     if (lo < hi) {
-    uint64_t* full = bars->full[warp];
-    uint8_t* ring = smem + warp * kStages * C::kStageBytes;
+    uint64_t* full = bars->full + warp * C::kStages;
+    uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
     FewUnit u = few_seek(v, prefix, lo);
 
     // ---- loads: u_ld runs ahead of the unit in hand; 32 block-table entries, one per
@@ -217,7 +220,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
         }
     };
     ask(true);
-    for (int s = 0; s < kStages && sent < hi; ++s) send(s);
+    for (int s = 0; s < C::kStages && sent < hi; ++s) send(s);
 
     Request rq;
     int j_begin = u.j, len = 0, nt_used = NT;
@@ -314,10 +317,10 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
     const uint32_t v_row = ((lane & 7) + ((lane >> 4) & 1) * 8) * 128, v_chunk = (lane >> 3) & 1;
     const float c_half = 0.5f * pp.inv_sqrt_d, c_self = c_half / pp.tau_S;
     for (int it = 0; it < hi - lo; ++it) {
-        const int s = it % kStages;
-        if (!ptx::mbar_wait_warp(&full[s], (it / kStages) & 1, abort_flag, v.status, kDevTimeoutFull)) {
+        const int s = it % C::kStages;
+        if (!ptx::mbar_wait_warp(&full[s], (it / C::kStages) & 1, abort_flag, v.status, kDevTimeoutFull)) {
             for (int x = it; x < sent - lo; ++x)  // let what is in flight land
-                ptx::mbar_drain(&full[x % kStages], (x / kStages) & 1, v.status);
+                ptx::mbar_drain(&full[x % C::kStages], (x / C::kStages) & 1, v.status);
             break;
         }
         const uint32_t sk = ring_u + s * C::kStageBytes, sv = sk + C::kTensorBytes;
@@ -448,7 +451,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
         for (int p = 0; p < n; ++p) {
             const int w = w0 + p;
             const bool last = p + 1 < pc.pieces || pc.end == share.begin(worker0 + w + 1);  // ends its stretch
-            const float* src = last ? reinterpret_cast<const float*>(smem + w * kStages * C::kStageBytes)
+            const float* src = last ? reinterpret_cast<const float*>(smem + w * C::kStages * C::kStageBytes)
                                     : part + (size_t)(worker0 + w) * C::kSlot;
             const float2 ml = *reinterpret_cast<const float2*>(src + C::kRows * C::kWidth + 2 * rho);
             float4 x[kQuads];

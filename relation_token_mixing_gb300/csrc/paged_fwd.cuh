@@ -44,11 +44,11 @@ __device__ __forceinline__ Request request_of(const FwdView& v, int r) {
     return q;
 }
 
-// prefix[r] = sum over requests 0..r of tiles_of(request), the line's tiles of one
+// prefix[r] = sum over requests 0..r of places_of(request), the line's places of one
 // cache head.  All threads of the block; sums: one per warp.  Returns the line's
-// length over all cache heads, or 0 (and a report) if it passes 2^31 - 1 tiles.
-template <typename TilesOf>
-__device__ __forceinline__ int schedule_build(const FwdView& v, int* prefix, int64_t* sums, TilesOf tiles_of) {
+// length over all cache heads, or 0 (and a report) if it passes 2^31 - 1 places.
+template <typename PlacesOf>
+__device__ __forceinline__ int schedule_build(const FwdView& v, int* prefix, int64_t* sums, PlacesOf places_of) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x >> 5;
     int64_t base = 0;
     for (int r0 = 0; r0 < v.pp.R; r0 += (int)blockDim.x) {
@@ -56,7 +56,7 @@ __device__ __forceinline__ int schedule_build(const FwdView& v, int* prefix, int
         int64_t x = 0;
         if (r < v.pp.R) {
             const Request q = request_of(v, r);
-            if (q.rows) x = tiles_of(q);
+            if (q.rows) x = places_of(q);
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -82,7 +82,7 @@ __device__ __forceinline__ int schedule_build(const FwdView& v, int* prefix, int
     return (int)total;
 }
 
-// The request that has tile f of the line: the first whose sum passes f / G.
+// The request that has place f of the line: the first whose sum passes f / G.
 __device__ __forceinline__ int schedule_find(const FwdView& v, const int* prefix, int f) {
     const int want = v.pp.by_G.div(f);
     int lo = 0, hi = v.pp.R - 1;
@@ -95,7 +95,7 @@ __device__ __forceinline__ int schedule_find(const FwdView& v, const int* prefix
 
 // A worker's position on a line of units with many row tiles.
 struct Cursor {
-    int f;              // tile on the line
+    int f;              // the key tile's place on the line
     int r, g, q, j, n;  // request, cache head, row tile, key tile, the unit's key tiles
     Request rq;
 };
@@ -107,7 +107,8 @@ __device__ __forceinline__ void cursor_request(Cursor& k, const FwdView& v, int 
     k.rq.rows = (__ldg(v.starts + r + 1) - k.rq.first) * v.pp.group;
 }
 
-// Places the cursor on tile f (f below the line's end).
+// Puts the cursor on the first key tile of its unit at or after place f (f below the
+// line's end); that may be past a worker's end.
 template <typename Tl>
 __device__ __forceinline__ void cursor_seek(Cursor& k, const FwdView& v, const int* prefix, int f) {
     const int r = schedule_find(v, prefix, f), before = r ? prefix[r - 1] : 0, S = prefix[r] - before;
@@ -118,19 +119,20 @@ __device__ __forceinline__ void cursor_seek(Cursor& k, const FwdView& v, const i
     int a = 0, b = Tl::row_tiles(k.rq.rows) - 1;
     while (a < b) {  // last row tile that begins at or before rem
         const int mid = (a + b + 1) >> 1;
-        if (Tl::tiles_before(k.rq.c, k.rq.rows, v.pp.group, mid) <= rem) a = mid; else b = mid - 1;
+        if (Tl::places(k.rq.c, k.rq.rows, v.pp.group, mid) <= rem) a = mid; else b = mid - 1;
     }
     k.q = a;
-    k.j = rem - (int)Tl::tiles_before(k.rq.c, k.rq.rows, v.pp.group, a);
+    const int in = rem - (int)Tl::places(k.rq.c, k.rq.rows, v.pp.group, a);
+    k.j = max(0, in - Tl::extra);
     k.n = Tl::tiles(k.rq.c, k.rq.rows, v.pp.group, a);
-    k.f = f;
+    k.f = f + Tl::extra + k.j - in;
 }
 
 // From a unit's end to the next unit (end: the worker's end of the line).
 template <typename Tl>
 __device__ __forceinline__ void cursor_next_unit(Cursor& k, const FwdView& v, const int* prefix, int end) {
     k.j = 0;
-    if (k.f >= end) return;
+    if (k.f >= end || (k.f += Tl::extra) >= end) return;
     if (++k.q == Tl::row_tiles(k.rq.rows)) {
         k.q = 0;
         if (++k.g == v.pp.G) {

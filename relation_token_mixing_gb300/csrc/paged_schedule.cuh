@@ -3,10 +3,10 @@
 // Unit: one (request, cache head, row tile): `rows_per_tile` of the request's
 // packed rows (row = token * group + head in the group) against the history its
 // last token sees, in key tiles of `keys`.  All units' key tiles in a fixed order
-// (request, cache head, row tile, key tile) form one line, and the workers take
-// consecutive stretches of it that differ by one tile at most, whatever the
-// requests' lengths are.  A unit that a boundary cuts is merged from its pieces
-// afterwards.
+// (request, cache head, row tile, key tile), each unit preceded by the places that
+// its beginning and end are worth, form one line, and the workers take consecutive
+// stretches of it that differ by one place at most, whatever the requests' lengths
+// are.  A unit that a boundary cuts is merged from its pieces afterwards.
 //
 // The line's length is known on the device only: every block sums the requests'
 // tiles itself, so the host launches a fixed grid.
@@ -36,24 +36,26 @@ __host__ __device__ inline int64_t floor_sum(int64_t n, int64_t m, int64_t a, in
     return sum;
 }
 
-template <int kRowsPerTile, int kKeys>
+// kExtra: the places before each unit's key tiles.
+template <int kRowsPerTile, int kKeys, int kExtra>
 struct Tiling {
+    static constexpr int extra = kExtra;
     // Key tiles of row tile q of a request with `rows` packed rows and c cached tokens.
     __host__ __device__ static int tiles(int c, int rows, int group, int q) {
         const int last = (rows < (q + 1) * kRowsPerTile ? rows : (q + 1) * kRowsPerTile) - 1;
         return (int)(((int64_t)c + last / group + kKeys) / kKeys);
     }
     __host__ __device__ static int row_tiles(int rows) { return (rows + kRowsPerTile - 1) / kRowsPerTile; }
-    // Key tiles of the first n row tiles.  Full row tiles: ceil((c + ceil(x / g)) / k)
+    // Places of the first n row tiles.  Key tiles of full row tiles: ceil((c + ceil(x / g)) / k)
     // with x = (q + 1) rows_per_tile is ceil((c g + x) / (g k)).
-    __host__ __device__ static int64_t tiles_before(int c, int rows, int group, int n) {
+    __host__ __device__ static int64_t places(int c, int rows, int group, int n) {
         const int full = n < rows / kRowsPerTile ? n : rows / kRowsPerTile;
-        int64_t s = 0;
+        int64_t s = (int64_t)n * kExtra;
         if (full <= 2) {
             for (int q = 0; q < full; ++q) s += tiles(c, rows, group, q);
         } else {
             const int64_t m = (int64_t)group * kKeys;
-            s = floor_sum(full, m, kRowsPerTile, (int64_t)c * group + kRowsPerTile + m - 1);
+            s += floor_sum(full, m, kRowsPerTile, (int64_t)c * group + kRowsPerTile + m - 1);
         }
         return n > full ? s + tiles(c, rows, group, full) : s;
     }

@@ -27,6 +27,7 @@
 // 128) of tensor-core time, so the special-function unit, not the tensor core, is
 // the limit at d = 64 and is near it at d = 128.
 #include <cuda_bf16.h>
+#include <string.h>
 
 #include <algorithm>
 #include <mutex>
@@ -42,8 +43,10 @@ constexpr int kThreads = 384;
 // 128 * 56 + 256 * 224 = 64512 = 384 * 168 registers.
 constexpr uint32_t kRegsControl = 56, kRegsSoftmax = 224;
 constexpr int kPanelBytes = 128 * 128;  // 128 rows x 64 bf16
-constexpr int kMinTiles = 2;
-using TcTiling = Tiling<kRows, kKeys>;
+constexpr int kMinTiles = 4;
+// A unit's beginning and end (queries, first scores, output: 7 to 12 thousand cycles)
+// cost about two key tiles (5 thousand each).
+using TcTiling = Tiling<kRows, kKeys, 2>;
 
 template <int D>
 struct TcCfg {
@@ -52,28 +55,45 @@ struct TcCfg {
     static constexpr int kPanels = D / 64;
     static constexpr int kTileBytes = kBM * D * 2;
     static constexpr int kStages = D == 64 ? 4 : 2;
-    static constexpr int kTiles = (2 + 2 * kStages) * kTileBytes;
+    // At d <= 64 the next unit's queries have a place of their own while this one's last
+    // scores are formed.
+    static constexpr int kQBufs = D == 64 ? 2 : 1;
+    static constexpr int kTiles = (2 * kQBufs + 2 * kStages) * kTileBytes;
     static int smem(int R) { return 1024 + kTiles + 1024 + (R * 4 + 15) / 16 * 16; }
     static constexpr size_t kSlotFloats = slot_floats(kRows, D);
 };
 
 struct TcBars {
-    uint64_t q_full, q_free;
+    uint64_t q_full[2], q_free[2];
     uint64_t k_full[4], v_full[4], kv_empty[4];
-    // In turn: the cleared tile of a piece may be ready before the one of the piece
-    // before has been waited for (never two pieces ahead: q_free holds that back).
-    uint64_t v_clean[2];
+    // In turn: the cleared tile of a piece may be ready before those of the pieces before
+    // have been waited for, but no more than kQBufs pieces ahead (q_free holds that back).
+    uint64_t v_clean[3];
     uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
     uint64_t turn[2][4];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
     int64_t sums[12];
+    // The softmax warps' cursors while they are among a piece's keys, where every
+    // register is a score's.
+    Cursor parked[8];
 };
 static_assert(sizeof(TcBars) <= 1024, "the barriers' region");
 
 __device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t as_u(float f) { return __float_as_uint(f); }
+
+// Reads a cursor back from shared memory (volatile: the compiler must not keep the
+// registers instead).
+__device__ __forceinline__ void unpark(Cursor& k, const Cursor* from) {
+    static_assert(sizeof(Cursor) % 4 == 0, "words");
+    int w[sizeof(Cursor) / 4];
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(Cursor) / 4; ++i)
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(ptx::smem_u32(from) + 4 * i) : "memory");
+    memcpy(&k, w, sizeof(Cursor));
+}
 
 // One worker's piece of a unit: key tiles j0 .. j1 - 1, and for each half of the
 // rows how many of them it sees.
@@ -119,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
-    uint8_t* sK = sQ + 2 * C::kTileBytes;
+    uint8_t* sK = sQ + 2 * C::kQBufs * C::kTileBytes;
     uint8_t* sV = sK + C::kStages * C::kTileBytes;
     TcBars* bars = reinterpret_cast<TcBars*>(smem + C::kTiles);
     int* prefix = reinterpret_cast<int*>(smem + C::kTiles + 1024);
@@ -128,16 +148,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The pass before (paged_few.cu) waited for this one's inputs; this one's end waits for it.
     dependency_release();
     if (threadIdx.x == 0) {
-        ptx::mbar_init(&bars->q_full, 2);
-        ptx::mbar_init(&bars->q_free, 1);
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(&bars->s_full[t], 1);
             ptx::mbar_init(&bars->s_free[t], 128);
             ptx::mbar_init(&bars->p_full[t], 128);
             ptx::mbar_init(&bars->o_done[t], 1);
-            ptx::mbar_init(&bars->v_clean[t], 2);
+            
+            ptx::mbar_init(&bars->q_full[t], 2);
+            ptx::mbar_init(&bars->q_free[t], 1);
             for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[t][q], 1);
         }
+        for (int x = 0; x < 3; ++x) ptx::mbar_init(&bars->v_clean[x], 2);
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(&bars->k_full[s], 1);
             ptx::mbar_init(&bars->v_full[s], 1);
@@ -150,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tma_prefetch_desc(&tm_v);
     }
     const int total = schedule_build(v, prefix, bars->sums, [&](const Request& q) {
-        return TcTiling::tiles_before(q.c, q.rows, pp.group, TcTiling::row_tiles(q.rows));
+        return TcTiling::places(q.c, q.rows, pp.group, TcTiling::row_tiles(q.rows));
     });
     const int worker = blockIdx.x;
     const Share share(total, (int)gridDim.x, kMinTiles);
@@ -236,11 +257,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dk0 = ptx::smem_desc(ptx::smem_u32(sK), 16, 1024, ptx::kSwizzle128B);
         const uint64_t dv0 = ptx::smem_desc(ptx::smem_u32(sV), kPanelBytes, 1024, ptx::kSwizzle128B);
         constexpr uint64_t kTileStep = C::kTileBytes >> 4, kPanelStep = kPanelBytes >> 4;
+        int qb = 0;
         auto issue_s = [&](int t, int s) {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint64_t off = (ks / 4) * kPanelStep + (ks % 4) * 2;  // 32 bytes per K-step
-                ptx::mma_ss_elect(tmem + t * 128, dq0 + t * kTileStep + off, dk0 + s * kTileStep + off, id_s,
+                ptx::mma_ss_elect(tmem + t * 128, dq0 + (2 * qb + t) * kTileStep + off, dk0 + s * kTileStep + off, id_s,
                                   ks > 0 ? 1u : 0u);
             }
             ptx::mma_commit_elect(&bars->s_full[t]);
@@ -260,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         int kt = 0, seg = 0, tails = 0, st[2] = {0, 0};
         while (ok && k.f < hi) {
             const Segment sg = segment_of(k, pp.group, hi);
-            if (!wait(&bars->q_full, seg, kDevTimeoutFull)) break;
+            qb = seg % C::kQBufs;
+            if (!wait(&bars->q_full[qb], seg / C::kQBufs, kDevTimeoutFull)) break;
             if (!wait(&bars->k_full[kt % C::kStages], kt / C::kStages, kDevTimeoutFull)) break;
             for (int t = 0; t < 2; ++t) {
                 if (sg.steps[t] == 0) continue;
@@ -270,13 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 issue_s(t, kt % C::kStages);
             }
             if (!ok) break;
-            if (sg.most == 1) ptx::mma_commit_elect(&bars->q_free);
+            if (sg.most == 1) ptx::mma_commit_elect(&bars->q_free[qb]);
             for (int j = 0; ok && j < sg.most; ++j) {
                 const int s = (kt + j) % C::kStages, s1 = (kt + j + 1) % C::kStages, next = (kt + j + 1) / C::kStages;
                 bool v_ready = false, k_next = false;
                 auto v_wait = [&]() {
                     if (v_ready) return true;
-                    v_ready = sg.j0 + j == sg.tail ? wait(&bars->v_clean[tails & 1], tails >> 1, kDevTimeoutFull)
+                    v_ready = sg.j0 + j == sg.tail ? wait(&bars->v_clean[tails % 3], tails / 3, kDevTimeoutFull)
                                                    : wait(&bars->v_full[s], (kt + j) / C::kStages, kDevTimeoutFull);
                     return v_ready;
                 };
@@ -291,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tc_fence_after();
                         issue_s(t, s1);
                     }
-                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free);
+                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                     for (int t = 0; t < 2 && ok; ++t) {
                         if (j >= sg.steps[t]) continue;
                         if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
@@ -310,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             issue_s(t, s1);
                         }
                     }
-                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free);
+                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                 }
                 if (ok) ptx::mma_commit_elect(&bars->kv_empty[s]);
             }
@@ -335,7 +358,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int kt = 0, seg = 0, tails = 0;
         while (ok && k.f < hi) {
             const Segment sg = segment_of(k, pp.group, hi);
-            if (seg > 0 && !ptx::mbar_wait_warp(&bars->q_free, (seg - 1) & 1, abort_flag, v.status, kDevTimeoutEmpty)) {
+            const int qb = seg % C::kQBufs;
+            if (seg >= C::kQBufs && !ptx::mbar_wait_warp(&bars->q_free[qb], (seg / C::kQBufs - 1) & 1, abort_flag,
+                                                         v.status, kDevTimeoutEmpty)) {
                 ok = false;
                 break;
             }
@@ -347,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int t = in ? pp.by_group.div(rho) : 0, hd = k.g * pp.group + (in ? rho - t * pp.group : 0);
                 const __nv_bfloat16* src = P1 + ((size_t)(k.rq.first + t) * pp.H + hd) * pp.d + (cols ? chunk * 8 : 0);
                 const int bytes = in ? cols * 2 : 0, rr = r & 127;
-                const uint32_t dst = q_u + (r >> 7) * C::kTileBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4);
+                const uint32_t dst = q_u + (2 * qb + (r >> 7)) * C::kTileBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4);
                 if ((pp.d & 7) == 0) {
                     cp_async16(dst, src, bytes);
                 } else {  // rows of 120 bytes start on 8
@@ -358,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
             ptx::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->q_full);
+            if (lane == 0) ptx::mbar_arrive(&bars->q_full[qb]);
             if (sg.tail >= 0) {
                 // Weight 0 times whatever a page holds past the end must be 0.
                 const int x = kt + sg.tail - sg.j0, s = x % C::kStages;
@@ -374,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_uint4(0, 0, 0, 0);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bars->v_clean[tails & 1]);
+                if (lane == 0) ptx::mbar_arrive(&bars->v_clean[tails % 3]);
                 ++tails;
             }
             if (sg.j0 == 0 && sg.j1 < k.n) 
@@ -397,14 +422,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* turn_next = &bars->turn[t ^ 1][quarter];
         int st = 0, pairs = 0;  // steps of this half, and steps both halves took in turn
         while (ok && k.f < hi) {
-            const Segment sg = segment_of(k, pp.group, hi);
-            const int steps = sg.steps[t], n_pair = C::kSepP ? 0 : min(sg.steps[0], sg.steps[1]);
-            const int base = k.q * kRows + t * kBM;
-            const int rho = min(base + r, k.rq.rows - 1);
-            const int token = pp.by_group.div(rho);
-            const int pos = k.rq.c + token;  // the row's own token: the last key it sees
-            const int first_pos = __shfl_sync(0xffffffffu, pos, 0);  // the warp's least
-            const float corr = pp.lambda * __logf((float)(pos + 1));
+            int steps, n_pair, own, first_own;  // the row's own token (the last key it sees), the warp's least
+            {
+                const Segment sg = segment_of(k, pp.group, hi);
+                steps = sg.steps[t];
+                n_pair = C::kSepP ? 0 : min(sg.steps[0], sg.steps[1]);
+                const int rho = min(k.q * kRows + t * kBM + r, k.rq.rows - 1);
+                own = k.rq.c + pp.by_group.div(rho) - sg.j0 * kKeys;  // as a column of the piece's first tile
+                first_own = __shfl_sync(0xffffffffu, own, 0);
+            }
+            const float corr = pp.lambda * __logf((float)(own + k.j * kKeys + 1));
+            __syncwarp();
+            if (lane == 0) bars->parked[warp - 4] = k;
+            __syncwarp();
             float m = -INFINITY, l = 0.f;
             for (int j = 0; ok && j < steps; ++j) {
                 if (!ptx::mbar_wait_warp(&bars->s_full[t], (st + j) & 1, abort_flag, v.status, kDevTimeoutMma)) {
@@ -430,8 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ptx::pin_regs(sv);  // the loops below start after the turn is taken
                 }
-                const int own = pos - (sg.j0 + j) * kKeys;  // the Self entry's column; later ones are masked
-                const bool edge = first_pos < (sg.j0 + j + 1) * kKeys;
+                const bool edge = first_own < kKeys;  // own: the Self entry's column; later ones are masked
                 float self = 0.f;
                 if (edge) {
 #pragma unroll
@@ -517,7 +546,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&bars->p_full[t]);
+                own -= kKeys;
+                first_own -= kKeys;
             }
+            unpark(k, &bars->parked[warp - 4]);
+            const Segment sg = segment_of(k, pp.group, hi);
+            const int rho = min(k.q * kRows + t * kBM + r, k.rq.rows - 1), token = pp.by_group.div(rho);
             if (ok && steps > 0) {
                 ok = ptx::mbar_wait_warp(&bars->o_done[t], (st + steps - 1) & 1, abort_flag, v.status, kDevTimeoutMma);
                 ptx::tc_fence_after();

@@ -1,5 +1,5 @@
 // Host walk of the paged forward's schedule (csrc/paged_schedule.cuh): prints
-// "ok" when every request's row tiles add up to what tiles_before says, for every
+// "ok" when every request's row tiles add up to what places says, for every
 // prefix, by direct summation.  Built and run on the host by test_paged_schedule.py.
 #include <cstdio>
 
@@ -7,16 +7,16 @@
 
 using namespace relation;
 
-template <int ROWS, int KEYS>
+template <int ROWS, int KEYS, int EXTRA>
 bool check() {
-    using T = Tiling<ROWS, KEYS>;
+    using T = Tiling<ROWS, KEYS, EXTRA>;
     for (int group : {1, 2, 3, 4, 5, 7, 8, 16, 17, 40, 128, 300})
         for (int c : {0, 1, 15, 16, 31, 32, 33, 127, 128, 129, 1000, 32767})
             for (int fresh : {1, 2, 3, 15, 16, 17, 31, 64, 100, 129, 777, 2048}) {
                 const int rows = fresh * group;
                 int64_t sum = 0;
                 for (int q = 0; q <= T::row_tiles(rows); ++q) {
-                    if (T::tiles_before(c, rows, group, q) != sum) {
+                    if (T::places(c, rows, group, q) != sum) {
                         std::printf("rows/tile %d keys %d group %d cached %d fresh %d: first %d tiles\n", ROWS, KEYS, group,
                                     c, fresh, q);
                         return false;
@@ -24,7 +24,7 @@ bool check() {
                     if (q == T::row_tiles(rows)) break;
                     // by definition: the tiles up to the position of the row tile's last token
                     const int last = (rows < (q + 1) * ROWS ? rows : (q + 1) * ROWS) - 1;
-                    sum += (c + last / group) / KEYS + 1;
+                    sum += EXTRA + (c + last / group) / KEYS + 1;
                 }
             }
     return true;
@@ -39,7 +39,7 @@ int main() {
                     for (int64_t i = 0; i < n; ++i) s += (a * i + b) / m;
                     if (s != floor_sum(n, m, a, b)) return std::printf("floor_sum %ld %ld %ld %ld\n", (long)n, (long)m, (long)a, (long)b), 1;
                 }
-    if (!check<256, 128>() || !check<64, 64>()) return 1;
+    if (!check<256, 128, 2>() || !check<64, 64, 1>() || !check<16, 64, 0>()) return 1;
     // The workers' stretches tile the line, differ by one tile at most, and owner() inverts begin().
     for (int total : {0, 1, 2, 3, 7, 152, 153, 1000, 4097})
         for (int workers : {1, 2, 5, 152, 1824})

@@ -1,5 +1,5 @@
 """The paged forward's schedule (csrc/paged_schedule.cuh) on the host: a small program compiled from the same header
-compares the closed form of the key tiles before each row tile with direct summation, over groups, cached lengths,
+compares the closed form of the places before each row tile with direct summation, over groups, cached lengths,
 new tokens and the kernels' tile sizes."""
 import os
 import subprocess
@@ -10,7 +10,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 OUT = os.path.join(HERE, "_build", "paged_schedule_check")
 
 
-def test_tiles_before_equals_direct_summation():
+def test_places_equal_direct_summation():
     os.makedirs(os.path.dirname(OUT), exist_ok=True)
     src = os.path.join(HERE, "paged_schedule_check.cu")
     cmd = [rbuild._nvcc(), *rbuild.ARCH, "-std=c++17", "-O2", "-I", rbuild.CSRC, src, "-o", OUT]
