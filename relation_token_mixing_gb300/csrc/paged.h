@@ -5,23 +5,9 @@
 #include <stdint.h>
 
 #include "kernels.h"
+#include "paged_schedule.cuh"
 
 namespace relation {
-
-// Quotients by a number known on the host, for dividends of 31 bits: with s =
-// ceil(log2 n) and m = ceil(2^(31 + s) / n), x / n = (x m) >> (31 + s) for all x < 2^31
-// (m n exceeds 2^(31 + s) by less than 2^s, so the error stays below 1 / n).
-struct FastDiv {
-    uint32_t n, m, shift;
-    FastDiv() = default;
-    explicit FastDiv(uint32_t d) : n(d), shift(0) {
-        while ((1ull << shift) < d) ++shift;
-        m = (uint32_t)(((1ull << (31 + shift)) + d - 1) / d);
-    }
-    __host__ __device__ __forceinline__ int div(int x) const {
-        return (int)(((uint64_t)(uint32_t)x * m) >> (31 + shift));
-    }
-};
 
 // Kernel-side view of one relation_paged_t.
 struct PagedProblem {

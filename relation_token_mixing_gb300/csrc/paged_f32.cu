@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, F32Cfg<kPairs, kPer>::kPerSm)
     if (kPer == 1) dependency_wait();
     dependency_release();
     const int total = schedule_build(v, prefix, sums, [&](const Request& q) {
-        return Tl::places(q.c, q.rows, pp.group, Tl::row_tiles(q.rows));
+        return Tl::places(q.c, q.rows, pp.by_group, Tl::row_tiles(q.rows));
     });
     const int worker = blockIdx.x;
     const Share share(total, (int)gridDim.x, kMinTiles);

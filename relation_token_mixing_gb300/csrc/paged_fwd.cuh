@@ -119,12 +119,12 @@ __device__ __forceinline__ void cursor_seek(Cursor& k, const FwdView& v, const i
     int a = 0, b = Tl::row_tiles(k.rq.rows) - 1;
     while (a < b) {  // last row tile that begins at or before rem
         const int mid = (a + b + 1) >> 1;
-        if (Tl::places(k.rq.c, k.rq.rows, v.pp.group, mid) <= rem) a = mid; else b = mid - 1;
+        if (Tl::places(k.rq.c, k.rq.rows, v.pp.by_group, mid) <= rem) a = mid; else b = mid - 1;
     }
     k.q = a;
-    const int in = rem - (int)Tl::places(k.rq.c, k.rq.rows, v.pp.group, a);
+    const int in = rem - (int)Tl::places(k.rq.c, k.rq.rows, v.pp.by_group, a);
     k.j = max(0, in - Tl::extra);
-    k.n = Tl::tiles(k.rq.c, k.rq.rows, v.pp.group, a);
+    k.n = Tl::tiles(k.rq.c, k.rq.rows, v.pp.by_group, a);
     k.f = f + Tl::extra + k.j - in;
 }
 
@@ -142,7 +142,7 @@ __device__ __forceinline__ void cursor_next_unit(Cursor& k, const FwdView& v, co
             cursor_request(k, v, r);
         }
     }
-    k.n = Tl::tiles(k.rq.c, k.rq.rows, v.pp.group, k.q);
+    k.n = Tl::tiles(k.rq.c, k.rq.rows, v.pp.by_group, k.q);
 }
 
 // A block's partial rows in the workspace: slot 0 of its unit that continues the

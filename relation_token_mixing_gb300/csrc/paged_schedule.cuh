@@ -16,6 +16,21 @@
 
 namespace relation {
 
+// Quotients by a number known on the host, for dividends of 31 bits: with s =
+// ceil(log2 n) and m = ceil(2^(31 + s) / n), x / n = (x m) >> (31 + s) for all x < 2^31
+// (m n exceeds 2^(31 + s) by less than 2^s, so the error stays below 1 / n).
+struct FastDiv {
+    uint32_t n, m, shift;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t d) : n(d), shift(0) {
+        while ((1ull << shift) < d) ++shift;
+        m = (uint32_t)(((1ull << (31 + shift)) + d - 1) / d);
+    }
+    __host__ __device__ __forceinline__ int div(int x) const {
+        return (int)(((uint64_t)(uint32_t)x * m) >> (31 + shift));
+    }
+};
+
 // sum_{i < n} floor((a i + b) / m) for n, a, b >= 0, m >= 1, by the Euclidean
 // recursion: whole multiples of m leave a and b, then the lattice points under the
 // line are counted along the other axis.
@@ -41,21 +56,21 @@ template <int kRowsPerTile, int kKeys, int kExtra>
 struct Tiling {
     static constexpr int extra = kExtra;
     // Key tiles of row tile q of a request with `rows` packed rows and c cached tokens.
-    __host__ __device__ static int tiles(int c, int rows, int group, int q) {
+    __host__ __device__ static int tiles(int c, int rows, const FastDiv& group, int q) {
         const int last = (rows < (q + 1) * kRowsPerTile ? rows : (q + 1) * kRowsPerTile) - 1;
-        return (int)(((int64_t)c + last / group + kKeys) / kKeys);
+        return (int)(((uint32_t)c + (uint32_t)group.div(last) + kKeys) / kKeys);
     }
     __host__ __device__ static int row_tiles(int rows) { return (rows + kRowsPerTile - 1) / kRowsPerTile; }
     // Places of the first n row tiles.  Key tiles of full row tiles: ceil((c + ceil(x / g)) / k)
     // with x = (q + 1) rows_per_tile is ceil((c g + x) / (g k)).
-    __host__ __device__ static int64_t places(int c, int rows, int group, int n) {
+    __host__ __device__ static int64_t places(int c, int rows, const FastDiv& group, int n) {
         const int full = n < rows / kRowsPerTile ? n : rows / kRowsPerTile;
         int64_t s = (int64_t)n * kExtra;
         if (full <= 2) {
             for (int q = 0; q < full; ++q) s += tiles(c, rows, group, q);
         } else {
-            const int64_t m = (int64_t)group * kKeys;
-            s += floor_sum(full, m, kRowsPerTile, (int64_t)c * group + kRowsPerTile + m - 1);
+            const int64_t m = (int64_t)group.n * kKeys;
+            s += floor_sum(full, m, kRowsPerTile, (int64_t)c * group.n + kRowsPerTile + m - 1);
         }
         return n > full ? s + tiles(c, rows, group, full) : s;
     }

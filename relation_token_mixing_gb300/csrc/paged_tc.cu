@@ -11,7 +11,9 @@
 // blocks cut all units' key tiles into equal parts (paged_schedule.cuh), so a few
 // long rows fill the GPU as well as many short ones, and a second kernel merges the
 // units that the cuts divide.
-//   warp 0      key producer: the pages of each key tile by TMA, one copy per lane
+//   warp 0      walks the block's stretch of the line, one piece of a unit after another,
+//               hands each to the others, and loads its keys: the pages of each tile by
+//               TMA, one copy per lane
 //   warp 1      MMA issuer and TMEM owner
 //   warps 2-3   query rows into shared memory; clear the keys past a request's end
 //   warps 4-7   softmax of rows 0-127 (one thread per row)
@@ -27,7 +29,6 @@
 // 128) of tensor-core time, so the special-function unit, not the tensor core, is
 // the limit at d = 64 and is near it at d = 128.
 #include <cuda_bf16.h>
-#include <string.h>
 
 #include <algorithm>
 #include <mutex>
@@ -63,7 +64,20 @@ struct TcCfg {
     static constexpr size_t kSlotFloats = slot_floats(kRows, D);
 };
 
+// A piece of a unit, as warp 0 hands it out (words of one 64-byte slot).
+struct Piece {
+    int first, c, rows, g;      // the request and cache head
+    int q, j0, j1, n;           // row tile; its key tiles j0 .. j1 - 1 of n
+    int steps[2], most, tail;   // key tiles that each half of the rows sees, the most of
+                                // them (-1: no more pieces), and the one that the
+                                // request ends inside (-1: not in this piece)
+    int place, pad[3];          // of tile j0 on the line
+};
+static_assert(sizeof(Piece) == 64, "a slot");
+constexpr int kSlots = 4;  // pieces handed out and not yet done with
+
 struct TcBars {
+    uint64_t piece_full[kSlots], piece_free[kSlots];
     uint64_t q_full[2], q_free[2];
     uint64_t k_full[4], v_full[4], kv_empty[4];
     // In turn: the cleared tile of a piece may be ready before those of the pieces before
@@ -75,51 +89,35 @@ struct TcBars {
     uint32_t tmem_base;
     int abort_flag;
     int64_t sums[12];
-    // The softmax warps' cursors while they are among a piece's keys, where every
-    // register is a score's.
-    Cursor parked[8];
+    alignas(16) Piece pieces[kSlots];
 };
 static_assert(sizeof(TcBars) <= 1024, "the barriers' region");
 
 __device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t as_u(float f) { return __float_as_uint(f); }
 
-// Reads a cursor back from shared memory (volatile: the compiler must not keep the
-// registers instead).
-__device__ __forceinline__ void unpark(Cursor& k, const Cursor* from) {
-    static_assert(sizeof(Cursor) % 4 == 0, "words");
-    int w[sizeof(Cursor) / 4];
-#pragma unroll
-    for (unsigned i = 0; i < sizeof(Cursor) / 4; ++i)
-        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[i]) : "r"(ptx::smem_u32(from) + 4 * i) : "memory");
-    memcpy(&k, w, sizeof(Cursor));
-}
-
-// One worker's piece of a unit: key tiles j0 .. j1 - 1, and for each half of the
-// rows how many of them it sees.
-struct Segment {
-    int j0, j1;
-    int rows[2], steps[2], most;
-    int len;    // the request's tokens
-    int tail;   // key tile that the request ends inside (-1: not in this piece)
-};
-__device__ __forceinline__ Segment segment_of(const Cursor& k, int group, int end) {
-    Segment s;
-    s.j0 = k.j;
-    s.j1 = min(k.n, k.j + (end - k.f));
-    s.most = 0;
+__device__ __forceinline__ Piece piece_of(const Cursor& k, const FastDiv& by_group, int end) {
+    Piece p;
+    p.first = k.rq.first;
+    p.c = k.rq.c;
+    p.rows = k.rq.rows;
+    p.g = k.g;
+    p.q = k.q;
+    p.j0 = k.j;
+    p.j1 = min(k.n, k.j + (end - k.f));
+    p.n = k.n;
+    p.most = 0;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const int base = k.q * kRows + t * kBM;
-        s.rows[t] = max(0, min(kBM, k.rq.rows - base));
-        const int n = s.rows[t] ? (k.rq.c + (base + s.rows[t] - 1) / group + kKeys) / kKeys : 0;
-        s.steps[t] = max(0, min(s.j1, n) - s.j0);
-        s.most = max(s.most, s.steps[t]);
+        const int base = k.q * kRows + t * kBM, rows = max(0, min(kBM, k.rq.rows - base));
+        const int n = rows ? (int)(((uint32_t)k.rq.c + by_group.div(base + rows - 1) + kKeys) / kKeys) : 0;
+        p.steps[t] = max(0, min(p.j1, n) - p.j0);
+        p.most = max(p.most, p.steps[t]);
     }
-    s.len = k.rq.c + k.rq.rows / group;
-    const int tail = s.len / kKeys;
-    s.tail = (s.len % kKeys != 0 && tail >= s.j0 && tail < s.j0 + s.most) ? tail : -1;
-    return s;
+    const int len = k.rq.c + by_group.div(k.rq.rows), tail = len / kKeys;
+    p.tail = (len % kKeys != 0 && tail >= p.j0 && tail < p.j0 + p.most) ? tail : -1;
+    p.place = k.f;
+    return p;
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
@@ -148,17 +146,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     // The pass before (paged_few.cu) waited for this one's inputs; this one's end waits for it.
     dependency_release();
     if (threadIdx.x == 0) {
+        for (int x = 0; x < kSlots; ++x) {
+            ptx::mbar_init(&bars->piece_full[x], 1);
+            ptx::mbar_init(&bars->piece_free[x], 11);  // the other warps
+        }
+        for (int x = 0; x < 3; ++x) ptx::mbar_init(&bars->v_clean[x], 2);
         for (int t = 0; t < 2; ++t) {
+            ptx::mbar_init(&bars->q_full[t], 2);
+            ptx::mbar_init(&bars->q_free[t], 1);
             ptx::mbar_init(&bars->s_full[t], 1);
             ptx::mbar_init(&bars->s_free[t], 128);
             ptx::mbar_init(&bars->p_full[t], 128);
             ptx::mbar_init(&bars->o_done[t], 1);
-            
-            ptx::mbar_init(&bars->q_full[t], 2);
-            ptx::mbar_init(&bars->q_free[t], 1);
             for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[t][q], 1);
         }
-        for (int x = 0; x < 3; ++x) ptx::mbar_init(&bars->v_clean[x], 2);
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(&bars->k_full[s], 1);
             ptx::mbar_init(&bars->v_full[s], 1);
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tma_prefetch_desc(&tm_v);
     }
     const int total = schedule_build(v, prefix, bars->sums, [&](const Request& q) {
-        return TcTiling::places(q.c, q.rows, pp.group, TcTiling::row_tiles(q.rows));
+        return TcTiling::places(q.c, q.rows, pp.by_group, TcTiling::row_tiles(q.rows));
     });
     const int worker = blockIdx.x;
     const Share share(total, (int)gridDim.x, kMinTiles);
@@ -192,19 +193,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tc_fence_after();
     const uint32_t tmem = bars->tmem_base;
     volatile int* abort_flag = &bars->abort_flag;
-    Cursor k;
-    cursor_seek<TcTiling>(k, v, prefix, lo);
     bool ok = true;
+    // The other roles' side of the pieces: the slot of piece `seg` once it is there.
+    auto take = [&](int seg) -> const Piece* {
+        if (!ptx::mbar_wait_warp(&bars->piece_full[seg % kSlots], (seg / kSlots) & 1, abort_flag, v.status,
+                                 kDevTimeoutFull)) {
+            ok = false;
+            return nullptr;
+        }
+        return &bars->pieces[seg % kSlots];
+    };
+    auto give = [&](int seg) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bars->piece_free[seg % kSlots]);
+    };
     if (warp == 0) {
-        // ------------------------------------------------------------ keys
+        // ------------------------------------------------------- pieces, keys
         ptx::regs_dec<kRegsControl>();
+        Cursor k;
+        cursor_seek<TcTiling>(k, v, prefix, lo);
         const int box = min(pp.page, kKeys);
         const int boxes = kKeys / box;
-        int kt = 0, tb0 = -1, tb_r = -1, tb = 0;
-        while (ok && k.f < hi) {
-            const Segment sg = segment_of(k, pp.group, hi);
-            const int need = (sg.len + pp.page_mask) >> pp.page_shift;
-            for (int j = sg.j0; j < sg.j0 + sg.most; ++j, ++kt) {
+        int kt = 0, seg = 0, tb0 = -1, tb_r = -1, tb = 0;
+        for (bool more = true; ok && more; ++seg) {
+            more = k.f < hi;
+            if (seg >= kSlots && !ptx::mbar_wait_warp(&bars->piece_free[seg % kSlots], (seg / kSlots - 1) & 1,
+                                                      abort_flag, v.status, kDevTimeoutEmpty)) {
+                ok = false;
+                break;
+            }
+            Piece pc{};  // no steps of either half
+            pc.most = -1;
+            if (more) pc = piece_of(k, pp.by_group, hi);
+            if (lane == 0) {
+                bars->pieces[seg % kSlots] = pc;
+                ptx::mbar_arrive(&bars->piece_full[seg % kSlots]);
+            }
+            __syncwarp();
+            if (!more) break;
+            const int need = (pc.c + pp.by_group.div(pc.rows) + pp.page_mask) >> pp.page_shift;
+            for (int j = pc.j0; j < pc.j0 + pc.most; ++j, ++kt) {
                 const int s = kt % C::kStages;
                 const int tok = j * kKeys, k0 = tok >> pp.page_shift;
                 if (k.r != tb_r || k0 < tb0 || k0 + boxes > tb0 + 32) {
@@ -212,9 +240,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tb0 = k0;
                     tb = 0;
                     if (tb0 + lane < need) {
-                        tb = v.table[(size_t)k.r * pp.width + tb0 + lane];
+                        tb = __ldg(v.table + (size_t)k.r * pp.width + tb0 + lane);
                         // Out of range reads as zeros (the map's bound), and is reported.
-                        if (tb < 0 || tb >= pp.pages) {
+                        if ((unsigned)tb >= (unsigned)pp.pages) {
                             record_status(v.status, kDevBadPosition);
                             tb = pp.pages;
                         }
@@ -238,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane < copies)
                     ptx::tma_load_4d(sV + s * C::kTileBytes + off, &tm_v, &bars->v_full[s], panel * 64, y, k.g, page);
             }
-            k.f += sg.j1 - sg.j0;
+            k.f += pc.j1 - pc.j0;
             cursor_next_unit<TcTiling>(k, v, prefix, hi);
         }
         if (*abort_flag) {
@@ -257,8 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t dk0 = ptx::smem_desc(ptx::smem_u32(sK), 16, 1024, ptx::kSwizzle128B);
         const uint64_t dv0 = ptx::smem_desc(ptx::smem_u32(sV), kPanelBytes, 1024, ptx::kSwizzle128B);
         constexpr uint64_t kTileStep = C::kTileBytes >> 4, kPanelStep = kPanelBytes >> 4;
-        int qb = 0;
-        auto issue_s = [&](int t, int s) {
+        auto issue_s = [&](int t, int s, int qb) {
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint64_t off = (ks / 4) * kPanelStep + (ks % 4) * 2;  // 32 bytes per K-step
@@ -279,40 +306,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok) ok = ptx::mbar_wait_warp(bar, phase & 1, abort_flag, v.status, code);
             return ok;
         };
-        int kt = 0, seg = 0, tails = 0, st[2] = {0, 0};
-        while (ok && k.f < hi) {
-            const Segment sg = segment_of(k, pp.group, hi);
-            qb = seg % C::kQBufs;
-            if (!wait(&bars->q_full[qb], seg / C::kQBufs, kDevTimeoutFull)) break;
-            if (!wait(&bars->k_full[kt % C::kStages], kt / C::kStages, kDevTimeoutFull)) break;
+        auto k_wait = [&](int x) { return wait(&bars->k_full[x % C::kStages], x / C::kStages, kDevTimeoutFull); };
+        auto q_wait = [&](int seg) { return wait(&bars->q_full[seg % C::kQBufs], seg / C::kQBufs, kDevTimeoutFull); };
+        // What of a piece the products need.
+        struct Steps {
+            int steps[2], most, tail;
+        };
+        auto read = [&](int seg) {
+            Steps x{{0, 0}, -1, -1};
+            const Piece* pc = take(seg);
+            if (pc != nullptr) {
+                x = Steps{{pc->steps[0], pc->steps[1]}, pc->most, pc->tail < 0 ? -1 : pc->tail - pc->j0};
+                give(seg);
+            }
+            return x;
+        };
+        int kt = 0, tails = 0, st[2] = {0, 0};
+        bool begun[2] = {false, false};  // the next piece's first S is already issued
+        Steps sg = read(0);
+        for (int seg = 0; ok && sg.most >= 0; ++seg) {
+            const int qb = seg % C::kQBufs;
+            if (!q_wait(seg) || !k_wait(kt)) break;
             for (int t = 0; t < 2; ++t) {
-                if (sg.steps[t] == 0) continue;
+                if (sg.steps[t] == 0 || begun[t]) continue;
                 // S of the piece before has been read (d > 64: its P V, issued before, read it).
                 if (C::kSepP && st[t] > 0 && !wait(&bars->s_free[t], st[t] - 1, kDevTimeoutFull)) break;
                 ptx::tc_fence_after();
-                issue_s(t, kt % C::kStages);
+                issue_s(t, kt % C::kStages, qb);
             }
+            begun[0] = begun[1] = false;
             if (!ok) break;
             if (sg.most == 1) ptx::mma_commit_elect(&bars->q_free[qb]);
+            Steps next{{0, 0}, -2, -1};  // not read yet
             for (int j = 0; ok && j < sg.most; ++j) {
-                const int s = (kt + j) % C::kStages, s1 = (kt + j + 1) % C::kStages, next = (kt + j + 1) / C::kStages;
-                bool v_ready = false, k_next = false;
+                const int s = (kt + j) % C::kStages;
+                bool v_ready = false;
                 auto v_wait = [&]() {
                     if (v_ready) return true;
-                    v_ready = sg.j0 + j == sg.tail ? wait(&bars->v_clean[tails % 3], tails / 3, kDevTimeoutFull)
-                                                   : wait(&bars->v_full[s], (kt + j) / C::kStages, kDevTimeoutFull);
+                    v_ready = j == sg.tail ? wait(&bars->v_clean[tails % 3], tails / 3, kDevTimeoutFull)
+                                           : wait(&bars->v_full[s], (kt + j) / C::kStages, kDevTimeoutFull);
                     return v_ready;
                 };
-                auto k_wait = [&]() {
-                    if (!k_next) k_next = wait(&bars->k_full[s1], next, kDevTimeoutFull);
-                    return k_next;
-                };
                 if constexpr (C::kSepP) {
-                    for (int t = 0; t < 2; ++t) {  // the next S as soon as the softmax holds this one
-                        if (j + 1 >= sg.steps[t]) continue;
-                        if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait()) break;
-                        ptx::tc_fence_after();
-                        issue_s(t, s1);
+                    // Each half's next S as soon as the softmax holds this one, past the
+                    // piece's end too.
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j + 1 < sg.steps[t]) {
+                            if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait(kt + j + 1)) break;
+                            ptx::tc_fence_after();
+                            issue_s(t, (kt + j + 1) % C::kStages, qb);
+                        } else if (j + 1 == sg.steps[t]) {
+                            if (next.most == -2) next = read(seg + 1);
+                            if (!ok || next.steps[t] == 0) continue;
+                            if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !q_wait(seg + 1) ||
+                                !k_wait(kt + sg.most))
+                                break;
+                            ptx::tc_fence_after();
+                            issue_s(t, (kt + sg.most) % C::kStages, (seg + 1) % C::kQBufs);
+                            begun[t] = true;
+                        }
                     }
                     if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                     for (int t = 0; t < 2 && ok; ++t) {
@@ -328,22 +380,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tc_fence_after();
                         issue_pv(t, s, j > 0);
                         if (j + 1 < sg.steps[t]) {
-                            if (!k_wait()) break;
+                            if (!k_wait(kt + j + 1)) break;
                             ptx::tc_fence_after();
-                            issue_s(t, s1);
+                            issue_s(t, (kt + j + 1) % C::kStages, qb);
                         }
                     }
                     if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                 }
                 if (ok) ptx::mma_commit_elect(&bars->kv_empty[s]);
             }
+            if (ok && next.most == -2) next = read(seg + 1);
             kt += sg.most;
-            ++seg;
             tails += sg.tail >= 0;
             st[0] += sg.steps[0];
             st[1] += sg.steps[1];
-            k.f += sg.j1 - sg.j0;
-            cursor_next_unit<TcTiling>(k, v, prefix, hi);
+            sg = next;
         }
         ptx::mma_commit_elect(&bars->drain);
         ptx::mbar_drain(&bars->drain, 0, v.status);
@@ -355,9 +406,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t q_u = ptx::smem_u32(sQ) + (chunk / 8) * kPanelBytes;
         const int cols = max(0, min(8, pp.d - chunk * 8));
         PieceMeta mine{};
-        int kt = 0, seg = 0, tails = 0;
-        while (ok && k.f < hi) {
-            const Segment sg = segment_of(k, pp.group, hi);
+        int kt = 0, tails = 0;
+        for (int seg = 0; ok; ++seg) {
+            const Piece* slot = take(seg);
+            if (slot == nullptr) break;
+            const Piece pc = *slot;
+            give(seg);
+            if (pc.most < 0) break;
             const int qb = seg % C::kQBufs;
             if (seg >= C::kQBufs && !ptx::mbar_wait_warp(&bars->q_free[qb], (seg / C::kQBufs - 1) & 1, abort_flag,
                                                          v.status, kDevTimeoutEmpty)) {
@@ -365,14 +420,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             }
             // Rows past the unit's are zero.
-            const int row_end = (sg.rows[1] ? 2 : 1) * kBM;
+            const int row_end = pc.rows - pc.q * kRows > kBM ? 2 * kBM : kBM;
             for (int r = tr / kChunks; r < row_end; r += kStep) {
-                const int rho = k.q * kRows + r;
-                const bool in = rho < k.rq.rows;
-                const int t = in ? pp.by_group.div(rho) : 0, hd = k.g * pp.group + (in ? rho - t * pp.group : 0);
-                const __nv_bfloat16* src = P1 + ((size_t)(k.rq.first + t) * pp.H + hd) * pp.d + (cols ? chunk * 8 : 0);
+                const int rho = pc.q * kRows + r;
+                const bool in = rho < pc.rows;
+                const int t = in ? pp.by_group.div(rho) : 0, hd = pc.g * pp.group + (in ? rho - t * pp.group : 0);
+                const __nv_bfloat16* src = P1 + ((size_t)(pc.first + t) * pp.H + hd) * pp.d + (cols ? chunk * 8 : 0);
                 const int bytes = in ? cols * 2 : 0, rr = r & 127;
-                const uint32_t dst = q_u + (2 * qb + (r >> 7)) * C::kTileBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4);
+                const uint32_t dst =
+                    q_u + (2 * qb + (r >> 7)) * C::kTileBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4);
                 if ((pp.d & 7) == 0) {
                     cp_async16(dst, src, bytes);
                 } else {  // rows of 120 bytes start on 8
@@ -384,15 +440,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars->q_full[qb]);
-            if (sg.tail >= 0) {
+            if (pc.tail >= 0) {
                 // Weight 0 times whatever a page holds past the end must be 0.
-                const int x = kt + sg.tail - sg.j0, s = x % C::kStages;
+                const int x = kt + pc.tail - pc.j0, s = x % C::kStages;
                 if (!ptx::mbar_wait_warp(&bars->v_full[s], (x / C::kStages) & 1, abort_flag, v.status, kDevTimeoutFull)) {
                     ok = false;
                     break;
                 }
                 uint8_t* tile = sV + s * C::kTileBytes;
-                for (int r = sg.len - sg.tail * kKeys + tr / 8; r < kKeys; r += 8)
+                const int len = pc.c + pp.by_group.div(pc.rows);
+                for (int r = len - pc.tail * kKeys + tr / 8; r < kKeys; r += 8)
 #pragma unroll
                     for (int p = 0; p < C::kPanels; ++p)
                         *reinterpret_cast<uint4*>(tile + p * kPanelBytes + r * 128 + (tr & 7) * 16) =
@@ -402,12 +459,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) ptx::mbar_arrive(&bars->v_clean[tails % 3]);
                 ++tails;
             }
-            if (sg.j0 == 0 && sg.j1 < k.n) 
-                mine = PieceMeta{share.owner(k.f + k.n - 1) - worker + 1, k.rq.first, k.rq.c, k.rq.rows, k.g, k.q};
-            kt += sg.most;
-            ++seg;
-            k.f += sg.j1 - sg.j0;
-            cursor_next_unit<TcTiling>(k, v, prefix, hi);
+            if (pc.j0 == 0 && pc.j1 < pc.n)
+                mine = PieceMeta{share.owner(pc.place + pc.n - 1) - worker + 1, pc.first, pc.c, pc.rows, pc.g, pc.q};
+            kt += pc.most;
         }
         if (threadIdx.x == 64) meta[worker] = ok ? mine : PieceMeta{};
     } else {
@@ -421,20 +475,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* turn_mine = &bars->turn[t][quarter];
         uint64_t* turn_next = &bars->turn[t ^ 1][quarter];
         int st = 0, pairs = 0;  // steps of this half, and steps both halves took in turn
-        while (ok && k.f < hi) {
-            int steps, n_pair, own, first_own;  // the row's own token (the last key it sees), the warp's least
-            {
-                const Segment sg = segment_of(k, pp.group, hi);
-                steps = sg.steps[t];
-                n_pair = C::kSepP ? 0 : min(sg.steps[0], sg.steps[1]);
-                const int rho = min(k.q * kRows + t * kBM + r, k.rq.rows - 1);
-                own = k.rq.c + pp.by_group.div(rho) - sg.j0 * kKeys;  // as a column of the piece's first tile
-                first_own = __shfl_sync(0xffffffffu, own, 0);
-            }
-            const float corr = pp.lambda * __logf((float)(own + k.j * kKeys + 1));
-            __syncwarp();
-            if (lane == 0) bars->parked[warp - 4] = k;
-            __syncwarp();
+        for (int seg = 0; ok; ++seg) {
+            const Piece* pc = take(seg);  // the slot stays this warp's until the piece is done
+            if (pc == nullptr || pc->most < 0) break;
+            const int steps = pc->steps[t], n_pair = C::kSepP ? 0 : min(pc->steps[0], pc->steps[1]);
+            // The row's own token (the last key it sees) as a column of the piece's first
+            // tile, and the warp's least.
+            int own = pc->c + pp.by_group.div(min(pc->q * kRows + t * kBM + r, pc->rows - 1));
+            const float corr = pp.lambda * __logf((float)(own + 1));
+            own -= pc->j0 * kKeys;
+            int own_lo = __shfl_sync(0xffffffffu, own, 0);
             float m = -INFINITY, l = 0.f;
             for (int j = 0; ok && j < steps; ++j) {
                 if (!ptx::mbar_wait_warp(&bars->s_full[t], (st + j) & 1, abort_flag, v.status, kDevTimeoutMma)) {
@@ -460,14 +510,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     ptx::pin_regs(sv);  // the loops below start after the turn is taken
                 }
-                const bool edge = first_own < kKeys;  // own: the Self entry's column; later ones are masked
+                const float2 ch2 = make_float2(c_half, c_half);
+                // The two long loops run over every column of every tile, also those that the
+                // mask drops: with branches around blocks of them the whole kernel was slower
+                // (whole prompts, heads of 64: 0.48 ms for 0.42).
+                const bool edge = own_lo < kKeys;  // some row's own token is in this tile or before it
                 float self = 0.f;
                 if (edge) {
 #pragma unroll
                     for (int c = 0; c < 128; ++c) self = c == own ? as_f(sv[c]) : self;
                     self = fmaf(0.5f, ptx::tanh_approx(self * c_diag), 0.5f) + corr;
                 }
-                const float2 ch2 = make_float2(c_half, c_half);
 #pragma unroll
                 for (int e = 0; e < 64; ++e) {
                     const float2 h = ptx::mul2(make_float2(as_f(sv[2 * e]), as_f(sv[2 * e + 1])), ch2);
@@ -514,6 +567,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float2 sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
                     l += sum.x + sum.y;
                 }
+                own -= kKeys;
+                own_lo -= kKeys;
                 if constexpr (!C::kSepP) {
                     ptx::pin_regs(pk[0]);  // and end before it is passed on
                     ptx::pin_regs(pk[1]);
@@ -546,20 +601,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&bars->p_full[t]);
-                own -= kKeys;
-                first_own -= kKeys;
             }
-            unpark(k, &bars->parked[warp - 4]);
-            const Segment sg = segment_of(k, pp.group, hi);
-            const int rho = min(k.q * kRows + t * kBM + r, k.rq.rows - 1), token = pp.by_group.div(rho);
             if (ok && steps > 0) {
                 ok = ptx::mbar_wait_warp(&bars->o_done[t], (st + steps - 1) & 1, abort_flag, v.status, kDevTimeoutMma);
                 ptx::tc_fence_after();
             }
-            if (ok && sg.rows[t] > 0) {
-                const bool direct = sg.j0 == 0 && sg.j1 == k.n, mine = r < sg.rows[t];
-                const size_t yr = (size_t)(k.rq.first + token) * pp.H + k.g * pp.group + (rho - token * pp.group);
-                float* slot = part + ((size_t)worker * 2 + (sg.j0 == 0 ? 1 : 0)) * C::kSlotFloats;
+            const int row = pc->q * kRows + t * kBM + r, rows = pc->rows;  // row: of the request
+            if (ok && row - r < rows) {
+                const bool direct = pc->j0 == 0 && pc->j1 == pc->n, mine = row < rows;
+                const int rho = min(row, rows - 1), token = pp.by_group.div(rho);
+                const size_t yr = (size_t)(pc->first + token) * pp.H + pc->g * pp.group + (rho - token * pp.group);
+                float* slot = part + ((size_t)worker * 2 + (pc->j0 == 0 ? 1 : 0)) * C::kSlotFloats;
                 const float inv = direct ? 1.f / l : 1.f;
 #pragma unroll
                 for (int c0 = 0; c0 < D / 32; ++c0) {
@@ -592,8 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             st += steps;
             pairs += n_pair;
-            k.f += sg.j1 - sg.j0;
-            cursor_next_unit<TcTiling>(k, v, prefix, hi);
+            give(seg);
         }
     }
     ptx::tc_fence_before();

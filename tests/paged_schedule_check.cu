@@ -16,7 +16,7 @@ bool check() {
                 const int rows = fresh * group;
                 int64_t sum = 0;
                 for (int q = 0; q <= T::row_tiles(rows); ++q) {
-                    if (T::places(c, rows, group, q) != sum) {
+                    if (T::places(c, rows, FastDiv(group), q) != sum) {
                         std::printf("rows/tile %d keys %d group %d cached %d fresh %d: first %d tiles\n", ROWS, KEYS, group,
                                     c, fresh, q);
                         return false;
@@ -31,6 +31,10 @@ bool check() {
 }
 
 int main() {
+    for (uint32_t n : {1u, 2u, 3u, 5u, 7u, 12u, 40u, 127u, 128u, 129u, 1000u, 1024u})
+        for (int64_t x : {0ll, 1ll, 2ll, 126ll, 127ll, 128ll, 999999ll, 2147483646ll, 2147483647ll})
+            for (int64_t y = x > 3 ? x - 3 : 0; y <= x; ++y)
+                if (FastDiv(n).div((int)y) != (int)(y / n)) return std::printf("div %u %ld\n", n, (long)y), 1;
     for (int64_t n : {0, 1, 2, 5, 17})
         for (int64_t m : {1, 2, 7, 128})
             for (int64_t a : {0, 1, 5, 129, 1000})
