@@ -12,17 +12,22 @@
 // long rows fill the GPU as well as many short ones, and a second kernel merges the
 // units that the cuts divide.
 //   warp 0      walks the block's stretch of the line, one piece of a unit after another,
-//               hands each to the others, and loads its keys: the pages of each tile by
-//               TMA, one copy per lane
+//               hands each to the others, and loads P2: the pages of each tile by TMA, one
+//               copy per lane
 //   warp 1      MMA issuer and TMEM owner
-//   warps 2-3   query rows into shared memory; clear the keys past a request's end
+//   warp 2      query rows into shared memory; clears the keys past a request's end
+//   warp 3      loads I~
 //   warps 4-7   softmax of rows 0-127 (one thread per row)
 //   warps 8-11  softmax of rows 128-255
-// Per key tile, per 128-row half: S = Q K^T (both in shared memory) -> registers:
-// SiLU, mask and Self where the tile reaches the rows' own tokens, online softmax ->
-// P as bf16 in TMEM -> O += P V.  At d <= 64 P has TMEM columns of its own and the
-// next S is issued while the softmax works; at d 80 and 128 P overwrites S and the
-// two halves take turns on the special-function unit.
+// Per key tile, per 128-row half: S = Q K^T (both in shared memory) -> registers, 32
+// columns at a time: SiLU, mask and Self where the tile reaches the rows' own tokens,
+// online softmax -> P as bf16 in TMEM -> O += P V.  The softmax warps should never wait:
+//  - d <= 64: P has TMEM columns of its own, and the next S is issued once the softmax
+//    has read this one;
+//  - d 80 and 128, where S and O fill TMEM: P takes the place of S's left 64 columns, so
+//    the next tile's right 64 scores are issued as soon as this tile's are read, the left
+//    ones after P V; the softmax begins with the right ones and keeps their weights in
+//    registers until it has read the left.
 //
 // Bound: two special functions per score (tanh, 16 results a cycle and SM; ex2, 32)
 // give 3/32 cycle a score, against 4 d / 8192 = 1/32 cycle (d = 64) or 1/16 (d =
@@ -41,8 +46,8 @@ namespace {
 
 constexpr int kBM = 128, kRows = 256, kKeys = 128;
 constexpr int kThreads = 384;
-// 128 * 56 + 256 * 224 = 64512 = 384 * 168 registers.
-constexpr uint32_t kRegsControl = 56, kRegsSoftmax = 224;
+// 128 * 104 + 256 * 200 = 64512 = 384 * 168 registers.
+constexpr uint32_t kRegsControl = 104, kRegsSoftmax = 200;
 constexpr int kPanelBytes = 128 * 128;  // 128 rows x 64 bf16
 constexpr int kMinTiles = 4;
 // A unit's beginning and end (queries, first scores, output: 7 to 12 thousand cycles)
@@ -71,7 +76,8 @@ struct Piece {
     int steps[2], most, tail;   // key tiles that each half of the rows sees, the most of
                                 // them (-1: no more pieces), and the one that the
                                 // request ends inside (-1: not in this piece)
-    int place, pad[3];          // of tile j0 on the line
+    int place;                  // of tile j0 on the line
+    int r, pad[2];              // row of the block table
 };
 static_assert(sizeof(Piece) == 64, "a slot");
 constexpr int kSlots = 4;  // pieces handed out and not yet done with
@@ -79,12 +85,12 @@ constexpr int kSlots = 4;  // pieces handed out and not yet done with
 struct TcBars {
     uint64_t piece_full[kSlots], piece_free[kSlots];
     uint64_t q_full[2], q_free[2];
-    uint64_t k_full[4], v_full[4], kv_empty[4];
+    uint64_t k_full[4], v_full[4], k_empty[4], v_empty[4];
     // In turn: the cleared tile of a piece may be ready before those of the pieces before
     // have been waited for, but no more than kQBufs pieces ahead (q_free holds that back).
     uint64_t v_clean[3];
-    uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
-    uint64_t turn[2][4];
+    // S of a half there and read (d > 64: its right columns; s_left: the left ones there).
+    uint64_t s_full[2], s_left[2], s_free[2], p_full[2], o_done[2];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -117,6 +123,7 @@ __device__ __forceinline__ Piece piece_of(const Cursor& k, const FastDiv& by_gro
     const int len = k.rq.c + by_group.div(k.rq.rows), tail = len / kKeys;
     p.tail = (len % kKeys != 0 && tail >= p.j0 && tail < p.j0 + p.most) ? tail : -1;
     p.place = k.f;
+    p.r = k.r;
     return p;
 }
 
@@ -150,20 +157,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&bars->piece_full[x], 1);
             ptx::mbar_init(&bars->piece_free[x], 11);  // the other warps
         }
-        for (int x = 0; x < 3; ++x) ptx::mbar_init(&bars->v_clean[x], 2);
+        for (int x = 0; x < 3; ++x) ptx::mbar_init(&bars->v_clean[x], 1);
         for (int t = 0; t < 2; ++t) {
-            ptx::mbar_init(&bars->q_full[t], 2);
+            ptx::mbar_init(&bars->q_full[t], 1);
             ptx::mbar_init(&bars->q_free[t], 1);
             ptx::mbar_init(&bars->s_full[t], 1);
+            ptx::mbar_init(&bars->s_left[t], 1);
             ptx::mbar_init(&bars->s_free[t], 128);
             ptx::mbar_init(&bars->p_full[t], 128);
             ptx::mbar_init(&bars->o_done[t], 1);
-            for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[t][q], 1);
         }
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(&bars->k_full[s], 1);
             ptx::mbar_init(&bars->v_full[s], 1);
-            ptx::mbar_init(&bars->kv_empty[s], 1);
+            ptx::mbar_init(&bars->k_empty[s], 1);
+            ptx::mbar_init(&bars->v_empty[s], 1);
         }
         ptx::mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
@@ -207,98 +215,111 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&bars->piece_free[seg % kSlots]);
     };
+    // One tensor's tiles of a piece, tile x of the block into stage x % kStages.
+    const int box = min(pp.page, kKeys), boxes = kKeys / box;
+    int x = 0, tb0 = -1, tb_r = -1, tb = 0;
+    auto load = [&](const Piece& pc, const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty) {
+        const int need = (pc.c + pp.by_group.div(pc.rows) + pp.page_mask) >> pp.page_shift;
+        for (int j = pc.j0; j < pc.j0 + pc.most; ++j, ++x) {
+            const int s = x % C::kStages;
+            const int tok = j * kKeys, k0 = tok >> pp.page_shift;
+            if (pc.r != tb_r || k0 < tb0 || k0 + boxes > tb0 + 32) {
+                tb_r = pc.r;
+                tb0 = k0;
+                tb = 0;
+                if (tb0 + lane < need) {
+                    tb = __ldg(v.table + (size_t)pc.r * pp.width + tb0 + lane);
+                    // Out of range reads as zeros (the map's bound), and is reported.
+                    if ((unsigned)tb >= (unsigned)pp.pages) {
+                        record_status(v.status, kDevBadPosition);
+                        tb = pp.pages;
+                    }
+                }
+            }
+            if (x >= C::kStages && !ptx::mbar_wait_warp(&empty[s], ((x / C::kStages) - 1) & 1, abort_flag, v.status,
+                                                        kDevTimeoutEmpty)) {
+                ok = false;
+                return;
+            }
+            const int copies = C::kPanels * min(boxes, need - k0);
+            const int p = lane / C::kPanels, panel = lane % C::kPanels;
+            const int page = __shfl_sync(0xffffffffu, tb, (k0 - tb0 + p) & 31);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], copies * box * 128);
+            __syncwarp();
+            if (lane < copies)
+                ptx::tma_load_4d(ring + s * C::kTileBytes + panel * kPanelBytes + p * box * 128, map, &full[s],
+                                 panel * 64, boxes > 1 ? 0 : (tok & pp.page_mask), pc.g, page);
+        }
+    };
+    auto drain = [&](uint64_t* full) {  // after an abort: let the copies already issued land
+        if (*abort_flag)
+            for (int y = max(0, x - C::kStages); y < x; ++y)
+                ptx::mbar_drain(&full[y % C::kStages], (y / C::kStages) & 1, v.status);
+    };
     if (warp == 0) {
-        // ------------------------------------------------------- pieces, keys
+        // --------------------------------------------------------- pieces, P2
         ptx::regs_dec<kRegsControl>();
         Cursor k;
         cursor_seek<TcTiling>(k, v, prefix, lo);
-        const int box = min(pp.page, kKeys);
-        const int boxes = kKeys / box;
-        int kt = 0, seg = 0, tb0 = -1, tb_r = -1, tb = 0;
-        for (bool more = true; ok && more; ++seg) {
-            more = k.f < hi;
+        for (int seg = 0; ok; ++seg) {
             if (seg >= kSlots && !ptx::mbar_wait_warp(&bars->piece_free[seg % kSlots], (seg / kSlots - 1) & 1,
-                                                      abort_flag, v.status, kDevTimeoutEmpty)) {
-                ok = false;
+                                                      abort_flag, v.status, kDevTimeoutEmpty))
                 break;
-            }
             Piece pc{};  // no steps of either half
             pc.most = -1;
-            if (more) pc = piece_of(k, pp.by_group, hi);
+            if (k.f < hi) pc = piece_of(k, pp.by_group, hi);
             if (lane == 0) {
                 bars->pieces[seg % kSlots] = pc;
                 ptx::mbar_arrive(&bars->piece_full[seg % kSlots]);
             }
             __syncwarp();
-            if (!more) break;
-            const int need = (pc.c + pp.by_group.div(pc.rows) + pp.page_mask) >> pp.page_shift;
-            for (int j = pc.j0; j < pc.j0 + pc.most; ++j, ++kt) {
-                const int s = kt % C::kStages;
-                const int tok = j * kKeys, k0 = tok >> pp.page_shift;
-                if (k.r != tb_r || k0 < tb0 || k0 + boxes > tb0 + 32) {
-                    tb_r = k.r;
-                    tb0 = k0;
-                    tb = 0;
-                    if (tb0 + lane < need) {
-                        tb = __ldg(v.table + (size_t)k.r * pp.width + tb0 + lane);
-                        // Out of range reads as zeros (the map's bound), and is reported.
-                        if ((unsigned)tb >= (unsigned)pp.pages) {
-                            record_status(v.status, kDevBadPosition);
-                            tb = pp.pages;
-                        }
-                    }
-                }
-                if (kt >= C::kStages && !ptx::mbar_wait_warp(&bars->kv_empty[s], ((kt / C::kStages) - 1) & 1,
-                                                             abort_flag, v.status, kDevTimeoutEmpty)) {
-                    ok = false;
-                    break;
-                }
-                const int parts = min(boxes, need - k0), copies = C::kPanels * parts;
-                const int p = lane / C::kPanels, panel = lane % C::kPanels;
-                const int page = __shfl_sync(0xffffffffu, tb, (k0 - tb0 + p) & 31);
-                const int off = panel * kPanelBytes + p * box * 128, y = boxes > 1 ? 0 : (tok & pp.page_mask);
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->k_full[s], copies * box * 128);
-                __syncwarp();
-                if (lane < copies)
-                    ptx::tma_load_4d(sK + s * C::kTileBytes + off, &tm_k, &bars->k_full[s], panel * 64, y, k.g, page);
-                if (lane == 0) ptx::mbar_arrive_expect_tx(&bars->v_full[s], copies * box * 128);
-                __syncwarp();
-                if (lane < copies)
-                    ptx::tma_load_4d(sV + s * C::kTileBytes + off, &tm_v, &bars->v_full[s], panel * 64, y, k.g, page);
-            }
+            if (pc.most < 0) break;
+            load(pc, &tm_k, sK, bars->k_full, bars->k_empty);
             k.f += pc.j1 - pc.j0;
             cursor_next_unit<TcTiling>(k, v, prefix, hi);
         }
-        if (*abort_flag) {
-            // Let the copies already issued land before the block exits.
-            for (int x = max(0, kt - C::kStages); x < kt; ++x) {
-                ptx::mbar_drain(&bars->k_full[x % C::kStages], (x / C::kStages) & 1, v.status);
-                ptx::mbar_drain(&bars->v_full[x % C::kStages], (x / C::kStages) & 1, v.status);
-            }
+        drain(bars->k_full);
+    } else if (warp == 3) {
+        // ------------------------------------------------------------------ I~
+        ptx::regs_dec<kRegsControl>();
+        for (int seg = 0; ok; ++seg) {
+            const Piece* slot = take(seg);
+            if (slot == nullptr) break;
+            const Piece pc = *slot;
+            give(seg);
+            if (pc.most < 0) break;
+            load(pc, &tm_v, sV, bars->v_full, bars->v_empty);
         }
+        drain(bars->v_full);
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
         ptx::regs_dec<kRegsControl>();
-        const uint32_t id_s = ptx::idesc_bf16(kBM, kKeys, false, false);
+        constexpr int kN = C::kSepP ? kKeys : kKeys / 2;  // keys of one S issue
+        const uint32_t id_s = ptx::idesc_bf16(kBM, kN, false, false);
         const uint32_t id_o = ptx::idesc_bf16(kBM, D, false, true);
         const uint64_t dq0 = ptx::smem_desc(ptx::smem_u32(sQ), 16, 1024, ptx::kSwizzle128B);
         const uint64_t dk0 = ptx::smem_desc(ptx::smem_u32(sK), 16, 1024, ptx::kSwizzle128B);
         const uint64_t dv0 = ptx::smem_desc(ptx::smem_u32(sV), kPanelBytes, 1024, ptx::kSwizzle128B);
-        constexpr uint64_t kTileStep = C::kTileBytes >> 4, kPanelStep = kPanelBytes >> 4;
-        auto issue_s = [&](int t, int s, int qb) {
+        // Only a descriptor's low word (the address) changes: an add of a constant a step.
+        constexpr uint32_t kTileStep = C::kTileBytes >> 4, kPanelStep = kPanelBytes >> 4;
+        // Keys n0 .. n0 + kN - 1 of the tile in stage s against half t of the queries.
+        auto issue_s = [&](int t, int s, int qb, int n0, uint64_t* full) {
+            const uint32_t q_lo = ptx::desc_lo(dq0) + (2 * qb + t) * kTileStep, q_hi = ptx::desc_hi(dq0);
+            const uint32_t k_lo = ptx::desc_lo(dk0) + s * kTileStep + n0 * 8, k_hi = ptx::desc_hi(dk0);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
-                const uint64_t off = (ks / 4) * kPanelStep + (ks % 4) * 2;  // 32 bytes per K-step
-                ptx::mma_ss_elect(tmem + t * 128, dq0 + (2 * qb + t) * kTileStep + off, dk0 + s * kTileStep + off, id_s,
-                                  ks > 0 ? 1u : 0u);
+                const uint32_t off = (ks / 4) * kPanelStep + (ks % 4) * 2;  // 32 bytes per K-step
+                ptx::mma_ss_elect(tmem + t * 128 + n0, q_lo + off, q_hi, k_lo + off, k_hi, id_s, ks > 0 ? 1u : 0u);
             }
-            ptx::mma_commit_elect(&bars->s_full[t]);
+            ptx::mma_commit_elect(full);
         };
+        constexpr int kRight = C::kSepP ? 0 : kN;  // the columns that can be issued early
         auto issue_pv = [&](int t, int s, bool accumulate) {
-            const uint32_t p_col = C::kSepP ? C::kColP + 64 * t : 128 * t;
+            const uint32_t p_col = tmem + (C::kSepP ? C::kColP + 64 * t : 128 * t);
+            const uint32_t v_lo = ptx::desc_lo(dv0) + s * kTileStep, v_hi = ptx::desc_hi(dv0);
 #pragma unroll
             for (int ks = 0; ks < kKeys / 16; ++ks)  // 16 keys of V per K-step: 2048 bytes of the MN-major tile
-                ptx::mma_ts_elect(tmem + 256 + t * D, tmem + p_col + ks * 8, dv0 + s * kTileStep + ks * 128, id_o,
+                ptx::mma_ts_elect(tmem + 256 + t * D, p_col + ks * 8, v_lo + ks * 128, v_hi, id_o,
                                   (accumulate || ks > 0) ? 1u : 0u);
             ptx::mma_commit_elect(&bars->o_done[t]);
         };
@@ -329,13 +350,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!q_wait(seg) || !k_wait(kt)) break;
             for (int t = 0; t < 2; ++t) {
                 if (sg.steps[t] == 0 || begun[t]) continue;
-                // S of the piece before has been read (d > 64: its P V, issued before, read it).
-                if (C::kSepP && st[t] > 0 && !wait(&bars->s_free[t], st[t] - 1, kDevTimeoutFull)) break;
+                // S of the piece before has been read (the left columns of d > 64: by its P V,
+                // issued before).
+                if (st[t] > 0 && !wait(&bars->s_free[t], st[t] - 1, kDevTimeoutFull)) break;
                 ptx::tc_fence_after();
-                issue_s(t, kt % C::kStages, qb);
+                issue_s(t, kt % C::kStages, qb, kRight, &bars->s_full[t]);
+                if (!C::kSepP) issue_s(t, kt % C::kStages, qb, 0, &bars->s_left[t]);
             }
             begun[0] = begun[1] = false;
             if (!ok) break;
+            ptx::mma_commit_elect(&bars->k_empty[kt % C::kStages]);
             if (sg.most == 1) ptx::mma_commit_elect(&bars->q_free[qb]);
             Steps next{{0, 0}, -2, -1};  // not read yet
             for (int j = 0; ok && j < sg.most; ++j) {
@@ -354,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (j + 1 < sg.steps[t]) {
                             if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait(kt + j + 1)) break;
                             ptx::tc_fence_after();
-                            issue_s(t, (kt + j + 1) % C::kStages, qb);
+                            issue_s(t, (kt + j + 1) % C::kStages, qb, 0, &bars->s_full[t]);
                         } else if (j + 1 == sg.steps[t]) {
                             if (next.most == -2) next = read(seg + 1);
                             if (!ok || next.steps[t] == 0) continue;
@@ -362,10 +386,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 !k_wait(kt + sg.most))
                                 break;
                             ptx::tc_fence_after();
-                            issue_s(t, (kt + sg.most) % C::kStages, (seg + 1) % C::kQBufs);
+                            issue_s(t, (kt + sg.most) % C::kStages, (seg + 1) % C::kQBufs, 0, &bars->s_full[t]);
                             begun[t] = true;
                         }
                     }
+                    if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
                     if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                     for (int t = 0; t < 2 && ok; ++t) {
                         if (j >= sg.steps[t]) continue;
@@ -374,20 +399,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                         issue_pv(t, s, j > 0);
                     }
                 } else {
+                    for (int t = 0; t < 2 && ok; ++t) {  // the next right scores once these are read
+                        if (j + 1 >= sg.steps[t]) continue;
+                        if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait(kt + j + 1)) break;
+                        ptx::tc_fence_after();
+                        issue_s(t, (kt + j + 1) % C::kStages, qb, kRight, &bars->s_full[t]);
+                    }
                     for (int t = 0; t < 2 && ok; ++t) {
                         if (j >= sg.steps[t]) continue;
                         if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
                         ptx::tc_fence_after();
                         issue_pv(t, s, j > 0);
-                        if (j + 1 < sg.steps[t]) {
-                            if (!k_wait(kt + j + 1)) break;
-                            ptx::tc_fence_after();
-                            issue_s(t, (kt + j + 1) % C::kStages, qb);
-                        }
+                        if (j + 1 < sg.steps[t]) issue_s(t, (kt + j + 1) % C::kStages, qb, 0, &bars->s_left[t]);
                     }
+                    if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
                     if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                 }
-                if (ok) ptx::mma_commit_elect(&bars->kv_empty[s]);
+                if (ok) ptx::mma_commit_elect(&bars->v_empty[s]);
             }
             if (ok && next.most == -2) next = read(seg + 1);
             kt += sg.most;
@@ -398,11 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::mma_commit_elect(&bars->drain);
         ptx::mbar_drain(&bars->drain, 0, v.status);
-    } else if (warp < 4) {
+    } else if (warp == 2) {
         // ------------------------------------------------ queries, keys past the end
         ptx::regs_dec<kRegsControl>();
-        constexpr int kChunks = D / 8, kStep = 64 / kChunks;  // 16-byte chunks of a row; rows at a time
-        const int tr = threadIdx.x - 64, chunk = tr % kChunks;
+        constexpr int kChunks = D / 8, kStep = 32 / kChunks;  // 16-byte chunks of a row; rows at a time
+        const int chunk = lane % kChunks;
         const uint32_t q_u = ptx::smem_u32(sQ) + (chunk / 8) * kPanelBytes;
         const int cols = max(0, min(8, pp.d - chunk * 8));
         PieceMeta mine{};
@@ -421,7 +449,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // Rows past the unit's are zero.
             const int row_end = pc.rows - pc.q * kRows > kBM ? 2 * kBM : kBM;
-            for (int r = tr / kChunks; r < row_end; r += kStep) {
+            for (int r = lane / kChunks; r < row_end; r += kStep) {
                 const int rho = pc.q * kRows + r;
                 const bool in = rho < pc.rows;
                 const int t = in ? pp.by_group.div(rho) : 0, hd = pc.g * pp.group + (in ? rho - t * pp.group : 0);
@@ -449,10 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint8_t* tile = sV + s * C::kTileBytes;
                 const int len = pc.c + pp.by_group.div(pc.rows);
-                for (int r = len - pc.tail * kKeys + tr / 8; r < kKeys; r += 8)
+                for (int r = len - pc.tail * kKeys + lane / 8; r < kKeys; r += 4)
 #pragma unroll
                     for (int p = 0; p < C::kPanels; ++p)
-                        *reinterpret_cast<uint4*>(tile + p * kPanelBytes + r * 128 + (tr & 7) * 16) =
+                        *reinterpret_cast<uint4*>(tile + p * kPanelBytes + r * 128 + (lane & 7) * 16) =
                             make_uint4(0, 0, 0, 0);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
@@ -463,7 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mine = PieceMeta{share.owner(pc.place + pc.n - 1) - worker + 1, pc.first, pc.c, pc.rows, pc.g, pc.q};
             kt += pc.most;
         }
-        if (threadIdx.x == 64) meta[worker] = ok ? mine : PieceMeta{};
+        if (lane == 0) meta[worker] = ok ? mine : PieceMeta{};
     } else {
         // ------------------------------------------------------------- softmax
         ptx::regs_inc<kRegsSoftmax>();
@@ -472,57 +500,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_col = t * 128, o_col = 256 + t * D;
         const float c_half = 0.5f * pp.inv_sqrt_d;                // U/2 per raw dot product
         const float c_diag = 0.5f * pp.inv_sqrt_d / pp.tau_S;     // U/(2 tau_S)
-        uint64_t* turn_mine = &bars->turn[t][quarter];
-        uint64_t* turn_next = &bars->turn[t ^ 1][quarter];
-        int st = 0, pairs = 0;  // steps of this half, and steps both halves took in turn
+        int st = 0;  // steps of this half so far
         for (int seg = 0; ok; ++seg) {
             const Piece* pc = take(seg);  // the slot stays this warp's until the piece is done
             if (pc == nullptr || pc->most < 0) break;
-            const int steps = pc->steps[t], n_pair = C::kSepP ? 0 : min(pc->steps[0], pc->steps[1]);
+            const int steps = pc->steps[t];
             // The row's own token (the last key it sees) as a column of the piece's first
-            // tile, and the warp's least.
+            // tile, the warp's least and greatest.
             int own = pc->c + pp.by_group.div(min(pc->q * kRows + t * kBM + r, pc->rows - 1));
             const float corr = pp.lambda * __logf((float)(own + 1));
             own -= pc->j0 * kKeys;
-            int own_lo = __shfl_sync(0xffffffffu, own, 0);
+            int own_lo = __shfl_sync(0xffffffffu, own, 0), own_hi = __shfl_sync(0xffffffffu, own, 31);
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; ok && j < steps; ++j) {
-                if (!ptx::mbar_wait_warp(&bars->s_full[t], (st + j) & 1, abort_flag, v.status, kDevTimeoutMma)) {
+            bool o_ready = false;  // O and P are free of this tile's predecessors
+            auto o_wait = [&](int j) {
+                if (o_ready) return;
+                o_ready = true;
+                if (j == 0) return;
+                if (!ptx::mbar_wait_warp(&bars->o_done[t], (st + j - 1) & 1, abort_flag, v.status, kDevTimeoutMma))
                     ok = false;
-                    break;
-                }
                 ptx::tc_fence_after();
-                uint32_t sv[128];
+            };
+            const uint32_t p_addr = lane_addr + (C::kSepP ? C::kColP + 64 * t : s_col);
+            uint32_t hold[2][16] = {};  // d > 64: the right columns' weights
+            auto scale_pairs = [](uint32_t& w, float f) {
+                const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+                w = ptx::pack_bf16x2(x.x * f, x.y * f);
+            };
+            // The maximum rises to m_new in block b of tile j (seldom after the first): what has
+            // been summed under the old one is scaled, in O, in l and in this tile's P so far.
+            // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
+            auto raise = [&](float m_new, int j, int b) {
+                const float f = m_new == -INFINITY ? 1.f : ptx::ex2_approx((m - m_new) * kLog2e);
+                l *= f;
+                m = m_new;
+                o_wait(j);
+                if (j > 0) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D / 32; ++c0) {
+                        uint32_t ov[32];
+                        ptx::tmem_ld32(lane_addr + o_col + 32 * c0, ov);
+                        ptx::tmem_ld_wait();
+                        ptx::pin_regs(ov);
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    ptx::tmem_ld32(lane_addr + s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
-                ptx::tmem_ld_wait();
-                ptx::pin_regs(sv);
-                if constexpr (C::kSepP) {
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive(&bars->s_free[t]);  // the next S may overwrite it
-                } else {
-                    const int x = pairs + j;
-                    if (j < n_pair && x + t > 0 &&
-                        !ptx::mbar_wait_warp(turn_mine, (x + t - 1) & 1, abort_flag, v.status, kDevTimeoutMma)) {
-                        ok = false;
-                        break;
+                        for (int e = 0; e < 32; ++e) ov[e] = as_u(as_f(ov[e]) * f);
+                        ptx::tmem_st32(lane_addr + o_col + 32 * c0, ov);
                     }
-                    ptx::pin_regs(sv);  // the loops below start after the turn is taken
                 }
-                const float2 ch2 = make_float2(c_half, c_half);
-                // The two long loops run over every column of every tile, also those that the
-                // mask drops: with branches around blocks of them the whole kernel was slower
-                // (whole prompts, heads of 64: 0.48 ms for 0.42).
-                const bool edge = own_lo < kKeys;  // some row's own token is in this tile or before it
+                if (!C::kSepP && b != 2) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        scale_pairs(hold[0][e], f);
+                        scale_pairs(hold[1][e], f);  // b = 3: not there yet
+                    }
+                }
+                ptx::tmem_st_wait();
+#pragma unroll 1
+                for (int x = 0; x < (C::kSepP || b == 1 ? b : 0); ++x) {
+                    uint32_t pv[16];
+                    ptx::tmem_ld16(p_addr + 16 * x, pv);
+                    ptx::tmem_ld_wait();
+                    ptx::pin_regs(pv);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) scale_pairs(pv[e], f);
+                    ptx::tmem_st16(p_addr + 16 * x, pv);
+                }
+            };
+            // 32 scores -> the weights of columns 32 b and on, and what they add to the row's
+            // sum and maximum.
+            auto block = [&](uint32_t (&sv)[32], uint32_t (&pk)[16], int j, int b) {
+                const int c0 = 32 * b;
+                if (c0 > own_hi) {  // past every row's own token
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) pk[e] = 0u;
+                    return;
+                }
+                const bool edge = c0 + 31 >= own_lo;  // at or past some row's
                 float self = 0.f;
                 if (edge) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) self = c == own ? as_f(sv[c]) : self;
+                    for (int c = 0; c < 32; ++c) self = c0 + c == own ? as_f(sv[c]) : self;
                     self = fmaf(0.5f, ptx::tanh_approx(self * c_diag), 0.5f) + corr;
                 }
+                const float2 ch2 = make_float2(c_half, c_half);
 #pragma unroll
-                for (int e = 0; e < 64; ++e) {
+                for (int e = 0; e < 16; ++e) {
                     const float2 h = ptx::mul2(make_float2(as_f(sv[2 * e]), as_f(sv[2 * e + 1])), ch2);
                     const float2 th = make_float2(ptx::tanh_approx(h.x), ptx::tanh_approx(h.y));
                     const float2 E = ptx::fma2(h, th, h);  // SiLU(U) = (U/2)(1 + tanh(U/2))
@@ -531,73 +593,83 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (edge) {
 #pragma unroll
-                    for (int c = 0; c < 128; ++c) {
-                        const float x = c > own ? -INFINITY : as_f(sv[c]);
-                        sv[c] = as_u(c == own ? self : x);
+                    for (int c = 0; c < 32; ++c) {
+                        const float x = c0 + c > own ? -INFINITY : as_f(sv[c]);
+                        sv[c] = as_u(c0 + c == own ? self : x);
                     }
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 128; c += 8) {
+                for (int c = 0; c < 32; c += 8) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) mx[q] = ptx::max3(mx[q], as_f(sv[c + 2 * q]), as_f(sv[c + 2 * q + 1]));
                 }
                 const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                const bool rescale = __any_sync(0xffffffffu, m_new > m + kRaise * kLn2);
-                float scale = 1.f;
-                if (rescale) {
-                    // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
-                    scale = m_new == -INFINITY ? 1.f : ptx::ex2_approx((m - m_new) * kLog2e);
-                    l *= scale;
-                    m = m_new;
-                }
+                if (__any_sync(0xffffffffu, m_new > m + kRaise * kLn2)) raise(m_new, j, b);
                 const float m_ref = m == -INFINITY ? 0.f : m;
                 const float2 l2e2 = make_float2(kLog2e, kLog2e), nm2 = make_float2(-m_ref * kLog2e, -m_ref * kLog2e);
-                float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                make_float2(0.f, 0.f)};
-                uint32_t pk[2][32];
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int c = 0; c < 64; ++c) {
-                    const float2 y = ptx::fma2(make_float2(as_f(sv[2 * c]), as_f(sv[2 * c + 1])), l2e2, nm2);
+                for (int e = 0; e < 16; ++e) {
+                    const float2 y = ptx::fma2(make_float2(as_f(sv[2 * e]), as_f(sv[2 * e + 1])), l2e2, nm2);
                     const float2 p = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
-                    ls[c & 3] = ptx::add2(ls[c & 3], p);
-                    pk[c >> 5][c & 31] = ptx::pack_bf16x2(p.x, p.y);
+                    ls[e & 1] = ptx::add2(ls[e & 1], p);
+                    pk[e] = ptx::pack_bf16x2(p.x, p.y);
                 }
-                {
-                    const float2 sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
-                    l += sum.x + sum.y;
+                const float2 sum = ptx::add2(ls[0], ls[1]);
+                l += sum.x + sum.y;
+            };
+            for (int j = 0; ok && j < steps; ++j) {
+                o_ready = false;
+                if (!ptx::mbar_wait_warp(&bars->s_full[t], (st + j) & 1, abort_flag, v.status, kDevTimeoutMma)) {
+                    ok = false;
+                    break;
                 }
+                ptx::tc_fence_after();
+                // A loop, not 128 columns in a row: its code stays in the instruction caches
+                // (whole prompts, heads of 64: 0.36 ms, unrolled 0.41).  The blocks' order: 0 1 2
+                // 3, or the right ones first.
+#pragma unroll 1
+                for (int i = 0; i < 4; ++i) {
+                    const int b = C::kSepP ? i : i ^ 2;
+                    uint32_t sv[32], pk[16];
+                    if (!C::kSepP && i == 2) {
+                        if (!ptx::mbar_wait_warp(&bars->s_left[t], (st + j) & 1, abort_flag, v.status,
+                                                 kDevTimeoutMma)) {
+                            ok = false;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                    }
+                    ptx::tmem_ld32(lane_addr + s_col + 32 * b, sv);
+                    ptx::tmem_ld_wait();
+                    ptx::pin_regs(sv);
+                    if (b == 3) {  // the next S may overwrite what has been read
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(&bars->s_free[t]);
+                    }
+                    block(sv, pk, j, b);
+                    if (C::kSepP) {
+                        if (b == 0) o_wait(j);  // P V of the tile before has read its P
+                        ptx::tmem_st16(p_addr + 16 * b, pk);
+                    } else if (b >= 2) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            if (b == 2) hold[0][e] = pk[e];
+                            if (b == 3) hold[1][e] = pk[e];
+                        }
+                    } else {  // in the place of columns already read
+                        ptx::tmem_st16(p_addr + 16 * b, pk);
+                        if (b == 1) {
+                            ptx::tmem_st16(p_addr + 32, hold[0]);
+                            ptx::tmem_st16(p_addr + 48, hold[1]);
+                        }
+                    }
+                }
+                if (!ok) break;
                 own -= kKeys;
                 own_lo -= kKeys;
-                if constexpr (!C::kSepP) {
-                    ptx::pin_regs(pk[0]);  // and end before it is passed on
-                    ptx::pin_regs(pk[1]);
-                    __syncwarp();
-                    if (j < n_pair && lane == 0) ptx::mbar_arrive(turn_next);
-                }
-                if (j > 0 && (C::kSepP || rescale)) {
-                    // P V of the tile before has read its P, and O is final for a rescale.
-                    if (!ptx::mbar_wait_warp(&bars->o_done[t], (st + j - 1) & 1, abort_flag, v.status, kDevTimeoutMma)) {
-                        ok = false;
-                        break;
-                    }
-                    ptx::tc_fence_after();
-                }
-                const uint32_t p_col = C::kSepP ? C::kColP + 64 * t : s_col;
-                ptx::tmem_st32(lane_addr + p_col, pk[0]);
-                ptx::tmem_st32(lane_addr + p_col + 32, pk[1]);
-                if (rescale && j > 0) {
-#pragma unroll
-                    for (int c0 = 0; c0 < D / 32; ++c0) {
-                        uint32_t ov[32];
-                        ptx::tmem_ld32(lane_addr + o_col + 32 * c0, ov);
-                        ptx::tmem_ld_wait();
-                        ptx::pin_regs(ov);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) ov[e] = as_u(as_f(ov[e]) * scale);
-                        ptx::tmem_st32(lane_addr + o_col + 32 * c0, ov);
-                    }
-                }
+                own_hi -= kKeys;
                 ptx::tmem_st_wait();
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&bars->p_full[t]);
@@ -643,7 +715,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     L[yr] = m + __log2f(l) * kLn2 - corr;
             }
             st += steps;
-            pairs += n_pair;
             give(seg);
         }
     }
