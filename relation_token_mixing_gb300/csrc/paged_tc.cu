@@ -15,8 +15,8 @@
 //               hands each to the others, and loads P2: the pages of each tile by TMA, one
 //               copy per lane
 //   warp 1      MMA issuer and TMEM owner
-//   warp 2      query rows into shared memory; clears the keys past a request's end
-//   warp 3      loads I~
+//   warp 2      query rows into shared memory
+//   warp 3      loads I~ and clears the keys past a request's end
 //   warps 4-7   softmax of rows 0-127 (one thread per row)
 //   warps 8-11  softmax of rows 128-255
 // Per key tile, per 128-row half: S = Q K^T (both in shared memory) -> registers, 32
@@ -86,9 +86,8 @@ struct TcBars {
     uint64_t piece_full[kSlots], piece_free[kSlots];
     uint64_t q_full[2], q_free[2];
     uint64_t k_full[4], v_full[4], k_empty[4], v_empty[4];
-    // In turn: the cleared tile of a piece may be ready before those of the pieces before
-    // have been waited for, but no more than kQBufs pieces ahead (q_free holds that back).
-    uint64_t v_clean[3];
+    // In turn: up to kStages cleared tiles may be there and not yet waited for.
+    uint64_t v_clean[4];
     // S of a half there and read (d > 64: its right columns; s_left: the left ones there).
     uint64_t s_full[2], s_left[2], s_free[2], p_full[2], o_done[2];
     uint64_t drain;
@@ -98,6 +97,19 @@ struct TcBars {
     alignas(16) Piece pieces[kSlots];
 };
 static_assert(sizeof(TcBars) <= 1024, "the barriers' region");
+
+// Whether the phase of the given parity has completed (no waiting).
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(ptx::smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 
 __device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t as_u(float f) { return __float_as_uint(f); }
@@ -157,10 +169,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&bars->piece_full[x], 1);
             ptx::mbar_init(&bars->piece_free[x], 11);  // the other warps
         }
-        for (int x = 0; x < 3; ++x) ptx::mbar_init(&bars->v_clean[x], 1);
+        for (int x = 0; x < 4; ++x) ptx::mbar_init(&bars->v_clean[x], 1);
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(&bars->q_full[t], 1);
-            ptx::mbar_init(&bars->q_free[t], 1);
+            ptx::mbar_init(&bars->q_free[t], 2);  // both halves
             ptx::mbar_init(&bars->s_full[t], 1);
             ptx::mbar_init(&bars->s_left[t], 1);
             ptx::mbar_init(&bars->s_free[t], 128);
@@ -170,8 +182,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(&bars->k_full[s], 1);
             ptx::mbar_init(&bars->v_full[s], 1);
-            ptx::mbar_init(&bars->k_empty[s], 1);
-            ptx::mbar_init(&bars->v_empty[s], 1);
+            ptx::mbar_init(&bars->k_empty[s], 2);  // both halves
+            ptx::mbar_init(&bars->v_empty[s], 2);
         }
         ptx::mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
@@ -282,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 3) {
         // ------------------------------------------------------------------ I~
         ptx::regs_dec<kRegsControl>();
+        int tails = 0;
         for (int seg = 0; ok; ++seg) {
             const Piece* slot = take(seg);
             if (slot == nullptr) break;
@@ -289,6 +302,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             give(seg);
             if (pc.most < 0) break;
             load(pc, &tm_v, sV, bars->v_full, bars->v_empty);
+            if (ok && pc.tail >= 0) {
+                // The request ends inside the piece's last tile, the one just sent for: weight 0
+                // times whatever its pages hold past the end must be 0.
+                const int s = (x - 1) % C::kStages;
+                if (!ptx::mbar_wait_warp(&bars->v_full[s], ((x - 1) / C::kStages) & 1, abort_flag, v.status,
+                                         kDevTimeoutFull))
+                    break;
+                uint8_t* tile = sV + s * C::kTileBytes;
+                const int len = pc.c + pp.by_group.div(pc.rows);
+                for (int r = len - pc.tail * kKeys + lane / 8; r < kKeys; r += 4)
+#pragma unroll
+                    for (int p = 0; p < C::kPanels; ++p)
+                        *reinterpret_cast<uint4*>(tile + p * kPanelBytes + r * 128 + (lane & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                ptx::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&bars->v_clean[tails % 4]);
+                ++tails;
+            }
         }
         drain(bars->v_full);
     } else if (warp == 1) {
@@ -323,118 +355,128 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   (accumulate || ks > 0) ? 1u : 0u);
             ptx::mma_commit_elect(&bars->o_done[t]);
         };
-        auto wait = [&](uint64_t* bar, int phase, unsigned code) {
-            if (ok) ok = ptx::mbar_wait_warp(bar, phase & 1, abort_flag, v.status, code);
-            return ok;
+        // Each half has its scores and its transport as two walks over the pieces' tiles, and
+        // this warp takes whichever can go on: no half waits for the other's softmax.
+        auto ready = [&](uint64_t* bar, int phase) {
+            return __all_sync(0xffffffffu, mbar_test_wait(bar, phase & 1)) != 0;
         };
-        auto k_wait = [&](int x) { return wait(&bars->k_full[x % C::kStages], x / C::kStages, kDevTimeoutFull); };
-        auto q_wait = [&](int seg) { return wait(&bars->q_full[seg % C::kQBufs], seg / C::kQBufs, kDevTimeoutFull); };
-        // What of a piece the products need.
-        struct Steps {
-            int steps[2], most, tail;
+        struct Walk {
+            int seg = 0, x = 0, step = 0;  // piece, tile and step of the block's
+            int j = 0, steps = 0, most = -1, tail = -1, tails = 0;
+            bool have = false, done = false;
         };
-        auto read = [&](int seg) {
-            Steps x{{0, 0}, -1, -1};
-            const Piece* pc = take(seg);
-            if (pc != nullptr) {
-                x = Steps{{pc->steps[0], pc->steps[1]}, pc->most, pc->tail < 0 ? -1 : pc->tail - pc->j0};
-                give(seg);
-            }
-            return x;
+        Walk ws[2], wl[2], wp[2];  // scores (d > 64: their right columns, then the left ones), transport
+        int given = 0;             // pieces given back
+        auto next_piece = [&](Walk& w) {
+            w.tails += w.tail >= 0;
+            ++w.seg;
+            w.have = false;
+            int least = min(min(ws[0].seg, ws[1].seg), min(wp[0].seg, wp[1].seg));
+            if (!C::kSepP) least = min(least, min(wl[0].seg, wl[1].seg));
+            while (given < least) give(given++);
         };
-        int kt = 0, tails = 0, st[2] = {0, 0};
-        bool begun[2] = {false, false};  // the next piece's first S is already issued
-        Steps sg = read(0);
-        for (int seg = 0; ok && sg.most >= 0; ++seg) {
-            const int qb = seg % C::kQBufs;
-            if (!q_wait(seg) || !k_wait(kt)) break;
-            for (int t = 0; t < 2; ++t) {
-                if (sg.steps[t] == 0 || begun[t]) continue;
-                // S of the piece before has been read (the left columns of d > 64: by its P V,
-                // issued before).
-                if (st[t] > 0 && !wait(&bars->s_free[t], st[t] - 1, kDevTimeoutFull)) break;
+        auto piece = [&](Walk& w, int t) {
+            if (w.have || w.done) return w.have;
+            if (!ready(&bars->piece_full[w.seg % kSlots], w.seg / kSlots)) return false;
+            const Piece& pc = bars->pieces[w.seg % kSlots];
+            w.most = pc.most;
+            w.steps = pc.steps[t];
+            w.tail = pc.tail < 0 ? -1 : pc.tail - pc.j0;
+            w.j = 0;
+            w.done = w.most < 0;
+            w.have = !w.done;
+            return w.have;
+        };
+        // The next scores of half t.  A tile that the half does not see is passed over, but
+        // only once it is there: its stage then belongs to no earlier tile.
+        auto scores = [&](int t) {
+            Walk& w = ws[t];
+            if (!piece(w, t)) return false;
+            const int s = w.x % C::kStages, qb = w.seg % C::kQBufs;
+            if (!ready(&bars->k_full[s], w.x / C::kStages) || !ready(&bars->q_full[qb], w.seg / C::kQBufs)) return false;
+            if (w.j < w.steps) {
+                if (w.step > 0 && !ready(&bars->s_free[t], w.step - 1)) return false;
                 ptx::tc_fence_after();
-                issue_s(t, kt % C::kStages, qb, kRight, &bars->s_full[t]);
-                if (!C::kSepP) issue_s(t, kt % C::kStages, qb, 0, &bars->s_left[t]);
+                issue_s(t, s, qb, kRight, &bars->s_full[t]);
+                ++w.step;
             }
-            begun[0] = begun[1] = false;
-            if (!ok) break;
-            ptx::mma_commit_elect(&bars->k_empty[kt % C::kStages]);
-            if (sg.most == 1) ptx::mma_commit_elect(&bars->q_free[qb]);
-            Steps next{{0, 0}, -2, -1};  // not read yet
-            for (int j = 0; ok && j < sg.most; ++j) {
-                const int s = (kt + j) % C::kStages;
-                bool v_ready = false;
-                auto v_wait = [&]() {
-                    if (v_ready) return true;
-                    v_ready = j == sg.tail ? wait(&bars->v_clean[tails % 3], tails / 3, kDevTimeoutFull)
-                                           : wait(&bars->v_full[s], (kt + j) / C::kStages, kDevTimeoutFull);
-                    return v_ready;
-                };
-                if constexpr (C::kSepP) {
-                    // Each half's next S as soon as the softmax holds this one, past the
-                    // piece's end too.
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j + 1 < sg.steps[t]) {
-                            if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait(kt + j + 1)) break;
-                            ptx::tc_fence_after();
-                            issue_s(t, (kt + j + 1) % C::kStages, qb, 0, &bars->s_full[t]);
-                        } else if (j + 1 == sg.steps[t]) {
-                            if (next.most == -2) next = read(seg + 1);
-                            if (!ok || next.steps[t] == 0) continue;
-                            if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !q_wait(seg + 1) ||
-                                !k_wait(kt + sg.most))
-                                break;
-                            ptx::tc_fence_after();
-                            issue_s(t, (kt + sg.most) % C::kStages, (seg + 1) % C::kQBufs, 0, &bars->s_full[t]);
-                            begun[t] = true;
-                        }
-                    }
-                    if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
-                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j >= sg.steps[t]) continue;
-                        if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
-                        ptx::tc_fence_after();
-                        issue_pv(t, s, j > 0);
-                    }
-                } else {
-                    for (int t = 0; t < 2 && ok; ++t) {  // the next right scores once these are read
-                        if (j + 1 >= sg.steps[t]) continue;
-                        if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait(kt + j + 1)) break;
-                        ptx::tc_fence_after();
-                        issue_s(t, (kt + j + 1) % C::kStages, qb, kRight, &bars->s_full[t]);
-                    }
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j >= sg.steps[t]) continue;
-                        if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
-                        ptx::tc_fence_after();
-                        issue_pv(t, s, j > 0);
-                        if (j + 1 < sg.steps[t]) issue_s(t, (kt + j + 1) % C::kStages, qb, 0, &bars->s_left[t]);
-                    }
-                    if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
-                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
+            if (C::kSepP) ptx::mma_commit_elect(&bars->k_empty[s]);
+            ++w.x;
+            if (++w.j == w.most) {
+                if (C::kSepP) ptx::mma_commit_elect(&bars->q_free[qb]);
+                next_piece(w);
+            }
+            return true;
+        };
+        // d > 64: the left columns, whose place the weights of the step before have until its
+        // P V (issued before: the tensor core keeps the order) has read them.
+        auto left = [&](int t) {
+            Walk& w = wl[t];
+            if (!piece(w, t)) return false;
+            const int s = w.x % C::kStages, qb = w.seg % C::kQBufs;
+            if (w.x >= ws[t].x || (w.j < w.steps && w.step > wp[t].step)) return false;
+            if (w.j < w.steps) {
+                issue_s(t, s, qb, 0, &bars->s_left[t]);
+                ++w.step;
+            }
+            ptx::mma_commit_elect(&bars->k_empty[s]);
+            ++w.x;
+            if (++w.j == w.most) {
+                ptx::mma_commit_elect(&bars->q_free[qb]);
+                next_piece(w);
+            }
+            return true;
+        };
+        auto transport = [&](int t) {
+            Walk& w = wp[t];
+            if (!piece(w, t)) return false;
+            const int s = w.x % C::kStages;
+            if (w.j < w.steps && !ready(&bars->p_full[t], w.step)) return false;
+            if (w.j == w.tail ? !ready(&bars->v_clean[w.tails % 4], w.tails / 4)
+                              : !ready(&bars->v_full[s], w.x / C::kStages))
+                return false;
+            if (w.j < w.steps) {
+                ptx::tc_fence_after();
+                issue_pv(t, s, w.j > 0);
+                ++w.step;
+            }
+            ptx::mma_commit_elect(&bars->v_empty[s]);
+            ++w.x;
+            if (++w.j == w.most) next_piece(w);
+            return true;
+        };
+        uint32_t idle = 0;
+        uint64_t since = 0;
+        while (!(wp[0].done && wp[1].done)) {
+            bool any = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                any |= transport(t);
+                if (!C::kSepP) any |= left(t);
+                any |= scores(t);
+            }
+            if (any) {
+                idle = 0;
+            } else if ((++idle & 255u) == 0) {
+                const uint64_t now = global_ns();
+                if (idle == 256) since = now;
+                if (now - since > RELATION_WAIT_LIMIT_NS) {
+                    record_status(v.status, kDevTimeoutMma);
+                    *abort_flag = 1;
                 }
-                if (ok) ptx::mma_commit_elect(&bars->v_empty[s]);
+                if (__any_sync(0xffffffffu, *abort_flag)) break;
             }
-            if (ok && next.most == -2) next = read(seg + 1);
-            kt += sg.most;
-            tails += sg.tail >= 0;
-            st[0] += sg.steps[0];
-            st[1] += sg.steps[1];
-            sg = next;
         }
         ptx::mma_commit_elect(&bars->drain);
         ptx::mbar_drain(&bars->drain, 0, v.status);
     } else if (warp == 2) {
-        // ------------------------------------------------ queries, keys past the end
+        // ------------------------------------------------------------- queries
         ptx::regs_dec<kRegsControl>();
         constexpr int kChunks = D / 8, kStep = 32 / kChunks;  // 16-byte chunks of a row; rows at a time
         const int chunk = lane % kChunks;
         const uint32_t q_u = ptx::smem_u32(sQ) + (chunk / 8) * kPanelBytes;
         const int cols = max(0, min(8, pp.d - chunk * 8));
         PieceMeta mine{};
-        int kt = 0, tails = 0;
         for (int seg = 0; ok; ++seg) {
             const Piece* slot = take(seg);
             if (slot == nullptr) break;
@@ -468,28 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(&bars->q_full[qb]);
-            if (pc.tail >= 0) {
-                // Weight 0 times whatever a page holds past the end must be 0.
-                const int x = kt + pc.tail - pc.j0, s = x % C::kStages;
-                if (!ptx::mbar_wait_warp(&bars->v_full[s], (x / C::kStages) & 1, abort_flag, v.status, kDevTimeoutFull)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t* tile = sV + s * C::kTileBytes;
-                const int len = pc.c + pp.by_group.div(pc.rows);
-                for (int r = len - pc.tail * kKeys + lane / 8; r < kKeys; r += 4)
-#pragma unroll
-                    for (int p = 0; p < C::kPanels; ++p)
-                        *reinterpret_cast<uint4*>(tile + p * kPanelBytes + r * 128 + (lane & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                ptx::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&bars->v_clean[tails % 3]);
-                ++tails;
-            }
             if (pc.j0 == 0 && pc.j1 < pc.n)
                 mine = PieceMeta{share.owner(pc.place + pc.n - 1) - worker + 1, pc.first, pc.c, pc.rows, pc.g, pc.q};
-            kt += pc.most;
         }
         if (lane == 0) meta[worker] = ok ? mine : PieceMeta{};
     } else {

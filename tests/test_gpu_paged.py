@@ -243,6 +243,26 @@ def test_forward(name):
     case.check(Y, L)
 
 
+LONG = {  # so many heads that a block's pieces are many tiles long, ends inside tiles among them
+    "long_pieces_d64": dict(rows=[(0, 2000), (77, 300)], H=32, G=32, d=64, page=64),
+    "long_pieces_g4_d128": dict(rows=[(3001, 700), (0, 1100)], H=64, G=16, d=128, page=32, layout=BTHD),
+    "long_pieces_d80": dict(rows=[(1, 1999)], H=40, G=40, d=80, page=128),
+    "long_histories_d64": dict(rows=[(4000, 1), (9000, 3), (300, 1), (5000, 2)], H=32, G=16, d=64, page=16),
+    "long_f32_d64": dict(rows=[(500, 700), (0, 333)], H=24, G=24, d=64, page=16, dtype=F32),
+}
+
+
+@pytest.mark.parametrize("name", list(LONG))
+def test_forward_over_long_pieces(name):
+    case = Case(**LONG[name], extra=1)
+    Y, L = case.run()
+    assert rb.relation_check_device_status() == 0
+    assert torch.isfinite(Y[: int(case.starts[-1])].float()).all()
+    rng = np.random.default_rng(1)
+    ends = case.starts[1:].tolist()
+    case.check(Y, L, only=sorted({*rng.integers(0, ends[-1], 12).tolist(), 0, *(e - 1 for e in ends)}))
+
+
 @pytest.mark.parametrize("name", ["mixed", "mixed_d128", "few_rows", "f32_d64", "decode_long", "chunk_d64"])
 def test_forward_is_the_same_from_run_to_run(name):
     case = Case(**FWD[name])
