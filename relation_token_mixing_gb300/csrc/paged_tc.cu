@@ -19,15 +19,14 @@
 //   warp 3      loads I~ and clears the keys past a request's end
 //   warps 4-7   softmax of rows 0-127 (one thread per row)
 //   warps 8-11  softmax of rows 128-255
-// Per key tile, per 128-row half: S = Q K^T (both in shared memory) -> registers, 32
-// columns at a time: SiLU, mask and Self where the tile reaches the rows' own tokens,
-// online softmax -> P as bf16 in TMEM -> O += P V.  The softmax warps should never wait:
-//  - d <= 64: P has TMEM columns of its own, and the next S is issued once the softmax
-//    has read this one;
-//  - d 80 and 128, where S and O fill TMEM: P takes the place of S's left 64 columns, so
-//    the next tile's right 64 scores are issued as soon as this tile's are read, the left
-//    ones after P V; the softmax begins with the right ones and keeps their weights in
-//    registers until it has read the left.
+// Per key tile, per 128-row half: S = Q K^T (both in shared memory) -> registers: SiLU,
+// mask and Self where the tile reaches the rows' own tokens, online softmax -> P as bf16
+// in TMEM -> O += P V.
+//  - d <= 64: P has TMEM columns of its own, and the next S is issued once the softmax has
+//    read this one.  The softmax takes 32 columns at a time in a loop.
+//  - d 80 and 128: S and O fill TMEM, P overwrites S, and the next S waits for P V.  So
+//    the softmax takes the 128 columns at once, to be done with S soon, and the two halves
+//    take turns on the special-function unit: one computes while the other's products run.
 //
 // Bound: two special functions per score (tanh, 16 results a cycle and SM; ex2, 32)
 // give 3/32 cycle a score, against 4 d / 8192 = 1/32 cycle (d = 64) or 1/16 (d =
@@ -46,8 +45,8 @@ namespace {
 
 constexpr int kBM = 128, kRows = 256, kKeys = 128;
 constexpr int kThreads = 384;
-// 128 * 104 + 256 * 200 = 64512 = 384 * 168 registers.
-constexpr uint32_t kRegsControl = 104, kRegsSoftmax = 200;
+// 128 * 72 + 256 * 216 = 64512 = 384 * 168 registers.
+constexpr uint32_t kRegsControl = 72, kRegsSoftmax = 216;
 constexpr int kPanelBytes = 128 * 128;  // 128 rows x 64 bf16
 constexpr int kMinTiles = 4;
 // A unit's beginning and end (queries, first scores, output: 7 to 12 thousand cycles)
@@ -88,8 +87,8 @@ struct TcBars {
     uint64_t k_full[4], v_full[4], k_empty[4], v_empty[4];
     // In turn: up to kStages cleared tiles may be there and not yet waited for.
     uint64_t v_clean[4];
-    // S of a half there and read (d > 64: its right columns; s_left: the left ones there).
-    uint64_t s_full[2], s_left[2], s_free[2], p_full[2], o_done[2];
+    uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
+    uint64_t turn[2][4];
     uint64_t drain;
     uint32_t tmem_base;
     int abort_flag;
@@ -97,19 +96,6 @@ struct TcBars {
     alignas(16) Piece pieces[kSlots];
 };
 static_assert(sizeof(TcBars) <= 1024, "the barriers' region");
-
-// Whether the phase of the given parity has completed (no waiting).
-__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(ptx::smem_u32(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
 
 __device__ __forceinline__ float as_f(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ uint32_t as_u(float f) { return __float_as_uint(f); }
@@ -172,9 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 4; ++x) ptx::mbar_init(&bars->v_clean[x], 1);
         for (int t = 0; t < 2; ++t) {
             ptx::mbar_init(&bars->q_full[t], 1);
-            ptx::mbar_init(&bars->q_free[t], 2);  // both halves
+            ptx::mbar_init(&bars->q_free[t], 1);
             ptx::mbar_init(&bars->s_full[t], 1);
-            ptx::mbar_init(&bars->s_left[t], 1);
+            for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[t][q], 1);
             ptx::mbar_init(&bars->s_free[t], 128);
             ptx::mbar_init(&bars->p_full[t], 128);
             ptx::mbar_init(&bars->o_done[t], 1);
@@ -182,8 +168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < C::kStages; ++s) {
             ptx::mbar_init(&bars->k_full[s], 1);
             ptx::mbar_init(&bars->v_full[s], 1);
-            ptx::mbar_init(&bars->k_empty[s], 2);  // both halves
-            ptx::mbar_init(&bars->v_empty[s], 2);
+            ptx::mbar_init(&bars->k_empty[s], 1);
+            ptx::mbar_init(&bars->v_empty[s], 1);
         }
         ptx::mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
@@ -326,26 +312,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
         ptx::regs_dec<kRegsControl>();
-        constexpr int kN = C::kSepP ? kKeys : kKeys / 2;  // keys of one S issue
-        const uint32_t id_s = ptx::idesc_bf16(kBM, kN, false, false);
+        const uint32_t id_s = ptx::idesc_bf16(kBM, kKeys, false, false);
         const uint32_t id_o = ptx::idesc_bf16(kBM, D, false, true);
         const uint64_t dq0 = ptx::smem_desc(ptx::smem_u32(sQ), 16, 1024, ptx::kSwizzle128B);
         const uint64_t dk0 = ptx::smem_desc(ptx::smem_u32(sK), 16, 1024, ptx::kSwizzle128B);
         const uint64_t dv0 = ptx::smem_desc(ptx::smem_u32(sV), kPanelBytes, 1024, ptx::kSwizzle128B);
         // Only a descriptor's low word (the address) changes: an add of a constant a step.
         constexpr uint32_t kTileStep = C::kTileBytes >> 4, kPanelStep = kPanelBytes >> 4;
-        // Keys n0 .. n0 + kN - 1 of the tile in stage s against half t of the queries.
-        auto issue_s = [&](int t, int s, int qb, int n0, uint64_t* full) {
+        auto issue_s = [&](int t, int s, int qb) {
             const uint32_t q_lo = ptx::desc_lo(dq0) + (2 * qb + t) * kTileStep, q_hi = ptx::desc_hi(dq0);
-            const uint32_t k_lo = ptx::desc_lo(dk0) + s * kTileStep + n0 * 8, k_hi = ptx::desc_hi(dk0);
+            const uint32_t k_lo = ptx::desc_lo(dk0) + s * kTileStep, k_hi = ptx::desc_hi(dk0);
 #pragma unroll
             for (int ks = 0; ks < D / 16; ++ks) {
                 const uint32_t off = (ks / 4) * kPanelStep + (ks % 4) * 2;  // 32 bytes per K-step
-                ptx::mma_ss_elect(tmem + t * 128 + n0, q_lo + off, q_hi, k_lo + off, k_hi, id_s, ks > 0 ? 1u : 0u);
+                ptx::mma_ss_elect(tmem + t * 128, q_lo + off, q_hi, k_lo + off, k_hi, id_s, ks > 0 ? 1u : 0u);
             }
-            ptx::mma_commit_elect(full);
+            ptx::mma_commit_elect(&bars->s_full[t]);
         };
-        constexpr int kRight = C::kSepP ? 0 : kN;  // the columns that can be issued early
         auto issue_pv = [&](int t, int s, bool accumulate) {
             const uint32_t p_col = tmem + (C::kSepP ? C::kColP + 64 * t : 128 * t);
             const uint32_t v_lo = ptx::desc_lo(dv0) + s * kTileStep, v_hi = ptx::desc_hi(dv0);
@@ -355,117 +338,102 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   (accumulate || ks > 0) ? 1u : 0u);
             ptx::mma_commit_elect(&bars->o_done[t]);
         };
-        // Each half has its scores and its transport as two walks over the pieces' tiles, and
-        // this warp takes whichever can go on: no half waits for the other's softmax.
-        auto ready = [&](uint64_t* bar, int phase) {
-            return __all_sync(0xffffffffu, mbar_test_wait(bar, phase & 1)) != 0;
+        auto wait = [&](uint64_t* bar, int phase, unsigned code) {
+            if (ok) ok = ptx::mbar_wait_warp(bar, phase & 1, abort_flag, v.status, code);
+            return ok;
         };
-        struct Walk {
-            int seg = 0, x = 0, step = 0;  // piece, tile and step of the block's
-            int j = 0, steps = 0, most = -1, tail = -1, tails = 0;
-            bool have = false, done = false;
+        auto k_wait = [&](int x) { return wait(&bars->k_full[x % C::kStages], x / C::kStages, kDevTimeoutFull); };
+        auto q_wait = [&](int seg) { return wait(&bars->q_full[seg % C::kQBufs], seg / C::kQBufs, kDevTimeoutFull); };
+        // What of a piece the products need.
+        struct Steps {
+            int steps[2], most, tail;
         };
-        Walk ws[2], wl[2], wp[2];  // scores (d > 64: their right columns, then the left ones), transport
-        int given = 0;             // pieces given back
-        auto next_piece = [&](Walk& w) {
-            w.tails += w.tail >= 0;
-            ++w.seg;
-            w.have = false;
-            int least = min(min(ws[0].seg, ws[1].seg), min(wp[0].seg, wp[1].seg));
-            if (!C::kSepP) least = min(least, min(wl[0].seg, wl[1].seg));
-            while (given < least) give(given++);
-        };
-        auto piece = [&](Walk& w, int t) {
-            if (w.have || w.done) return w.have;
-            if (!ready(&bars->piece_full[w.seg % kSlots], w.seg / kSlots)) return false;
-            const Piece& pc = bars->pieces[w.seg % kSlots];
-            w.most = pc.most;
-            w.steps = pc.steps[t];
-            w.tail = pc.tail < 0 ? -1 : pc.tail - pc.j0;
-            w.j = 0;
-            w.done = w.most < 0;
-            w.have = !w.done;
-            return w.have;
-        };
-        // The next scores of half t.  A tile that the half does not see is passed over, but
-        // only once it is there: its stage then belongs to no earlier tile.
-        auto scores = [&](int t) {
-            Walk& w = ws[t];
-            if (!piece(w, t)) return false;
-            const int s = w.x % C::kStages, qb = w.seg % C::kQBufs;
-            if (!ready(&bars->k_full[s], w.x / C::kStages) || !ready(&bars->q_full[qb], w.seg / C::kQBufs)) return false;
-            if (w.j < w.steps) {
-                if (w.step > 0 && !ready(&bars->s_free[t], w.step - 1)) return false;
-                ptx::tc_fence_after();
-                issue_s(t, s, qb, kRight, &bars->s_full[t]);
-                ++w.step;
+        auto read = [&](int seg) {
+            Steps x{{0, 0}, -1, -1};
+            const Piece* pc = take(seg);
+            if (pc != nullptr) {
+                x = Steps{{pc->steps[0], pc->steps[1]}, pc->most, pc->tail < 0 ? -1 : pc->tail - pc->j0};
+                give(seg);
             }
-            if (C::kSepP) ptx::mma_commit_elect(&bars->k_empty[s]);
-            ++w.x;
-            if (++w.j == w.most) {
-                if (C::kSepP) ptx::mma_commit_elect(&bars->q_free[qb]);
-                next_piece(w);
-            }
-            return true;
+            return x;
         };
-        // d > 64: the left columns, whose place the weights of the step before have until its
-        // P V (issued before: the tensor core keeps the order) has read them.
-        auto left = [&](int t) {
-            Walk& w = wl[t];
-            if (!piece(w, t)) return false;
-            const int s = w.x % C::kStages, qb = w.seg % C::kQBufs;
-            if (w.x >= ws[t].x || (w.j < w.steps && w.step > wp[t].step)) return false;
-            if (w.j < w.steps) {
-                issue_s(t, s, qb, 0, &bars->s_left[t]);
-                ++w.step;
-            }
-            ptx::mma_commit_elect(&bars->k_empty[s]);
-            ++w.x;
-            if (++w.j == w.most) {
-                ptx::mma_commit_elect(&bars->q_free[qb]);
-                next_piece(w);
-            }
-            return true;
-        };
-        auto transport = [&](int t) {
-            Walk& w = wp[t];
-            if (!piece(w, t)) return false;
-            const int s = w.x % C::kStages;
-            if (w.j < w.steps && !ready(&bars->p_full[t], w.step)) return false;
-            if (w.j == w.tail ? !ready(&bars->v_clean[w.tails % 4], w.tails / 4)
-                              : !ready(&bars->v_full[s], w.x / C::kStages))
-                return false;
-            if (w.j < w.steps) {
-                ptx::tc_fence_after();
-                issue_pv(t, s, w.j > 0);
-                ++w.step;
-            }
-            ptx::mma_commit_elect(&bars->v_empty[s]);
-            ++w.x;
-            if (++w.j == w.most) next_piece(w);
-            return true;
-        };
-        uint32_t idle = 0;
-        uint64_t since = 0;
-        while (!(wp[0].done && wp[1].done)) {
-            bool any = false;
-#pragma unroll
+        int kt = 0, tails = 0, st[2] = {0, 0};
+        bool begun[2] = {false, false};  // the next piece's first S is already issued
+        Steps sg = read(0);
+        for (int seg = 0; ok && sg.most >= 0; ++seg) {
+            const int qb = seg % C::kQBufs;
+            if (!q_wait(seg) || !k_wait(kt)) break;
             for (int t = 0; t < 2; ++t) {
-                any |= transport(t);
-                if (!C::kSepP) any |= left(t);
-                any |= scores(t);
+                if (sg.steps[t] == 0 || begun[t]) continue;
+                // S of the piece before has been read (d > 64: its P V, issued before, read it).
+                if (C::kSepP && st[t] > 0 && !wait(&bars->s_free[t], st[t] - 1, kDevTimeoutFull)) break;
+                ptx::tc_fence_after();
+                issue_s(t, kt % C::kStages, qb);
             }
-            if (any) {
-                idle = 0;
-            } else if ((++idle & 255u) == 0) {
-                const uint64_t now = global_ns();
-                if (idle == 256) since = now;
-                if (now - since > RELATION_WAIT_LIMIT_NS) {
-                    record_status(v.status, kDevTimeoutMma);
-                    *abort_flag = 1;
+            begun[0] = begun[1] = false;
+            if (!ok) break;
+            ptx::mma_commit_elect(&bars->k_empty[kt % C::kStages]);
+            if (sg.most == 1) ptx::mma_commit_elect(&bars->q_free[qb]);
+            Steps next{{0, 0}, -2, -1};  // not read yet
+            for (int j = 0; ok && j < sg.most; ++j) {
+                const int s = (kt + j) % C::kStages;
+                bool v_ready = false;
+                auto v_wait = [&]() {
+                    if (v_ready) return true;
+                    v_ready = j == sg.tail ? wait(&bars->v_clean[tails % 4], tails / 4, kDevTimeoutFull)
+                                           : wait(&bars->v_full[s], (kt + j) / C::kStages, kDevTimeoutFull);
+                    return v_ready;
+                };
+                if constexpr (C::kSepP) {
+                    // Each half's next S as soon as the softmax holds this one, past the
+                    // piece's end too.
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j + 1 < sg.steps[t]) {
+                            if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait(kt + j + 1)) break;
+                            ptx::tc_fence_after();
+                            issue_s(t, (kt + j + 1) % C::kStages, qb);
+                        } else if (j + 1 == sg.steps[t]) {
+                            if (next.most == -2) next = read(seg + 1);
+                            if (!ok || next.steps[t] == 0) continue;
+                            if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !q_wait(seg + 1) ||
+                                !k_wait(kt + sg.most))
+                                break;
+                            ptx::tc_fence_after();
+                            issue_s(t, (kt + sg.most) % C::kStages, (seg + 1) % C::kQBufs);
+                            begun[t] = true;
+                        }
+                    }
+                    if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
+                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j >= sg.steps[t]) continue;
+                        if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
+                        ptx::tc_fence_after();
+                        issue_pv(t, s, j > 0);
+                    }
+                } else {
+                    for (int t = 0; t < 2 && ok; ++t) {
+                        if (j >= sg.steps[t]) continue;
+                        if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
+                        ptx::tc_fence_after();
+                        issue_pv(t, s, j > 0);
+                        if (j + 1 < sg.steps[t]) {
+                            if (!k_wait(kt + j + 1)) break;
+                            ptx::tc_fence_after();
+                            issue_s(t, (kt + j + 1) % C::kStages, qb);
+                        }
+                    }
+                    if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
+                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                 }
-                if (__any_sync(0xffffffffu, *abort_flag)) break;
+                if (ok) ptx::mma_commit_elect(&bars->v_empty[s]);
             }
+            if (ok && next.most == -2) next = read(seg + 1);
+            kt += sg.most;
+            tails += sg.tail >= 0;
+            st[0] += sg.steps[0];
+            st[1] += sg.steps[1];
+            sg = next;
         }
         ptx::mma_commit_elect(&bars->drain);
         ptx::mbar_drain(&bars->drain, 0, v.status);
@@ -522,11 +490,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t s_col = t * 128, o_col = 256 + t * D;
         const float c_half = 0.5f * pp.inv_sqrt_d;                // U/2 per raw dot product
         const float c_diag = 0.5f * pp.inv_sqrt_d / pp.tau_S;     // U/(2 tau_S)
-        int st = 0;  // steps of this half so far
+        uint64_t* turn_mine = &bars->turn[t][quarter];
+        uint64_t* turn_next = &bars->turn[t ^ 1][quarter];
+        int st = 0, pairs = 0;  // steps of this half, and steps both halves took in turn
         for (int seg = 0; ok; ++seg) {
             const Piece* pc = take(seg);  // the slot stays this warp's until the piece is done
             if (pc == nullptr || pc->most < 0) break;
-            const int steps = pc->steps[t];
+            const int steps = pc->steps[t], n_pair = C::kSepP ? 0 : min(pc->steps[0], pc->steps[1]);
             // The row's own token (the last key it sees) as a column of the piece's first
             // tile, the warp's least and greatest.
             int own = pc->c + pp.by_group.div(min(pc->q * kRows + t * kBM + r, pc->rows - 1));
@@ -544,12 +514,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after();
             };
             const uint32_t p_addr = lane_addr + (C::kSepP ? C::kColP + 64 * t : s_col);
-            uint32_t hold[2][16] = {};  // d > 64: the right columns' weights
             auto scale_pairs = [](uint32_t& w, float f) {
                 const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
                 w = ptx::pack_bf16x2(x.x * f, x.y * f);
             };
-            // The maximum rises to m_new in block b of tile j (seldom after the first): what has
+            // d <= 64: the maximum rises to m_new in block b of tile j (seldom after the first): what has
             // been summed under the old one is scaled, in O, in l and in this tile's P so far.
             // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
             auto raise = [&](float m_new, int j, int b) {
@@ -569,16 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tmem_st32(lane_addr + o_col + 32 * c0, ov);
                     }
                 }
-                if (!C::kSepP && b != 2) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        scale_pairs(hold[0][e], f);
-                        scale_pairs(hold[1][e], f);  // b = 3: not there yet
-                    }
-                }
                 ptx::tmem_st_wait();
 #pragma unroll 1
-                for (int x = 0; x < (C::kSepP || b == 1 ? b : 0); ++x) {
+                for (int x = 0; x < b; ++x) {
                     uint32_t pv[16];
                     ptx::tmem_ld16(p_addr + 16 * x, pv);
                     ptx::tmem_ld_wait();
@@ -588,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_st16(p_addr + 16 * x, pv);
                 }
             };
-            // 32 scores -> the weights of columns 32 b and on, and what they add to the row's
+            // d <= 64: 32 scores -> the weights of columns 32 b and on, and what they add to the row's
             // sum and maximum.
             auto block = [&](uint32_t (&sv)[32], uint32_t (&pk)[16], int j, int b) {
                 const int c0 = 32 * b;
@@ -648,47 +610,116 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 ptx::tc_fence_after();
-                // A loop, not 128 columns in a row: its code stays in the instruction caches
-                // (whole prompts, heads of 64: 0.36 ms, unrolled 0.41).  The blocks' order: 0 1 2
-                // 3, or the right ones first.
+                if constexpr (C::kSepP) {
+                    // A loop, not 128 columns in a row: its code stays in the instruction caches
+                    // (whole prompts, heads of 64: 0.36 ms, unrolled 0.41).
 #pragma unroll 1
-                for (int i = 0; i < 4; ++i) {
-                    const int b = C::kSepP ? i : i ^ 2;
-                    uint32_t sv[32], pk[16];
-                    if (!C::kSepP && i == 2) {
-                        if (!ptx::mbar_wait_warp(&bars->s_left[t], (st + j) & 1, abort_flag, v.status,
-                                                 kDevTimeoutMma)) {
-                            ok = false;
-                            break;
+                    for (int b = 0; b < 4; ++b) {
+                        uint32_t sv[32], pk[16];
+                        ptx::tmem_ld32(lane_addr + s_col + 32 * b, sv);
+                        ptx::tmem_ld_wait();
+                        ptx::pin_regs(sv);
+                        if (b == 3) {  // the next S may overwrite it
+                            ptx::tc_fence_before();
+                            ptx::mbar_arrive(&bars->s_free[t]);
                         }
-                        ptx::tc_fence_after();
-                    }
-                    ptx::tmem_ld32(lane_addr + s_col + 32 * b, sv);
-                    ptx::tmem_ld_wait();
-                    ptx::pin_regs(sv);
-                    if (b == 3) {  // the next S may overwrite what has been read
-                        ptx::tc_fence_before();
-                        ptx::mbar_arrive(&bars->s_free[t]);
-                    }
-                    block(sv, pk, j, b);
-                    if (C::kSepP) {
+                        block(sv, pk, j, b);
                         if (b == 0) o_wait(j);  // P V of the tile before has read its P
                         ptx::tmem_st16(p_addr + 16 * b, pk);
-                    } else if (b >= 2) {
+                    }
+                    if (!ok) break;
+                } else {
+                    uint32_t sv[128];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            if (b == 2) hold[0][e] = pk[e];
-                            if (b == 3) hold[1][e] = pk[e];
+                    for (int c = 0; c < 4; ++c)
+                        ptx::tmem_ld32(lane_addr + s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
+                    ptx::tmem_ld_wait();
+                    ptx::pin_regs(sv);
+                    const int x = pairs + j;
+                    if (j < n_pair && x + t > 0 &&
+                        !ptx::mbar_wait_warp(turn_mine, (x + t - 1) & 1, abort_flag, v.status, kDevTimeoutMma)) {
+                        ok = false;
+                        break;
+                    }
+                    ptx::pin_regs(sv);  // the loops below start after the turn is taken
+                    const float2 ch2 = make_float2(c_half, c_half);
+                    // The two long loops run over every column, also those that the mask drops: with
+                    // branches around blocks of them the kernel was slower (two chunks of 1024 over
+                    // 16k and 32k, heads of 128: 0.91 ms for 0.85).
+                    const bool edge = own_lo < kKeys;  // some row's own token is in this tile or before it
+                    float self = 0.f;
+                    if (edge) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) self = c == own ? as_f(sv[c]) : self;
+                        self = fmaf(0.5f, ptx::tanh_approx(self * c_diag), 0.5f) + corr;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) {
+                        const float2 h = ptx::mul2(make_float2(as_f(sv[2 * e]), as_f(sv[2 * e + 1])), ch2);
+                        const float2 th = make_float2(ptx::tanh_approx(h.x), ptx::tanh_approx(h.y));
+                        const float2 E = ptx::fma2(h, th, h);  // SiLU(U) = (U/2)(1 + tanh(U/2))
+                        sv[2 * e] = as_u(E.x);
+                        sv[2 * e + 1] = as_u(E.y);
+                    }
+                    if (edge) {
+#pragma unroll
+                        for (int c = 0; c < 128; ++c) {
+                            const float x = c > own ? -INFINITY : as_f(sv[c]);
+                            sv[c] = as_u(c == own ? self : x);
                         }
-                    } else {  // in the place of columns already read
-                        ptx::tmem_st16(p_addr + 16 * b, pk);
-                        if (b == 1) {
-                            ptx::tmem_st16(p_addr + 32, hold[0]);
-                            ptx::tmem_st16(p_addr + 48, hold[1]);
+                    }
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < 128; c += 8) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) mx[q] = ptx::max3(mx[q], as_f(sv[c + 2 * q]), as_f(sv[c + 2 * q + 1]));
+                    }
+                    const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    const bool rescale = __any_sync(0xffffffffu, m_new > m + kRaise * kLn2);
+                    float scale = 1.f;
+                    if (rescale) {
+                        // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
+                        scale = m_new == -INFINITY ? 1.f : ptx::ex2_approx((m - m_new) * kLog2e);
+                        l *= scale;
+                        m = m_new;
+                    }
+                    const float m_ref = m == -INFINITY ? 0.f : m;
+                    const float2 l2e2 = make_float2(kLog2e, kLog2e), nm2 = make_float2(-m_ref * kLog2e, -m_ref * kLog2e);
+                    float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                    make_float2(0.f, 0.f)};
+                    uint32_t pk[2][32];
+#pragma unroll
+                    for (int c = 0; c < 64; ++c) {
+                        const float2 y = ptx::fma2(make_float2(as_f(sv[2 * c]), as_f(sv[2 * c + 1])), l2e2, nm2);
+                        const float2 p = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+                        ls[c & 3] = ptx::add2(ls[c & 3], p);
+                        pk[c >> 5][c & 31] = ptx::pack_bf16x2(p.x, p.y);
+                    }
+                    {
+                        const float2 sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
+                        l += sum.x + sum.y;
+                    }
+                    ptx::pin_regs(pk[0]);  // and end before it is passed on
+                    ptx::pin_regs(pk[1]);
+                    __syncwarp();
+                    if (j < n_pair && lane == 0) ptx::mbar_arrive(turn_next);
+                    ptx::tmem_st32(p_addr, pk[0]);
+                    ptx::tmem_st32(p_addr + 32, pk[1]);
+                    if (rescale && j > 0) {
+                        o_wait(j);  // O is final
+                        if (!ok) break;
+#pragma unroll
+                        for (int c0 = 0; c0 < D / 32; ++c0) {
+                            uint32_t ov[32];
+                            ptx::tmem_ld32(lane_addr + o_col + 32 * c0, ov);
+                            ptx::tmem_ld_wait();
+                            ptx::pin_regs(ov);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) ov[e] = as_u(as_f(ov[e]) * scale);
+                            ptx::tmem_st32(lane_addr + o_col + 32 * c0, ov);
                         }
                     }
                 }
-                if (!ok) break;
                 own -= kKeys;
                 own_lo -= kKeys;
                 own_hi -= kKeys;
@@ -737,6 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     L[yr] = m + __log2f(l) * kLn2 - corr;
             }
             st += steps;
+            pairs += n_pair;
             give(seg);
         }
     }
