@@ -89,6 +89,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Loads the in-tree library (building it first when missing or stale)."""
     global _lib
+    if _lib is not None:  # set once, when every entry point has its types
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -207,8 +209,8 @@ def _host_ptr(t) -> int | None:
 
 
 def _stream_ptr(stream) -> int | None:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the handle alone: a Stream object costs 2.5 us more on the host
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
     return stream.cuda_stream or None
 
 
@@ -566,6 +568,7 @@ def bwd(P1, P2, V, Y, L, dY, tau_S: float, lam: float, causal: bool = True, stre
 
 # ------------------------------------------------------- paged Relation Cache
 _DTYPE_CODES = {torch.bfloat16: RELATION_BF16, torch.float32: RELATION_F32}
+_I32, _I64 = torch.int32, torch.int64
 
 
 def paged_row(d_h: int, dtype) -> int:
@@ -578,11 +581,6 @@ def paged_pages(pages: int, G: int, page_size: int, d_h: int, dtype, layout: int
     """A pair of page pools (P2_pages, I_pages), zeroed."""
     shape = (pages, G, page_size) if layout == RELATION_LAYOUT_BHTD else (pages, page_size, G)
     return tuple(torch.zeros(*shape, paged_row(d_h, dtype), dtype=dtype, device=device) for _ in range(2))
-
-
-def _want(t, dtype, name):
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
 def paged_for(heads, pages, R: int, table_width: int, tau_S: float, lam: float, layout: int) -> Paged:
@@ -605,16 +603,14 @@ def paged_plan(cached, fresh, free_pages, block_table, pages: int, page_size: in
                stream=None) -> None:
     """Block tables and slot maps of a step: fills block_table (new entries), starts [R + 1], slots [N],
     positions [N] and used [1] from the requests' lengths (all int32, slots int64)."""
-    for t, name in ((cached, "cached"), (fresh, "fresh"), (block_table, "block_table"), (starts, "starts"),
-                    (positions, "positions"), (used, "used")):
-        _want(t, torch.int32, name)
-    _want(slots, torch.int64, "slots")
+    if not (cached.dtype is fresh.dtype is block_table.dtype is starts.dtype is positions.dtype is used.dtype is _I32):
+        raise ValueError("cached, fresh, block_table, starts, positions and used are torch.int32")
+    if slots.dtype is not _I64 or (free_pages is not None and free_pages.dtype is not _I32):
+        raise ValueError("slots are torch.int64, free_pages torch.int32")
     R, width = block_table.shape
-    N = slots.shape[0]
-    if cached.shape[0] != R or fresh.shape[0] != R or starts.shape[0] != R + 1 or positions.shape[0] != N:
+    N = slots.numel()
+    if cached.numel() != R or fresh.numel() != R or starts.numel() != R + 1 or positions.numel() != N:
         raise ValueError("cached and fresh are [R], starts [R + 1], positions and slots [N]")
-    if free_pages is not None:
-        _want(free_pages, torch.int32, "free_pages")
     # The plan reads sizes only: heads, width and dtype are stand-ins.
     relation_paged_plan(Paged(R, N, 1, 1, 64, pages, page_size, width, RELATION_BF16, 1.0, 0.0, RELATION_LAYOUT_BHTD),
                         cached, fresh, free_pages, block_table, starts, slots, positions, used, stream)
@@ -624,15 +620,15 @@ def paged_store(X1, X2, I, theta, pairing: int, rope_base: float, positions, slo
                 layout: int = RELATION_LAYOUT_BHTD, stream=None) -> None:
     """RoPE and Givens mixing of packed new tokens, P1 [N, H, d_h] written in place of a copy and the cached rows
     into their pages; theta None stores the states unmixed."""
-    _want(positions, torch.int32, "positions")
-    _want(slots, torch.int64, "slots")
+    if positions.dtype is not _I32 or slots.dtype is not _I64:
+        raise ValueError("positions are torch.int32, slots torch.int64")
     prob = paged_for(X1, P2_pages, 1, 1, 1.0, 0.0, layout)
-    N, G = prob.N, prob.G
-    if X2.shape != I.shape or X2.shape[:2] != (N, G) or X2.shape[2] != prob.d_h or P1.shape != X1.shape or \
-            I_pages.shape != P2_pages.shape or positions.shape[0] != N or slots.shape[0] != N:
+    N = prob.N
+    if X2.shape != (N, prob.G, prob.d_h) or I.shape != X2.shape or P1.shape != X1.shape or \
+            I_pages.shape != P2_pages.shape or positions.numel() != N or slots.numel() != N:
         raise ValueError("X1, P1 are [N, H, d_h], X2, I [N, G, d_h], positions, slots [N], both page pools alike")
-    for t in (X2, I, P1, I_pages):
-        _want(t, X1.dtype, "X2, I, P1 and the pages")
+    if not (X2.dtype is I.dtype is P1.dtype is I_pages.dtype is X1.dtype):
+        raise ValueError(f"X2, I, P1 and the pages must be {X1.dtype}, as X1")
     relation_paged_store(prob, X1, X2, I, theta, pairing, rope_base, positions, slots, P1, P2_pages, I_pages, stream)
 
 
@@ -650,9 +646,9 @@ def paged_fwd(P1, P2_pages, I_pages, block_table, starts, cached, max_fresh: int
     when not given; L [N, H] float32 is filled when given."""
     R, width = block_table.shape
     prob = paged_for(P1, P2_pages, R, width, tau_S, lam, layout)
-    for t, name in ((block_table, "block_table"), (starts, "starts"), (cached, "cached")):
-        _want(t, torch.int32, name)
-    if starts.shape[0] != R + 1 or cached.shape[0] != R or I_pages.shape != P2_pages.shape or \
+    if not (block_table.dtype is starts.dtype is cached.dtype is _I32):
+        raise ValueError("block_table, starts and cached are torch.int32")
+    if starts.numel() != R + 1 or cached.numel() != R or I_pages.shape != P2_pages.shape or \
             I_pages.dtype is not P1.dtype:
         raise ValueError("starts is [R + 1], cached [R], both page pools alike")
     if Y is None:
@@ -660,9 +656,8 @@ def paged_fwd(P1, P2_pages, I_pages, block_table, starts, cached, max_fresh: int
     elif Y.shape != P1.shape or Y.dtype is not P1.dtype:
         raise ValueError("Y is like P1")
     if L is not None:
-        _want(L, torch.float32, "L")
-        if L.shape != P1.shape[:2]:
-            raise ValueError("L is [N, H]")
+        if L.dtype is not torch.float32 or L.shape != (prob.N, prob.H):
+            raise ValueError("L is [N, H] of torch.float32")
     if workspace is None:
         workspace = paged_workspace(prob, max_fresh, P1.device)
     relation_paged_fwd(prob, P1, P2_pages, I_pages, block_table, starts, cached, max_fresh, Y, L, workspace, stream)
