@@ -385,32 +385,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                     return v_ready;
                 };
                 if constexpr (C::kSepP) {
-                    // Each half's next S as soon as the softmax holds this one, past the
-                    // piece's end too.
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j + 1 < sg.steps[t]) {
-                            if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !k_wait(kt + j + 1)) break;
-                            ptx::tc_fence_after();
-                            issue_s(t, (kt + j + 1) % C::kStages, qb);
-                        } else if (j + 1 == sg.steps[t]) {
-                            if (next.most == -2) next = read(seg + 1);
-                            if (!ok || next.steps[t] == 0) continue;
-                            if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull) || !q_wait(seg + 1) ||
-                                !k_wait(kt + sg.most))
-                                break;
-                            ptx::tc_fence_after();
-                            issue_s(t, (kt + sg.most) % C::kStages, (seg + 1) % C::kQBufs);
-                            begun[t] = true;
-                        }
-                    }
-                    if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
-                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
+                    // Each half's next S once the softmax holds this one, past the piece's end too,
+                    // and its P V: one half after the other, so that they settle half a step apart
+                    // and neither waits for the other's.
                     for (int t = 0; t < 2 && ok; ++t) {
                         if (j >= sg.steps[t]) continue;
+                        if (!wait(&bars->s_free[t], st[t] + j, kDevTimeoutFull)) break;
+                        if (j + 1 < sg.steps[t]) {
+                            if (!k_wait(kt + j + 1)) break;
+                            ptx::tc_fence_after();
+                            issue_s(t, (kt + j + 1) % C::kStages, qb);
+                        } else {
+                            if (next.most == -2) next = read(seg + 1);
+                            if (!ok) break;
+                            if (next.steps[t] > 0) {
+                                if (!q_wait(seg + 1) || !k_wait(kt + sg.most)) break;
+                                ptx::tc_fence_after();
+                                issue_s(t, (kt + sg.most) % C::kStages, (seg + 1) % C::kQBufs);
+                                begun[t] = true;
+                            }
+                        }
                         if (!wait(&bars->p_full[t], st[t] + j, kDevTimeoutFull) || !v_wait()) break;
                         ptx::tc_fence_after();
                         issue_pv(t, s, j > 0);
                     }
+                    if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
+                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                 } else {
                     for (int t = 0; t < 2 && ok; ++t) {
                         if (j >= sg.steps[t]) continue;
