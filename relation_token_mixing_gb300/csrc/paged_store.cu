@@ -23,16 +23,18 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;  // of one block
 
-// HALF: d/2.  VC: columns of one access; HALF is a multiple of it.
-template <typename T, int HALF, int VC>
+// HALF: d/2.  VC: columns of one access; HALF is a multiple of it.  BATCH: pairs of vectors that a
+// thread has in flight.
+template <typename T, int HALF, int VC, int BATCH>
 __global__ void __launch_bounds__(kThreads)
     paged_store_kernel(PagedProblem pp, const T* __restrict__ X1, const T* __restrict__ X2, const T* __restrict__ I,
                        const float* __restrict__ theta, int pairing, const __grid_constant__ RopeTable tab,
                        const int* __restrict__ positions, const int64_t* __restrict__ slots, T* __restrict__ P1,
-                       T* __restrict__ P2_pages, T* __restrict__ I_pages, unsigned int* status, int tokens) {
+                       T* __restrict__ P2_pages, T* __restrict__ I_pages, unsigned int* status, int tokens, FastDiv by_heads) {
     constexpr int D = 2 * HALF, PER = HALF / VC;
     extern __shared__ float2 sh[];  // (cos, sin) [tokens][HALF], then [G/2] of the head pairs
     __shared__ int64_t s_slot[kMaxTokens];
+    __shared__ float2 same;  // no mixing
     float2* turn = sh;
     float2* mix = sh + kMaxTokens * HALF;
     const int n0 = blockIdx.x * tokens, count = min(tokens, pp.N - n0);
@@ -50,6 +52,7 @@ __global__ void __launch_bounds__(kThreads)
         if (tab.enabled) rope_sincos((float)positions[n0 + t], tab.hi[c], tab.lo[c], &sn, &cs);
         turn[k] = make_float2(cs, sn);
     }
+    if (threadIdx.x == 0) same = make_float2(1.f, 0.f);
     if (theta != nullptr)
         for (int k = threadIdx.x; k < pp.G / 2; k += kThreads) {
             float sn, cs;
@@ -59,63 +62,75 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     // Items of one token: H heads of X1, G of X2, G of I (pairs of heads, each half
     // the columns: the same number of items), PER vector pairs each.
-    const int heads = pp.H + 2 * pp.G;
-    for (int k = threadIdx.x; k < count * heads * PER; k += kThreads) {
-        const int v = k % PER, u = k / PER;
-        const int t = u / heads, hd = u - t * heads, c = v * VC;
-        const int64_t n = n0 + t, slot = s_slot[t];
-        const int64_t page = slot >> pp.page_shift;
-        const int off = (int)(slot & pp.page_mask);
-        const T *a_src, *b_src;
-        T *a_dst, *b_dst;
-        const float2* cs = turn + t * HALF + c;
-        float2 one = make_float2(1.f, 0.f);
-        bool each = true;  // an angle per column (RoPE) or one for all (Givens)
-        if (hd < pp.H) {
-            a_src = X1 + ((size_t)n * pp.H + hd) * D + c;
-            a_dst = P1 + ((size_t)n * pp.H + hd) * D + c;
-            b_src = a_src + HALF;
-            b_dst = a_dst + HALF;
-        } else if (slot < 0) {
-            continue;
-        } else if (hd < pp.H + pp.G) {
-            const int g = hd - pp.H;
-            a_src = X2 + ((size_t)n * pp.G + g) * D + c;
-            a_dst = P2_pages + page_row_offset(pp, page, off, g) + c;
-            b_src = a_src + HALF;
-            b_dst = a_dst + HALF;
-        } else {
-            const int g = hd - pp.H - pp.G;
-            each = false;
-            int ga = g, gb = g, ca = c, cb = c + HALF;
-            if (theta != nullptr) {  // item g: pair g/2, the first or second half of its columns
-                const int pair = g >> 1;
-                one = mix[pair];
-                ga = 2 * pair + pairing;
-                gb = ga + 1 == pp.G ? 0 : ga + 1;
-                ca = cb = c + (g & 1) * HALF;
-            }
-            a_src = I + ((size_t)n * pp.G + ga) * D + ca;
-            b_src = I + ((size_t)n * pp.G + gb) * D + cb;
-            a_dst = I_pages + page_row_offset(pp, page, off, ga) + ca;
-            b_dst = I_pages + page_row_offset(pp, page, off, gb) + cb;
-        }
-        Vec<T, VC> va, vb;
-        va.load(a_src);
-        vb.load(b_src);
-        float a[VC], b[VC], ra[VC], rb[VC];
-        va.unpack(a);
-        vb.unpack(b);
+    const int heads = pp.H + 2 * pp.G, items = count * heads * PER;
+    for (int k0 = threadIdx.x; k0 < items; k0 += kThreads * BATCH) {
+        Vec<T, VC> va[BATCH], vb[BATCH];
+        T *a_dst[BATCH], *b_dst[BATCH];
+        const float2* cs[BATCH];
+        bool each[BATCH];  // an angle per column (RoPE) or one for all (Givens)
 #pragma unroll
-        for (int e = 0; e < VC; ++e) {
-            const float2 w = each ? cs[e] : one;
-            ra[e] = w.x * a[e] - w.y * b[e];
-            rb[e] = w.y * a[e] + w.x * b[e];
+        for (int i = 0; i < BATCH; ++i) {
+            const int k = k0 + i * kThreads;
+            a_dst[i] = nullptr;
+            if (k >= items) continue;
+            const int v = k % PER, u = k / PER;
+            const int t = (int)by_heads.div((uint32_t)u), hd = u - t * heads, c = v * VC;
+            const int64_t n = n0 + t, slot = s_slot[t];
+            const int64_t page = slot >> pp.page_shift;
+            const int off = (int)(slot & pp.page_mask);
+            const T *a_src, *b_src;
+            cs[i] = turn + t * HALF + c;
+            each[i] = true;
+            if (hd < pp.H) {
+                a_src = X1 + ((size_t)n * pp.H + hd) * D + c;
+                b_src = a_src + HALF;
+                a_dst[i] = P1 + ((size_t)n * pp.H + hd) * D + c;
+                b_dst[i] = a_dst[i] + HALF;
+            } else if (slot < 0) {
+                continue;
+            } else if (hd < pp.H + pp.G) {
+                const int g = hd - pp.H;
+                a_src = X2 + ((size_t)n * pp.G + g) * D + c;
+                b_src = a_src + HALF;
+                a_dst[i] = P2_pages + page_row_offset(pp, page, off, g) + c;
+                b_dst[i] = a_dst[i] + HALF;
+            } else {
+                const int g = hd - pp.H - pp.G;
+                int ga = g, gb = g, ca = c, cb = c + HALF;
+                each[i] = false;
+                cs[i] = &same;
+                if (theta != nullptr) {  // item g: pair g/2, the first or second half of its columns
+                    const int pair = g >> 1;
+                    cs[i] = mix + pair;
+                    ga = 2 * pair + pairing;
+                    gb = ga + 1 == pp.G ? 0 : ga + 1;
+                    ca = cb = c + (g & 1) * HALF;
+                }
+                a_src = I + ((size_t)n * pp.G + ga) * D + ca;
+                b_src = I + ((size_t)n * pp.G + gb) * D + cb;
+                a_dst[i] = I_pages + page_row_offset(pp, page, off, ga) + ca;
+                b_dst[i] = I_pages + page_row_offset(pp, page, off, gb) + cb;
+            }
+            va[i].load(a_src);
+            vb[i].load(b_src);
         }
-        va.pack(ra);
-        vb.pack(rb);
-        va.store(a_dst);
-        vb.store(b_dst);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            if (a_dst[i] == nullptr) continue;
+            float a[VC], b[VC], ra[VC], rb[VC];
+            va[i].unpack(a);
+            vb[i].unpack(b);
+#pragma unroll
+            for (int e = 0; e < VC; ++e) {
+                const float2 w = cs[i][each[i] ? e : 0];
+                ra[e] = w.x * a[e] - w.y * b[e];
+                rb[e] = w.y * a[e] + w.x * b[e];
+            }
+            va[i].pack(ra);
+            vb[i].pack(rb);
+            va[i].store(a_dst[i]);
+            vb[i].store(b_dst[i]);
+        }
     }
 }
 
@@ -123,13 +138,14 @@ template <typename T, int HALF, int VC>
 cudaError_t launch_store(const PagedProblem& pp, const void* X1, const void* X2, const void* I, const float* theta,
                          int pairing, const RopeTable& tab, const int* positions, const int64_t* slots, void* P1,
                          void* P2_pages, void* I_pages, unsigned int* status, int num_sms, cudaStream_t s) {
+    constexpr int kBatch = VC * sizeof(T) >= 16 ? 2 : 4;
     // A few blocks per SM first, then more tokens to a block.
     const int tokens = (int)std::min<int64_t>(kMaxTokens, std::max<int64_t>(1, (int64_t)pp.N / (4 * num_sms)));
     const unsigned blocks = (unsigned)(((int64_t)pp.N + tokens - 1) / tokens);
     const size_t sh = (size_t)(kMaxTokens * HALF + pp.G / 2) * sizeof(float2);
-    paged_store_kernel<T, HALF, VC><<<blocks, kThreads, sh, s>>>(
+    paged_store_kernel<T, HALF, VC, kBatch><<<blocks, kThreads, sh, s>>>(
         pp, (const T*)X1, (const T*)X2, (const T*)I, theta, pairing, tab, positions, slots, (T*)P1, (T*)P2_pages,
-        (T*)I_pages, status, tokens);
+        (T*)I_pages, status, tokens, FastDiv((uint32_t)(pp.H + 2 * pp.G)));
     return cudaGetLastError();
 }
 
