@@ -15,7 +15,7 @@
 //               hands each to the others, and loads P2: the pages of each tile by TMA, one
 //               copy per lane
 //   warp 1      MMA issuer and TMEM owner
-//   warp 2      query rows into shared memory
+//   warp 2      query rows into shared memory (d <= 64)
 //   warp 3      loads I~ and clears the keys past a request's end
 //   warps 4-7   softmax of rows 0-127 (one thread per row)
 //   warps 8-11  softmax of rows 128-255
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int x = 0; x < 4; ++x) ptx::mbar_init(&bars->v_clean[x], 1);
         for (int t = 0; t < 2; ++t) {
-            ptx::mbar_init(&bars->q_full[t], 1);
+            ptx::mbar_init(&bars->q_full[t], C::kSepP ? 1 : 4);  // a buffer, or a half
             ptx::mbar_init(&bars->q_free[t], 1);
             ptx::mbar_init(&bars->s_full[t], 1);
             for (int q = 0; q < 4; ++q) ptx::mbar_init(&bars->turn[t][q], 1);
@@ -254,6 +254,42 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int y = max(0, x - C::kStages); y < x; ++y)
                 ptx::mbar_drain(&full[y % C::kStages], (y / C::kStages) & 1, v.status);
     };
+    // Query rows r_begin .. r_end - 1 of a piece into buffer qb, by one warp; rows past the
+    // unit's are zero.  Eight steps' addresses at a time: one after the other they cost a lone
+    // warp 150 cycles each.
+    auto load_q = [&](const Piece& pc, int qb, int r_begin, int r_end, uint64_t* full) {
+        constexpr int kChunks = D / 8, kStep = 32 / kChunks;  // 16-byte chunks of a row; rows at a time
+        const int chunk = lane % kChunks, cols = max(0, min(8, pp.d - chunk * 8));
+        const uint32_t q_u = ptx::smem_u32(sQ) + (chunk / 8) * kPanelBytes;
+        for (int r0 = r_begin + lane / kChunks; r0 < r_end; r0 += 8 * kStep) {
+            const __nv_bfloat16* src[8];
+            uint32_t dst[8];
+            int bytes[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = r0 + i * kStep, rho = pc.q * kRows + r, rr = r & 127;
+                const bool in = rho < pc.rows;
+                const int t = in ? pp.by_group.div(rho) : 0, hd = pc.g * pp.group + (in ? rho - t * pp.group : 0);
+                src[i] = P1 + ((size_t)(pc.first + t) * pp.H + hd) * pp.d + (cols ? chunk * 8 : 0);
+                bytes[i] = in ? cols * 2 : 0;
+                dst[i] = q_u + (2 * qb + (r >> 7)) * C::kTileBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4);
+            }
+            if ((pp.d & 7) == 0) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) cp_async16(dst[i], src[i], bytes[i]);
+            } else {  // rows of 120 bytes start on 8
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    cp_async8(dst[i], src[i], min(bytes[i], 8));
+                    cp_async8(dst[i] + 8, bytes[i] > 8 ? src[i] + 4 : src[i], max(bytes[i] - 8, 0));
+                }
+            }
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(full);
+    };
     if (warp == 0) {
         // --------------------------------------------------------- pieces, P2
         ptx::regs_dec<kRegsControl>();
@@ -343,7 +379,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             return ok;
         };
         auto k_wait = [&](int x) { return wait(&bars->k_full[x % C::kStages], x / C::kStages, kDevTimeoutFull); };
-        auto q_wait = [&](int seg) { return wait(&bars->q_full[seg % C::kQBufs], seg / C::kQBufs, kDevTimeoutFull); };
+        // The queries of a piece (d > 64: of its half t, in the pieces where it has steps).
+        int halves[2] = {0, 0};
+        auto q_wait = [&](int seg, int t) {
+            return C::kSepP ? wait(&bars->q_full[seg % 2], seg / 2, kDevTimeoutFull)
+                            : wait(&bars->q_full[t], halves[t]++, kDevTimeoutFull);
+        };
         // What of a piece the products need.
         struct Steps {
             int steps[2], most, tail;
@@ -362,9 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         Steps sg = read(0);
         for (int seg = 0; ok && sg.most >= 0; ++seg) {
             const int qb = seg % C::kQBufs;
-            if (!q_wait(seg) || !k_wait(kt)) break;
+            if (!k_wait(kt)) break;
             for (int t = 0; t < 2; ++t) {
                 if (sg.steps[t] == 0 || begun[t]) continue;
+                if (!q_wait(seg, t)) break;
                 // S of the piece before has been read (d > 64: its P V, issued before, read it).
                 if (C::kSepP && st[t] > 0 && !wait(&bars->s_free[t], st[t] - 1, kDevTimeoutFull)) break;
                 ptx::tc_fence_after();
@@ -373,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             begun[0] = begun[1] = false;
             if (!ok) break;
             ptx::mma_commit_elect(&bars->k_empty[kt % C::kStages]);
-            if (sg.most == 1) ptx::mma_commit_elect(&bars->q_free[qb]);
+            if (C::kSepP && sg.most == 1) ptx::mma_commit_elect(&bars->q_free[qb]);
             Steps next{{0, 0}, -2, -1};  // not read yet
             for (int j = 0; ok && j < sg.most; ++j) {
                 const int s = (kt + j) % C::kStages;
@@ -399,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (next.most == -2) next = read(seg + 1);
                             if (!ok) break;
                             if (next.steps[t] > 0) {
-                                if (!q_wait(seg + 1) || !k_wait(kt + sg.most)) break;
+                                if (!q_wait(seg + 1, t) || !k_wait(kt + sg.most)) break;
                                 ptx::tc_fence_after();
                                 issue_s(t, (kt + sg.most) % C::kStages, (seg + 1) % C::kQBufs);
                                 begun[t] = true;
@@ -424,7 +466,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                     if (ok && j + 1 < sg.most) ptx::mma_commit_elect(&bars->k_empty[(kt + j + 1) % C::kStages]);
-                    if (ok && j + 2 == sg.most) ptx::mma_commit_elect(&bars->q_free[qb]);
                 }
                 if (ok) ptx::mma_commit_elect(&bars->v_empty[s]);
             }
@@ -440,10 +481,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 2) {
         // ------------------------------------------------------------- queries
         ptx::regs_dec<kRegsControl>();
-        constexpr int kChunks = D / 8, kStep = 32 / kChunks;  // 16-byte chunks of a row; rows at a time
-        const int chunk = lane % kChunks;
-        const uint32_t q_u = ptx::smem_u32(sQ) + (chunk / 8) * kPanelBytes;
-        const int cols = max(0, min(8, pp.d - chunk * 8));
         PieceMeta mine{};
         for (int seg = 0; ok; ++seg) {
             const Piece* slot = take(seg);
@@ -451,43 +488,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Piece pc = *slot;
             give(seg);
             if (pc.most < 0) break;
-            const int qb = seg % C::kQBufs;
-            if (seg >= C::kQBufs && !ptx::mbar_wait_warp(&bars->q_free[qb], (seg / C::kQBufs - 1) & 1, abort_flag,
-                                                         v.status, kDevTimeoutEmpty)) {
-                ok = false;
-                break;
-            }
-            // Rows past the unit's are zero.  Eight steps' addresses at a time: one after the other
-            // they cost a lone warp 150 cycles each (20 thousand cycles a unit at d = 128).
-            const int row_end = pc.rows - pc.q * kRows > kBM ? 2 * kBM : kBM;
-            for (int r0 = lane / kChunks; r0 < row_end; r0 += 8 * kStep) {
-                const __nv_bfloat16* src[8];
-                uint32_t dst[8];
-                int bytes[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = r0 + i * kStep, rho = pc.q * kRows + r, rr = r & 127;
-                    const bool in = rho < pc.rows;
-                    const int t = in ? pp.by_group.div(rho) : 0, hd = pc.g * pp.group + (in ? rho - t * pp.group : 0);
-                    src[i] = P1 + ((size_t)(pc.first + t) * pp.H + hd) * pp.d + (cols ? chunk * 8 : 0);
-                    bytes[i] = in ? cols * 2 : 0;
-                    dst[i] = q_u + (2 * qb + (r >> 7)) * C::kTileBytes + rr * 128 + (((chunk & 7) ^ (rr & 7)) << 4);
+            if constexpr (C::kSepP) {
+                const int qb = seg % C::kQBufs;
+                if (seg >= C::kQBufs && !ptx::mbar_wait_warp(&bars->q_free[qb], (seg / C::kQBufs - 1) & 1, abort_flag,
+                                                             v.status, kDevTimeoutEmpty)) {
+                    ok = false;
+                    break;
                 }
-                if ((pp.d & 7) == 0) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) cp_async16(dst[i], src[i], bytes[i]);
-                } else {  // rows of 120 bytes start on 8
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        cp_async8(dst[i], src[i], min(bytes[i], 8));
-                        cp_async8(dst[i] + 8, bytes[i] > 8 ? src[i] + 4 : src[i], max(bytes[i] - 8, 0));
-                    }
-                }
+                load_q(pc, qb, 0, pc.rows - pc.q * kRows > kBM ? 2 * kBM : kBM, &bars->q_full[qb]);
             }
-            asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&bars->q_full[qb]);
             if (pc.j0 == 0 && pc.j1 < pc.n)
                 mine = PieceMeta{share.owner(pc.place + pc.n - 1) - worker + 1, pc.first, pc.c, pc.rows, pc.g, pc.q};
         }
@@ -503,6 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* turn_mine = &bars->turn[t][quarter];
         uint64_t* turn_next = &bars->turn[t ^ 1][quarter];
         int st = 0, pairs = 0;  // steps of this half, and steps both halves took in turn
+        // d > 64: this warp's 32 query rows of piece seg, once this half's last scores of the piece
+        // before are there, so nothing reads its queries any more.
+        auto next_q = [&](int seg) {
+            if (C::kSepP || !ok) return;
+            const Piece* pc = take(seg);
+            if (pc != nullptr && pc->steps[t] > 0)
+                load_q(*pc, 0, t * kBM + quarter * 32, t * kBM + quarter * 32 + 32, &bars->q_full[t]);
+        };
+        next_q(0);
         for (int seg = 0; ok; ++seg) {
             const Piece* pc = take(seg);  // the slot stays this warp's until the piece is done
             if (pc == nullptr || pc->most < 0) break;
@@ -737,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_before();
                 ptx::mbar_arrive(&bars->p_full[t]);
             }
+            next_q(seg + 1);
             if (ok && steps > 0) {
                 ok = ptx::mbar_wait_warp(&bars->o_done[t], (st + steps - 1) & 1, abort_flag, v.status, kDevTimeoutMma);
                 ptx::tc_fence_after();
