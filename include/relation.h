@@ -470,6 +470,8 @@ typedef struct {
  * it could not serve are -1 (as is the slot of a token past the table's width, or
  * of one whose page is outside [0, pages)), and the caller frees pages or drops
  * requests before going on.  Rows starts[R] .. N - 1 get slot -1 and position 0.
+ * If the new tokens are more than N, those past N get neither slot nor page, and
+ * relation_check_device_status() reports RELATION_ERR_INVALID_ARGUMENT.
  * cached, fresh: int32 [R].  free_pages: int32 [free_count] (may be NULL when
  * free_count = 0).  starts: int32 [R + 1].  slots: int64 [N].  positions: int32
  * [N].  used: int32 [1].  Running it again with the same arguments gives the same
@@ -516,7 +518,13 @@ relation_status_t relation_paged_store(const relation_paged_t* p, const void* X1
  * problem), 16-byte aligned, contents ignored on entry.
  * The history is split over the whole GPU whatever the requests' lengths; cut rows
  * are merged from the workspace in a fixed order, so results are the same from run
- * to run.
+ * to run.  The call's work, one place per key tile of every 16 to 256 packed rows
+ * and cache head, may be 2^31 - 1 places; more is reported and nothing is written.
+ * What pages hold past a request's last token never matters, NaN and infinities
+ * included.  Within a request, a masked key has weight 0 and is still multiplied,
+ * so a non-finite I~ row of a new token can reach rows of the same call before it.
+ * Launches: 2, or 4 when max_fresh lets a request exceed 16 packed rows (new
+ * tokens times H / G).
  */
 size_t relation_paged_workspace_bytes(const relation_paged_t* p, int max_fresh);
 relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, const void* P2_pages,
@@ -532,7 +540,8 @@ relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, 
  * and the kernel's second, also bounded, wait for its own copies or products in
  * flight expired too, so it returned while they may still have been writing
  * shared memory: discard the outputs and recreate the context),
- * RELATION_ERR_INVALID_ARGUMENT (a decode position outside its cache) or
+ * RELATION_ERR_INVALID_ARGUMENT (a decode position outside its cache, or a value
+ * that a paged call could not follow) or
  * RELATION_ERR_CUDA.
  */
 relation_status_t relation_check_device_status(void);
