@@ -523,7 +523,7 @@ relation_status_t relation_paged_store(const relation_paged_t* p, const void* X1
  * What pages hold past a request's last token never matters, NaN and infinities
  * included.  Within a request, a masked key has weight 0 and is still multiplied,
  * so a non-finite I~ row of a new token can reach rows of the same call before it.
- * Launches: 2, or 4 when max_fresh lets a request exceed 16 packed rows (new
+ * Launches: 2, or 3 when max_fresh lets a request exceed 16 packed rows (new
  * tokens times H / G).
  */
 size_t relation_paged_workspace_bytes(const relation_paged_t* p, int max_fresh);

@@ -268,7 +268,8 @@ size_t f32_bytes(int num_sms) {
 }
 
 template <int kPairs, int kPer>
-cudaError_t launch_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, cudaStream_t s) {
+cudaError_t launch_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, MergeSide* small, bool last,
+                       cudaStream_t s) {
     using C = F32Cfg<kPairs, kPer>;
     static_assert(C::kFloats * 4 + 64 + kPagedMaxRequests * 4 <= 232448, "shared memory budget");
     auto kern = paged_f32_kernel<kPairs, kPer>;
@@ -287,16 +288,23 @@ cudaError_t launch_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, 
                                          (const float*)a.P1, (const float*)a.P2_pages, (const float*)a.I_pages,
                                          (float*)a.Y, a.L, part, meta);
     if (e != cudaSuccess) return e;
-    return launch_merge<float, C::kRows, C::kWidth>(v, part, meta, workers, a.Y, a.L, s);
+    const MergeSide side{part, meta, workers};
+    if constexpr (kPer == 1) {
+        *small = side;
+        return last ? launch_merge<float, C::kRows, 0, C::kWidth>(v, side, MergeSide{}, a.Y, a.L, s) : cudaSuccess;
+    } else {
+        return launch_merge<float, kSmallRows, C::kRows, C::kWidth>(v, *small, side, a.Y, a.L, s);
+    }
 }
 
 template <int kPairs>
 cudaError_t launch_f32_width(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, int* launches, cudaStream_t s) {
-    const cudaError_t e = launch_f32<kPairs, 1>(pp, a, ws, s);
-    *launches = 2;
-    if (e != cudaSuccess || (int64_t)a.max_fresh * pp.group <= kSmallRows) return e;
-    *launches = 4;
-    return launch_f32<kPairs, kLong>(pp, a, static_cast<char*>(ws) + f32_bytes<kPairs, 1>(a.num_sms), s);
+    const bool last = (int64_t)a.max_fresh * pp.group <= kSmallRows;
+    MergeSide small;
+    const cudaError_t e = launch_f32<kPairs, 1>(pp, a, ws, &small, last, s);
+    *launches = last ? 2 : 3;
+    if (e != cudaSuccess || last) return e;
+    return launch_f32<kPairs, kLong>(pp, a, static_cast<char*>(ws) + f32_bytes<kPairs, 1>(a.num_sms), &small, true, s);
 }
 
 template <int kPairs>

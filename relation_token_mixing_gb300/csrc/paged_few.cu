@@ -482,7 +482,7 @@ size_t few_bytes(int num_sms) {
 }
 
 template <int DK, int NT>
-cudaError_t launch_few(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, cudaStream_t s) {
+cudaError_t launch_few(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, MergeSide* left, cudaStream_t s) {
     using C = FewCfg<DK, NT>;
     auto kern = paged_few_kernel<DK, NT>;
     static std::once_flag once;
@@ -505,15 +505,20 @@ cudaError_t launch_few(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, 
     e = launch_chained(kern, dim3((unsigned)a.num_sms), C::kThreads, C::smem(pp.R), s, mk, mv, v,
                        (const __nv_bfloat16*)a.P1, (__nv_bfloat16*)a.Y, a.L, part, meta);
     if (e != cudaSuccess) return e;
-    return launch_merge<__nv_bfloat16, C::kRows, C::kWidth>(v, slots, meta, a.num_sms, a.Y, a.L, s);
+    const MergeSide side{slots, meta, a.num_sms};
+    if (left != nullptr) {
+        *left = side;
+        return cudaSuccess;
+    }
+    return launch_merge<__nv_bfloat16, C::kRows, 0, C::kWidth>(v, side, MergeSide{}, a.Y, a.L, s);
 }
 
 // Whether the host's bound on the new tokens keeps every unit within 8 rows.
 bool few_rows(const PagedProblem& pp, int max_fresh) { return (int64_t)max_fresh * pp.group <= 8; }
 
 template <int DK>
-cudaError_t launch_few_d(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, cudaStream_t s) {
-    return few_rows(pp, a.max_fresh) ? launch_few<DK, 1>(pp, a, ws, s) : launch_few<DK, 2>(pp, a, ws, s);
+cudaError_t launch_few_d(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, MergeSide* left, cudaStream_t s) {
+    return few_rows(pp, a.max_fresh) ? launch_few<DK, 1>(pp, a, ws, left, s) : launch_few<DK, 2>(pp, a, ws, left, s);
 }
 
 template <int DK>
@@ -534,13 +539,14 @@ size_t paged_few_workspace(const PagedProblem& pp, int max_fresh, int num_sms) {
     }
 }
 
-cudaError_t launch_paged_few(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s) {
+cudaError_t launch_paged_few(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, paged::MergeSide* left,
+                             cudaStream_t s) {
     using namespace paged;
     switch ((pp.d + 15) / 16) {
-        case 3: return launch_few_d<3>(pp, a, workspace, s);
-        case 4: return launch_few_d<4>(pp, a, workspace, s);
-        case 5: return launch_few_d<5>(pp, a, workspace, s);
-        default: return launch_few_d<8>(pp, a, workspace, s);
+        case 3: return launch_few_d<3>(pp, a, workspace, left, s);
+        case 4: return launch_few_d<4>(pp, a, workspace, left, s);
+        case 5: return launch_few_d<5>(pp, a, workspace, left, s);
+        default: return launch_few_d<8>(pp, a, workspace, left, s);
     }
 }
 

@@ -18,11 +18,14 @@ size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, int max_fresh, int
 
 cudaError_t launch_paged_fwd(const PagedProblem& pp, bool bf16, const PagedFwdArgs& a, int* launches, cudaStream_t s) {
     if (!bf16) return launch_paged_f32(pp, a, a.workspace, launches, s);
-    const cudaError_t e = launch_paged_few(pp, a, a.workspace, s);
     *launches = 2;
-    if (e != cudaSuccess || (int64_t)a.max_fresh * pp.group <= kPagedFewRows) return e;
-    *launches = 4;
-    return launch_paged_tc(pp, a, static_cast<char*>(a.workspace) + paged_few_workspace(pp, a.max_fresh, a.num_sms), s);
+    if ((int64_t)a.max_fresh * pp.group <= kPagedFewRows) return launch_paged_few(pp, a, a.workspace, nullptr, s);
+    paged::MergeSide few;  // both passes are merged in one launch
+    const cudaError_t e = launch_paged_few(pp, a, a.workspace, &few, s);
+    *launches = 3;
+    if (e != cudaSuccess) return e;
+    return launch_paged_tc(pp, a, static_cast<char*>(a.workspace) + paged_few_workspace(pp, a.max_fresh, a.num_sms), few,
+                           s);
 }
 
 }  // namespace relation

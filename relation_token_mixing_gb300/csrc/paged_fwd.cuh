@@ -170,9 +170,9 @@ __device__ __forceinline__ void store_pair(float* p, float a, float b) {
 
 // The kernels of a forward are launched as programmatic dependents, each on the SMs
 // as soon as there is room.  The first one waits for what ran before it and only then
-// releases the next, so whatever starts after that finds its inputs complete; a merge
-// releases the next pass before it waits for its own; and a pass that did not wait at
-// its beginning waits at its end, so that the last kernel's end is that of all.
+// releases the next, so whatever starts after that finds its inputs complete; the long
+// requests' pass, which reads nothing of the one before, waits at its end only; and the
+// merge waits for it, so the last kernel's end is that of all.
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dependency_release() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -214,30 +214,35 @@ struct MergedRow {
     }
 };
 
-// Merges the units that blocks begin and others continue, pieces in the line's
-// order.  Block (x, y): the unit of the pass's block x, rows 16 y and on, eight threads
-// a row.  The time is that of the dependent loads: the unit, then four pieces' rows
-// at once (a unit seldom has more).
+// What a pass leaves to merge: its blocks' two partial slots each, and the unit that each
+// begins and others continue.
+struct MergeSide {
+    const float* part;
+    const PieceMeta* meta;
+    int blocks;
+};
+
+// Merges 16 rows, from row0 on, of the unit that block x of the pass begins, pieces in the
+// line's order, eight threads a row.  The time is that of the dependent loads: the unit, then
+// four pieces' rows at once (a unit seldom has more).
 constexpr int kMergeThreads = 128, kMergeRows = 16;
 
 template <typename T, int kRows, int kWidth>
-__global__ void __launch_bounds__(kMergeThreads)
-    paged_merge_kernel(const __grid_constant__ FwdView v, const float* __restrict__ part,
-                       const PieceMeta* __restrict__ meta, T* __restrict__ Y, float* __restrict__ L) {
+__device__ __forceinline__ void merge_rows(const PagedProblem& pp, const MergeSide& side, int x, int row0, T* Y,
+                                           float* L) {
     constexpr int kQuads = kWidth / 32, kBatch = 4;
     constexpr size_t slot = slot_floats(kRows, kWidth);
-    dependency_release();
-    dependency_wait();
-    const int sub = threadIdx.x & 7, row = blockIdx.y * kMergeRows + (threadIdx.x >> 3);
-    const PieceMeta mt = meta[blockIdx.x];
+    const int sub = threadIdx.x & 7, row = row0 + (threadIdx.x >> 3);
+    if (x >= side.blocks) return;
+    const PieceMeta mt = side.meta[x];
     const int rho = mt.q * kRows + row;
     if (mt.pieces == 0 || row >= kRows || rho >= mt.rows) return;
     // Piece 0 is this block's slot 1, piece p block (x + p)'s slot 0.
-    const float* base = part + (size_t)blockIdx.x * 2 * slot;
+    const float* base = side.part + (size_t)x * 2 * slot;
     MergedRow<kQuads> out;
     for (int p0 = 0; p0 < mt.pieces; p0 += kBatch) {
         float2 ml[kBatch];
-        float4 x[kBatch][kQuads];
+        float4 v[kBatch][kQuads];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
             const int p = min(p0 + b, mt.pieces - 1);
@@ -246,12 +251,29 @@ __global__ void __launch_bounds__(kMergeThreads)
             if (p0 + b >= mt.pieces) ml[b].x = -INFINITY;
 #pragma unroll
             for (int e = 0; e < kQuads; ++e)
-                x[b][e] = *reinterpret_cast<const float4*>(src + (size_t)row * kWidth + 32 * e + 4 * sub);
+                v[b][e] = *reinterpret_cast<const float4*>(src + (size_t)row * kWidth + 32 * e + 4 * sub);
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) out.add(ml[b].x, ml[b].y, x[b]);
+        for (int b = 0; b < kBatch; ++b) out.add(ml[b].x, ml[b].y, v[b]);
     }
-    out.finish(v.pp, mt.first, mt.c, mt.g, rho, sub, Y, L);
+    out.finish(pp, mt.first, mt.c, mt.g, rho, sub, Y, L);
+}
+
+// Merges the few rows' units alone (kFew rows each), or (kLong > 0) those of both passes.
+template <typename T, int kFew, int kLong, int kWidth>
+__global__ void __launch_bounds__(kMergeThreads)
+    paged_merge_kernel(const __grid_constant__ FwdView v, const MergeSide few, const MergeSide longer,
+                       T* __restrict__ Y, float* __restrict__ L) {
+    static_assert(kFew <= kMergeRows, "one block a unit");
+    dependency_release();
+    dependency_wait();
+    if constexpr (kLong > 0) {
+        if (blockIdx.y > 0) {
+            merge_rows<T, kLong, kWidth>(v.pp, longer, blockIdx.x, (blockIdx.y - 1) * kMergeRows, Y, L);
+            return;
+        }
+    }
+    merge_rows<T, kFew, kWidth>(v.pp, few, blockIdx.x, 0, Y, L);
 }
 
 // One kernel of the chain on stream s, resident before the kernel before it ends.
@@ -270,12 +292,13 @@ cudaError_t launch_chained(void (*kern)(P...), dim3 grid, int threads, size_t sm
     return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
-template <typename T, int kRows, int kWidth>
-cudaError_t launch_merge(const FwdView& v, const float* part, const PieceMeta* meta, int blocks, void* Y, float* L,
+template <typename T, int kFew, int kLong, int kWidth>
+cudaError_t launch_merge(const FwdView& v, const MergeSide& few, const MergeSide& longer, void* Y, float* L,
                          cudaStream_t s) {
-    return launch_chained(paged_merge_kernel<T, kRows, kWidth>,
-                          dim3((unsigned)blocks, (kRows + kMergeRows - 1) / kMergeRows), kMergeThreads, 0, s, v, part,
-                          meta, (T*)Y, L);
+    return launch_chained(paged_merge_kernel<T, kFew, kLong, kWidth>,
+                          dim3((unsigned)(few.blocks > longer.blocks ? few.blocks : longer.blocks),
+                               1 + kLong / kMergeRows),
+                          kMergeThreads, 0, s, v, few, longer, (T*)Y, L);
 }
 
 }  // namespace paged
@@ -284,9 +307,12 @@ cudaError_t launch_merge(const FwdView& v, const float* part, const PieceMeta* m
 // more; paged_f32.cu: float32).
 constexpr int kPagedFewRows = 16;
 size_t paged_few_workspace(const PagedProblem& pp, int max_fresh, int num_sms);
-cudaError_t launch_paged_few(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s);
+// left: what it leaves to the long requests' pass to merge, if that follows.
+cudaError_t launch_paged_few(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, paged::MergeSide* left,
+                             cudaStream_t s);
 size_t paged_tc_workspace(const PagedProblem& pp, int num_sms);
-cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s);
+cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace,
+                            const paged::MergeSide& few, cudaStream_t s);
 size_t paged_f32_workspace(const PagedProblem& pp, int max_fresh, int num_sms);
 cudaError_t launch_paged_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, int* launches,
                              cudaStream_t s);

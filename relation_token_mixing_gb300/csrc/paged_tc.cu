@@ -826,7 +826,7 @@ size_t tc_bytes(int num_sms) {
 }
 
 template <int D>
-cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, cudaStream_t s) {
+cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, const MergeSide& few, cudaStream_t s) {
     using C = TcCfg<D>;
     static_assert(1024 + C::kTiles + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory budget");
     static std::once_flag once;
@@ -848,7 +848,7 @@ cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, c
     e = launch_chained(paged_tc_kernel<D>, dim3((unsigned)workers), kThreads, C::smem(pp.R), s, mk, mv, v,
                        (const __nv_bfloat16*)a.P1, (__nv_bfloat16*)a.Y, a.L, part, meta);
     if (e != cudaSuccess) return e;
-    return launch_merge<__nv_bfloat16, kRows, D>(v, part, meta, workers, a.Y, a.L, s);
+    return launch_merge<__nv_bfloat16, kPagedFewRows, kRows, D>(v, few, MergeSide{part, meta, workers}, a.Y, a.L, s);
 }
 
 }  // namespace
@@ -858,8 +858,9 @@ size_t paged_tc_workspace(const PagedProblem& pp, int num_sms) {
     return pp.d <= 64 ? paged::tc_bytes<64>(num_sms) : paged::tc_bytes<128>(num_sms);
 }
 
-cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, cudaStream_t s) {
-    return pp.d <= 64 ? paged::launch_tc<64>(pp, a, workspace, s) : paged::launch_tc<128>(pp, a, workspace, s);
+cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace,
+                            const paged::MergeSide& few, cudaStream_t s) {
+    return pp.d <= 64 ? paged::launch_tc<64>(pp, a, workspace, few, s) : paged::launch_tc<128>(pp, a, workspace, few, s);
 }
 
 }  // namespace relation
