@@ -198,14 +198,6 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
-def _ptrs(*tensors) -> list[int | None]:
-    """_ptr of each, without a call each (a serving step makes three such calls)."""
-    for t in tensors:
-        if t is not None and not (t.is_cuda and t.is_contiguous()):
-            _ptr(t)  # raises
-    return [None if t is None else t.data_ptr() for t in tensors]
-
-
 def _host_ptr(t) -> int | None:
     if t is None:
         return None
@@ -431,20 +423,17 @@ def linear_gate_fwd_bwd(P1, P2, I, R, A_log, dt_bias, dY, tau_S: float, layout: 
 
 def relation_paged_plan(prob: Paged, cached, fresh, free_pages, block_table, starts, slots, positions, used,
                         stream=None) -> None:
-    c, f, free, table, s, sl, pos, u = _ptrs(cached, fresh, free_pages, block_table, starts, slots, positions, used)
-    code = load().relation_paged_plan(ctypes.byref(prob), c, f, free, 0 if free_pages is None else free_pages.numel(),
-                                      table, s, sl, pos, u, _stream_ptr(stream))
-    if code:
-        _check(code, "relation_paged_plan")
+    _check(load().relation_paged_plan(ctypes.byref(prob), _ptr(cached), _ptr(fresh), _ptr(free_pages),
+                                      0 if free_pages is None else free_pages.numel(), _ptr(block_table),
+                                      _ptr(starts), _ptr(slots), _ptr(positions), _ptr(used), _stream_ptr(stream)),
+           "relation_paged_plan")
 
 
 def relation_paged_store(prob: Paged, X1, X2, I, theta, pairing, rope_base, positions, slots, P1, P2_pages, I_pages,
                          stream=None) -> None:
-    x1, x2, i, th, pos, sl, p1, p2, ip = _ptrs(X1, X2, I, theta, positions, slots, P1, P2_pages, I_pages)
-    code = load().relation_paged_store(ctypes.byref(prob), x1, x2, i, th, pairing, rope_base, pos, sl, p1, p2, ip,
-                                       _stream_ptr(stream))
-    if code:
-        _check(code, "relation_paged_store")
+    _check(load().relation_paged_store(ctypes.byref(prob), _ptr(X1), _ptr(X2), _ptr(I), _ptr(theta), pairing,
+                                       rope_base, _ptr(positions), _ptr(slots), _ptr(P1), _ptr(P2_pages),
+                                       _ptr(I_pages), _stream_ptr(stream)), "relation_paged_store")
 
 
 def relation_paged_workspace_bytes(prob: Paged, max_fresh: int) -> int:
@@ -453,11 +442,9 @@ def relation_paged_workspace_bytes(prob: Paged, max_fresh: int) -> int:
 
 def relation_paged_fwd(prob: Paged, P1, P2_pages, I_pages, block_table, starts, cached, max_fresh, Y, L, workspace,
                        stream=None) -> None:
-    p1, p2, i, table, s, c, y, l, ws = _ptrs(P1, P2_pages, I_pages, block_table, starts, cached, Y, L, workspace)
-    code = load().relation_paged_fwd(ctypes.byref(prob), p1, p2, i, table, s, c, max_fresh, y, l, ws, workspace.nbytes,
-                                     _stream_ptr(stream))
-    if code:
-        _check(code, "relation_paged_fwd")
+    _check(load().relation_paged_fwd(ctypes.byref(prob), _ptr(P1), _ptr(P2_pages), _ptr(I_pages), _ptr(block_table),
+                                     _ptr(starts), _ptr(cached), max_fresh, _ptr(Y), _ptr(L), _ptr(workspace),
+                                     workspace.nbytes, _stream_ptr(stream)), "relation_paged_fwd")
 
 
 def relation_check_device_status() -> int:
