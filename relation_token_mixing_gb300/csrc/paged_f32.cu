@@ -15,7 +15,9 @@
 // requests of at most 16 rows, whose time is mostly the copies'.  Measured at 4 requests of
 // 100 to 500 new tokens over up to 2048, 16 heads over 8 of 64: 0.192 ms, 0.41 of the fp32 pipes
 // (a 16 x 16 grid of threads with pairs of columns 0.218; this grid with them 0.200; two
-// blocks an SM and more in flight a warp 0.22).  Work is cut as in the bf16 kernels
+// blocks an SM and more in flight a warp 0.22); 16 decoding requests of 100 to 16384, 16 heads
+// over 8 of 64: 0.165 ms, 3.1 TB/s (warps without a row of the unit skip the products: 0.29 if
+// they do not).  Work is cut as in the bf16 kernels
 // (paged_schedule.cuh).
 //
 // Exponentials use ex2 and the sigmoid's quotient a reciprocal, both within 2^-22;
@@ -31,7 +33,7 @@ namespace {
 
 constexpr int kKeys = 64, kTx = 8;
 constexpr int kSmallRows = 16;  // requests of at most this many rows take kPer = 1
-constexpr int kMinTiles = 2;
+constexpr int kMinTiles = 2;  // of a worker (kPer = 1: 1, the tile's latency is the time)
 constexpr int kLong = 4;      // and longer ones this kPer
 constexpr int kPitchP = 68;  // rows start on 16 bytes; four rows on are 16 banks on
 
@@ -47,10 +49,10 @@ struct F32Cfg {
     static constexpr int kPitchQ = kPer > 1 ? kRows + 4 : kPitch, kQ = kPer > 1 ? kWidth * kPitchQ : kRows * kPitch;
     static constexpr int kFloats = kQ + kKeys * kPitch + kKeys * kWidth + kRows * kPitchP;
     static int smem(int R) { return kFloats * 4 + 64 + (R * 4 + 15) / 16 * 16; }
-    // Blocks an SM holds, by registers and by shared memory (the schedule's summary of R
+    // Blocks an SM holds (kPer = 1: of 3, 4 and 5, three were fastest), by registers and by shared memory (the schedule's summary of R
     // requests takes little unless R is thousands).
     static constexpr int kPerSm =
-        std::max(1, std::min(kPer == 1 ? 5 : kQuads == 2 ? 3 : 2, 222 * 1024 / (kFloats * 4 + 2048)));
+        std::max(1, std::min(kPer == 1 || kQuads == 2 ? 3 : 2, 222 * 1024 / (kFloats * 4 + 2048)));
     using Line = Tiling<kRows, kKeys, 1>;
 };
 
@@ -91,7 +93,7 @@ __global__ void __launch_bounds__(F32Cfg<kQuads, kPer>::kThreads, F32Cfg<kQuads,
         return Tl::places(q.c, q.rows, pp.by_group, Tl::row_tiles(q.rows));
     });
     const int worker = blockIdx.x;
-    const Share share(total, (int)gridDim.x, kMinTiles);
+    const Share share(total, (int)gridDim.x, kPer == 1 ? 1 : kMinTiles);
     const int lo = share.begin(worker), hi = share.begin(worker + 1);
     PieceMeta mine{};
     if (lo >= hi) {
@@ -135,6 +137,7 @@ __global__ void __launch_bounds__(F32Cfg<kQuads, kPer>::kThreads, F32Cfg<kQuads,
         const int j0 = k.j, j1 = min(k.n, k.j + (hi - k.f));
         const int len = k.rq.c + pp.by_group.div(k.rq.rows);
         __syncthreads();  // the unit before has been read
+        const bool live = k.q * kRows + kPer * (ty & ~3) < k.rq.rows;  // some row of the warp is the unit's
         int page = page_of(j0, len);
         copy(P2, k_u, C::kPitch, j0, page, len);
         int pos[kPer];
@@ -166,103 +169,107 @@ __global__ void __launch_bounds__(F32Cfg<kQuads, kPer>::kThreads, F32Cfg<kQuads,
             __syncthreads();  // and I~ of the one before has been read
             copy(I, v_u, C::kWidth, j, page, len);
             if (j + 1 < j1) page = page_of(j + 1, len);
-            float sc[kPer][8];
-            if constexpr (kPer > 1) {  // pairs of rows, a key's column for both
-                float2 s2[kPer / 2][8] = {};
+            if (live) {
+                float sc[kPer][8];
+                if constexpr (kPer > 1) {  // pairs of rows, a key's column for both
+                    float2 s2[kPer / 2][8] = {};
 #pragma unroll 1
-                for (int c = 0; c < quads; ++c) {
-                    float4 q[4];
-                    static_assert(kPer == 4, "a row's four");
+                    for (int c = 0; c < quads; ++c) {
+                        float4 q[4];
+                        static_assert(kPer == 4, "a row's four");
 #pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        q[x] = *reinterpret_cast<const float4*>(sQ + (4 * c + x) * C::kPitchQ + 4 * ty);
+                        for (int x = 0; x < 4; ++x)
+                            q[x] = *reinterpret_cast<const float4*>(sQ + (4 * c + x) * C::kPitchQ + 4 * ty);
 #pragma unroll
-                    for (int n = 0; n < 8; ++n) {
-                        const float4 kk = *reinterpret_cast<const float4*>(sK + (tx + kTx * n) * C::kPitch + 4 * c);
+                        for (int n = 0; n < 8; ++n) {
+                            const float4 kk = *reinterpret_cast<const float4*>(sK + (tx + kTx * n) * C::kPitch + 4 * c);
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            const float w = x == 0 ? kk.x : x == 1 ? kk.y : x == 2 ? kk.z : kk.w;
-                            s2[0][n] = ptx::fma2(make_float2(w, w), make_float2(q[x].x, q[x].y), s2[0][n]);
-                            s2[1][n] = ptx::fma2(make_float2(w, w), make_float2(q[x].z, q[x].w), s2[1][n]);
+                            for (int x = 0; x < 4; ++x) {
+                                const float w = x == 0 ? kk.x : x == 1 ? kk.y : x == 2 ? kk.z : kk.w;
+                                s2[0][n] = ptx::fma2(make_float2(w, w), make_float2(q[x].x, q[x].y), s2[0][n]);
+                                s2[1][n] = ptx::fma2(make_float2(w, w), make_float2(q[x].z, q[x].w), s2[1][n]);
+                            }
                         }
                     }
+#pragma unroll
+                    for (int i = 0; i < kPer; ++i)
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) sc[i][n] = (i & 1) ? s2[i / 2][n].y : s2[i / 2][n].x;
+                } else {  // pairs of columns
+                    float2 s2[8] = {};
+#pragma unroll 4
+                    for (int c = 0; c < quads; ++c) {
+                        const float4 q = *reinterpret_cast<const float4*>(sQ + ty * C::kPitchQ + 4 * c);
+#pragma unroll
+                        for (int n = 0; n < 8; ++n) {
+                            const float4 kk = *reinterpret_cast<const float4*>(sK + (tx + kTx * n) * C::kPitch + 4 * c);
+                            s2[n] = ptx::fma2(make_float2(q.x, q.y), make_float2(kk.x, kk.y), s2[n]);
+                            s2[n] = ptx::fma2(make_float2(q.z, q.w), make_float2(kk.z, kk.w), s2[n]);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) sc[0][n] = s2[n].x + s2[n].y;
                 }
+                const int col = j * kKeys + tx;
 #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-#pragma unroll
-                    for (int n = 0; n < 8; ++n) sc[i][n] = (i & 1) ? s2[i / 2][n].y : s2[i / 2][n].x;
-            } else {  // pairs of columns
-                float2 s2[8] = {};
-#pragma unroll 2
-                for (int c = 0; c < quads; ++c) {
-                    const float4 q = *reinterpret_cast<const float4*>(sQ + ty * C::kPitchQ + 4 * c);
+                for (int i = 0; i < kPer; ++i) {
+                    float r[8], mt = -INFINITY;
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
-                        const float4 kk = *reinterpret_cast<const float4*>(sK + (tx + kTx * n) * C::kPitch + 4 * c);
-                        s2[n] = ptx::fma2(make_float2(q.x, q.y), make_float2(kk.x, kk.y), s2[n]);
-                        s2[n] = ptx::fma2(make_float2(q.z, q.w), make_float2(kk.z, kk.w), s2[n]);
+                        const float u = sc[i][n] * pp.inv_sqrt_d;
+                        r[n] = u * sigmoid_f32(u);
                     }
-                }
+                    if (j * kKeys + kKeys > pos[i]) {  // the row's own token is in this tile or before it
 #pragma unroll
-                for (int n = 0; n < 8; ++n) sc[0][n] = s2[n].x + s2[n].y;
-            }
-            const int col = j * kKeys + tx;
+                        for (int n = 0; n < 8; ++n) {
+                            if (col + kTx * n == pos[i])
+                                r[n] = sigmoid_f32(sc[i][n] * inv_diag) + corr[i];
+                            if (col + kTx * n > pos[i]) r[n] = -INFINITY;
+                        }
+                    }
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-                float r[8], mt = -INFINITY;
+                    for (int n = 0; n < 8; ++n) mt = fmaxf(mt, r[n]);
 #pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float u = sc[i][n] * pp.inv_sqrt_d;
-                    r[n] = u * sigmoid_f32(u);
-                }
-                if (j * kKeys + kKeys > pos[i]) {  // the row's own token is in this tile or before it
+                    for (int x = kTx / 2; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
+                    const float mn = fmaxf(m[i], mt);
+                    // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
+                    const float f = mn == -INFINITY ? 1.f : ptx::ex2_approx((m[i] - mn) * kLog2e);
+                    const float ref = mn == -INFINITY ? 0.f : mn;
+                    m[i] = mn;
+                    float sum = 0.f;
 #pragma unroll
                     for (int n = 0; n < 8; ++n) {
-                        if (col + kTx * n == pos[i])
-                            r[n] = sigmoid_f32(sc[i][n] * inv_diag) + corr[i];
-                        if (col + kTx * n > pos[i]) r[n] = -INFINITY;
+                        const float p = ptx::ex2_approx((r[n] - ref) * kLog2e);
+                        sum += p;
+                        sP[(kPer * ty + i) * kPitchP + tx + kTx * n] = p;
                     }
+                    l[i] = l[i] * f + sum;  // this thread's keys; summed over tx at the end
+#pragma unroll
+                    for (int e = 0; e < 2 * kQuads; ++e) o[i][e].x *= f, o[i][e].y *= f;
                 }
-#pragma unroll
-                for (int n = 0; n < 8; ++n) mt = fmaxf(mt, r[n]);
-#pragma unroll
-                for (int x = kTx / 2; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-                const float mn = fmaxf(m[i], mt);
-                // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
-                const float f = mn == -INFINITY ? 1.f : ptx::ex2_approx((m[i] - mn) * kLog2e);
-                const float ref = mn == -INFINITY ? 0.f : mn;
-                m[i] = mn;
-                float sum = 0.f;
-#pragma unroll
-                for (int n = 0; n < 8; ++n) {
-                    const float p = ptx::ex2_approx((r[n] - ref) * kLog2e);
-                    sum += p;
-                    sP[(kPer * ty + i) * kPitchP + tx + kTx * n] = p;
-                }
-                l[i] = l[i] * f + sum;  // this thread's keys; summed over tx at the end
-#pragma unroll
-                for (int e = 0; e < 2 * kQuads; ++e) o[i][e].x *= f, o[i][e].y *= f;
             }
             cp_wait<0>();  // I~ of this tile
             __syncthreads();  // and P2 has been read
             if (j + 1 < j1) copy(P2, k_u, C::kPitch, j + 1, page, len);
-#pragma unroll 1
-            for (int c = 0; c < kKeys / 4; ++c) {
-                float4 p[kPer];
+            if (live) {
+#pragma unroll (kPer == 1 ? 4 : 1)
+                for (int c = 0; c < kKeys / 4; ++c) {
+                    float4 p[kPer];
 #pragma unroll
-                for (int i = 0; i < kPer; ++i)
-                    p[i] = *reinterpret_cast<const float4*>(sP + (kPer * ty + i) * kPitchP + 4 * c);
+                    for (int i = 0; i < kPer; ++i)
+                        p[i] = *reinterpret_cast<const float4*>(sP + (kPer * ty + i) * kPitchP + 4 * c);
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
+                    for (int n = 0; n < 4; ++n) {
 #pragma unroll
-                    for (int e = 0; e < kQuads; ++e) {
-                        const float4 vv =
-                            *reinterpret_cast<const float4*>(sV + (4 * c + n) * C::kWidth + 4 * tx + 32 * e);
+                        for (int e = 0; e < kQuads; ++e) {
+                            const float4 vv =
+                                *reinterpret_cast<const float4*>(sV + (4 * c + n) * C::kWidth + 4 * tx + 32 * e);
 #pragma unroll
-                        for (int i = 0; i < kPer; ++i) {
-                            const float w = n == 0 ? p[i].x : n == 1 ? p[i].y : n == 2 ? p[i].z : p[i].w;
-                            o[i][2 * e] = ptx::fma2(make_float2(w, w), make_float2(vv.x, vv.y), o[i][2 * e]);
-                            o[i][2 * e + 1] = ptx::fma2(make_float2(w, w), make_float2(vv.z, vv.w), o[i][2 * e + 1]);
+                            for (int i = 0; i < kPer; ++i) {
+                                const float w = n == 0 ? p[i].x : n == 1 ? p[i].y : n == 2 ? p[i].z : p[i].w;
+                                o[i][2 * e] = ptx::fma2(make_float2(w, w), make_float2(vv.x, vv.y), o[i][2 * e]);
+                                o[i][2 * e + 1] = ptx::fma2(make_float2(w, w), make_float2(vv.z, vv.w), o[i][2 * e + 1]);
+                            }
                         }
                     }
                 }
