@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(F32Cfg<kQuads, kPer>::kThreads, F32Cfg<kQuads,
                      float* __restrict__ part, PieceMeta* __restrict__ meta) {
     using C = F32Cfg<kQuads, kPer>;
     using Tl = typename C::Line;
-    constexpr int kRows = C::kRows, kTy = C::kTy, kThreads = C::kThreads;
+    constexpr int kRows = C::kRows, kThreads = C::kThreads;
     extern __shared__ float4 smem4[];
     float* sQ = reinterpret_cast<float*>(smem4);
     float* sK = sQ + C::kQ;
