@@ -33,9 +33,10 @@
 // give 3/32 cycle a score, against 4 d / 8192 = 1/32 cycle (d = 64) or 1/16 (d =
 // 128) of tensor-core time, so the special-function unit is the limit.  The packed half
 // forms of both functions run at half the rate, so they gain nothing.
-// Measured: nine prompts of 1 to 4096 tokens, 16 heads of 64: 0.347 ms, half of it the special
-// functions' time; two chunks of 1024 tokens over 16k and 31k, 32 heads over 8 of 128: 0.82 ms,
-// 996 TFLOP/s, 62% the special functions' time.  At d <= 64 the rest is the softmax's own
+// Measured: nine prompts of 1 to 4096 tokens, 16 heads of 64: 0.344 ms, half of it the special
+// functions' time; two chunks of 1024 tokens over 16k and 31k, 32 heads over 8 of 128: 0.81 ms,
+// 1.0 PFLOP/s, 63% the special functions' time (with a pass for the maximum between the two
+// functions 0.347 and 0.82).  At d <= 64 the rest is the softmax's own
 // latencies, with two warps to hide them (4.2 thousand cycles a tile of both halves, 3.1 of
 // them special functions), and a unit's beginning and end; at d = 128 the latencies of one
 // warp in its turn.  Other shapes measured on the two: tiles of 64 keys with two score
@@ -55,8 +56,8 @@ namespace {
 
 constexpr int kBM = 128, kRows = 256, kKeys = 128;
 constexpr int kThreads = 384;
-// 128 * 72 + 256 * 216 = 64512 = 384 * 168 registers.
-constexpr uint32_t kRegsControl = 72, kRegsSoftmax = 216;
+// 128 * 104 + 256 * 200 = 64512 = 384 * 168 registers.
+constexpr uint32_t kRegsControl = 104, kRegsSoftmax = 200;
 constexpr int kPanelBytes = 128 * 128;  // 128 rows x 64 bf16
 constexpr int kMinTiles = 4;
 // A unit's beginning and end (queries, first scores, output: 7 to 12 thousand cycles)
@@ -541,7 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float corr = pp.lambda * __logf((float)(own + 1));
             own -= pc->j0 * kKeys;
             int own_lo = __shfl_sync(0xffffffffu, own, 0), own_hi = __shfl_sync(0xffffffffu, own, 31);
-            float m = -INFINITY, l = 0.f;
+            // The row's reference and the sum of its weights under it.  SiLU is above -0.28 and Self above 0,
+            // so 0 is a fair reference to begin with; it rises when a score passes it by 2^kRaise.
+            float m = 0.f, l = 0.f;
             bool o_ready = false;  // O and P are free of this tile's predecessors
             auto o_wait = [&](int j) {
                 if (o_ready) return;
@@ -556,11 +559,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
                 w = ptx::pack_bf16x2(x.x * f, x.y * f);
             };
-            // d <= 64: the maximum rises to m_new in block b of tile j (seldom after the first): what has
-            // been summed under the old one is scaled, in O, in l and in this tile's P so far.
-            // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
+            // The reference rises to m_new in block b of tile j (seldom): what has been summed under the
+            // old one is scaled, in O, in l and in this tile's P so far.
             auto raise = [&](float m_new, int j, int b) {
-                const float f = m_new == -INFINITY ? 1.f : ptx::ex2_approx((m - m_new) * kLog2e);
+                const float f = ptx::ex2_approx((m - m_new) * kLog2e);
                 l *= f;
                 m = m_new;
                 o_wait(j);
@@ -588,8 +590,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_st16(p_addr + 16 * x, pv);
                 }
             };
-            // d <= 64: 32 scores -> the weights of columns 32 b and on, and what they add to the row's
-            // sum and maximum.
+            const float2 ch2 = make_float2(c_half, c_half), l2e2 = make_float2(kLog2e, kLog2e);
+            // Two scores -> R (left in their place), and their weights under the reference.
+            auto pair = [&](uint32_t& s0, uint32_t& s1, float2 nm2, float2& sum) {
+                const float2 h = ptx::mul2(make_float2(as_f(s0), as_f(s1)), ch2);
+                const float2 th = make_float2(ptx::tanh_approx(h.x), ptx::tanh_approx(h.y));
+                const float2 E = ptx::fma2(h, th, h);  // SiLU(U) = (U/2)(1 + tanh(U/2))
+                const float2 y = ptx::fma2(E, l2e2, nm2);
+                const float2 p = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+                s0 = as_u(E.x), s1 = as_u(E.y);
+                sum = ptx::add2(sum, p);
+                return ptx::pack_bf16x2(p.x, p.y);
+            };
+            // 32 scores -> the weights of columns 32 b and on, and what they add to the row's sum.
             auto block = [&](uint32_t (&sv)[32], uint32_t (&pk)[16], int j, int b) {
                 const int c0 = 32 * b;
                 if (c0 > own_hi) {  // past every row's own token
@@ -597,40 +610,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = 0; e < 16; ++e) pk[e] = 0u;
                     return;
                 }
-                const bool edge = c0 + 31 >= own_lo;  // at or past some row's
-                float self = 0.f;
-                if (edge) {
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                if (c0 + 31 < own_lo) {
+                    // Before every row's own token: both functions in one run, under the reference so
+                    // far, with no wait for the maximum between them.
+                    const float2 nm2 = make_float2(-m * kLog2e, -m * kLog2e);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        pk[e] = pair(sv[2 * e], sv[2 * e + 1], nm2, ls[e & 1]);
+                        mx[e & 3] = ptx::max3(mx[e & 3], as_f(sv[2 * e]), as_f(sv[2 * e + 1]));
+                    }
+                    const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    if (!__any_sync(0xffffffffu, m_new > m + kRaise * kLn2)) {
+                        const float2 sum = ptx::add2(ls[0], ls[1]);
+                        l += sum.x + sum.y;
+                        return;
+                    }
+                    raise(m_new, j, b);
+                } else {
+                    float self = 0.f;
 #pragma unroll
                     for (int c = 0; c < 32; ++c) self = c0 + c == own ? as_f(sv[c]) : self;
                     self = fmaf(0.5f, ptx::tanh_approx(self * c_diag), 0.5f) + corr;
-                }
-                const float2 ch2 = make_float2(c_half, c_half);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float2 h = ptx::mul2(make_float2(as_f(sv[2 * e]), as_f(sv[2 * e + 1])), ch2);
-                    const float2 th = make_float2(ptx::tanh_approx(h.x), ptx::tanh_approx(h.y));
-                    const float2 E = ptx::fma2(h, th, h);  // SiLU(U) = (U/2)(1 + tanh(U/2))
-                    sv[2 * e] = as_u(E.x);
-                    sv[2 * e + 1] = as_u(E.y);
-                }
-                if (edge) {
 #pragma unroll
                     for (int c = 0; c < 32; ++c) {
-                        const float x = c0 + c > own ? -INFINITY : as_f(sv[c]);
+                        const float h = as_f(sv[c]) * c_half;
+                        const float x = c0 + c > own ? -INFINITY : fmaf(h, ptx::tanh_approx(h), h);
                         sv[c] = as_u(c0 + c == own ? self : x);
                     }
-                }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < 32; c += 8) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) mx[q] = ptx::max3(mx[q], as_f(sv[c + 2 * q]), as_f(sv[c + 2 * q + 1]));
+                    for (int e = 0; e < 16; ++e)
+                        mx[e & 3] = ptx::max3(mx[e & 3], as_f(sv[2 * e]), as_f(sv[2 * e + 1]));
+                    const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    if (__any_sync(0xffffffffu, m_new > m + kRaise * kLn2)) raise(m_new, j, b);
                 }
-                const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                if (__any_sync(0xffffffffu, m_new > m + kRaise * kLn2)) raise(m_new, j, b);
-                const float m_ref = m == -INFINITY ? 0.f : m;
-                const float2 l2e2 = make_float2(kLog2e, kLog2e), nm2 = make_float2(-m_ref * kLog2e, -m_ref * kLog2e);
-                float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                const float2 nm2 = make_float2(-m * kLog2e, -m * kLog2e);
+                ls[0] = ls[1] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                     const float2 y = ptx::fma2(make_float2(as_f(sv[2 * e]), as_f(sv[2 * e + 1])), l2e2, nm2);
@@ -641,6 +657,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float2 sum = ptx::add2(ls[0], ls[1]);
                 l += sum.x + sum.y;
             };
+            // A tile, 32 columns at a time in a loop, not 128 in a row: its code stays in the instruction
+            // caches (whole prompts, heads of 64: 0.36 ms, unrolled 0.41).
+            auto blocks = [&](int j) {
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    uint32_t sv[32], pk[16];
+                    ptx::tmem_ld32(lane_addr + s_col + 32 * b, sv);
+                    ptx::tmem_ld_wait();
+                    ptx::pin_regs(sv);
+                    if (C::kSepP && b == 3) {  // the next S may overwrite it
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive(&bars->s_free[t]);
+                    }
+                    block(sv, pk, j, b);
+                    if (C::kSepP && b == 0) o_wait(j);  // P V of the tile before has read its P
+                    ptx::tmem_st16(p_addr + 16 * b, pk);
+                }
+            };
             for (int j = 0; ok && j < steps; ++j) {
                 o_ready = false;
                 if (!ptx::mbar_wait_warp(&bars->s_full[t], (st + j) & 1, abort_flag, v.status, kDevTimeoutMma)) {
@@ -649,115 +683,59 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 ptx::tc_fence_after();
                 if constexpr (C::kSepP) {
-                    // A loop, not 128 columns in a row: its code stays in the instruction caches
-                    // (whole prompts, heads of 64: 0.36 ms, unrolled 0.41).
-#pragma unroll 1
-                    for (int b = 0; b < 4; ++b) {
-                        uint32_t sv[32], pk[16];
-                        ptx::tmem_ld32(lane_addr + s_col + 32 * b, sv);
+                    blocks(j);
+                } else {
+                    // The 128 columns at once where every row's own token is past them.
+                    bool whole = own_lo >= kKeys;
+                    const int x = pairs + j;
+                    auto take_turn = [&] {
+                        return j >= n_pair || x + t == 0 ||
+                               ptx::mbar_wait_warp(turn_mine, (x + t - 1) & 1, abort_flag, v.status, kDevTimeoutMma);
+                    };
+                    if (whole) {
+                        uint32_t sv[128], pk[2][32];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            ptx::tmem_ld32(lane_addr + s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
                         ptx::tmem_ld_wait();
                         ptx::pin_regs(sv);
-                        if (b == 3) {  // the next S may overwrite it
-                            ptx::tc_fence_before();
-                            ptx::mbar_arrive(&bars->s_free[t]);
+                        if (!take_turn()) {
+                            ok = false;
+                            break;
                         }
-                        block(sv, pk, j, b);
-                        if (b == 0) o_wait(j);  // P V of the tile before has read its P
-                        ptx::tmem_st16(p_addr + 16 * b, pk);
-                    }
-                    if (!ok) break;
-                } else {
-                    uint32_t sv[128];
+                        ptx::pin_regs(sv);  // the run below starts after the turn is taken
+                        const float2 nm2 = make_float2(-m * kLog2e, -m * kLog2e);
+                        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
+                                        make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        ptx::tmem_ld32(lane_addr + s_col + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(sv + 32 * c));
-                    ptx::tmem_ld_wait();
-                    ptx::pin_regs(sv);
-                    const int x = pairs + j;
-                    if (j < n_pair && x + t > 0 &&
-                        !ptx::mbar_wait_warp(turn_mine, (x + t - 1) & 1, abort_flag, v.status, kDevTimeoutMma)) {
+                        for (int e = 0; e < 64; ++e) {
+                            pk[e >> 5][e & 31] = pair(sv[2 * e], sv[2 * e + 1], nm2, ls[e & 3]);
+                            mx[e & 3] = ptx::max3(mx[e & 3], as_f(sv[2 * e]), as_f(sv[2 * e + 1]));
+                        }
+                        const float m_new = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                        whole = !__any_sync(0xffffffffu, m_new > m + kRaise * kLn2);
+                        if (whole) {
+                            const float2 sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
+                            l += sum.x + sum.y;
+                            ptx::pin_regs(pk[0]);  // and ends before it is passed on
+                            ptx::pin_regs(pk[1]);
+                            __syncwarp();
+                            if (j < n_pair && lane == 0) ptx::mbar_arrive(turn_next);
+                            ptx::tmem_st32(p_addr, pk[0]);
+                            ptx::tmem_st32(p_addr + 32, pk[1]);
+                        }
+                    } else if (!take_turn()) {
                         ok = false;
                         break;
                     }
-                    ptx::pin_regs(sv);  // the loops below start after the turn is taken
-                    const float2 ch2 = make_float2(c_half, c_half);
-                    // The two long loops run over every column, also those that the mask drops: with
-                    // branches around blocks of them the kernel was slower (two chunks of 1024 over
-                    // 16k and 32k, heads of 128: 0.91 ms for 0.85).
-                    const bool edge = own_lo < kKeys;  // some row's own token is in this tile or before it
-                    float self = 0.f;
-                    if (edge) {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c) self = c == own ? as_f(sv[c]) : self;
-                        self = fmaf(0.5f, ptx::tanh_approx(self * c_diag), 0.5f) + corr;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) {
-                        const float2 h = ptx::mul2(make_float2(as_f(sv[2 * e]), as_f(sv[2 * e + 1])), ch2);
-                        const float2 th = make_float2(ptx::tanh_approx(h.x), ptx::tanh_approx(h.y));
-                        const float2 E = ptx::fma2(h, th, h);  // SiLU(U) = (U/2)(1 + tanh(U/2))
-                        sv[2 * e] = as_u(E.x);
-                        sv[2 * e + 1] = as_u(E.y);
-                    }
-                    if (edge) {
-#pragma unroll
-                        for (int c = 0; c < 128; ++c) {
-                            const float x = c > own ? -INFINITY : as_f(sv[c]);
-                            sv[c] = as_u(c == own ? self : x);
-                        }
-                    }
-                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                    for (int c = 0; c < 128; c += 8) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) mx[q] = ptx::max3(mx[q], as_f(sv[c + 2 * q]), as_f(sv[c + 2 * q + 1]));
-                    }
-                    const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                    const bool rescale = __any_sync(0xffffffffu, m_new > m + kRaise * kLn2);
-                    float scale = 1.f;
-                    if (rescale) {
-                        // A row that has seen nothing yet (a piece that begins past its token) stays at -inf.
-                        scale = m_new == -INFINITY ? 1.f : ptx::ex2_approx((m - m_new) * kLog2e);
-                        l *= scale;
-                        m = m_new;
-                    }
-                    const float m_ref = m == -INFINITY ? 0.f : m;
-                    const float2 l2e2 = make_float2(kLog2e, kLog2e), nm2 = make_float2(-m_ref * kLog2e, -m_ref * kLog2e);
-                    float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f),
-                                    make_float2(0.f, 0.f)};
-                    uint32_t pk[2][32];
-#pragma unroll
-                    for (int c = 0; c < 64; ++c) {
-                        const float2 y = ptx::fma2(make_float2(as_f(sv[2 * c]), as_f(sv[2 * c + 1])), l2e2, nm2);
-                        const float2 p = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
-                        ls[c & 3] = ptx::add2(ls[c & 3], p);
-                        pk[c >> 5][c & 31] = ptx::pack_bf16x2(p.x, p.y);
-                    }
-                    {
-                        const float2 sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
-                        l += sum.x + sum.y;
-                    }
-                    ptx::pin_regs(pk[0]);  // and end before it is passed on
-                    ptx::pin_regs(pk[1]);
-                    __syncwarp();
-                    if (j < n_pair && lane == 0) ptx::mbar_arrive(turn_next);
-                    ptx::tmem_st32(p_addr, pk[0]);
-                    ptx::tmem_st32(p_addr + 32, pk[1]);
-                    if (rescale && j > 0) {
-                        o_wait(j);  // O is final
-                        if (!ok) break;
-#pragma unroll
-                        for (int c0 = 0; c0 < D / 32; ++c0) {
-                            uint32_t ov[32];
-                            ptx::tmem_ld32(lane_addr + o_col + 32 * c0, ov);
-                            ptx::tmem_ld_wait();
-                            ptx::pin_regs(ov);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) ov[e] = as_u(as_f(ov[e]) * scale);
-                            ptx::tmem_st32(lane_addr + o_col + 32 * c0, ov);
-                        }
+                    if (!whole) {  // S is still there
+                        blocks(j);
+                        __syncwarp();
+                        if (j < n_pair && lane == 0) ptx::mbar_arrive(turn_next);
                     }
                 }
+                if (!ok) break;
                 own -= kKeys;
                 own_lo -= kKeys;
                 own_hi -= kKeys;
@@ -802,7 +780,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!direct)
-                    *reinterpret_cast<float2*>(slot + (size_t)kRows * D + 2 * (t * kBM + r)) = make_float2(m * kLog2e, l);
+                    // A row that has seen nothing (a piece that begins past its token) is left out.
+                    *reinterpret_cast<float2*>(slot + (size_t)kRows * D + 2 * (t * kBM + r)) =
+                        make_float2(l > 0.f ? m * kLog2e : -INFINITY, l);
                 else if (L != nullptr && mine)
                     L[yr] = m + __log2f(l) * kLn2 - corr;
             }
