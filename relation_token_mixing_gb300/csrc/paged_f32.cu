@@ -324,7 +324,7 @@ template <int kQuads, int kPer>
 cudaError_t launch_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, MergeSide* small, bool last,
                        cudaStream_t s) {
     using C = F32Cfg<kQuads, kPer>;
-    static_assert(C::kFloats * 4 + 64 + kPagedMaxRequests * 4 <= 232448, "shared memory budget");
+    static_assert(C::kFloats * 4 + 64 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
     auto kern = paged_f32_kernel<kQuads, kPer>;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;

@@ -542,8 +542,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float corr = pp.lambda * __logf((float)(own + 1));
             own -= pc->j0 * kKeys;
             int own_lo = __shfl_sync(0xffffffffu, own, 0), own_hi = __shfl_sync(0xffffffffu, own, 31);
-            // The row's reference and the sum of its weights under it.  SiLU is above -0.28 and Self above 0,
-            // so 0 is a fair reference to begin with; it rises when a score passes it by 2^kRaise.
+            // The row's reference and the sum of its weights under it.  SiLU is above -0.28, and the first
+            // row's Self, which has no correction, above 0: no row's sum vanishes under the reference 0.
+            // It rises when a score passes it by 2^kRaise.
             float m = 0.f, l = 0.f;
             bool o_ready = false;  // O and P are free of this tile's predecessors
             auto o_wait = [&](int j) {
@@ -808,7 +809,7 @@ size_t tc_bytes(int num_sms) {
 template <int D>
 cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, const MergeSide& few, cudaStream_t s) {
     using C = TcCfg<D>;
-    static_assert(1024 + C::kTiles + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory budget");
+    static_assert(1024 + C::kTiles + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
