@@ -521,8 +521,10 @@ relation_status_t relation_paged_store(const relation_paged_t* p, const void* X1
  * to run.  The call's work, one place per key tile of every 16 to 256 packed rows
  * and cache head, may be 2^31 - 1 places; more is reported and nothing is written.
  * What pages hold past a request's last token never matters, NaN and infinities
- * included.  Within a request, a masked key has weight 0 and is still multiplied,
- * so a non-finite I~ row of a new token can reach rows of the same call before it.
+ * included.  A non-finite score makes the rows that see its key NaN (Y and L),
+ * however their history is cut.  Within a request, a masked key has weight 0 and is
+ * still multiplied, so a non-finite I~ row of a new token can reach rows of the same
+ * call before it.
  * Launches: 2, or 3 when max_fresh lets a request exceed 16 packed rows (new
  * tokens times H / G).
  */

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(F32Cfg<kQuads, kPer>::kThreads, F32Cfg<kQuads,
                 if (direct) {
                     if (L != nullptr) L[yr[i]] = m[i] + logf(ls) - corr[i];
                 } else {
-                    store_pair(slot + kRows * C::kWidth + 2 * row, m[i] * kLog2e, ls);
+                    store_pair(slot + kRows * C::kWidth + 2 * row, piece_max(j0 * kKeys <= pos[i], m[i] * kLog2e), ls);
                 }
             }
         }

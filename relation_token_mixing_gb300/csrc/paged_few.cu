@@ -306,7 +306,9 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
                             slot[rho * C::kWidth + dt * 16 + h * 8 + key0] = o[n][dt][2 * h + e];
-                    if (key0 == 0) store_pair(slot + C::kRows * C::kWidth + 2 * rho, m[n][e], l[n][e]);
+                    if (key0 == 0)
+                        store_pair(slot + C::kRows * C::kWidth + 2 * rho,
+                                   piece_max(j_begin * kKeys <= pos[n][e], m[n][e]), l[n][e]);
                 } else if (L != nullptr && key0 == 0) {
                     const int t = pp.by_group.div(rho);
                     L[(size_t)(rq.first + t) * pp.H + u.g * pp.group + (rho - t * pp.group)] =

@@ -158,6 +158,13 @@ struct PieceMeta {
 // this much (a factor 256): exact, numerator and denominator share it.
 constexpr float kRaise = 8.f;
 
+// The maximum that a piece leaves of a row: -inf says that it begins past the row's own token
+// and has none of its keys.  A piece that has some leaves a finite one or +inf even where all its
+// scores are NaN (which no maximum takes in), so that the merge does not pass over its sum.
+__device__ __forceinline__ float piece_max(bool has_keys, float m) {
+    return has_keys ? fmaxf(m, -3.402823466e38f) : -INFINITY;
+}
+
 // A slot: `rows` rows of `width` values, then (m, l) each.
 __host__ __device__ constexpr size_t slot_floats(int rows, int width) { return (size_t)rows * (width + 2); }
 

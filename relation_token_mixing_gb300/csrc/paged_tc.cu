@@ -781,9 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 if (!direct)
-                    // A row that has seen nothing (a piece that begins past its token) is left out.
                     *reinterpret_cast<float2*>(slot + (size_t)kRows * D + 2 * (t * kBM + r)) =
-                        make_float2(l > 0.f ? m * kLog2e : -INFINITY, l);
+                        make_float2(piece_max(pc->c + token >= pc->j0 * kKeys, m * kLog2e), l);
                 else if (L != nullptr && mine)
                     L[yr] = m + __log2f(l) * kLn2 - corr;
             }
