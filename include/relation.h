@@ -294,7 +294,8 @@ relation_status_t relation_decode(const relation_problem_t* p, const void* P1_ne
  *   forward's I_mixed -> dX1, dX2, dI and, when dtheta is not NULL, dtheta
  *   [H/2] float32 (overwritten; dtheta_k = sum dI~b . I~a - dI~a . I~b).
  * theta: device float32 [H/2].  pos0: optional device int32 [B] (NULL: 0),
- * e.g. the decode position.  Outputs must not overlap inputs.  Two kernel
+ * e.g. the decode position; a position pos0 + t above 2^24 is rounded to float32
+ * before it is turned (relation_paged_store keeps it).  Outputs must not overlap inputs.  Two kernel
  * launches each (HBM-bound elementwise passes).
  */
 relation_status_t relation_prologue_fwd(const relation_problem_t* p, const void* X1, const void* X2, const void* I,
@@ -490,7 +491,8 @@ relation_status_t relation_paged_plan(const relation_paged_t* p, const int32_t* 
  *   P1[n] = RoPE(X1[n], positions[n]); page row slots[n] of P2_pages =
  *   RoPE(X2[n], positions[n]) and of I_pages = the mixed I[n].
  * theta: float32 [G/2], pairs of cache heads as in relation_prologue_fwd (G even);
- * NULL stores the states unmixed.  rope_base <= 0: no rotation.  Tokens whose slot
+ * NULL stores the states unmixed.  rope_base <= 0: no rotation.  Any int32 position
+ * keeps its angle (within 4e-7 + position 2^-49 radians).  Tokens whose slot
  * is negative are not cached (their P1 row is still written); a slot past the
  * last page is reported and skipped.  Two tokens must not share a slot.
  * P1 must not overlap any input.
