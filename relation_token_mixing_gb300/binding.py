@@ -629,6 +629,8 @@ def paged_store(X1, X2, I, theta, pairing: int, rope_base: float, positions, slo
         raise ValueError("X1, P1 are [N, H, d_h], X2, I [N, G, d_h], positions, slots [N], both page pools alike")
     if not (X2.dtype is I.dtype is P1.dtype is I_pages.dtype is X1.dtype):
         raise ValueError(f"X2, I, P1 and the pages must be {X1.dtype}, as X1")
+    if theta is not None and (theta.dtype is not torch.float32 or theta.numel() != prob.G // 2):
+        raise ValueError("theta is [G / 2] of torch.float32")
     relation_paged_store(prob, X1, X2, I, theta, pairing, rope_base, positions, slots, P1, P2_pages, I_pages, stream)
 
 
