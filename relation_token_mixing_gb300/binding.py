@@ -645,7 +645,8 @@ def paged_workspace(prob: Paged, max_fresh: int, device="cuda") -> torch.Tensor:
 def paged_fwd(P1, P2_pages, I_pages, block_table, starts, cached, max_fresh: int, tau_S: float, lam: float, Y=None,
               L=None, workspace=None, layout: int = RELATION_LAYOUT_BHTD, stream=None):
     """Relation of packed new tokens P1 [N, H, d_h] over the pages; returns (Y, L).  Y and workspace are allocated
-    when not given; L [N, H] float32 is filled when given."""
+    when not given, from the stream that the kernels run on; L [N, H] float32 is filled when given.  Tensors passed in
+    for another stream than their own are the caller's to order and to keep."""
     R, width = block_table.shape
     prob = paged_for(P1, P2_pages, R, width, tau_S, lam, layout)
     if not (block_table.dtype is starts.dtype is cached.dtype is _I32):
@@ -654,13 +655,18 @@ def paged_fwd(P1, P2_pages, I_pages, block_table, starts, cached, max_fresh: int
             I_pages.dtype is not P1.dtype:
         raise ValueError("starts is [R + 1], cached [R], both page pools alike")
     if Y is None:
-        Y = torch.empty_like(P1)
+        with torch.cuda.stream(stream):  # None: the current one
+            Y = torch.empty_like(P1)
+        if stream is not None:
+            Y.record_stream(torch.cuda.current_stream())  # where the caller reads it
     elif Y.shape != P1.shape or Y.dtype is not P1.dtype:
         raise ValueError("Y is like P1")
     if L is not None:
         if L.dtype is not torch.float32 or L.shape != (prob.N, prob.H):
             raise ValueError("L is [N, H] of torch.float32")
     if workspace is None:
-        workspace = paged_workspace(prob, max_fresh, P1.device)
+        # Freed on return: the stream's own memory goes to its next work only, which runs after the kernels.
+        with torch.cuda.stream(stream):
+            workspace = paged_workspace(prob, max_fresh, P1.device)
     relation_paged_fwd(prob, P1, P2_pages, I_pages, block_table, starts, cached, max_fresh, Y, L, workspace, stream)
     return Y, L
