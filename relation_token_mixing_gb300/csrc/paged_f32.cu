@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(F32Cfg<kQuads, kPer>::kThreads, F32Cfg<kQuads,
                         const float u = sc[i][n] * pp.inv_sqrt_d;
                         r[n] = u * sigmoid_f32(u);
                     }
-                    if (j * kKeys + kKeys > pos[i]) {  // the row's own token is in this tile or before it
+                    if (j * kKeys > pos[i] - kKeys) {  // the row's own token is in this tile (whose end may be 2^31) or before it
 #pragma unroll
                         for (int n = 0; n < 8; ++n) {
                             if (col + kTx * n == pos[i])

@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
         }
         const uint32_t sk = ring_u + s * C::kStageBytes, sv = sk + C::kTensorBytes;
         const int tok = u.j * kKeys;
-        if (tok + kKeys > len) {
+        if (tok > len - kKeys) {  // (tok + kKeys may be 2^31)
             // Keys past the request's end hold whatever their page holds: weight 0 times
             // a NaN is a NaN, so they are cleared.
             if (lane >= len - tok) {
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
                 for (int n = 0; n < NT; ++n)
                     if (n < nt_used) mma16816(sc[n][mt], a, qf[n][ks][0], qf[n][ks][1]);
             }
-        const bool edge = tok + kKeys > rq.c;  // new tokens or the history's end in this tile
+        const bool edge = tok > rq.c - kKeys;  // new tokens or the history's end in this tile
         float mt_[NT][2];
         bool raise = false;
 #pragma unroll
