@@ -513,7 +513,9 @@ relation_status_t relation_paged_store(const relation_paged_t* p, const void* X1
  * outside the requests' ranges are left unwritten.  cached: int32 [R].
  * max_fresh: an upper bound of the new tokens of any request, known to the host
  * (0: none known).  It selects kernels and sizes the workspace; a request with
- * more new tokens is reported and skipped.
+ * more new tokens is reported and skipped.  The bound (N where none is known) times
+ * H / G, a request's packed rows, is at most 2^31 - 256 (else
+ * RELATION_ERR_UNSUPPORTED).
  * Y: [N, H, d_h].  L: optional float32 [N, H], log sum_j exp(R_ij) in the
  * paper's convention.
  * workspace: relation_paged_workspace_bytes(p, max_fresh) bytes (0 = invalid

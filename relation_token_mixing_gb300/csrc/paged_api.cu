@@ -97,6 +97,11 @@ int fresh_bound(const relation_paged_t* p, int max_fresh) {
     return max_fresh == 0 || (int64_t)max_fresh > p->N ? (int)p->N : max_fresh;
 }
 
+// A request's packed rows are counted in 32 bits, in row tiles of up to 256.
+bool rows_fit(const relation_paged_t* p, int max_fresh) {
+    return (int64_t)fresh_bound(p, max_fresh) * (p->H / p->G) <= (int64_t)INT32_MAX - 255;
+}
+
 }  // namespace
 }  // namespace relation
 
@@ -175,7 +180,7 @@ relation_status_t relation_paged_store(const relation_paged_t* p, const void* X1
 }
 
 size_t relation_paged_workspace_bytes(const relation_paged_t* p, int max_fresh) {
-    if (check_paged(p) != RELATION_OK || max_fresh < 0 || p->R > kPagedMaxRequests) return 0;
+    if (check_paged(p) != RELATION_OK || max_fresh < 0 || p->R > kPagedMaxRequests || !rows_fit(p, max_fresh)) return 0;
     unsigned int* status;
     int sms;
     if (api_device(&status, &sms) != RELATION_OK) return 0;
@@ -190,6 +195,7 @@ relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, 
     if (st != RELATION_OK) return st;
     if (p->R > kPagedMaxRequests) return RELATION_ERR_UNSUPPORTED;
     if (max_fresh < 0) return RELATION_ERR_INVALID_ARGUMENT;
+    if (!rows_fit(p, max_fresh)) return RELATION_ERR_UNSUPPORTED;
     if (p->N == 0) {
         api_set_launches(0);
         return RELATION_OK;
