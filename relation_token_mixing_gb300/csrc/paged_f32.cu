@@ -23,8 +23,8 @@
 // Exponentials use ex2 and the sigmoid's quotient a reciprocal, both within 2^-22;
 // the argument's own rounding (|R| 2^-24) is of that size.
 #include <algorithm>
-#include <mutex>
 
+#include "once_per_device.h"
 #include "paged_fwd.cuh"
 
 namespace relation {
@@ -326,20 +326,16 @@ cudaError_t launch_f32(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, 
     using C = F32Cfg<kQuads, kPer>;
     static_assert(C::kFloats * 4 + 64 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
     auto kern = paged_f32_kernel<kQuads, kPer>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(kPagedMaxRequests));
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static OncePerDevice once;
+    cudaError_t e = allow_dynamic_smem(once, kern, C::smem(kPagedMaxRequests));
+    if (e != cudaSuccess) return e;
     const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, kPer == 1 ? 0 : kSmallRows,
                     kPer == 1 ? kSmallRows : INT32_MAX, a.status};
     const int workers = a.num_sms * C::kPerSm;
     float* part = static_cast<float*>(ws);
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(part + (size_t)workers * 2 * slot_floats(C::kRows, C::kWidth));
-    const cudaError_t e = launch_chained(kern, dim3((unsigned)workers), C::kThreads, C::smem(pp.R), s, v,
-                                         (const float*)a.P1, (const float*)a.P2_pages, (const float*)a.I_pages,
-                                         (float*)a.Y, a.L, part, meta);
+    e = launch_chained(kern, dim3((unsigned)workers), C::kThreads, C::smem(pp.R), s, v, (const float*)a.P1,
+                       (const float*)a.P2_pages, (const float*)a.I_pages, (float*)a.Y, a.L, part, meta);
     if (e != cudaSuccess) return e;
     const MergeSide side{part, meta, workers};
     if constexpr (kPer == 1) {

@@ -30,8 +30,8 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <mutex>
 
+#include "once_per_device.h"
 #include "paged_fwd.cuh"
 #include "tmap.h"
 
@@ -493,20 +493,16 @@ template <int DK, int NT>
 cudaError_t launch_few(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, MergeSide* left, cudaStream_t s) {
     using C = FewCfg<DK, NT>;
     auto kern = paged_few_kernel<DK, NT>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::smem(kPagedMaxRequests));
-    });
+    static OncePerDevice once;
     static_assert(1024 + C::kRingBytes + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
-    if (attr_err != cudaSuccess) return attr_err;
+    cudaError_t e = allow_dynamic_smem(once, kern, C::smem(kPagedMaxRequests));
+    if (e != cudaSuccess) return e;
     const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, 0, kPagedFewRows, a.status};
     // A piece of each worker, two of each block, the blocks' units.
     float* part = static_cast<float*>(ws);
     float* slots = part + (size_t)a.num_sms * C::kWarps * C::kSlot;
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(slots + (size_t)a.num_sms * 2 * C::kSlot);
     CUtensorMap mk, mv;
-    cudaError_t e;
     const int box = std::min(pp.page, kKeys);
     if ((e = make_page_map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
     if ((e = make_page_map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;

@@ -46,8 +46,8 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
-#include <mutex>
 
+#include "once_per_device.h"
 #include "paged_fwd.cuh"
 
 namespace relation {
@@ -809,19 +809,14 @@ template <int D>
 cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, const MergeSide& few, cudaStream_t s) {
     using C = TcCfg<D>;
     static_assert(1024 + C::kTiles + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        C::smem(kPagedMaxRequests));
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static OncePerDevice once;
+    cudaError_t e = allow_dynamic_smem(once, paged_tc_kernel<D>, C::smem(kPagedMaxRequests));
+    if (e != cudaSuccess) return e;
     const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, kPagedFewRows, INT32_MAX, a.status};
     const int workers = a.num_sms;
     float* part = static_cast<float*>(ws);
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(part + (size_t)workers * 2 * C::kSlotFloats);
     CUtensorMap mk, mv;
-    cudaError_t e;
     const int box = std::min(pp.page, kKeys);
     if ((e = make_page_map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
     if ((e = make_page_map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
