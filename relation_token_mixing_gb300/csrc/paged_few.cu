@@ -20,8 +20,8 @@
 //    wide side, a key's fragment is loaded once for all rows, and the weights' 8 x 8
 //    blocks are turned by movmatrix between the products.  With 16 rows at most there
 //    is nothing for the 128-row tcgen05 tile and its trip through TMEM to gain.
-// Measured: decoding 32 requests of 1000 to 32767, 32 heads over 8 of 128: 0.264 ms, 6.8 TB/s,
-// the copy rate; 8 requests of up to 4095, 16 heads of 64: 22 us, of which 3.3 until the first
+// Measured: decoding 32 requests of 1000 to 32767, 32 heads over 8 of 128: 0.264 to 0.270 ms,
+// 6.7 to 6.8 TB/s, the copy rate; 8 requests of up to 4095, 16 heads of 64: 22 us, of which 3.3 until the first
 // bytes and 4 for the merge; 48 requests of up to 8192 with 0 to 5 new tokens, 10 heads over 5 of
 // 64: 46 us, 4.5 TB/s.
 // The sigmoid is (1 + tanh)/2 by the hardware's tanh (2^-11), below the rounding of

@@ -6,9 +6,10 @@
 // passes over the other's requests, and the second is launched only where the
 // host's bound on the new tokens lets a request be that long.  At 16 rows, 16 requests of
 // 100 to 16384 tokens, the first takes 24, 36 and 52 us (16 heads over 2 of 64, of 128, 32
-// over 8 of 64), the second 46, 59 and 129.  float32 has its own pair of kernels on the
-// CUDA cores, with the same limit: 84 us against 75 (16 over 2 of 64) and 602 against 1002
-// (32 over 8 of 128).
+// over 8 of 64), the second 46, 59 and 129: the limit is where the first kernel's fragments
+// end (two groups of 8 rows), below where the two would cross.  float32 has its own pair of
+// kernels on the CUDA cores, with the same limit: 85 us against 75 (16 over 2 of 64) and 594
+// against 1002 (32 over 8 of 128).
 #include "paged_fwd.cuh"
 
 namespace relation {
