@@ -413,6 +413,67 @@ relation_status_t relation_linear_bwd_gate(const relation_problem_t* p, const vo
                                            size_t workspace_bytes, void* stream);
 
 /*
+ * Linear Relation over a pool of states: serving many requests (Sec. 5.2
+ * eq.(15)-(17); Appendix A.4).
+ *
+ * A request's whole history in a Linear Relation layer is its state C, d_h x d_h
+ * floats a head.  The states of all requests live in a pool, and a step takes every
+ * request's new tokens from one slot of the pool to another:
+ *   C_0 = the state in slot slots_in[r], then for its new tokens in order
+ *   Y_t = I~_t + S_t (C-_t)^T p^1_t, C_t = C-_t + S_t p^2_t I~_t^T as in
+ *   relation_linear_fwd, and the last C_t is stored to slot slots_out[r].
+ * slots_in[r] negative: a new request, C_0 = 0.  slots_out[r] negative: the state is
+ * not kept (drafted tokens that may be rejected).  Both the same: in place.  Two
+ * requests may read the same slot (a shared prefix), but a slot that one request
+ * writes must be no other request's, neither to read nor to write.  A request
+ * without new tokens has its state copied.
+ *
+ * R requests; N rows of the packed token tensors; H heads; `states` slots.
+ * P1, P2 (after RoPE), I (= I~), Y: [N, H, d_h] bfloat16, packed one request after
+ *   another.  G: [N, H, d_h] float32, the log-retention, or with A_log and dt_bias
+ *   (float32 [H, d_h]; both or neither) the gate's input as in
+ *   relation_linear_fwd_gate.  Any finite value is accepted.
+ * states: float32 [states, H, d_h, d_h] (row = key channel, as relation_linear_fwd
+ *   leaves it).  slots_in, slots_out: device int32 [R].
+ * Supported: d_h in {48, 60, 64}, RELATION_BF16 (else RELATION_ERR_UNSUPPORTED).
+ * Sizes: 1 <= R <= 2^20, 0 <= N <= 2^31 - 1, H <= 1024, 1 <= states <= 2^31 - 1,
+ *   every tensor at most 10^12 elements.
+ * A slot past the pool, packed offsets that do not ascend or pass N, or more new
+ * tokens than max_fresh are never followed: such a request's rows or state are
+ * skipped (a slot past the pool counts as negative) and
+ * relation_check_device_status() reports RELATION_ERR_INVALID_ARGUMENT.
+ * Outputs must not overlap inputs or each other.
+ *
+ * relation_linear_step: one new token a request (row r is request r's; N >= R, rows
+ *   from R on are left unwritten); one launch.
+ * relation_linear_packed_fwd: any number of new tokens a request.  starts: device
+ *   int32 [R + 1] ascending, request r's rows are starts[r] .. starts[r + 1] - 1;
+ *   rows outside all requests' are left unwritten.  max_fresh: an upper bound of any
+ *   request's new tokens, known to the host (0: none known); it selects kernels and
+ *   sizes the workspace (relation_linear_packed_workspace_bytes, 16-byte aligned,
+ *   contents ignored on entry; 0: none needed or p invalid).  Requests of up to 16
+ *   new tokens run token by token, longer ones in chunks of 64 tokens on the tensor
+ *   cores, the longest split over the GPU.  1, 2 or 4 launches; results are the
+ *   same from run to run.
+ */
+typedef struct {
+    int64_t R, N, H, d_h, states;
+    int32_t dtype; /* relation_dtype_t */
+    float tau_S;   /* as in relation_problem_t */
+} relation_linear_packed_t;
+
+relation_status_t relation_linear_step(const relation_linear_packed_t* p, const void* P1, const void* P2,
+                                       const void* I, const float* G, const float* A_log, const float* dt_bias,
+                                       float* states, const int32_t* slots_in, const int32_t* slots_out, void* Y,
+                                       void* stream);
+size_t relation_linear_packed_workspace_bytes(const relation_linear_packed_t* p, int max_fresh);
+relation_status_t relation_linear_packed_fwd(const relation_linear_packed_t* p, const void* P1, const void* P2,
+                                             const void* I, const float* G, const float* A_log, const float* dt_bias,
+                                             const int32_t* starts, int max_fresh, float* states,
+                                             const int32_t* slots_in, const int32_t* slots_out, void* Y,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Paged Relation Cache: serving many requests whose histories live in pages.
  *
  * The cache of Sec. 5.3 / Appendix A.5 (the P2 rows and information states I~

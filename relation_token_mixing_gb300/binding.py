@@ -75,6 +75,20 @@ class Paged(ctypes.Structure):
     ]
 
 
+class LinearPacked(ctypes.Structure):
+    """Mirror of relation_linear_packed_t."""
+
+    _fields_ = [
+        ("R", ctypes.c_int64),
+        ("N", ctypes.c_int64),
+        ("H", ctypes.c_int64),
+        ("d_h", ctypes.c_int64),
+        ("states", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("tau_S", ctypes.c_float),
+    ]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -152,6 +166,14 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.relation_linear_bwd.argtypes = [ctypes.POINTER(Problem), _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                             ctypes.c_int, _VP, ctypes.c_size_t, _VP]
         lib.relation_linear_bwd.restype = ctypes.c_int
+        _LP = ctypes.POINTER(LinearPacked)
+        lib.relation_linear_step.argtypes = [_LP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]
+        lib.relation_linear_step.restype = ctypes.c_int
+        lib.relation_linear_packed_workspace_bytes.argtypes = [_LP, ctypes.c_int]
+        lib.relation_linear_packed_workspace_bytes.restype = ctypes.c_size_t
+        lib.relation_linear_packed_fwd.argtypes = [_LP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int, _VP, _VP, _VP,
+                                                   _VP, _VP, ctypes.c_size_t, _VP]
+        lib.relation_linear_packed_fwd.restype = ctypes.c_int
         _PP = ctypes.POINTER(Paged)
         lib.relation_paged_plan.argtypes = [_PP, _VP, _VP, _VP, ctypes.c_size_t, _VP, _VP, _VP, _VP, _VP, _VP]
         lib.relation_paged_plan.restype = ctypes.c_int
@@ -421,6 +443,26 @@ def linear_gate_fwd_bwd(P1, P2, I, R, A_log, dt_bias, dY, tau_S: float, layout: 
     return Y, dP1, dP2, dI, dR, dA, dB
 
 
+def relation_linear_step(prob: LinearPacked, P1, P2, I, G, A_log, dt_bias, states, slots_in, slots_out, Y,
+                         stream=None) -> None:
+    _check(load().relation_linear_step(ctypes.byref(prob), _ptr(P1), _ptr(P2), _ptr(I), _ptr(G), _ptr(A_log),
+                                       _ptr(dt_bias), _ptr(states), _ptr(slots_in), _ptr(slots_out), _ptr(Y),
+                                       _stream_ptr(stream)), "relation_linear_step")
+
+
+def relation_linear_packed_workspace_bytes(prob: LinearPacked, max_fresh: int) -> int:
+    return int(load().relation_linear_packed_workspace_bytes(ctypes.byref(prob), int(max_fresh)))
+
+
+def relation_linear_packed_fwd(prob: LinearPacked, P1, P2, I, G, A_log, dt_bias, starts, max_fresh, states, slots_in,
+                               slots_out, Y, workspace, stream=None) -> None:
+    _check(load().relation_linear_packed_fwd(ctypes.byref(prob), _ptr(P1), _ptr(P2), _ptr(I), _ptr(G), _ptr(A_log),
+                                             _ptr(dt_bias), _ptr(starts), max_fresh, _ptr(states), _ptr(slots_in),
+                                             _ptr(slots_out), _ptr(Y), _ptr(workspace),
+                                             0 if workspace is None else workspace.nbytes, _stream_ptr(stream)),
+           "relation_linear_packed_fwd")
+
+
 def relation_paged_plan(prob: Paged, cached, fresh, free_pages, block_table, starts, slots, positions, used,
                         stream=None) -> None:
     _check(load().relation_paged_plan(ctypes.byref(prob), _ptr(cached), _ptr(fresh), _ptr(free_pages),
@@ -564,6 +606,90 @@ def bwd(P1, P2, V, Y, L, dY, tau_S: float, lam: float, causal: bool = True, stre
         workspace = torch.empty((nbytes + 3) // 4, dtype=torch.float32, device=P1.device)
     relation_bwd(prob, P1, P2, V, Y, L, dY, dP1, dP2, dV, dlam, workspace, stream)
     return dP1, dP2, dV, dlam
+
+
+# ------------------------------------------- Linear Relation over a pool of states
+def linear_states(states: int, H: int, d_h: int, device="cuda") -> torch.Tensor:
+    """A pool of states [states, H, d_h, d_h] float32, zeroed."""
+    return torch.zeros(states, H, d_h, d_h, dtype=torch.float32, device=device)
+
+
+def linear_packed_for(P1, states, R: int, tau_S: float) -> LinearPacked:
+    """Problem for packed tensors [N, H, d_h] (P1: one of them) and a pool of states."""
+    N, H, d = P1.shape
+    if P1.dtype not in _DTYPE_CODES:
+        raise ValueError(f"unsupported dtype {P1.dtype}")
+    if states.dtype is not torch.float32 or states.shape[1:] != (H, d, d):
+        raise ValueError("states are [states, H, d_h, d_h] of torch.float32")
+    return LinearPacked(R, N, H, d, states.shape[0], _DTYPE_CODES[P1.dtype], tau_S)
+
+
+def _on_current_device(*tensors) -> None:
+    """The library launches on the current device: tensors of another are refused."""
+    device = tensors[0].device
+    for x in tensors:
+        if x is not None and x.device != device:
+            raise ValueError("Relation tensors must be on one device")
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError("Relation tensors must be on the current device")
+
+
+def _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias):
+    _on_current_device(P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias)
+    if P2.shape != P1.shape or I.shape != P1.shape or G.shape != P1.shape:
+        raise ValueError("P1, P2, I and G are [N, H, d_h]")
+    if P2.dtype is not P1.dtype or I.dtype is not P1.dtype or G.dtype is not torch.float32:
+        raise ValueError(f"P2 and I are {P1.dtype}, as P1, and G is torch.float32")
+    if not (slots_in.dtype is slots_out.dtype is _I32) or slots_in.numel() != prob.R or slots_out.numel() != prob.R:
+        raise ValueError("slots_in and slots_out are [R] of torch.int32")
+    if (A_log is None) != (dt_bias is None):
+        raise ValueError("A_log and dt_bias are given both or neither")
+    for x in (A_log, dt_bias):
+        if x is not None and (x.dtype is not torch.float32 or x.shape != (prob.H, prob.d_h)):
+            raise ValueError("A_log and dt_bias are [H, d_h] of torch.float32")
+
+
+def _like_on(x, Y, stream):
+    """Y, or a tensor like x from the stream that the kernels run on, marked as used by the caller's stream."""
+    if Y is None:
+        with torch.cuda.stream(stream):  # None: the current one
+            Y = torch.empty_like(x)
+        if stream is not None:
+            Y.record_stream(torch.cuda.current_stream())
+    elif Y.shape != x.shape or Y.dtype is not x.dtype:
+        raise ValueError("Y is like P1")
+    return Y
+
+
+def linear_step(P1, P2, I, G, states, slots_in, slots_out, tau_S: float, A_log=None, dt_bias=None, Y=None, stream=None):
+    """Linear Relation of one new token per request, rows [R, H, d_h], from and to slots of a pool of states
+    (slots_in, slots_out [R] int32; negative: no state yet, not kept); returns Y.  With A_log and dt_bias [H, d_h] G
+    holds the retention gate's input."""
+    prob = linear_packed_for(P1, states, slots_in.numel(), tau_S)
+    _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias)
+    Y = _like_on(P1, Y, stream)
+    relation_linear_step(prob, P1, P2, I, G, A_log, dt_bias, states, slots_in, slots_out, Y, stream)
+    return Y
+
+
+def linear_packed_fwd(P1, P2, I, G, starts, states, slots_in, slots_out, max_fresh: int, tau_S: float, A_log=None,
+                      dt_bias=None, Y=None, workspace=None, stream=None):
+    """Linear Relation of packed requests of any lengths (starts [R + 1] int32) from and to slots of a pool of states;
+    returns Y.  max_fresh: a bound of any request's new tokens (0: none known).  Y and workspace are allocated when not
+    given, from the stream that the kernels run on."""
+    prob = linear_packed_for(P1, states, slots_in.numel(), tau_S)
+    _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias)
+    if starts.dtype is not _I32 or starts.numel() != prob.R + 1:
+        raise ValueError("starts is [R + 1] of torch.int32")
+    Y = _like_on(P1, Y, stream)
+    if workspace is None:
+        n = relation_linear_packed_workspace_bytes(prob, max_fresh)
+        if n:  # freed on return: the stream's own memory goes to its next work only, which runs after the kernels
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(n, dtype=torch.uint8, device=P1.device)
+    relation_linear_packed_fwd(prob, P1, P2, I, G, A_log, dt_bias, starts, max_fresh, states, slots_in, slots_out, Y,
+                               workspace, stream)
+    return Y
 
 
 # ------------------------------------------------------- paged Relation Cache

@@ -4,34 +4,11 @@
 #include <stdint.h>
 
 #include "api_internal.h"
+#include "api_spans.h"
 #include "paged.h"
 
 namespace relation {
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-struct Span {
-    const void* p;
-    size_t n;
-};
-
-bool overlap(const Span& a, const Span& b) {
-    if (a.p == nullptr || b.p == nullptr || a.n == 0 || b.n == 0) return false;
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-    return x < y + b.n && y < x + a.n;
-}
-
-// Every output apart from every input and every other output.
-bool disjoint(const Span* in, int n_in, const Span* out, int n_out) {
-    for (int o = 0; o < n_out; ++o) {
-        for (int i = 0; i < n_in; ++i)
-            if (overlap(out[o], in[i])) return false;
-        for (int q = o + 1; q < n_out; ++q)
-            if (overlap(out[o], out[q])) return false;
-    }
-    return true;
-}
 
 size_t elem(const relation_paged_t* p) { return p->dtype == RELATION_BF16 ? 2 : 4; }
 
@@ -125,8 +102,8 @@ relation_status_t relation_paged_plan(const relation_paged_t* p, const int32_t* 
     for (const void* x : {(const void*)block_table, (const void*)slots, (const void*)positions})
         if (!aligned(x, 16)) return RELATION_ERR_MISALIGNED;
     const size_t R = (size_t)p->R, N = (size_t)p->N;
-    const Span in[] = {{cached, R * 4}, {fresh, R * 4}, {free_pages, free_count * 4}};
-    const Span out[] = {{block_table, R * (size_t)p->table_width * 4}, {starts, (R + 1) * 4}, {slots, N * 8},
+    const ByteSpan in[] = {{cached, R * 4}, {fresh, R * 4}, {free_pages, free_count * 4}};
+    const ByteSpan out[] = {{block_table, R * (size_t)p->table_width * 4}, {starts, (R + 1) * 4}, {slots, N * 8},
                         {positions, N * 4}, {used, 4}};
     if (!disjoint(in, 3, out, 5)) return RELATION_ERR_INVALID_ARGUMENT;
     unsigned int* status;
@@ -156,9 +133,9 @@ relation_status_t relation_paged_store(const relation_paged_t* p, const void* X1
         if (!aligned(x, 16)) return RELATION_ERR_MISALIGNED;
     if (!aligned(theta, 4)) return RELATION_ERR_MISALIGNED;
     const size_t N = (size_t)p->N, hb = heads_bytes(p, p->H), gb = heads_bytes(p, p->G), cb = pages_bytes(p);
-    const Span in[] = {{X1, hb}, {X2, gb}, {I, gb}, {positions, N * 4}, {slots, N * 8},
+    const ByteSpan in[] = {{X1, hb}, {X2, gb}, {I, gb}, {positions, N * 4}, {slots, N * 8},
                        {theta, theta ? (size_t)(p->G / 2) * 4 : 0}};
-    const Span out[] = {{P1, hb}, {P2_pages, cb}, {I_pages, cb}};
+    const ByteSpan out[] = {{P1, hb}, {P2_pages, cb}, {I_pages, cb}};
     if (!disjoint(in, 6, out, 3)) return RELATION_ERR_INVALID_ARGUMENT;
     unsigned int* status;
     int sms;
@@ -217,9 +194,9 @@ relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, 
                    status, sms};
     const size_t need = paged_fwd_workspace(pp, bf16, a.max_fresh, sms);
     if (workspace_bytes < need) return RELATION_ERR_WORKSPACE_TOO_SMALL;
-    const Span in[] = {{P1, hb}, {P2_pages, cb}, {I_pages, cb}, {block_table, R * (size_t)p->table_width * 4},
+    const ByteSpan in[] = {{P1, hb}, {P2_pages, cb}, {I_pages, cb}, {block_table, R * (size_t)p->table_width * 4},
                        {starts, (R + 1) * 4}, {cached, R * 4}};
-    const Span out[] = {{Y, hb}, {L, L ? N * (size_t)p->H * 4 : 0}, {workspace, need}};
+    const ByteSpan out[] = {{Y, hb}, {L, L ? N * (size_t)p->H * 4 : 0}, {workspace, need}};
     if (!disjoint(in, 6, out, 3)) return RELATION_ERR_INVALID_ARGUMENT;
     int launches = 0;
     st = from_cuda(launch_paged_fwd(pp, bf16, a, &launches, static_cast<cudaStream_t>(stream)));

@@ -1,0 +1,268 @@
+"""Linear Relation over a pool of states on the GPU against the recurrence in 64 bits: packed requests of any lengths,
+single tokens, slots of every kind, strong and weak retention, streams, graphs and values that cannot be followed."""
+import numpy as np
+import pytest
+import torch
+
+from linear_pool_cases import TAU, check, inputs, on_gpu, packed
+from relation_token_mixing_gb300 import binding as rb
+
+pytestmark = pytest.mark.gpu
+
+
+def _ok():
+    torch.cuda.synchronize()
+    assert rb.relation_check_device_status() == 0
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("H,d", [(1, 64), (3, 60), (8, 48), (16, 64)])
+def test_single_tokens(H, d, gate):
+    x = inputs([1] * 9, H, d, gate, seed=H)
+    c = on_gpu(x)
+    Y = rb.linear_step(c["P1"], c["P2"], c["I"], c["G"], c["states"], c["slots_in"], c["slots_out"], TAU, c["A_log"],
+                       c["dt_bias"])
+    _ok()
+    assert rb.relation_last_launch_count() == 1
+    check(x, Y, c["states"], chunked=False)
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("H,d", [(1, 64), (3, 60), (2, 48)])
+def test_few_tokens(H, d, gate):
+    x = inputs([0, 1, 2, 5, 16, 15, 3, 0], H, d, gate, seed=7)
+    c = on_gpu(x)
+    Y = packed(c, max_fresh=16)
+    _ok()
+    assert rb.relation_last_launch_count() == 1
+    check(x, Y, c["states"], chunked=False)
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("H,d", [(1, 64), (3, 60), (2, 48)])
+@pytest.mark.parametrize("lengths", [[17], [64], [65, 63], [1, 0, 17, 128, 5, 200, 64, 2], [33, 16, 250, 31]])
+def test_requests_of_one_stretch(lengths, H, d, gate):
+    x = inputs(lengths, H, d, gate, seed=len(lengths))
+    c = on_gpu(x)
+    Y = packed(c, max_fresh=max(lengths))
+    _ok()
+    assert rb.relation_last_launch_count() == 2
+    check(x, Y, c["states"])
+
+
+@pytest.mark.parametrize("gate", [False, True])
+@pytest.mark.parametrize("H,d", [(2, 64), (3, 60), (1, 48)])
+@pytest.mark.parametrize("lengths,bound", [([257], 257), ([1100, 17, 300, 1, 0, 256], 0), ([3, 512, 513, 255, 70], 1000)])
+def test_requests_of_many_segments(lengths, bound, H, d, gate):
+    x = inputs(lengths, H, d, gate, seed=11)
+    c = on_gpu(x)
+    Y = packed(c, max_fresh=bound)
+    _ok()
+    assert rb.relation_last_launch_count() == 4
+    check(x, Y, c["states"])
+
+
+@pytest.mark.parametrize("lengths", [[40, 100, 64], [300, 20, 64]])
+@pytest.mark.parametrize("kind", ["strong", "one_channel", "resets", "none", "growing", "lowest", "ragged"])
+def test_retention(kind, lengths):
+    """Factors that leave the range of a chunk with one reference, retention of nothing and of everything."""
+    x = inputs(lengths, 2, 64, seed=5)
+    N = x["G"].shape[0]
+    if kind == "strong":
+        x["G"] *= 20.0 / x["G"].abs().mean()
+    elif kind == "one_channel":
+        x["G"][:, 1, 13] = -9.0
+    elif kind == "resets":
+        x["G"][::23] = -1e9
+    elif kind == "none":
+        x["G"].zero_()
+    elif kind == "growing":
+        x["G"] = 0.002 * torch.rand(x["G"].shape, generator=torch.Generator().manual_seed(1))
+    elif kind == "lowest":
+        x["G"][N // 2:] = torch.finfo(torch.float32).min
+    else:  # strong in some chunks only
+        x["G"][: N // 2] *= 40.0
+    c = on_gpu(x)
+    Y = packed(c, max_fresh=max(lengths))
+    _ok()
+    check(x, Y, c["states"])
+
+
+def test_zero_rows_and_large_states():
+    x = inputs([70, 4, 20], 2, 60, seed=3)
+    x["P1"][3] = 0
+    x["P2"][10:30] = 0
+    x["I"][40:] *= 1000
+    x["states"] *= 50
+    c = on_gpu(x)
+    Y = packed(c)
+    _ok()
+    check(x, Y, c["states"])
+
+
+def test_slots_in_place_shared_and_not_kept():
+    """Two requests go on from one slot, one in place, one is new, one's state is not kept, one has no new tokens."""
+    x = inputs([20, 3, 70, 1, 0, 0], 2, 64, slots=([0, 0, 2, -1, 5, -1], [1, 4, 2, -1, 3, 6]), seed=9)
+    before = x["states"].clone()
+    c = on_gpu(x)
+    Y = packed(c)
+    _ok()
+    check(x, Y, c["states"])
+    assert torch.equal(c["states"][3].cpu(), before[5]) and (c["states"][6] == 0).all()
+    for k in (0, 5):  # read, not written
+        assert torch.equal(c["states"][k].cpu(), before[k])
+
+
+def test_rows_behind_the_last_request_stay():
+    x = inputs([30, 2, 18], 3, 60, spare=9, seed=2)
+    x["P1"][-9:], x["G"][-9:] = float("nan"), float("nan")
+    c = on_gpu(x)
+    Y = torch.full_like(c["P1"], 7.0)
+    packed(c, Y=Y)
+    _ok()
+    assert (Y[50:] == 7.0).all()
+    for k in ("P1", "G"):
+        x[k][-9:] = 0
+    check(x, Y, c["states"])
+
+
+def test_a_request_goes_on_as_if_it_had_never_stopped():
+    """A prompt in pieces, from slot to slot, in every split between the kernels."""
+    whole = inputs([400], 2, 64, True, slots=([-1], [0]), seed=4)
+    cw = on_gpu(whole)
+    Yw = packed(cw)
+    pool = torch.zeros(2, 2, 64, 64, device="cuda")
+    at, ys = 0, []
+    for n in (1, 100, 16, 17, 2, 264):
+        c = dict(cw, starts=torch.tensor([0, n], dtype=torch.int32, device="cuda"), states=pool)
+        for k in ("P1", "P2", "I", "G"):
+            c[k] = cw[k][at: at + n].contiguous()
+        c["slots_in"] = torch.tensor([-1 if at == 0 else 1], dtype=torch.int32, device="cuda")
+        c["slots_out"] = torch.tensor([1], dtype=torch.int32, device="cuda")
+        ys.append(packed(c))
+        at += n
+    _ok()
+    check(whole, Yw, cw["states"])
+    whole["states"] = torch.zeros(1, 2, 64, 64)
+    check(whole, torch.cat(ys), pool[1:])
+
+
+def test_same_results_from_run_to_run():
+    x = on_gpu(inputs([700, 40, 1, 300], 3, 60, True, seed=8))
+    first = None
+    for _ in range(4):
+        pool = x["states"].clone()
+        got = packed(dict(x, states=pool)), pool
+        if first is None:
+            first = got
+        assert torch.equal(first[0], got[0]) and torch.equal(first[1], got[1])
+    _ok()
+
+
+def test_captured_and_replayed_with_other_lengths():
+    lengths = [[300, 17, 1], [5, 290, 23], [0, 16, 302]]
+    xs = [inputs(n, 2, 64, slots=([0, 1, 2], [0, 1, 2]), seed=20 + k) for k, n in enumerate(lengths)]
+    c = on_gpu(xs[0])
+    Y = torch.empty_like(c["P1"])
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    packed(c, max_fresh=310, Y=Y, workspace=ws)  # loads the kernels
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        packed(c, max_fresh=310, Y=Y, workspace=ws)
+    for x in xs:
+        for k, t in x.items():
+            if t is not None:
+                c[k].copy_(t)
+        graph.replay()
+        _ok()
+        check(x, Y, c["states"])
+
+
+def test_on_another_stream():
+    x = inputs([300, 2, 40], 2, 64, seed=6)
+    c = on_gpu(x)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    Y = packed(c, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    _ok()
+    check(x, Y, c["states"])
+
+
+def test_calls_in_flight_over_one_workspace():
+    """Steps queued one after another, each going on from the state of the one before."""
+    x = inputs([280, 30, 1], 2, 64, slots=([0, 1, 2], [0, 1, 2]), seed=12)
+    c = on_gpu(x)
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    ys = [packed(c, workspace=ws) for _ in range(5)]
+    _ok()
+    for Y in ys:  # the same steps one at a time
+        alone = on_gpu(x)
+        assert torch.equal(packed(alone), Y)
+        check(x, Y, alone["states"])
+        x["states"] = alone["states"].cpu()
+    assert torch.equal(x["states"], c["states"].cpu())
+
+
+@pytest.mark.parametrize("what", ["past", "descending", "bound", "slot_in", "slot_out"])
+def test_values_that_cannot_be_followed_are_reported(what):
+    x = inputs([20, 3, 40], 2, 64, slots=([0, 1, 2], [3, 4, 5]), seed=13)
+    before = x["states"].clone()
+    c = on_gpu(x)
+    if what == "past":
+        c["starts"][3] = 64
+    elif what == "descending":
+        c["starts"][1], c["starts"][2] = 23, 20
+    elif what == "slot_in":
+        c["slots_in"][1] = 6
+    elif what == "slot_out":
+        c["slots_out"][1] = 1 << 30
+    Y = torch.full_like(c["P1"], 7.0)
+    packed(c, max_fresh=30 if what == "bound" else 0, Y=Y)
+    torch.cuda.synchronize()
+    assert rb.relation_check_device_status() == 1 and rb.relation_check_device_status() == 0
+    states = c["states"].cpu()
+    if what in ("past", "bound"):  # the third request is skipped, the others are not
+        assert (Y[23:] == 7.0).all() and torch.equal(states[5], before[5]) and not torch.equal(states[3], before[3])
+    elif what == "descending":
+        assert torch.equal(states[4], before[4])
+    elif what == "slot_in":  # as a new request
+        x["slots_in"][1] = -1
+        check(x, Y, c["states"])
+    else:
+        x["slots_out"][1] = -1
+        check(x, Y, c["states"])
+
+
+def test_more_requests_than_a_block_has_threads():
+    lengths = [(7 * r) % 40 if r % 50 else 300 for r in range(400)]
+    x = inputs(lengths, 1, 48, slots=(list(range(400)), list(range(400))), seed=14)
+    c = on_gpu(x)
+    Y = packed(c)
+    _ok()
+    check(x, Y, c["states"])
+
+
+def test_no_new_tokens_at_all():
+    x = inputs([0, 0], 2, 64, slots=([0, -1], [2, 1]), seed=15)
+    before = x["states"].clone()
+    c = on_gpu(x)
+    Y = packed(c)
+    _ok()
+    assert Y.shape[0] == 0
+    assert torch.equal(c["states"][2].cpu(), before[0]) and (c["states"][1] == 0).all()
+
+
+def test_agrees_with_the_dense_forward():
+    B, H, T, d = 2, 3, 333, 60
+    x = inputs([T] * B, H, d, slots=([-1] * B, list(range(B))), seed=16)
+    c = on_gpu(x)
+    Y = packed(c)
+    dense = {k: c[k].view(B, T, H, d) for k in ("P1", "P2", "I", "G")}
+    Yd, state = rb.linear_fwd(dense["P1"], dense["P2"], dense["I"], dense["G"], TAU, rb.RELATION_LAYOUT_BTHD, True)
+    _ok()
+    check(x, Y, c["states"])
+    scale = float(Yd.float().abs().max())
+    assert float((Y.view(B, T, H, d).float() - Yd.float()).abs().max()) <= 2e-2 * scale  # both within 1e-2
+    assert float((c["states"] - state).abs().max()) <= 2e-2 * float(np.abs(state.cpu().numpy()).max())
