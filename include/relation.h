@@ -600,6 +600,35 @@ relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, 
                                      size_t workspace_bytes, void* stream);
 
 /*
+ * The paged Relation Cache in 8 bits: half the bytes of the bf16 pages.
+ *
+ * A cached row x (float32 after the prologue) is kept as d_h whole numbers q_c, int8,
+ * |q_c| <= 127, and one scale s, a power of two in bfloat16: the least (2^-126 at
+ * least) with max |x_c| <= 127 s, and q_c = x_c / s rounded to nearest even.  q_c s is
+ * a bfloat16 value, so what every reader forms is exactly what is kept; it is within
+ * s / 2 of x_c.  A row with a non-finite value gets a NaN scale and reads as NaN.
+ * P2_pages, I_pages: int8 [pages, G, page_size, row] (RELATION_LAYOUT_BHTD) or
+ *   [pages, page_size, G, row] (RELATION_LAYOUT_BTHD), contiguous, row = d_h rounded up
+ *   to 16 (d_h = 60: 64; the padding is never read as data).
+ * scales: bfloat16 [pages, G, page_size, 2] or [pages, page_size, G, 2] by the same
+ *   layout, 16-byte aligned: the scale of the token's P2 row and of its I~ row.
+ * relation_paged_t as above with dtype RELATION_BF16, the packed tensors' (else
+ * RELATION_ERR_UNSUPPORTED); relation_paged_plan serves both kinds of pages.
+ *
+ * relation_paged_store_q8: relation_paged_store with the rows quantised as they are
+ *   written (P1 stays bf16; one launch).
+ * relation_paged_read_q8: rows [N, G, d_h] bf16 of slots [N], P2 and I (the mixed I~), as
+ *   the values that the pages hold; rows of negative slots are zero, and so are those of
+ *   slots past the last page, which are reported (one launch).
+ */
+relation_status_t relation_paged_store_q8(const relation_paged_t* p, const void* X1, const void* X2, const void* I,
+                                          const float* theta, int pairing, float rope_base, const int32_t* positions,
+                                          const int64_t* slots, void* P1, void* P2_pages, void* I_pages, void* scales,
+                                          void* stream);
+relation_status_t relation_paged_read_q8(const relation_paged_t* p, const int64_t* slots, const void* P2_pages,
+                                         const void* I_pages, const void* scales, void* P2, void* I, void* stream);
+
+/*
  * Reads and clears the device status word of the current device.  Call after
  * synchronising the streams used.  Returns RELATION_OK,
  * RELATION_ERR_DEVICE_TIMEOUT (a bounded wait expired; outputs of the calls

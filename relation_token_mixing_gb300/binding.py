@@ -185,6 +185,11 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.relation_paged_fwd.argtypes = [_PP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int, _VP, _VP, _VP,
                                            ctypes.c_size_t, _VP]
         lib.relation_paged_fwd.restype = ctypes.c_int
+        lib.relation_paged_store_q8.argtypes = [_PP, _VP, _VP, _VP, _VP, ctypes.c_int, ctypes.c_float, _VP, _VP, _VP, _VP,
+                                                _VP, _VP, _VP]
+        lib.relation_paged_store_q8.restype = ctypes.c_int
+        lib.relation_paged_read_q8.argtypes = [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]
+        lib.relation_paged_read_q8.restype = ctypes.c_int
         lib.relation_selftest_wait_timeout.argtypes = [ctypes.c_uint32, _VP]
         lib.relation_selftest_wait_timeout.restype = ctypes.c_int
         lib.relation_check_device_status.argtypes = []
@@ -487,6 +492,18 @@ def relation_paged_fwd(prob: Paged, P1, P2_pages, I_pages, block_table, starts, 
     _check(load().relation_paged_fwd(ctypes.byref(prob), _ptr(P1), _ptr(P2_pages), _ptr(I_pages), _ptr(block_table),
                                      _ptr(starts), _ptr(cached), max_fresh, _ptr(Y), _ptr(L), _ptr(workspace),
                                      workspace.nbytes, _stream_ptr(stream)), "relation_paged_fwd")
+
+
+def relation_paged_store_q8(prob: Paged, X1, X2, I, theta, pairing, rope_base, positions, slots, P1, P2_pages, I_pages,
+                            scales, stream=None) -> None:
+    _check(load().relation_paged_store_q8(ctypes.byref(prob), _ptr(X1), _ptr(X2), _ptr(I), _ptr(theta), pairing,
+                                          rope_base, _ptr(positions), _ptr(slots), _ptr(P1), _ptr(P2_pages),
+                                          _ptr(I_pages), _ptr(scales), _stream_ptr(stream)), "relation_paged_store_q8")
+
+
+def relation_paged_read_q8(prob: Paged, slots, P2_pages, I_pages, scales, P2, I, stream=None) -> None:
+    _check(load().relation_paged_read_q8(ctypes.byref(prob), _ptr(slots), _ptr(P2_pages), _ptr(I_pages), _ptr(scales),
+                                         _ptr(P2), _ptr(I), _stream_ptr(stream)), "relation_paged_read_q8")
 
 
 def relation_check_device_status() -> int:
@@ -796,3 +813,78 @@ def paged_fwd(P1, P2_pages, I_pages, block_table, starts, cached, max_fresh: int
             workspace = paged_workspace(prob, max_fresh, P1.device)
     relation_paged_fwd(prob, P1, P2_pages, I_pages, block_table, starts, cached, max_fresh, Y, L, workspace, stream)
     return Y, L
+
+
+# ------------------------------------------------------- paged Relation Cache in 8 bits
+def paged_row_q8(d_h: int) -> int:
+    """Bytes from one cached row to the next (rows start on 16)."""
+    return -(-d_h // 16) * 16
+
+
+def paged_pages_q8(pages: int, G: int, page_size: int, d_h: int, layout: int = RELATION_LAYOUT_BHTD, device="cuda"):
+    """8-bit page pools and their scales (P2_pages, I_pages, scales), zeroed."""
+    shape = (pages, G, page_size) if layout == RELATION_LAYOUT_BHTD else (pages, page_size, G)
+    P2, I = (torch.zeros(*shape, paged_row_q8(d_h), dtype=torch.int8, device=device) for _ in range(2))
+    return P2, I, torch.zeros(*shape, 2, dtype=torch.bfloat16, device=device)
+
+
+def paged_q8_for(N: int, H: int, d_h: int, P2_pages, I_pages, scales, R: int, table_width: int, tau_S: float,
+                 lam: float, layout: int) -> Paged:
+    """Problem for N packed rows of H heads over 8-bit pages."""
+    if not (P2_pages.dtype is I_pages.dtype is torch.int8) or scales.dtype is not torch.bfloat16:
+        raise ValueError("8-bit pages are torch.int8, their scales torch.bfloat16")
+    if P2_pages.dim() != 4 or I_pages.shape != P2_pages.shape or scales.shape != (*P2_pages.shape[:3], 2):
+        raise ValueError("both page pools are alike, 4-D, and scales have two values for each of their rows")
+    if layout == RELATION_LAYOUT_BHTD:
+        P, G, page, row = P2_pages.shape
+    elif layout == RELATION_LAYOUT_BTHD:
+        P, page, G, row = P2_pages.shape
+    else:
+        raise ValueError(f"unknown layout {layout}")
+    if row != paged_row_q8(d_h):
+        raise ValueError(f"pages hold rows of {row}, heads of {d_h} need {paged_row_q8(d_h)}")
+    return Paged(R, N, H, G, d_h, P, page, table_width, RELATION_BF16, tau_S, lam, layout)
+
+
+def paged_store_q8(X1, X2, I, theta, pairing: int, rope_base: float, positions, slots, P1, P2_pages, I_pages, scales,
+                   layout: int = RELATION_LAYOUT_BHTD, stream=None) -> None:
+    """paged_store into 8-bit pages: RoPE and Givens mixing of packed new tokens, the cached rows quantised as they are
+    written, with one power of two a row (scales)."""
+    _on_current_device(X1, X2, I, theta, positions, slots, P1, P2_pages, I_pages, scales)
+    if positions.dtype is not _I32 or slots.dtype is not _I64:
+        raise ValueError("positions are torch.int32, slots torch.int64")
+    N, H, d = X1.shape
+    prob = paged_q8_for(N, H, d, P2_pages, I_pages, scales, 1, 1, 1.0, 0.0, layout)
+    if X2.shape != (N, prob.G, d) or I.shape != X2.shape or P1.shape != X1.shape or positions.numel() != N or \
+            slots.numel() != N:
+        raise ValueError("X1, P1 are [N, H, d_h], X2, I [N, G, d_h], positions, slots [N]")
+    if not (X1.dtype is X2.dtype is I.dtype is P1.dtype is torch.bfloat16):
+        raise ValueError("X1, X2, I and P1 are torch.bfloat16")
+    if theta is not None and (theta.dtype is not torch.float32 or theta.numel() != prob.G // 2):
+        raise ValueError("theta is [G / 2] of torch.float32")
+    relation_paged_store_q8(prob, X1, X2, I, theta, pairing, rope_base, positions, slots, P1, P2_pages, I_pages, scales,
+                            stream)
+
+
+def paged_read_q8(slots, P2_pages, I_pages, scales, d_h: int, P2=None, I=None, layout: int = RELATION_LAYOUT_BHTD,
+                  stream=None):
+    """The rows (P2, I) [N, G, d_h] bf16 that 8-bit pages hold in some slots [N] int64 (negative: zeros); allocated when
+    not given."""
+    _on_current_device(slots, P2_pages, I_pages, scales, P2, I)
+    N = slots.numel()
+    if slots.dtype is not _I64:
+        raise ValueError("slots are torch.int64")
+    prob = paged_q8_for(N, 1, d_h, P2_pages, I_pages, scales, 1, 1, 1.0, 0.0, layout)
+    prob.H = prob.G
+    rows = []
+    for x in (P2, I):
+        if x is None:
+            with torch.cuda.stream(stream):  # None: the current one
+                x = torch.empty(N, prob.G, d_h, dtype=torch.bfloat16, device=slots.device)
+            if stream is not None:
+                x.record_stream(torch.cuda.current_stream())
+        elif x.shape != (N, prob.G, d_h) or x.dtype is not torch.bfloat16:
+            raise ValueError("P2 and I are [N, G, d_h] of torch.bfloat16")
+        rows.append(x)
+    relation_paged_read_q8(prob, slots, P2_pages, I_pages, scales, *rows, stream)
+    return tuple(rows)

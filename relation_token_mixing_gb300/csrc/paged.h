@@ -22,10 +22,13 @@ struct PagedProblem {
     int layout;
 };
 
-// Element offset of a cached row: token `off` of a page, cache head g.
+// A cached row among the pool's: token `off` of a page, cache head g.
+__host__ __device__ __forceinline__ size_t page_row_index(const PagedProblem& pp, int64_t page, int off, int g) {
+    return (size_t)(pp.layout == 0 ? (page * pp.G + g) * pp.page + off : (page * pp.page + off) * pp.G + g);
+}
+// Its element offset.
 __host__ __device__ __forceinline__ size_t page_row_offset(const PagedProblem& pp, int64_t page, int off, int g) {
-    const int64_t r = pp.layout == 0 ? (page * pp.G + g) * pp.page + off : (page * pp.page + off) * pp.G + g;
-    return (size_t)r * (size_t)pp.row;
+    return page_row_index(pp, page, off, g) * (size_t)pp.row;
 }
 
 // Requests the forward's schedule holds in shared memory.
@@ -39,6 +42,15 @@ cudaError_t launch_paged_store(const PagedProblem& pp, bool bf16, const void* X1
                                const float* theta, int pairing, const RopeTable& tab, const int* positions,
                                const int64_t* slots, void* P1, void* P2_pages, void* I_pages, unsigned int* status,
                                int num_sms, cudaStream_t s);
+
+// 8-bit pages (paged_q8_store.cu): rows of pp.row bytes, scales [.., 2] bf16 beside them.
+cudaError_t launch_paged_store_q8(const PagedProblem& pp, const void* X1, const void* X2, const void* I,
+                                  const float* theta, int pairing, const RopeTable& tab, const int* positions,
+                                  const int64_t* slots, void* P1, void* P2_pages, void* I_pages, void* scales,
+                                  unsigned int* status, int num_sms, cudaStream_t s);
+cudaError_t launch_paged_read_q8(const PagedProblem& pp, const int64_t* slots, const void* P2_pages, const void* I_pages,
+                                 const void* scales, void* P2, void* I, unsigned int* status, int num_sms,
+                                 cudaStream_t s);
 
 struct PagedFwdArgs {
     const void *P1, *P2_pages, *I_pages;

@@ -67,6 +67,37 @@ PagedProblem paged_problem(const relation_paged_t* p) {
     return pp;
 }
 
+// 8-bit pages: rows of bytes, which start on 16.
+int64_t row_bytes_q8(const relation_paged_t* p) { return (p->d_h + 15) / 16 * 16; }
+size_t pages_bytes_q8(const relation_paged_t* p) {
+    return (size_t)p->pages * (size_t)p->page_size * (size_t)p->G * (size_t)row_bytes_q8(p);
+}
+size_t scales_bytes(const relation_paged_t* p) {
+    return (size_t)p->pages * (size_t)p->page_size * (size_t)p->G * 4;
+}
+relation_status_t check_q8(const relation_paged_t* p) {
+    const relation_status_t st = check_paged(p);
+    return st == RELATION_OK && p->dtype != RELATION_BF16 ? RELATION_ERR_UNSUPPORTED : st;
+}
+PagedProblem paged_problem_q8(const relation_paged_t* p) {
+    PagedProblem pp = paged_problem(p);
+    pp.row = (int)row_bytes_q8(p);
+    return pp;
+}
+
+// The last table made on a thread is kept: a program has one (d_h, base).
+const RopeTable& kept_rope_table(int d, float base) {
+    static thread_local RopeTable tab{};
+    static thread_local int tab_d = 0;
+    static thread_local float tab_base = 0.f;
+    if (tab_d != d || tab_base != base) {
+        tab = rope_table(d, base);
+        tab_d = d;
+        tab_base = base;
+    }
+    return tab;
+}
+
 relation_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? RELATION_OK : RELATION_ERR_CUDA; }
 
 // The bound the forward works with: max_fresh, or N when none is known.
@@ -140,18 +171,69 @@ relation_status_t relation_paged_store(const relation_paged_t* p, const void* X1
     unsigned int* status;
     int sms;
     if ((st = api_device(&status, &sms)) != RELATION_OK) return st;
-    // The last table made on this thread is kept: a program has one (d_h, base).
-    static thread_local RopeTable tab{};
-    static thread_local int tab_d = 0;
-    static thread_local float tab_base = 0.f;
-    if (tab_d != (int)p->d_h || tab_base != rope_base) {
-        tab = rope_table((int)p->d_h, rope_base);
-        tab_d = (int)p->d_h;
-        tab_base = rope_base;
-    }
+    const RopeTable& tab = kept_rope_table((int)p->d_h, rope_base);
     st = from_cuda(launch_paged_store(paged_problem(p), p->dtype == RELATION_BF16, X1, X2, I, theta, pairing, tab,
                                       positions, slots, P1, P2_pages, I_pages, status, sms,
                                       static_cast<cudaStream_t>(stream)));
+    if (st == RELATION_OK) api_set_launches(1);
+    return st;
+}
+
+relation_status_t relation_paged_store_q8(const relation_paged_t* p, const void* X1, const void* X2, const void* I,
+                                          const float* theta, int pairing, float rope_base, const int32_t* positions,
+                                          const int64_t* slots, void* P1, void* P2_pages, void* I_pages, void* scales,
+                                          void* stream) {
+    relation_status_t st = check_q8(p);
+    if (st != RELATION_OK) return st;
+    if ((pairing != 0 && pairing != 1) || !isfinite(rope_base) || (theta != nullptr && p->G % 2 != 0))
+        return RELATION_ERR_INVALID_ARGUMENT;
+    if (p->N == 0) {
+        api_set_launches(0);
+        return RELATION_OK;
+    }
+    const void* ptrs[] = {X1, X2, I, positions, slots, P1, P2_pages, I_pages, scales};
+    for (const void* x : ptrs)
+        if (x == nullptr) return RELATION_ERR_INVALID_ARGUMENT;
+    for (const void* x : ptrs)
+        if (!aligned(x, 16)) return RELATION_ERR_MISALIGNED;
+    if (!aligned(theta, 4)) return RELATION_ERR_MISALIGNED;
+    const size_t N = (size_t)p->N, hb = heads_bytes(p, p->H), gb = heads_bytes(p, p->G), cb = pages_bytes_q8(p);
+    const ByteSpan in[] = {{X1, hb}, {X2, gb}, {I, gb}, {positions, N * 4}, {slots, N * 8},
+                           {theta, theta ? (size_t)(p->G / 2) * 4 : 0}};
+    const ByteSpan out[] = {{P1, hb}, {P2_pages, cb}, {I_pages, cb}, {scales, scales_bytes(p)}};
+    if (!disjoint(in, 6, out, 4)) return RELATION_ERR_INVALID_ARGUMENT;
+    unsigned int* status;
+    int sms;
+    if ((st = api_device(&status, &sms)) != RELATION_OK) return st;
+    st = from_cuda(launch_paged_store_q8(paged_problem_q8(p), X1, X2, I, theta, pairing,
+                                         kept_rope_table((int)p->d_h, rope_base), positions, slots, P1, P2_pages,
+                                         I_pages, scales, status, sms, static_cast<cudaStream_t>(stream)));
+    if (st == RELATION_OK) api_set_launches(1);
+    return st;
+}
+
+relation_status_t relation_paged_read_q8(const relation_paged_t* p, const int64_t* slots, const void* P2_pages,
+                                         const void* I_pages, const void* scales, void* P2, void* I, void* stream) {
+    relation_status_t st = check_q8(p);
+    if (st != RELATION_OK) return st;
+    if (p->N == 0) {
+        api_set_launches(0);
+        return RELATION_OK;
+    }
+    const void* ptrs[] = {slots, P2_pages, I_pages, scales, P2, I};
+    for (const void* x : ptrs)
+        if (x == nullptr) return RELATION_ERR_INVALID_ARGUMENT;
+    for (const void* x : ptrs)
+        if (!aligned(x, 16)) return RELATION_ERR_MISALIGNED;
+    const size_t N = (size_t)p->N, gb = heads_bytes(p, p->G), cb = pages_bytes_q8(p);
+    const ByteSpan in[] = {{slots, N * 8}, {P2_pages, cb}, {I_pages, cb}, {scales, scales_bytes(p)}};
+    const ByteSpan out[] = {{P2, gb}, {I, gb}};
+    if (!disjoint(in, 4, out, 2)) return RELATION_ERR_INVALID_ARGUMENT;
+    unsigned int* status;
+    int sms;
+    if ((st = api_device(&status, &sms)) != RELATION_OK) return st;
+    st = from_cuda(launch_paged_read_q8(paged_problem_q8(p), slots, P2_pages, I_pages, scales, P2, I, status, sms,
+                                        static_cast<cudaStream_t>(stream)));
     if (st == RELATION_OK) api_set_launches(1);
     return st;
 }
