@@ -620,6 +620,12 @@ relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, 
  * relation_paged_read_q8: rows [N, G, d_h] bf16 of slots [N], P2 and I (the mixed I~), as
  *   the values that the pages hold; rows of negative slots are zero, and so are those of
  *   slots past the last page, which are reported (one launch).
+ * relation_paged_fwd_q8: relation_paged_fwd over such pages, with its workspace from
+ *   relation_paged_q8_workspace_bytes, its limits, masks and launches.  P1's rows are
+ *   taken to float16 under a power of two of their own where there are few of them
+ *   (2^-25 of the row's largest value is lost), and the weights, times the scale of
+ *   their I~ row, to float16 or bfloat16; an I~ row whose scale is below 2^-64 counts
+ *   for less than that times its weight.
  */
 relation_status_t relation_paged_store_q8(const relation_paged_t* p, const void* X1, const void* X2, const void* I,
                                           const float* theta, int pairing, float rope_base, const int32_t* positions,
@@ -627,6 +633,11 @@ relation_status_t relation_paged_store_q8(const relation_paged_t* p, const void*
                                           void* stream);
 relation_status_t relation_paged_read_q8(const relation_paged_t* p, const int64_t* slots, const void* P2_pages,
                                          const void* I_pages, const void* scales, void* P2, void* I, void* stream);
+size_t relation_paged_q8_workspace_bytes(const relation_paged_t* p, int max_fresh);
+relation_status_t relation_paged_fwd_q8(const relation_paged_t* p, const void* P1, const void* P2_pages,
+                                        const void* I_pages, const void* scales, const int32_t* block_table,
+                                        const int32_t* starts, const int32_t* cached, int max_fresh, void* Y, float* L,
+                                        void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Reads and clears the device status word of the current device.  Call after

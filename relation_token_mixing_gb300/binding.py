@@ -190,6 +190,11 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.relation_paged_store_q8.restype = ctypes.c_int
         lib.relation_paged_read_q8.argtypes = [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]
         lib.relation_paged_read_q8.restype = ctypes.c_int
+        lib.relation_paged_q8_workspace_bytes.argtypes = [_PP, ctypes.c_int]
+        lib.relation_paged_q8_workspace_bytes.restype = ctypes.c_size_t
+        lib.relation_paged_fwd_q8.argtypes = [_PP, _VP, _VP, _VP, _VP, _VP, _VP, _VP, ctypes.c_int, _VP, _VP, _VP,
+                                              ctypes.c_size_t, _VP]
+        lib.relation_paged_fwd_q8.restype = ctypes.c_int
         lib.relation_selftest_wait_timeout.argtypes = [ctypes.c_uint32, _VP]
         lib.relation_selftest_wait_timeout.restype = ctypes.c_int
         lib.relation_check_device_status.argtypes = []
@@ -504,6 +509,17 @@ def relation_paged_store_q8(prob: Paged, X1, X2, I, theta, pairing, rope_base, p
 def relation_paged_read_q8(prob: Paged, slots, P2_pages, I_pages, scales, P2, I, stream=None) -> None:
     _check(load().relation_paged_read_q8(ctypes.byref(prob), _ptr(slots), _ptr(P2_pages), _ptr(I_pages), _ptr(scales),
                                          _ptr(P2), _ptr(I), _stream_ptr(stream)), "relation_paged_read_q8")
+
+
+def relation_paged_q8_workspace_bytes(prob: Paged, max_fresh: int) -> int:
+    return int(load().relation_paged_q8_workspace_bytes(ctypes.byref(prob), int(max_fresh)))
+
+
+def relation_paged_fwd_q8(prob: Paged, P1, P2_pages, I_pages, scales, block_table, starts, cached, max_fresh, Y, L,
+                          workspace, stream=None) -> None:
+    _check(load().relation_paged_fwd_q8(ctypes.byref(prob), _ptr(P1), _ptr(P2_pages), _ptr(I_pages), _ptr(scales),
+                                        _ptr(block_table), _ptr(starts), _ptr(cached), max_fresh, _ptr(Y), _ptr(L),
+                                        _ptr(workspace), workspace.nbytes, _stream_ptr(stream)), "relation_paged_fwd_q8")
 
 
 def relation_check_device_status() -> int:
@@ -888,3 +904,37 @@ def paged_read_q8(slots, P2_pages, I_pages, scales, d_h: int, P2=None, I=None, l
         rows.append(x)
     relation_paged_read_q8(prob, slots, P2_pages, I_pages, scales, *rows, stream)
     return tuple(rows)
+
+
+def paged_q8_workspace(prob: Paged, max_fresh: int, device="cuda") -> torch.Tensor:
+    """Workspace tensor for relation_paged_fwd_q8."""
+    n = relation_paged_q8_workspace_bytes(prob, max_fresh)
+    if n == 0:
+        raise ValueError("relation_paged_fwd_q8 has no workspace for this problem")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def paged_fwd_q8(P1, P2_pages, I_pages, scales, block_table, starts, cached, max_fresh: int, tau_S: float, lam: float,
+                 Y=None, L=None, workspace=None, layout: int = RELATION_LAYOUT_BHTD, stream=None):
+    """paged_fwd over 8-bit pages and their scales; returns (Y, L).  Y and workspace are allocated when not given, from
+    the stream that the kernels run on; L [N, H] float32 is filled when given."""
+    _on_current_device(P1, P2_pages, I_pages, scales, block_table, starts, cached, Y, L, workspace)
+    R, width = block_table.shape
+    N, H, d = P1.shape
+    if P1.dtype is not torch.bfloat16:
+        raise ValueError("P1 is torch.bfloat16")
+    prob = paged_q8_for(N, H, d, P2_pages, I_pages, scales, R, width, tau_S, lam, layout)
+    if not (block_table.dtype is starts.dtype is cached.dtype is _I32):
+        raise ValueError("block_table, starts and cached are torch.int32")
+    if starts.numel() != R + 1 or cached.numel() != R:
+        raise ValueError("starts is [R + 1], cached [R]")
+    if L is not None and (L.dtype is not torch.float32 or L.shape != (N, H)):
+        raise ValueError("L is [N, H] of torch.float32")
+    Y = _like_on(P1, Y, stream)
+    if workspace is None:
+        # Freed on return: the stream's own memory goes to its next work only, which runs after the kernels.
+        with torch.cuda.stream(stream):
+            workspace = paged_q8_workspace(prob, max_fresh, P1.device)
+    relation_paged_fwd_q8(prob, P1, P2_pages, I_pages, scales, block_table, starts, cached, max_fresh, Y, L, workspace,
+                          stream)
+    return Y, L

@@ -54,6 +54,7 @@ cudaError_t launch_paged_read_q8(const PagedProblem& pp, const int64_t* slots, c
 
 struct PagedFwdArgs {
     const void *P1, *P2_pages, *I_pages;
+    const void* scales;  // of 8-bit pages, else nullptr
     const int *table, *starts, *cached;
     int max_fresh;
     void* Y;
@@ -63,7 +64,7 @@ struct PagedFwdArgs {
     int num_sms;
 };
 // Workspace bytes and launches of one forward.
-size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, int max_fresh, int num_sms);
+size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, bool q8, int max_fresh, int num_sms);
 cudaError_t launch_paged_fwd(const PagedProblem& pp, bool bf16, const PagedFwdArgs& a, int* launches, cudaStream_t s);
 
 }  // namespace relation

@@ -110,6 +110,60 @@ bool rows_fit(const relation_paged_t* p, int max_fresh) {
     return (int64_t)fresh_bound(p, max_fresh) * (p->H / p->G) <= (int64_t)INT32_MAX - 255;
 }
 
+size_t fwd_workspace_bytes(const relation_paged_t* p, bool q8, int max_fresh) {
+    const relation_status_t st = q8 ? check_q8(p) : check_paged(p);
+    if (st != RELATION_OK || max_fresh < 0 || p->R > kPagedMaxRequests || !rows_fit(p, max_fresh)) return 0;
+    unsigned int* status;
+    int sms;
+    if (api_device(&status, &sms) != RELATION_OK) return 0;
+    return paged_fwd_workspace(q8 ? paged_problem_q8(p) : paged_problem(p), p->dtype == RELATION_BF16, q8,
+                               fresh_bound(p, max_fresh), sms);
+}
+
+// Both kinds of pages: scales == nullptr, with q8 unset, for the packed tensors' own type.
+relation_status_t run_fwd(const relation_paged_t* p, bool q8, const void* P1, const void* P2_pages,
+                          const void* I_pages, const void* scales, const int32_t* block_table, const int32_t* starts,
+                          const int32_t* cached, int max_fresh, void* Y, float* L, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+    relation_status_t st = q8 ? check_q8(p) : check_paged(p);
+    if (st != RELATION_OK) return st;
+    if (p->R > kPagedMaxRequests) return RELATION_ERR_UNSUPPORTED;
+    if (max_fresh < 0) return RELATION_ERR_INVALID_ARGUMENT;
+    if (!rows_fit(p, max_fresh)) return RELATION_ERR_UNSUPPORTED;
+    if (p->N == 0) {
+        api_set_launches(0);
+        return RELATION_OK;
+    }
+    const void* ptrs[] = {P1, P2_pages, I_pages, block_table, starts, cached, Y, workspace};
+    for (const void* x : ptrs)
+        if (x == nullptr) return RELATION_ERR_INVALID_ARGUMENT;
+    for (const void* x : {P1, P2_pages, I_pages, (const void*)block_table, (const void*)Y, (const void*)workspace})
+        if (!aligned(x, 16)) return RELATION_ERR_MISALIGNED;
+    if (q8 && scales == nullptr) return RELATION_ERR_INVALID_ARGUMENT;
+    if (!aligned(scales, 16)) return RELATION_ERR_MISALIGNED;
+    for (const void* x : {(const void*)starts, (const void*)cached, (const void*)L})
+        if (!aligned(x, 4)) return RELATION_ERR_MISALIGNED;
+    const size_t N = (size_t)p->N, R = (size_t)p->R, hb = heads_bytes(p, p->H),
+                 cb = q8 ? pages_bytes_q8(p) : pages_bytes(p);
+    unsigned int* status;
+    int sms;
+    if ((st = api_device(&status, &sms)) != RELATION_OK) return st;
+    const PagedProblem pp = q8 ? paged_problem_q8(p) : paged_problem(p);
+    const bool bf16 = p->dtype == RELATION_BF16;
+    PagedFwdArgs a{P1, P2_pages, I_pages, scales, block_table, starts, cached, fresh_bound(p, max_fresh), Y, L, workspace,
+                   status, sms};
+    const size_t need = paged_fwd_workspace(pp, bf16, q8, a.max_fresh, sms);
+    if (workspace_bytes < need) return RELATION_ERR_WORKSPACE_TOO_SMALL;
+    const ByteSpan in[] = {{P1, hb}, {P2_pages, cb}, {I_pages, cb}, {block_table, R * (size_t)p->table_width * 4},
+                           {starts, (R + 1) * 4}, {cached, R * 4}, {scales, q8 ? scales_bytes(p) : 0}};
+    const ByteSpan out[] = {{Y, hb}, {L, L ? N * (size_t)p->H * 4 : 0}, {workspace, need}};
+    if (!disjoint(in, 7, out, 3)) return RELATION_ERR_INVALID_ARGUMENT;
+    int launches = 0;
+    st = from_cuda(launch_paged_fwd(pp, bf16, a, &launches, static_cast<cudaStream_t>(stream)));
+    if (st == RELATION_OK) api_set_launches(launches);
+    return st;
+}
+
 }  // namespace
 }  // namespace relation
 
@@ -239,51 +293,27 @@ relation_status_t relation_paged_read_q8(const relation_paged_t* p, const int64_
 }
 
 size_t relation_paged_workspace_bytes(const relation_paged_t* p, int max_fresh) {
-    if (check_paged(p) != RELATION_OK || max_fresh < 0 || p->R > kPagedMaxRequests || !rows_fit(p, max_fresh)) return 0;
-    unsigned int* status;
-    int sms;
-    if (api_device(&status, &sms) != RELATION_OK) return 0;
-    return paged_fwd_workspace(paged_problem(p), p->dtype == RELATION_BF16, fresh_bound(p, max_fresh), sms);
+    return fwd_workspace_bytes(p, false, max_fresh);
 }
 
 relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, const void* P2_pages,
                                      const void* I_pages, const int32_t* block_table, const int32_t* starts,
                                      const int32_t* cached, int max_fresh, void* Y, float* L, void* workspace,
                                      size_t workspace_bytes, void* stream) {
-    relation_status_t st = check_paged(p);
-    if (st != RELATION_OK) return st;
-    if (p->R > kPagedMaxRequests) return RELATION_ERR_UNSUPPORTED;
-    if (max_fresh < 0) return RELATION_ERR_INVALID_ARGUMENT;
-    if (!rows_fit(p, max_fresh)) return RELATION_ERR_UNSUPPORTED;
-    if (p->N == 0) {
-        api_set_launches(0);
-        return RELATION_OK;
-    }
-    const void* ptrs[] = {P1, P2_pages, I_pages, block_table, starts, cached, Y, workspace};
-    for (const void* x : ptrs)
-        if (x == nullptr) return RELATION_ERR_INVALID_ARGUMENT;
-    for (const void* x : {P1, P2_pages, I_pages, (const void*)block_table, (const void*)Y, (const void*)workspace})
-        if (!aligned(x, 16)) return RELATION_ERR_MISALIGNED;
-    for (const void* x : {(const void*)starts, (const void*)cached, (const void*)L})
-        if (!aligned(x, 4)) return RELATION_ERR_MISALIGNED;
-    const size_t N = (size_t)p->N, R = (size_t)p->R, hb = heads_bytes(p, p->H), cb = pages_bytes(p);
-    unsigned int* status;
-    int sms;
-    if ((st = api_device(&status, &sms)) != RELATION_OK) return st;
-    const PagedProblem pp = paged_problem(p);
-    const bool bf16 = p->dtype == RELATION_BF16;
-    PagedFwdArgs a{P1, P2_pages, I_pages, block_table, starts, cached, fresh_bound(p, max_fresh), Y, L, workspace,
-                   status, sms};
-    const size_t need = paged_fwd_workspace(pp, bf16, a.max_fresh, sms);
-    if (workspace_bytes < need) return RELATION_ERR_WORKSPACE_TOO_SMALL;
-    const ByteSpan in[] = {{P1, hb}, {P2_pages, cb}, {I_pages, cb}, {block_table, R * (size_t)p->table_width * 4},
-                       {starts, (R + 1) * 4}, {cached, R * 4}};
-    const ByteSpan out[] = {{Y, hb}, {L, L ? N * (size_t)p->H * 4 : 0}, {workspace, need}};
-    if (!disjoint(in, 6, out, 3)) return RELATION_ERR_INVALID_ARGUMENT;
-    int launches = 0;
-    st = from_cuda(launch_paged_fwd(pp, bf16, a, &launches, static_cast<cudaStream_t>(stream)));
-    if (st == RELATION_OK) api_set_launches(launches);
-    return st;
+    return run_fwd(p, false, P1, P2_pages, I_pages, nullptr, block_table, starts, cached, max_fresh, Y, L, workspace,
+                   workspace_bytes, stream);
+}
+
+size_t relation_paged_q8_workspace_bytes(const relation_paged_t* p, int max_fresh) {
+    return fwd_workspace_bytes(p, true, max_fresh);
+}
+
+relation_status_t relation_paged_fwd_q8(const relation_paged_t* p, const void* P1, const void* P2_pages,
+                                        const void* I_pages, const void* scales, const int32_t* block_table,
+                                        const int32_t* starts, const int32_t* cached, int max_fresh, void* Y, float* L,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+    return run_fwd(p, true, P1, P2_pages, I_pages, scales, block_table, starts, cached, max_fresh, Y, L, workspace,
+                   workspace_bytes, stream);
 }
 
 }  // extern "C"

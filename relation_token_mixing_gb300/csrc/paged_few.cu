@@ -54,6 +54,24 @@ cudaError_t make_page_map(CUtensorMap* map, const void* base, const PagedProblem
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The same map of 8-bit pages: boxes as wide as a row's 64 or 128 bytes, swizzled in that width.
+cudaError_t make_page_map_q8(CUtensorMap* map, const void* base, const PagedProblem& pp, int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t row = (cuuint64_t)pp.row;
+    const cuuint64_t dims[4] = {(cuuint64_t)pp.d, (cuuint64_t)pp.page, (cuuint64_t)pp.G, (cuuint64_t)pp.pages};
+    const cuuint64_t strides[3] = {pp.layout == 0 ? row : row * pp.G, pp.layout == 0 ? row * pp.page : row,
+                                   row * pp.G * pp.page};
+    const bool wide = pp.d > 64;
+    const cuuint32_t box[4] = {wide ? 128u : 64u, (cuuint32_t)box_rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              wide ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 namespace paged {
 namespace {
 
@@ -61,24 +79,27 @@ constexpr int kKeys = 32;     // keys of a stage
 constexpr int kMinTiles = 2;  // a worker's least: below that the merge costs more than it spreads
 
 // DK: 16-column steps of the head width (d = 60 reads its last 4 columns as zero).
-// NT: groups of 8 packed rows of a unit.
-template <int DK, int NT>
+// NT: groups of 8 packed rows of a unit.  Q8: 8-bit pages.
+template <int DK, int NT, bool Q8>
 struct FewCfg {
     static constexpr int kPanels = DK > 4 ? 2 : 1;  // 64-column panels
     // Workers of a block and stages of each: 192 KB in all.  128 columns and 8 rows: 4 x 3
     // (decode 32 x 32k: 268 us, 6 x 2: 278 us); 16 rows, more work a key: 6 x 2 (a mixed step
     // of 80-wide heads: 84 us, 4 x 3: 89 us).
-    static constexpr int kWarps = kPanels == 1 ? 12 : NT == 1 ? 4 : 6;
-    static constexpr int kStages = kPanels == 2 && NT == 1 ? 3 : 2;
+    static constexpr int kWarps = Q8 ? (kPanels == 1 ? 12 : NT == 1 ? 10 : 8) : kPanels == 1 ? 12 : NT == 1 ? 4 : 6;
+    static constexpr int kStages = Q8 ? (kPanels == 1 ? 3 : 2) : kPanels == 2 && NT == 1 ? 3 : 2;
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kPanelBytes = kKeys * 128;
-    static constexpr int kTensorBytes = kPanels * kPanelBytes;  // P2 or I~ of a stage
+    // A copy's rows: a panel's 128 bytes, or (Q8) all of a row's 64 or 128.
+    static constexpr int kRowBytes = Q8 ? kPanels * 64 : 128, kCopies = Q8 ? 1 : kPanels;
+    static constexpr int kPanelBytes = kKeys * kRowBytes;
+    static constexpr int kTensorBytes = kCopies * kPanelBytes;  // P2 or I~ of a stage
     static constexpr int kStageBytes = 2 * kTensorBytes;
     static constexpr int kRingBytes = kWarps * kStages * kStageBytes;
+    static constexpr int kScaleBytes = Q8 ? kWarps * kStages * kKeys * 4 : 0;  // a pair of scales a key
     static constexpr int kRows = 8 * NT, kWidth = kPanels * 64;  // of a partial slot
     static constexpr size_t kSlot = slot_floats(kRows, kWidth);
     static_assert(kSlot * 4 <= kStages * kStageBytes, "a worker's last piece takes its ring's place");
-    static int smem(int R) { return 1024 + kRingBytes + 1024 + (R * 4 + 15) / 16 * 16; }
+    static int smem(int R) { return 1024 + kRingBytes + kScaleBytes + 1024 + (R * 4 + 15) / 16 * 16; }
 };
 
 // What a worker leaves in shared memory of the unit that it begins and does not
@@ -90,7 +111,7 @@ struct FewPiece {
 };
 
 struct FewBars {
-    uint64_t full[24];  // a worker's stages one after another
+    uint64_t full[48];  // a worker's stages one after another
     int64_t sums[16];
     FewPiece begun[12], continued;
     int abort_flag;
@@ -109,6 +130,28 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
 __device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Bytes 0 and 2 of four whole numbers as a pair of f16, exactly: with the sign flipped a byte is b + 128, and
+// under f16's exponent of 1024 its low bits stand for 1024 + 128 + b.
+__device__ __forceinline__ uint32_t even_bytes_f16(uint32_t w) {
+    const uint32_t x = (w & 0x00ff00ffu) ^ 0x64806480u;
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0xe480e480u));  // - 1152
+    return r;
+}
+__device__ __forceinline__ uint32_t odd_bytes_f16(uint32_t w) { return even_bytes_f16(w >> 8); }
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 // An 8 x 8 block of 16-bit values, a lane holding columns 2 (lane % 4) and the next
 // of row lane / 4, transposed.
@@ -146,18 +189,30 @@ __device__ __forceinline__ Request few_request(const FwdView& v, int r) {
     return q;
 }
 
+// The least power of two of an 8-bit row's scale that the weights' reference follows (below): under it a row's
+// values are below 2^-57 and count for less than f16's least step.
+constexpr float kLeastScale = -64.f;
+
 // A unit has all of a request's packed rows of one cache head.
-template <int DK, int NT>
-__global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
+//
+// 8-bit pages (Q8).  The whole numbers go to the products as f16, which holds them exactly, so
+// the work a byte is a fetch by ldmatrix (of byte pairs), a masked exclusive-or and an f16 add for two.
+// The bytes of a 16-bit unit are neighbours in a row, so the columns (of P2) or channels (of I~) come in
+// another order, which P1's fragments and the output's columns follow.  P2's scale multiplies
+// the score; P1's rows are f16 under a power of two of their own.  I~'s scale s multiplies the weight
+// before it is rounded (to f16: 2^-12); so that no weight leaves f16's range, the running maximum is that of
+// R + log2 s, while the sum is of the weights themselves.
+template <int DK, int NT, bool Q8>
+__global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const __grid_constant__ FwdView v, const __nv_bfloat16* __restrict__ P1,
-                     __nv_bfloat16* __restrict__ Y, float* __restrict__ L, float* __restrict__ part,
-                     PieceMeta* __restrict__ meta) {
-    using C = FewCfg<DK, NT>;
+                     const uint32_t* __restrict__ scales, __nv_bfloat16* __restrict__ Y, float* __restrict__ L,
+                     float* __restrict__ part, PieceMeta* __restrict__ meta) {
+    using C = FewCfg<DK, NT, Q8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    FewBars* bars = reinterpret_cast<FewBars*>(smem + C::kRingBytes);
-    int* prefix = reinterpret_cast<int*>(smem + C::kRingBytes + 1024);
+    FewBars* bars = reinterpret_cast<FewBars*>(smem + C::kRingBytes + C::kScaleBytes);
+    int* prefix = reinterpret_cast<int*>(smem + C::kRingBytes + C::kScaleBytes + 1024);
     const PagedProblem& pp = v.pp;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x < C::kWarps * C::kStages) {
@@ -190,12 +245,14 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
     // ---- loads: u_ld runs ahead of the unit in hand; 32 block-table entries, one per
     // lane, are asked for as soon as the tile before has been sent for.
     FewUnit u_ld = u;
-    int need, tb0 = 0, tb = 0;
+    int need, len_ld = 0, tb0 = 0, tb = 0;
+    uint32_t* ring_scales = reinterpret_cast<uint32_t*>(smem + C::kRingBytes) + warp * C::kStages * kKeys;
     const int box = min(pp.page, kKeys);
     auto ask = [&](bool unit) {
         if (unit) {
             const Request q = few_request(v, u_ld.r);
-            need = (q.c + q.rows + pp.page_mask) >> pp.page_shift;
+            len_ld = q.c + q.rows;
+            need = (len_ld + pp.page_mask) >> pp.page_shift;
         }
         tb0 = (u_ld.j * kKeys) >> pp.page_shift;
         tb = 0;
@@ -205,18 +262,28 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
     auto send = [&](int s) {
         const int tok = u_ld.j * kKeys, k0 = tok >> pp.page_shift;
         const int parts = box < kKeys && k0 + 1 < need ? 2 : 1;  // pages of 16 tokens: two to a stage
-        const int copies = 2 * C::kPanels * parts;
-        const int which = lane % (2 * C::kPanels), half = lane / (2 * C::kPanels);
+        const int copies = 2 * C::kCopies * parts;
+        const int which = lane % (2 * C::kCopies), half = lane / (2 * C::kCopies);
         int page = __shfl_sync(0xffffffffu, tb, (k0 - tb0 + half) & 31);
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], copies * box * 128);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], copies * box * C::kRowBytes);
+        if constexpr (Q8) {  // a key's scales, a lane each; keys past the request's end count for nothing
+            const int key = tok + lane, at = key >> pp.page_shift;
+            const int of = __shfl_sync(0xffffffffu, tb, (at - tb0) & 31);
+            uint32_t* dst = ring_scales + s * kKeys + lane;
+            if (key < len_ld && (unsigned)of < (unsigned)pp.pages)
+                cp_async4(ptx::smem_u32(dst), scales + page_row_index(pp, of, key & pp.page_mask, u_ld.g));
+            else
+                *dst = 0;
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
         __syncwarp();
         if (lane < copies) {
             if ((unsigned)page >= (unsigned)pp.pages) {  // reads as zeros (the map's bound), and is reported
                 record_status(v.status, kDevBadPosition);
                 page = pp.pages;
             }
-            ptx::tma_load_4d(ring + s * C::kStageBytes + which * C::kPanelBytes + half * 2048,
-                             which >= C::kPanels ? &tm_v : &tm_k, &full[s], (which % C::kPanels) * 64,
+            ptx::tma_load_4d(ring + s * C::kStageBytes + which * C::kPanelBytes + half * 16 * C::kRowBytes,
+                             which >= C::kCopies ? &tm_v : &tm_k, &full[s], (which % C::kCopies) * 64,
                              half ? 0 : tok & pp.page_mask & ~(box - 1), u_ld.g, page);
         }
         if (++sent < hi) {
@@ -226,15 +293,19 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
         }
     };
     ask(true);
-    for (int s = 0; s < C::kStages && sent < hi; ++s) send(s);
+    for (int s = 0; s < C::kStages; ++s) {
+        if (sent < hi) send(s);
+        else if constexpr (Q8) asm volatile("cp.async.commit_group;" ::: "memory");  // a group a stage, always
+    }
 
     Request rq;
     int j_begin = u.j, len = 0, nt_used = NT;
     // A lane holds packed rows 8 n + 2 (lane % 4) and the next one, of keys lane / 4 (+ 8).
     uint32_t qf[NT][DK][2];
-    float o[NT][DK][4], m[NT][2], l[NT][2], corr[NT][2];
+    float o[NT][DK][4], m[NT][2], l[NT][2], corr[NT][2], row_scale[NT][2];
     int pos[NT][2];
     const int key0 = lane >> 2, col0 = 2 * (lane & 3);
+    const float c_half = 0.5f * pp.inv_sqrt_d, c_self = c_half / pp.tau_S, inv_tau = 1.f / pp.tau_S;
     auto begin_unit = [&]() {
         rq = few_request(v, u.r);
         len = rq.c + rq.rows;
@@ -245,13 +316,43 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
             const int rho = min(8 * n + key0, rq.rows - 1), t = pp.by_group.div(rho);
             const __nv_bfloat16* q =
                 P1 + ((size_t)(rq.first + t) * pp.H + u.g * pp.group + (rho - t * pp.group)) * pp.d;
+            if constexpr (Q8) {
+                // Columns 16 ks + 4 (lane % 4) and the next three; the row in f16 under 2^-k that takes its largest
+                // value to [1, 2): exact but for what is 2^-15 of it.
+                uint32_t top = 0;
 #pragma unroll
-            for (int ks = 0; ks < DK; ++ks)
+                for (int ks = 0; ks < DK; ++ks) {
+                    const int c = ks * 16 + 2 * col0;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = ks * 16 + e * 8 + col0;
-                    qf[n][ks][e] = c < pp.d ? __ldg(reinterpret_cast<const uint32_t*>(q + c)) : 0u;
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t w = c < pp.d ? __ldg(reinterpret_cast<const uint32_t*>(q + c) + e) : 0u;
+                        qf[n][ks][e] = w;
+                        top = max(top, max((w << 16) & 0x7fffffffu, w & 0x7fff0000u));
+                    }
                 }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const uint32_t ex = min(max(top >> 23, 1u), 253u);
+                const float inv = __uint_as_float((254u - ex) << 23);
+#pragma unroll
+                for (int ks = 0; ks < DK; ++ks) {
+                    const uint32_t w0 = qf[n][ks][0], w1 = qf[n][ks][1];
+                    qf[n][ks][0] = pack_f16x2(__uint_as_float(w0 << 16) * inv, __uint_as_float(w1 << 16) * inv);
+                    qf[n][ks][1] =
+                        pack_f16x2(__uint_as_float(w0 & 0xffff0000u) * inv, __uint_as_float(w1 & 0xffff0000u) * inv);
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    row_scale[n][e] = __uint_as_float(__shfl_sync(0xffffffffu, ex, 4 * (col0 + e)) << 23) * c_half;
+            } else {
+#pragma unroll
+                for (int ks = 0; ks < DK; ++ks)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int c = ks * 16 + e * 8 + col0;
+                        qf[n][ks][e] = c < pp.d ? __ldg(reinterpret_cast<const uint32_t*>(q + c)) : 0u;
+                    }
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 pos[n][e] = rq.c + pp.by_group.div(min(8 * n + col0 + e, rq.rows - 1));
@@ -287,14 +388,19 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
                 const size_t yr = (size_t)(rq.first + t) * pp.H + u.g * pp.group + (rho - t * pp.group);
                 const float i0 = 1.f / l[n][0], i1 = 1.f / l[n][1];
 #pragma unroll
-                for (int dt = 0; dt < DK; ++dt)
+                for (int dt = 0; dt < DK; ++dt) {
+                    uint32_t w[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t w =
-                            turn8(ptx::pack_bf16x2(o[n][dt][2 * h] * i0, o[n][dt][2 * h + 1] * i1));
+                        w[h] = turn8(ptx::pack_bf16x2(o[n][dt][2 * h] * i0, o[n][dt][2 * h + 1] * i1));
                         const int c = dt * 16 + h * 8 + col0;
-                        if (rho < rq.rows && c < pp.d) *reinterpret_cast<uint32_t*>(Y + yr * pp.d + c) = w;
+                        if (!Q8 && rho < rq.rows && c < pp.d) *reinterpret_cast<uint32_t*>(Y + yr * pp.d + c) = w[h];
                     }
+                    const int c = dt * 16 + 2 * col0;  // even channels in w[0], odd ones in w[1]
+                    if (Q8 && rho < rq.rows && c < pp.d)
+                        *reinterpret_cast<uint2*>(Y + yr * pp.d + c) =
+                            make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[0], w[1], 0x7632));
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -305,7 +411,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
                     for (int dt = 0; dt < DK; ++dt)
 #pragma unroll
                         for (int h = 0; h < 2; ++h)
-                            slot[rho * C::kWidth + dt * 16 + h * 8 + key0] = o[n][dt][2 * h + e];
+                            slot[rho * C::kWidth + dt * 16 + (Q8 ? 2 * key0 + h : h * 8 + key0)] = o[n][dt][2 * h + e];
                     if (key0 == 0)
                         store_pair(slot + C::kRows * C::kWidth + 2 * rho,
                                    piece_max(j_begin * kKeys <= pos[n][e], m[n][e]), l[n][e]);
@@ -321,9 +427,10 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
 
     const uint32_t ring_u = ptx::smem_u32(ring);
     const int sw = lane & 7;
+    // 16-byte chunks of row r are permuted by r % 8 (rows of 128 bytes) or r / 2 % 4 (of 64); r = lane, or lane % 16.
+    const int q8_swizzle = C::kRowBytes == 128 ? lane & 7 : (lane >> 1) & 3;
     const uint32_t k_row = ((lane & 7) + ((lane >> 3) & 1) * 8) * 128, k_chunk = lane >> 4;
     const uint32_t v_row = ((lane & 7) + ((lane >> 4) & 1) * 8) * 128, v_chunk = (lane >> 3) & 1;
-    const float c_half = 0.5f * pp.inv_sqrt_d, c_self = c_half / pp.tau_S;
     for (int it = 0; it < hi - lo; ++it) {
         const int s = it % C::kStages;
         if (!ptx::mbar_wait_warp(&full[s], (it / C::kStages) & 1, abort_flag, v.status, kDevTimeoutFull)) {
@@ -333,7 +440,21 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
         }
         const uint32_t sk = ring_u + s * C::kStageBytes, sv = sk + C::kTensorBytes;
         const int tok = u.j * kKeys;
-        if (tok > len - kKeys) {  // (tok + kKeys may be 2^31)
+        float key_scale[2][2], val_scale[2][2], val_log[2][2];  // of the lane's keys 16 mt + 8 h + lane / 4
+        if constexpr (Q8) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
+            __syncwarp();
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t w = ring_scales[s * kKeys + 16 * mt + 8 * h + key0];
+                    key_scale[mt][h] = __uint_as_float(w << 16);
+                    val_scale[mt][h] = __uint_as_float(w & 0xffff0000u);
+                    val_log[mt][h] = fmaxf((float)(int)((w >> 23) & 0xffu) - 127.f, kLeastScale);
+                }
+        }
+        if (!Q8 && tok > len - kKeys) {  // (tok + kKeys may be 2^31)
             // Keys past the request's end hold whatever their page holds: weight 0 times
             // a NaN is a NaN, so they are cleared.
             if (lane >= len - tok) {
@@ -348,8 +469,26 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
             __syncwarp();
         }
         float sc[NT][2][4] = {};
+        if constexpr (Q8) {
 #pragma unroll
-        for (int ks = 0; ks < DK; ++ks)
+            for (int k2 = 0; k2 < DK; k2 += 2)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    uint32_t w[4];  // rows 0-7 and 8-15 of 16-byte chunk k2, and of the next one
+                    ldsm4(w, sk + (mt * 16 + (lane & 15)) * C::kRowBytes + (((k2 + (lane >> 4)) ^ q8_swizzle) << 4));
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        if (k2 + x >= DK) break;
+                        const uint32_t a[4] = {even_bytes_f16(w[2 * x]), even_bytes_f16(w[2 * x + 1]),
+                                               odd_bytes_f16(w[2 * x]), odd_bytes_f16(w[2 * x + 1])};
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            if (n < nt_used) mma16816_f16(sc[n][mt], a, qf[n][k2 + x][0], qf[n][k2 + x][1]);
+                    }
+                }
+        }
+#pragma unroll
+        for (int ks = 0; ks < (Q8 ? 0 : DK); ++ks)
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
                 uint32_t a[4];
@@ -369,17 +508,19 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = sc[n][mt][e], h = x * c_half;
+                    const float x = sc[n][mt][e];
+                    const float h = Q8 ? x * key_scale[mt][e >> 1] * row_scale[n][e & 1] : x * c_half;
                     float r = fmaf(h, ptx::tanh_approx(h), h) * kLog2e;  // SiLU(U) = (U/2)(1 + tanh(U/2))
                     if (edge) {
                         const int j = tok + mt * 16 + key0 + (e >> 1) * 8;
                         if (j == pos[n][e & 1])
-                            r = fmaf(0.5f * kLog2e, ptx::tanh_approx(x * c_self), 0.5f * kLog2e) + corr[n][e & 1];
+                            r = fmaf(0.5f * kLog2e, ptx::tanh_approx(Q8 ? h * inv_tau : x * c_self), 0.5f * kLog2e) +
+                                corr[n][e & 1];
                         else if (j > pos[n][e & 1])
                             r = -INFINITY;
                     }
                     sc[n][mt][e] = r;
-                    mt_[n][e & 1] = fmaxf(mt_[n][e & 1], r);
+                    mt_[n][e & 1] = fmaxf(mt_[n][e & 1], Q8 ? r + val_log[mt][e >> 1] : r);
                 }
             raise |= mt_[n][0] > m[n][0] + kRaise || mt_[n][1] > m[n][1] + kRaise;
         }
@@ -415,11 +556,27 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
                     const float p1 = ptx::ex2_approx(sc[n][mt][2 * h + 1] - b1);
                     l[n][0] += p0;
                     l[n][1] += p1;
-                    pb[n][mt][h] = turn8(ptx::pack_bf16x2(p0, p1));
+                    pb[n][mt][h] = turn8(Q8 ? pack_f16x2(p0 * val_scale[mt][h], p1 * val_scale[mt][h])
+                                            : ptx::pack_bf16x2(p0, p1));
                 }
         }
+        if constexpr (Q8) {
 #pragma unroll
-        for (int dt = 0; dt < DK; ++dt)
+            for (int dt = 0; dt < DK; ++dt) {
+                uint32_t w[4];  // keys 8 i .. 8 i + 7 of 16 channels, turned
+                ldsm4t(w, sv + lane * C::kRowBytes + ((dt ^ q8_swizzle) << 4));
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt) {
+                    const uint32_t a[4] = {even_bytes_f16(w[2 * mt]), odd_bytes_f16(w[2 * mt]),
+                                           even_bytes_f16(w[2 * mt + 1]), odd_bytes_f16(w[2 * mt + 1])};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (n < nt_used) mma16816_f16(o[n][dt], a, pb[n][mt][0], pb[n][mt][1]);
+                }
+            }
+        }
+#pragma unroll
+        for (int dt = 0; dt < (Q8 ? 0 : DK); ++dt)
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt) {
                 uint32_t a[4];
@@ -430,6 +587,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
             }
         __syncwarp();  // every lane has read the stage
         if (sent < hi) send(s);
+        else if constexpr (Q8) asm volatile("cp.async.commit_group;" ::: "memory");
         ++u.j;
         if (u.j == u.n || it + 1 == hi - lo) {
             end_unit(lo + it + 1);
@@ -483,18 +641,18 @@ __global__ void __launch_bounds__(FewCfg<DK, NT>::kThreads, 1)
     }
 }
 
-template <int DK, int NT>
+template <int DK, int NT, bool Q8>
 size_t few_bytes(int num_sms) {
-    using C = FewCfg<DK, NT>;
+    using C = FewCfg<DK, NT, Q8>;
     return (size_t)num_sms * (sizeof(PieceMeta) + 8 + (C::kWarps + 2) * C::kSlot * sizeof(float));
 }
 
-template <int DK, int NT>
+template <int DK, int NT, bool Q8>
 cudaError_t launch_few(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, MergeSide* left, cudaStream_t s) {
-    using C = FewCfg<DK, NT>;
-    auto kern = paged_few_kernel<DK, NT>;
+    using C = FewCfg<DK, NT, Q8>;
+    auto kern = paged_few_kernel<DK, NT, Q8>;
     static OncePerDevice once;
-    static_assert(1024 + C::kRingBytes + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
+    static_assert(1024 + C::kRingBytes + C::kScaleBytes + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
     cudaError_t e = allow_dynamic_smem(once, kern, C::smem(kPagedMaxRequests));
     if (e != cudaSuccess) return e;
     const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, 0, kPagedFewRows, a.status};
@@ -504,10 +662,11 @@ cudaError_t launch_few(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, 
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(slots + (size_t)a.num_sms * 2 * C::kSlot);
     CUtensorMap mk, mv;
     const int box = std::min(pp.page, kKeys);
-    if ((e = make_page_map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
-    if ((e = make_page_map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
+    const auto map = Q8 ? make_page_map_q8 : make_page_map;
+    if ((e = map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
+    if ((e = map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
     e = launch_chained(kern, dim3((unsigned)a.num_sms), C::kThreads, C::smem(pp.R), s, mk, mv, v,
-                       (const __nv_bfloat16*)a.P1, (__nv_bfloat16*)a.Y, a.L, part, meta);
+                       (const __nv_bfloat16*)a.P1, (const uint32_t*)a.scales, (__nv_bfloat16*)a.Y, a.L, part, meta);
     if (e != cudaSuccess) return e;
     const MergeSide side{slots, meta, a.num_sms};
     if (left != nullptr) {
@@ -522,24 +681,29 @@ bool few_rows(const PagedProblem& pp, int max_fresh) { return (int64_t)max_fresh
 
 template <int DK>
 cudaError_t launch_few_d(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, MergeSide* left, cudaStream_t s) {
-    return few_rows(pp, a.max_fresh) ? launch_few<DK, 1>(pp, a, ws, left, s) : launch_few<DK, 2>(pp, a, ws, left, s);
+    if (a.scales != nullptr)
+        return few_rows(pp, a.max_fresh) ? launch_few<DK, 1, true>(pp, a, ws, left, s)
+                                         : launch_few<DK, 2, true>(pp, a, ws, left, s);
+    return few_rows(pp, a.max_fresh) ? launch_few<DK, 1, false>(pp, a, ws, left, s)
+                                     : launch_few<DK, 2, false>(pp, a, ws, left, s);
 }
 
 template <int DK>
-size_t few_bytes_d(const PagedProblem& pp, int max_fresh, int num_sms) {
-    return few_rows(pp, max_fresh) ? few_bytes<DK, 1>(num_sms) : few_bytes<DK, 2>(num_sms);
+size_t few_bytes_d(const PagedProblem& pp, bool q8, int max_fresh, int num_sms) {
+    if (q8) return few_rows(pp, max_fresh) ? few_bytes<DK, 1, true>(num_sms) : few_bytes<DK, 2, true>(num_sms);
+    return few_rows(pp, max_fresh) ? few_bytes<DK, 1, false>(num_sms) : few_bytes<DK, 2, false>(num_sms);
 }
 
 }  // namespace
 }  // namespace paged
 
-size_t paged_few_workspace(const PagedProblem& pp, int max_fresh, int num_sms) {
+size_t paged_few_workspace(const PagedProblem& pp, bool q8, int max_fresh, int num_sms) {
     using namespace paged;
     switch ((pp.d + 15) / 16) {
-        case 3: return few_bytes_d<3>(pp, max_fresh, num_sms);
-        case 4: return few_bytes_d<4>(pp, max_fresh, num_sms);
-        case 5: return few_bytes_d<5>(pp, max_fresh, num_sms);
-        default: return few_bytes_d<8>(pp, max_fresh, num_sms);
+        case 3: return few_bytes_d<3>(pp, q8, max_fresh, num_sms);
+        case 4: return few_bytes_d<4>(pp, q8, max_fresh, num_sms);
+        case 5: return few_bytes_d<5>(pp, q8, max_fresh, num_sms);
+        default: return few_bytes_d<8>(pp, q8, max_fresh, num_sms);
     }
 }
 

@@ -14,9 +14,9 @@
 
 namespace relation {
 
-size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, int max_fresh, int num_sms) {
+size_t paged_fwd_workspace(const PagedProblem& pp, bool bf16, bool q8, int max_fresh, int num_sms) {
     if (!bf16) return paged_f32_workspace(pp, max_fresh, num_sms);
-    const size_t few = paged_few_workspace(pp, max_fresh, num_sms);  // the two passes overlap: a part each
+    const size_t few = paged_few_workspace(pp, q8, max_fresh, num_sms);  // the two passes overlap: a part each
     return (int64_t)max_fresh * pp.group <= kPagedFewRows ? few : few + paged_tc_workspace(pp, num_sms);
 }
 
@@ -28,7 +28,7 @@ cudaError_t launch_paged_fwd(const PagedProblem& pp, bool bf16, const PagedFwdAr
     const cudaError_t e = launch_paged_few(pp, a, a.workspace, &few, s);
     *launches = 3;
     if (e != cudaSuccess) return e;
-    return launch_paged_tc(pp, a, static_cast<char*>(a.workspace) + paged_few_workspace(pp, a.max_fresh, a.num_sms), few,
+    return launch_paged_tc(pp, a, static_cast<char*>(a.workspace) + paged_few_workspace(pp, a.scales != nullptr, a.max_fresh, a.num_sms), few,
                            s);
 }
 

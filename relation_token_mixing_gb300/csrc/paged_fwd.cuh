@@ -313,7 +313,7 @@ cudaError_t launch_merge(const FwdView& v, const MergeSide& few, const MergeSide
 // The kernels' launches (paged_few.cu: a request's packed rows fit 16; paged_tc.cu:
 // more; paged_f32.cu: float32).
 constexpr int kPagedFewRows = 16;
-size_t paged_few_workspace(const PagedProblem& pp, int max_fresh, int num_sms);
+size_t paged_few_workspace(const PagedProblem& pp, bool q8, int max_fresh, int num_sms);
 // left: what it leaves to the long requests' pass to merge, if that follows.
 cudaError_t launch_paged_few(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace, paged::MergeSide* left,
                              cudaStream_t s);
@@ -327,5 +327,7 @@ cudaError_t launch_paged_f32(const PagedProblem& pp, const PagedFwdArgs& a, void
 // The 4-D map (column, token of a page, cache head, page) of a bf16 page pool, box
 // 64 columns x box_rows tokens, 128-byte swizzle; columns past d read as zero.
 cudaError_t make_page_map(CUtensorMap* map, const void* base, const PagedProblem& pp, int box_rows);
+// Of an 8-bit pool: boxes as wide as a row.
+cudaError_t make_page_map_q8(CUtensorMap* map, const void* base, const PagedProblem& pp, int box_rows);
 
 }  // namespace relation

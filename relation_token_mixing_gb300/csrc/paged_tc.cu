@@ -143,12 +143,30 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int byt
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-template <int D>
+// Four whole numbers times a scale as two pairs of bf16, exactly: with the sign flipped a byte is
+// b + 128, in the last place of 2^23 a float32.  (Shift and scale in one multiply-add would overflow at
+// scales from 2^105 on.)
+__device__ __forceinline__ uint2 scaled_bytes(uint32_t w, float2 scale) {
+    const uint32_t x = w ^ 0x80808080u;
+    const float2 shift = make_float2(-8388736.f, -8388736.f);
+    const float2 a = ptx::add2(make_float2(as_f(__byte_perm(x, 0x4b000000u, 0x7440)),
+                                           as_f(__byte_perm(x, 0x4b000000u, 0x7441))), shift);
+    const float2 b = ptx::add2(make_float2(as_f(__byte_perm(x, 0x4b000000u, 0x7442)),
+                                           as_f(__byte_perm(x, 0x4b000000u, 0x7443))), shift);
+    const float2 c = ptx::mul2(a, scale), d = ptx::mul2(b, scale);
+    return make_uint2(ptx::pack_bf16x2(c.x, c.y), ptx::pack_bf16x2(d.x, d.y));
+}
+
+// Q8: 8-bit pages.  The two loading warps fetch the whole numbers themselves, 16 a lane at a time, and
+// write them as bf16 with their row's scale in it, which holds them exactly, where the tiles' copies would
+// put them; the products and the softmax are the same.
+template <int D, bool Q8>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ FwdView v, const __nv_bfloat16* __restrict__ P1,
-                    __nv_bfloat16* __restrict__ Y, float* __restrict__ L, float* __restrict__ part,
-                    PieceMeta* __restrict__ meta) {
+                    const int8_t* __restrict__ k_pages, const int8_t* __restrict__ v_pages,
+                    const uint16_t* __restrict__ scales, __nv_bfloat16* __restrict__ Y, float* __restrict__ L,
+                    float* __restrict__ part, PieceMeta* __restrict__ meta) {
     using C = TcCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -185,8 +203,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
         ptx::fence_barrier_init();
-        ptx::tma_prefetch_desc(&tm_k);
-        ptx::tma_prefetch_desc(&tm_v);
+        if constexpr (!Q8) {
+            ptx::tma_prefetch_desc(&tm_k);
+            ptx::tma_prefetch_desc(&tm_v);
+        }
     }
     const int total = schedule_build(v, prefix, bars->sums, [&](const Request& q) {
         return TcTiling::places(q.c, q.rows, pp.by_group, TcTiling::row_tiles(q.rows));
@@ -227,6 +247,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One tensor's tiles of a piece, tile x of the block into stage x % kStages.
     const int box = min(pp.page, kKeys), boxes = kKeys / box;
     int x = 0, tb0 = -1, tb_r = -1, tb = 0;
+    // (8-bit pages) Tile x's keys from token tok on, of a request with len tokens, as bf16 into `tile`.
+    // A lane has 16 columns of every kStep-th row; a batch of 4 is asked for before the one
+    // before it is converted.  Rows past the request's end, or of a page that is not there, are zeros.
+    auto convert = [&](int tok, int len, int g, int which, uint8_t* tile, uint64_t* empty) {
+        constexpr int kChunks = D / 16, kStep = 32 / kChunks, kBatch = 4, kBatches = kKeys / (kBatch * kStep);
+        const int8_t* pool = which ? v_pages : k_pages;
+        const int chunk = lane % kChunks, r0 = lane / kChunks;
+        const bool in_row = chunk * 16 < pp.row;
+        uint32_t sc[4];  // rows 32 i + lane
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int key = tok + 32 * i + lane;
+            const int page = __shfl_sync(0xffffffffu, tb, ((key >> pp.page_shift) - tb0) & 31);
+            sc[i] = 0;
+            if (key < len && page < pp.pages)
+                sc[i] = __ldg(scales + 2 * page_row_index(pp, page, key & pp.page_mask, g) + which);
+        }
+        uint4 buf[2][kBatch];
+        auto fetch = [&](int b, uint4 (&w)[kBatch]) {
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int key = tok + (kBatch * b + i) * kStep + r0;
+                const int page = __shfl_sync(0xffffffffu, tb, ((key >> pp.page_shift) - tb0) & 31);
+                w[i] = make_uint4(0, 0, 0, 0);
+                if (in_row && key < len && page < pp.pages)
+                    w[i] = __ldg(reinterpret_cast<const uint4*>(
+                        pool + page_row_index(pp, page, key & pp.page_mask, g) * (size_t)pp.row + chunk * 16));
+            }
+        };
+        fetch(0, buf[0]);
+        if (x >= C::kStages && !ptx::mbar_wait_warp(empty, ((x / C::kStages) - 1) & 1, abort_flag, v.status,
+                                                    kDevTimeoutEmpty)) {
+            ok = false;
+            return;
+        }
+#pragma unroll
+        for (int b = 0; b < kBatches; ++b) {
+            if (b + 1 < kBatches) fetch(b + 1, buf[(b + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const int first = (kBatch * b + i) * kStep, r = first + r0;  // rows first .. first + kStep - 1: one of sc
+                const float s = as_f(__shfl_sync(0xffffffffu, sc[first / 32], r & 31) << 16);
+                const float2 s2 = make_float2(s, s);
+                const uint4 w = buf[b & 1][i];
+                const uint2 p0 = scaled_bytes(w.x, s2), p1 = scaled_bytes(w.y, s2),
+                            p2 = scaled_bytes(w.z, s2), p3 = scaled_bytes(w.w, s2);
+                uint8_t* row = tile + (chunk / 4) * kPanelBytes + r * 128;
+                const int c8 = 2 * (chunk % 4);
+                *reinterpret_cast<uint4*>(row + ((c8 ^ (r & 7)) << 4)) = make_uint4(p0.x, p0.y, p1.x, p1.y);
+                *reinterpret_cast<uint4*>(row + (((c8 + 1) ^ (r & 7)) << 4)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
+            }
+        }
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+    };
     auto load = [&](const Piece& pc, const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty) {
         const int need = (pc.c + pp.by_group.div(pc.rows) + pp.page_mask) >> pp.page_shift;
         for (int j = pc.j0; j < pc.j0 + pc.most; ++j, ++x) {
@@ -244,6 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tb = pp.pages;
                     }
                 }
+            }
+            if constexpr (Q8) {
+                convert(tok, pc.c + pp.by_group.div(pc.rows), pc.g, ring == sV, ring + s * C::kTileBytes, &empty[s]);
+                if (!ok) return;
+                if (lane == 0) ptx::mbar_arrive(&full[s]);
+                continue;
             }
             if (x >= C::kStages && !ptx::mbar_wait_warp(&empty[s], ((x / C::kStages) - 1) & 1, abort_flag, v.status,
                                                         kDevTimeoutEmpty)) {
@@ -546,6 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // row's Self, which has no correction, above 0: no row's sum vanishes under the reference 0.
             // It rises when a score passes it by 2^kRaise.
             float m = 0.f, l = 0.f;
+            // Some row's reference is above 2^20: the product m log2(e) is rounded to whole powers of two
+            // and more there, so the rows' scores are taken from m before they are multiplied.
+            bool large = false;
             bool o_ready = false;  // O and P are free of this tile's predecessors
             auto o_wait = [&](int j) {
                 if (o_ready) return;
@@ -566,6 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float f = ptx::ex2_approx((m - m_new) * kLog2e);
                 l *= f;
                 m = m_new;
+                large = large || __any_sync(0xffffffffu, m > 1048576.f);
                 o_wait(j);
                 if (j > 0) {
 #pragma unroll 1
@@ -613,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                if (c0 + 31 < own_lo) {
+                if (c0 + 31 < own_lo && !large) {
                     // Before every row's own token: both functions in one run, under the reference so
                     // far, with no wait for the maximum between them.
                     const float2 nm2 = make_float2(-m * kLog2e, -m * kLog2e);
@@ -646,7 +731,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
                     if (__any_sync(0xffffffffu, m_new > m + kRaise * kLn2)) raise(m_new, j, b);
                 }
-                const float2 nm2 = make_float2(-m * kLog2e, -m * kLog2e);
+                const float rest = large ? 0.f : -m * kLog2e;
+                if (large) {
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) sv[c] = as_u(as_f(sv[c]) - m);
+                }
+                const float2 nm2 = make_float2(rest, rest);
                 ls[0] = ls[1] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -687,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     blocks(j);
                 } else {
                     // The 128 columns at once where every row's own token is past them.
-                    bool whole = own_lo >= kKeys;
+                    bool whole = own_lo >= kKeys && !large;
                     const int x = pairs + j;
                     auto take_turn = [&] {
                         return j >= n_pair || x + t == 0 ||
@@ -805,23 +895,26 @@ size_t tc_bytes(int num_sms) {
     return num_sms * (sizeof(PieceMeta) + 8 + 2 * TcCfg<D>::kSlotFloats * sizeof(float));
 }
 
-template <int D>
+template <int D, bool Q8>
 cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, const MergeSide& few, cudaStream_t s) {
     using C = TcCfg<D>;
     static_assert(1024 + C::kTiles + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
     static OncePerDevice once;
-    cudaError_t e = allow_dynamic_smem(once, paged_tc_kernel<D>, C::smem(kPagedMaxRequests));
+    cudaError_t e = allow_dynamic_smem(once, paged_tc_kernel<D, Q8>, C::smem(kPagedMaxRequests));
     if (e != cudaSuccess) return e;
     const FwdView v{pp, a.table, a.starts, a.cached, a.max_fresh, kPagedFewRows, INT32_MAX, a.status};
     const int workers = a.num_sms;
     float* part = static_cast<float*>(ws);
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(part + (size_t)workers * 2 * C::kSlotFloats);
-    CUtensorMap mk, mv;
+    CUtensorMap mk{}, mv{};
     const int box = std::min(pp.page, kKeys);
-    if ((e = make_page_map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
-    if ((e = make_page_map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
-    e = launch_chained(paged_tc_kernel<D>, dim3((unsigned)workers), kThreads, C::smem(pp.R), s, mk, mv, v,
-                       (const __nv_bfloat16*)a.P1, (__nv_bfloat16*)a.Y, a.L, part, meta);
+    if constexpr (!Q8) {
+        if ((e = make_page_map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
+        if ((e = make_page_map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
+    }
+    e = launch_chained(paged_tc_kernel<D, Q8>, dim3((unsigned)workers), kThreads, C::smem(pp.R), s, mk, mv, v,
+                       (const __nv_bfloat16*)a.P1, (const int8_t*)a.P2_pages, (const int8_t*)a.I_pages,
+                       (const uint16_t*)a.scales, (__nv_bfloat16*)a.Y, a.L, part, meta);
     if (e != cudaSuccess) return e;
     return launch_merge<__nv_bfloat16, kPagedFewRows, kRows, D>(v, few, MergeSide{part, meta, workers}, a.Y, a.L, s);
 }
@@ -835,7 +928,11 @@ size_t paged_tc_workspace(const PagedProblem& pp, int num_sms) {
 
 cudaError_t launch_paged_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* workspace,
                             const paged::MergeSide& few, cudaStream_t s) {
-    return pp.d <= 64 ? paged::launch_tc<64>(pp, a, workspace, few, s) : paged::launch_tc<128>(pp, a, workspace, few, s);
+    if (a.scales != nullptr)
+        return pp.d <= 64 ? paged::launch_tc<64, true>(pp, a, workspace, few, s)
+                          : paged::launch_tc<128, true>(pp, a, workspace, few, s);
+    return pp.d <= 64 ? paged::launch_tc<64, false>(pp, a, workspace, few, s)
+                      : paged::launch_tc<128, false>(pp, a, workspace, few, s);
 }
 
 }  // namespace relation
