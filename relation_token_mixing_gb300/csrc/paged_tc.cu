@@ -56,15 +56,20 @@ namespace {
 
 constexpr int kBM = 128, kRows = 256, kKeys = 128;
 constexpr int kThreads = 384;
-// 128 * 104 + 256 * 200 = 64512 = 384 * 168 registers.
-constexpr uint32_t kRegsControl = 104, kRegsSoftmax = 200;
+// 128 * 104 + 256 * 200 = 64512 = 384 * 168 registers; with the warps that convert 8-bit pages
+// 256 * 104 + 256 * 152 = 65536 = 512 * 128.
+template <bool Q8>
+struct TcRoles {
+    static constexpr int kAll = Q8 ? kThreads + 128 : kThreads;
+    static constexpr uint32_t kRegsControl = 104, kRegsSoftmax = Q8 ? 152 : 200;
+};
 constexpr int kPanelBytes = 128 * 128;  // 128 rows x 64 bf16
 constexpr int kMinTiles = 4;
 // A unit's beginning and end (queries, first scores, output: 7 to 12 thousand cycles)
 // cost about two key tiles (5 thousand each).
 using TcTiling = Tiling<kRows, kKeys, 2>;
 
-template <int D>
+template <int D, bool Q8>
 struct TcCfg {
     static constexpr bool kSepP = D == 64;
     static constexpr uint32_t kColP = 384;
@@ -74,7 +79,12 @@ struct TcCfg {
     // At d <= 64 the next unit's queries have a place of their own while this one's last
     // scores are formed.
     static constexpr int kQBufs = D == 64 ? 2 : 1;
-    static constexpr int kTiles = (2 * kQBufs + 2 * kStages) * kTileBytes;
+    // 8-bit pages: half of I~'s stages make room for rings of whole numbers, as they lie in the pages.
+    static constexpr int kVStages = Q8 ? kStages / 2 : kStages;
+    static constexpr int kRing = Q8 ? kStages / 2 : kStages;  // of what the copies fill
+    static constexpr int kRowBytes = Q8 ? D : 128, kCopyBytes = Q8 ? kBM * D : kTileBytes;
+    static constexpr int kTiles =
+        (2 * kQBufs + kStages + kVStages) * kTileBytes + (Q8 ? 2 * kRing * kCopyBytes : 0);
     static int smem(int R) { return 1024 + kTiles + 1024 + (R * 4 + 15) / 16 * 16; }
     static constexpr size_t kSlotFloats = slot_floats(kRows, D);
 };
@@ -101,9 +111,10 @@ struct TcBars {
     uint64_t s_full[2], s_free[2], p_full[2], o_done[2];
     uint64_t turn[2][4];
     uint64_t drain;
+    uint64_t k8_full[2], v8_full[2], k8_empty[2], v8_empty[2];
     uint32_t tmem_base;
     int abort_flag;
-    int64_t sums[12];
+    int64_t sums[16];
     alignas(16) Piece pieces[kSlots];
 };
 static_assert(sizeof(TcBars) <= 1024, "the barriers' region");
@@ -143,36 +154,39 @@ __device__ __forceinline__ void cp_async8(uint32_t dst, const void* src, int byt
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Four whole numbers times a scale as two pairs of bf16, exactly: with the sign flipped a byte is
-// b + 128, in the last place of 2^23 a float32.  (Shift and scale in one multiply-add would overflow at
-// scales from 2^105 on.)
-__device__ __forceinline__ uint2 scaled_bytes(uint32_t w, float2 scale) {
+// Four whole numbers times a scale as two pairs of bf16, exactly: with the sign flipped a byte is b + 128, and
+// under 2^15 it is a float32 that one multiply-add shifts and scales.  `shift` is -(2^15 + 128) times the scale, so
+// the scale may be 2^111 at most; a larger one goes in two steps.
+__device__ __forceinline__ uint2 scaled_bytes(uint32_t w, float2 scale, float2 shift) {
     const uint32_t x = w ^ 0x80808080u;
-    const float2 shift = make_float2(-8388736.f, -8388736.f);
-    const float2 a = ptx::add2(make_float2(as_f(__byte_perm(x, 0x4b000000u, 0x7440)),
-                                           as_f(__byte_perm(x, 0x4b000000u, 0x7441))), shift);
-    const float2 b = ptx::add2(make_float2(as_f(__byte_perm(x, 0x4b000000u, 0x7442)),
-                                           as_f(__byte_perm(x, 0x4b000000u, 0x7443))), shift);
-    const float2 c = ptx::mul2(a, scale), d = ptx::mul2(b, scale);
-    return make_uint2(ptx::pack_bf16x2(c.x, c.y), ptx::pack_bf16x2(d.x, d.y));
+    const float2 a = ptx::fma2(make_float2(as_f(__byte_perm(x, 0x47000000u, 0x7404)),
+                                           as_f(__byte_perm(x, 0x47000000u, 0x7414))), scale, shift);
+    const float2 b = ptx::fma2(make_float2(as_f(__byte_perm(x, 0x47000000u, 0x7424)),
+                                           as_f(__byte_perm(x, 0x47000000u, 0x7434))), scale, shift);
+    return make_uint2(ptx::pack_bf16x2(a.x, a.y), ptx::pack_bf16x2(b.x, b.y));
 }
 
-// Q8: 8-bit pages.  The two loading warps fetch the whole numbers themselves, 16 a lane at a time, and
-// write them as bf16 with their row's scale in it, which holds them exactly, where the tiles' copies would
-// put them; the products and the softmax are the same.
+// Q8: 8-bit pages.  Warps 0 and 3 copy tiles of whole numbers, and four more warps (12-15) write them as bf16
+// with their rows' scales in them, which holds them exactly, where the copies of bf16 tiles would put
+// them; the products are the same.  What bounds it is the size of the code that runs at the same time: with the
+// softmax of 128 columns at once (d 80 and 128) and this conversion unrolled, the roles put one another out of the
+// instruction caches (two chunks over long histories, 32 heads over 8 of 128: 1.98 ms; the conversion in
+// loops 1.20; the softmax in blocks of 32 columns, without turns, 0.89, where bf16 pages take 0.84).
 template <int D, bool Q8>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(TcRoles<Q8>::kAll, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ FwdView v, const __nv_bfloat16* __restrict__ P1,
-                    const int8_t* __restrict__ k_pages, const int8_t* __restrict__ v_pages,
-                    const uint16_t* __restrict__ scales, __nv_bfloat16* __restrict__ Y, float* __restrict__ L,
+                    const uint32_t* __restrict__ scales, __nv_bfloat16* __restrict__ Y, float* __restrict__ L,
                     float* __restrict__ part, PieceMeta* __restrict__ meta) {
-    using C = TcCfg<D>;
+    using C = TcCfg<D, Q8>;
+    using Roles = TcRoles<Q8>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
     uint8_t* sK = sQ + 2 * C::kQBufs * C::kTileBytes;
     uint8_t* sV = sK + C::kStages * C::kTileBytes;
+    uint8_t* sK8 = sV + C::kVStages * C::kTileBytes;  // (8-bit pages)
+    uint8_t* sV8 = sK8 + C::kRing * C::kCopyBytes;
     TcBars* bars = reinterpret_cast<TcBars*>(smem + C::kTiles);
     int* prefix = reinterpret_cast<int*>(smem + C::kTiles + 1024);
     const PagedProblem& pp = v.pp;
@@ -182,7 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0) {
         for (int x = 0; x < kSlots; ++x) {
             ptx::mbar_init(&bars->piece_full[x], 1);
-            ptx::mbar_init(&bars->piece_free[x], 11);  // the other warps
+            if constexpr (Q8) ptx::mbar_init(&bars->piece_free[x], 15);
+            else ptx::mbar_init(&bars->piece_free[x], 11);  // the other warps
         }
         for (int x = 0; x < 4; ++x) ptx::mbar_init(&bars->v_clean[x], 1);
         for (int t = 0; t < 2; ++t) {
@@ -195,18 +210,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&bars->o_done[t], 1);
         }
         for (int s = 0; s < C::kStages; ++s) {
-            ptx::mbar_init(&bars->k_full[s], 1);
-            ptx::mbar_init(&bars->v_full[s], 1);
+            ptx::mbar_init(&bars->k_full[s], Q8 ? 4 : 1);  // the warps that convert, or the copies' one
+            ptx::mbar_init(&bars->v_full[s], Q8 ? 4 : 1);
             ptx::mbar_init(&bars->k_empty[s], 1);
             ptx::mbar_init(&bars->v_empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            ptx::mbar_init(&bars->k8_full[s], 1);
+            ptx::mbar_init(&bars->v8_full[s], 1);
+            ptx::mbar_init(&bars->k8_empty[s], 4);
+            ptx::mbar_init(&bars->v8_empty[s], 4);
         }
         ptx::mbar_init(&bars->drain, 1);
         bars->abort_flag = 0;
         ptx::fence_barrier_init();
-        if constexpr (!Q8) {
-            ptx::tma_prefetch_desc(&tm_k);
-            ptx::tma_prefetch_desc(&tm_v);
-        }
+        ptx::tma_prefetch_desc(&tm_k);
+        ptx::tma_prefetch_desc(&tm_v);
     }
     const int total = schedule_build(v, prefix, bars->sums, [&](const Request& q) {
         return TcTiling::places(q.c, q.rows, pp.by_group, TcTiling::row_tiles(q.rows));
@@ -247,65 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     // One tensor's tiles of a piece, tile x of the block into stage x % kStages.
     const int box = min(pp.page, kKeys), boxes = kKeys / box;
     int x = 0, tb0 = -1, tb_r = -1, tb = 0;
-    // (8-bit pages) Tile x's keys from token tok on, of a request with len tokens, as bf16 into `tile`.
-    // A lane has 16 columns of every kStep-th row; a batch of 4 is asked for before the one
-    // before it is converted.  Rows past the request's end, or of a page that is not there, are zeros.
-    auto convert = [&](int tok, int len, int g, int which, uint8_t* tile, uint64_t* empty) {
-        constexpr int kChunks = D / 16, kStep = 32 / kChunks, kBatch = 4, kBatches = kKeys / (kBatch * kStep);
-        const int8_t* pool = which ? v_pages : k_pages;
-        const int chunk = lane % kChunks, r0 = lane / kChunks;
-        const bool in_row = chunk * 16 < pp.row;
-        uint32_t sc[4];  // rows 32 i + lane
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int key = tok + 32 * i + lane;
-            const int page = __shfl_sync(0xffffffffu, tb, ((key >> pp.page_shift) - tb0) & 31);
-            sc[i] = 0;
-            if (key < len && page < pp.pages)
-                sc[i] = __ldg(scales + 2 * page_row_index(pp, page, key & pp.page_mask, g) + which);
-        }
-        uint4 buf[2][kBatch];
-        auto fetch = [&](int b, uint4 (&w)[kBatch]) {
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int key = tok + (kBatch * b + i) * kStep + r0;
-                const int page = __shfl_sync(0xffffffffu, tb, ((key >> pp.page_shift) - tb0) & 31);
-                w[i] = make_uint4(0, 0, 0, 0);
-                if (in_row && key < len && page < pp.pages)
-                    w[i] = __ldg(reinterpret_cast<const uint4*>(
-                        pool + page_row_index(pp, page, key & pp.page_mask, g) * (size_t)pp.row + chunk * 16));
-            }
-        };
-        fetch(0, buf[0]);
-        if (x >= C::kStages && !ptx::mbar_wait_warp(empty, ((x / C::kStages) - 1) & 1, abort_flag, v.status,
-                                                    kDevTimeoutEmpty)) {
-            ok = false;
-            return;
-        }
-#pragma unroll
-        for (int b = 0; b < kBatches; ++b) {
-            if (b + 1 < kBatches) fetch(b + 1, buf[(b + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < kBatch; ++i) {
-                const int first = (kBatch * b + i) * kStep, r = first + r0;  // rows first .. first + kStep - 1: one of sc
-                const float s = as_f(__shfl_sync(0xffffffffu, sc[first / 32], r & 31) << 16);
-                const float2 s2 = make_float2(s, s);
-                const uint4 w = buf[b & 1][i];
-                const uint2 p0 = scaled_bytes(w.x, s2), p1 = scaled_bytes(w.y, s2),
-                            p2 = scaled_bytes(w.z, s2), p3 = scaled_bytes(w.w, s2);
-                uint8_t* row = tile + (chunk / 4) * kPanelBytes + r * 128;
-                const int c8 = 2 * (chunk % 4);
-                *reinterpret_cast<uint4*>(row + ((c8 ^ (r & 7)) << 4)) = make_uint4(p0.x, p0.y, p1.x, p1.y);
-                *reinterpret_cast<uint4*>(row + (((c8 + 1) ^ (r & 7)) << 4)) = make_uint4(p2.x, p2.y, p3.x, p3.y);
-            }
-        }
-        ptx::fence_proxy_async_smem();
-        __syncwarp();
-    };
     auto load = [&](const Piece& pc, const CUtensorMap* map, uint8_t* ring, uint64_t* full, uint64_t* empty) {
         const int need = (pc.c + pp.by_group.div(pc.rows) + pp.page_mask) >> pp.page_shift;
         for (int j = pc.j0; j < pc.j0 + pc.most; ++j, ++x) {
-            const int s = x % C::kStages;
+            const int s = x % C::kRing;
             const int tok = j * kKeys, k0 = tok >> pp.page_shift;
             if (pc.r != tb_r || k0 < tb0 || k0 + boxes > tb0 + 32) {
                 tb_r = pc.r;
@@ -320,31 +284,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if constexpr (Q8) {
-                convert(tok, pc.c + pp.by_group.div(pc.rows), pc.g, ring == sV, ring + s * C::kTileBytes, &empty[s]);
-                if (!ok) return;
-                if (lane == 0) ptx::mbar_arrive(&full[s]);
-                continue;
-            }
-            if (x >= C::kStages && !ptx::mbar_wait_warp(&empty[s], ((x / C::kStages) - 1) & 1, abort_flag, v.status,
+            if (x >= C::kRing && !ptx::mbar_wait_warp(&empty[s], ((x / C::kRing) - 1) & 1, abort_flag, v.status,
                                                         kDevTimeoutEmpty)) {
                 ok = false;
                 return;
             }
-            const int copies = C::kPanels * min(boxes, need - k0);
-            const int p = lane / C::kPanels, panel = lane % C::kPanels;
+            constexpr int kWide = Q8 ? 1 : C::kPanels;  // copies side by side
+            const int copies = kWide * min(boxes, need - k0);
+            const int p = lane / kWide, panel = lane % kWide;
             const int page = __shfl_sync(0xffffffffu, tb, (k0 - tb0 + p) & 31);
-            if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], copies * box * 128);
+            if (lane == 0) ptx::mbar_arrive_expect_tx(&full[s], copies * box * C::kRowBytes);
             __syncwarp();
             if (lane < copies)
-                ptx::tma_load_4d(ring + s * C::kTileBytes + panel * kPanelBytes + p * box * 128, map, &full[s],
+                ptx::tma_load_4d(ring + s * C::kCopyBytes + panel * kPanelBytes + p * box * C::kRowBytes, map, &full[s],
                                  panel * 64, boxes > 1 ? 0 : (tok & pp.page_mask), pc.g, page);
         }
     };
     auto drain = [&](uint64_t* full) {  // after an abort: let the copies already issued land
         if (*abort_flag)
-            for (int y = max(0, x - C::kStages); y < x; ++y)
-                ptx::mbar_drain(&full[y % C::kStages], (y / C::kStages) & 1, v.status);
+            for (int y = max(0, x - C::kRing); y < x; ++y)
+                ptx::mbar_drain(&full[y % C::kRing], (y / C::kRing) & 1, v.status);
     };
     // Query rows r_begin .. r_end - 1 of a piece into buffer qb, by one warp; rows past the
     // unit's are zero.  Eight steps' addresses at a time: one after the other they cost a lone
@@ -384,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     if (warp == 0) {
         // --------------------------------------------------------- pieces, P2
-        ptx::regs_dec<kRegsControl>();
+        ptx::regs_dec<Roles::kRegsControl>();
         Cursor k;
         cursor_seek<TcTiling>(k, v, prefix, lo);
         for (int seg = 0; ok; ++seg) {
@@ -394,20 +353,134 @@ __global__ void __launch_bounds__(kThreads, 1)
             Piece pc{};  // no steps of either half
             pc.most = -1;
             if (k.f < hi) pc = piece_of(k, pp.by_group, hi);
+            if (Q8) pc.tail = -1;  // the keys past the end are zeros as they are written
             if (lane == 0) {
                 bars->pieces[seg % kSlots] = pc;
                 ptx::mbar_arrive(&bars->piece_full[seg % kSlots]);
             }
             __syncwarp();
             if (pc.most < 0) break;
-            load(pc, &tm_k, sK, bars->k_full, bars->k_empty);
+            if constexpr (Q8) load(pc, &tm_k, sK8, bars->k8_full, bars->k8_empty);
+            else load(pc, &tm_k, sK, bars->k_full, bars->k_empty);
             k.f += pc.j1 - pc.j0;
             cursor_next_unit<TcTiling>(k, v, prefix, hi);
         }
-        drain(bars->k_full);
+        drain(Q8 ? bars->k8_full : bars->k_full);
+    } else if (Q8 && warp >= 12) {
+        // --------------------------------------------- whole numbers to bf16 tiles
+        ptx::regs_dec<Roles::kRegsControl>();
+        // Warp w has rows 32 w .. 32 w + 31 of a tile, a lane a row: its scale is the lane's own, and both tiles'
+        // swizzles keep eight lanes' chunks apart.  (8 columns a lane with the scales shuffled: 3 thousand cycles a
+        // tile, this 2.)
+        const int first = 32 * (warp - 12), row = first + lane;
+        // A tile's scales, each lane's own row's, asked for a tile ahead; 0 past the request's end and in pages
+        // that are not there.
+        auto scales_of = [&](const Piece& pc, int tok) {
+            const int k0 = tok >> pp.page_shift, key = tok + row, len = pc.c + pp.by_group.div(pc.rows);
+            if (pc.r != tb_r || k0 < tb0 || k0 + boxes > tb0 + 32) {
+                tb_r = pc.r;
+                tb0 = k0;
+                tb = tb0 + lane < ((len + pp.page_mask) >> pp.page_shift)
+                         ? __ldg(v.table + (size_t)pc.r * pp.width + tb0 + lane) : -1;
+            }
+            const int page = __shfl_sync(0xffffffffu, tb, ((key >> pp.page_shift) - tb0) & 31);
+            uint32_t w = 0;
+            if (key < len && (unsigned)page < (unsigned)pp.pages)
+                // Volatile: stays here, a tile before its use.
+                asm volatile("ld.global.nc.b32 %0, [%1];"
+                             : "=r"(w) : "l"(scales + page_row_index(pp, page, key & pp.page_mask, pc.g)));
+            return w;
+        };
+        const int sw_in = D == 128 ? row & 7 : (row >> 1) & 3, sw_out = row & 7;
+        auto convert = [&](const uint8_t* src, uint8_t* tile, uint32_t sc) {
+            const float f = as_f(sc);
+            // A larger scale's values are made with a 2^16th of it and their exponents raised after (zeros stay).
+            const bool huge = __any_sync(0xffffffffu, f > 0x1p111f);
+            const float g = huge ? f * 0x1p-16f : f;
+            const float2 f2 = make_float2(g, g), m2 = make_float2(-32896.f * g, -32896.f * g);
+            // The next chunk is on its way while this one is converted.
+            const uint8_t* in = src + row * D;
+            uint8_t* out = tile + row * 128;
+            uint4 w = *reinterpret_cast<const uint4*>(in + (sw_in << 4));
+#pragma unroll (D == 128 ? 4 : 1)
+            for (int c = 0; c < D / 16; ++c) {
+                const uint4 ahead = *reinterpret_cast<const uint4*>(in + ((((c + 1) % (D / 16)) ^ sw_in) << 4));
+                uint8_t* to = out + (c >> 2) * kPanelBytes;
+                const uint2 x0 = scaled_bytes(w.x, f2, m2), x1 = scaled_bytes(w.y, f2, m2);
+                *reinterpret_cast<uint4*>(to + (((2 * (c & 3)) ^ sw_out) << 4)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                const uint2 x2 = scaled_bytes(w.z, f2, m2), x3 = scaled_bytes(w.w, f2, m2);
+                *reinterpret_cast<uint4*>(to + (((2 * (c & 3) + 1) ^ sw_out) << 4)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                w = ahead;
+            }
+            if (huge) {
+#pragma unroll 1
+                for (int i = 0; i < D; ++i) {
+                    __nv_bfloat16* x = reinterpret_cast<__nv_bfloat16*>(tile + (i / 64) * kPanelBytes + row * 128) + i % 64;
+                    *x = __float2bfloat16_rn(__bfloat162float(*x) * 0x1p16f);
+                }
+            }
+        };
+        // The next tile of the block's stretch: its scales.
+        Piece pc;
+        int seg = 0, left = 0, tok = 0;
+        auto next_tile = [&](uint32_t& w) {
+            if (left == 0) {
+                const Piece* slot = take(seg);
+                if (slot == nullptr) return false;
+                pc = *slot;
+                give(seg++);
+                left = pc.most;
+                if (left < 0) return false;
+                tok = pc.j0 * kKeys;
+            }
+            w = scales_of(pc, tok);
+            tok += kKeys;
+            --left;
+            return true;
+        };
+        // Tile y of P2 (which = 0) or I~.
+        auto item = [&](int which, int y, uint32_t w) {
+            const int stages = which ? C::kVStages : C::kStages, from = y % C::kRing, to = y % stages;
+            uint64_t* full8 = which ? bars->v8_full : bars->k8_full;
+            uint64_t* empty = which ? bars->v_empty : bars->k_empty;
+            if (!ptx::mbar_wait_warp(&full8[from], (y / C::kRing) & 1, abort_flag, v.status, kDevTimeoutFull) ||
+                (y >= stages && !ptx::mbar_wait_warp(&empty[to], (y / stages - 1) & 1, abort_flag, v.status,
+                                                     kDevTimeoutEmpty))) {
+                ok = false;
+                return;
+            }
+            convert((which ? sV8 : sK8) + from * C::kCopyBytes, (which ? sV : sK) + to * C::kTileBytes,
+                    which ? w & 0xffff0000u : w << 16);
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                ptx::mbar_arrive((which ? bars->v8_empty : bars->k8_empty) + from);
+                ptx::mbar_arrive((which ? bars->v_full : bars->k_full) + to);
+            }
+        };
+        // P2 is a tile ahead of I~, as the products want them (K0, K1, V0, K2, V1, ...), and the scales a tile
+        // ahead of P2.  One copy of the code for all: five roles share the instruction caches.
+        uint32_t before = 0, now = 0, after = 0;
+        bool more = next_tile(after), ended = !more;
+#pragma unroll 1
+        for (int z = 0; ok; ++z) {
+            const int which = z > 0 && (z & 1) == 0, y = which ? z / 2 - 1 : (z + 1) / 2;
+            if (which == 0) {
+                if (!more) {  // no tile y of P2; tile y - 1 of I~ is the last
+                    if (z == 0) break;
+                    ended = true;
+                    continue;
+                }
+                before = now;
+                now = after;
+                more = next_tile(after);
+            }
+            item(which, y, which && !ended ? before : now);
+            if (which && ended) break;
+        }
     } else if (warp == 3) {
         // ------------------------------------------------------------------ I~
-        ptx::regs_dec<kRegsControl>();
+        ptx::regs_dec<Roles::kRegsControl>();
         int tails = 0;
         for (int seg = 0; ok; ++seg) {
             const Piece* slot = take(seg);
@@ -415,6 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Piece pc = *slot;
             give(seg);
             if (pc.most < 0) break;
+            if constexpr (Q8) {
+                load(pc, &tm_v, sV8, bars->v8_full, bars->v8_empty);
+                continue;
+            }
             load(pc, &tm_v, sV, bars->v_full, bars->v_empty);
             if (ok && pc.tail >= 0) {
                 // The request ends inside the piece's last tile, the one just sent for: weight 0
@@ -436,10 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++tails;
             }
         }
-        drain(bars->v_full);
+        drain(Q8 ? bars->v8_full : bars->v_full);
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
-        ptx::regs_dec<kRegsControl>();
+        ptx::regs_dec<Roles::kRegsControl>();
         const uint32_t id_s = ptx::idesc_bf16(kBM, kKeys, false, false);
         const uint32_t id_o = ptx::idesc_bf16(kBM, D, false, true);
         const uint64_t dq0 = ptx::smem_desc(ptx::smem_u32(sQ), 16, 1024, ptx::kSwizzle128B);
@@ -510,12 +587,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (C::kSepP && sg.most == 1) ptx::mma_commit_elect(&bars->q_free[qb]);
             Steps next{{0, 0}, -2, -1};  // not read yet
             for (int j = 0; ok && j < sg.most; ++j) {
-                const int s = (kt + j) % C::kStages;
+                const int s = (kt + j) % C::kVStages;
                 bool v_ready = false;
                 auto v_wait = [&]() {
                     if (v_ready) return true;
                     v_ready = j == sg.tail ? wait(&bars->v_clean[tails % 4], tails / 4, kDevTimeoutFull)
-                                           : wait(&bars->v_full[s], (kt + j) / C::kStages, kDevTimeoutFull);
+                                           : wait(&bars->v_full[s], (kt + j) / C::kVStages, kDevTimeoutFull);
                     return v_ready;
                 };
                 if constexpr (C::kSepP) {
@@ -572,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_drain(&bars->drain, 0, v.status);
     } else if (warp == 2) {
         // ------------------------------------------------------------- queries
-        ptx::regs_dec<kRegsControl>();
+        ptx::regs_dec<Roles::kRegsControl>();
         PieceMeta mine{};
         for (int seg = 0; ok; ++seg) {
             const Piece* slot = take(seg);
@@ -595,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) meta[worker] = ok ? mine : PieceMeta{};
     } else {
         // ------------------------------------------------------------- softmax
-        ptx::regs_inc<kRegsSoftmax>();
+        ptx::regs_inc<Roles::kRegsSoftmax>();
         const int t = (warp - 4) >> 2, quarter = warp & 3, r = quarter * 32 + lane;
         const uint32_t lane_addr = tmem + ((uint32_t)(quarter * 32) << 16);
         const uint32_t s_col = t * 128, o_col = 256 + t * D;
@@ -616,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int seg = 0; ok; ++seg) {
             const Piece* pc = take(seg);  // the slot stays this warp's until the piece is done
             if (pc == nullptr || pc->most < 0) break;
-            const int steps = pc->steps[t], n_pair = C::kSepP ? 0 : min(pc->steps[0], pc->steps[1]);
+            const int steps = pc->steps[t], n_pair = C::kSepP || Q8 ? 0 : min(pc->steps[0], pc->steps[1]);
             // The row's own token (the last key it sees) as a column of the piece's first
             // tile, the warp's least and greatest.
             int own = pc->c + pp.by_group.div(min(pc->q * kRows + t * kBM + r, pc->rows - 1));
@@ -773,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 ptx::tc_fence_after();
-                if constexpr (C::kSepP) {
+                if constexpr (C::kSepP || Q8) {
                     blocks(j);
                 } else {
                     // The 128 columns at once where every row's own token is past them.
@@ -892,12 +969,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int D>
 size_t tc_bytes(int num_sms) {
-    return num_sms * (sizeof(PieceMeta) + 8 + 2 * TcCfg<D>::kSlotFloats * sizeof(float));
+    return num_sms * (sizeof(PieceMeta) + 8 + 2 * TcCfg<D, false>::kSlotFloats * sizeof(float));
 }
 
 template <int D, bool Q8>
 cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, const MergeSide& few, cudaStream_t s) {
-    using C = TcCfg<D>;
+    using C = TcCfg<D, Q8>;
     static_assert(1024 + C::kTiles + 1024 + kPagedMaxRequests * 4 <= 232448, "shared memory of a block");
     static OncePerDevice once;
     cudaError_t e = allow_dynamic_smem(once, paged_tc_kernel<D, Q8>, C::smem(kPagedMaxRequests));
@@ -906,15 +983,13 @@ cudaError_t launch_tc(const PagedProblem& pp, const PagedFwdArgs& a, void* ws, c
     const int workers = a.num_sms;
     float* part = static_cast<float*>(ws);
     PieceMeta* meta = reinterpret_cast<PieceMeta*>(part + (size_t)workers * 2 * C::kSlotFloats);
-    CUtensorMap mk{}, mv{};
+    CUtensorMap mk, mv;
     const int box = std::min(pp.page, kKeys);
-    if constexpr (!Q8) {
-        if ((e = make_page_map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
-        if ((e = make_page_map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
-    }
-    e = launch_chained(paged_tc_kernel<D, Q8>, dim3((unsigned)workers), kThreads, C::smem(pp.R), s, mk, mv, v,
-                       (const __nv_bfloat16*)a.P1, (const int8_t*)a.P2_pages, (const int8_t*)a.I_pages,
-                       (const uint16_t*)a.scales, (__nv_bfloat16*)a.Y, a.L, part, meta);
+    const auto map = Q8 ? make_page_map_q8 : make_page_map;
+    if ((e = map(&mk, a.P2_pages, pp, box)) != cudaSuccess) return e;
+    if ((e = map(&mv, a.I_pages, pp, box)) != cudaSuccess) return e;
+    e = launch_chained(paged_tc_kernel<D, Q8>, dim3((unsigned)workers), TcRoles<Q8>::kAll, C::smem(pp.R), s, mk, mv, v,
+                       (const __nv_bfloat16*)a.P1, (const uint32_t*)a.scales, (__nv_bfloat16*)a.Y, a.L, part, meta);
     if (e != cudaSuccess) return e;
     return launch_merge<__nv_bfloat16, kPagedFewRows, kRows, D>(v, few, MergeSide{part, meta, workers}, a.Y, a.L, s);
 }
