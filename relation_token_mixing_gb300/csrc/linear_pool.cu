@@ -279,83 +279,100 @@ struct ChunkSmem {
     uint8_t kl[kTile];    // what bf16 leaves of k~
     uint8_t c[kTile];     // the state as an operand, [value channel][key channel]
     float tot[8][kDp];    // a warp's 8 tokens: sum of log2 of their retentions
-    float size[8][kDp];   // and of its magnitude
-    float c_op[kDp], c_pre[kDp], c_post[kDp];  // per channel: the state's factor as an operand, before and after the update
+    float c_op[kDp], c_pre[kDp];  // per channel: the state's factor as an operand and before the update
     float2 rs[kT];        // (S / |p1|, S / |p2|) of a token
 };
 
-// Rows t0 .. t0 + 63 of a stretch of `count` tokens, whose first row is at `row` (rows of a
-// head are H d elements apart): the ones past its end are zero, as the columns past d stay.
-__device__ __forceinline__ void load_chunk(ChunkStage& s, const LinearPool& p, size_t row, int t0, int count) {
-    const size_t stride = (size_t)p.H * p.d;
-    const int tid = threadIdx.x;
-    const __nv_bfloat16* src[3] = {static_cast<const __nv_bfloat16*>(p.P1) + row, static_cast<const __nv_bfloat16*>(p.P2) + row,
-                                   static_cast<const __nv_bfloat16*>(p.I) + row};
-    uint8_t* dst[3] = {s.p1, s.p2, s.v};
-    if ((p.d & 7) == 0) {
-        const int q = tid & 7, col = 8 * q;
-        if (col < p.d)
-#pragma unroll
-            for (int k = 0; k < 6; ++k) {
-                const int r = (tid >> 3) + 32 * (k & 1);
-                const uint32_t to = ptx::smem_u32(dst[k >> 1]) + swz(r, col);
-                if (t0 + r < count) cp_async_16(to, src[k >> 1] + (size_t)(t0 + r) * stride + col);
-                else st_zero16(to);
-            }
-    } else {  // rows of 120 bytes start on 8
-        const int q = tid & 15, col = 4 * q;
-        if (col < p.d)
-#pragma unroll
-            for (int k = 0; k < 12; ++k) {
-                const int r = (tid >> 4) + 16 * (k & 3);
-                const uint32_t to = ptx::smem_u32(dst[k >> 2]) + swz(r, col);
-                if (t0 + r < count) cp_async_8(to, src[k >> 2] + (size_t)(t0 + r) * stride + col);
-                else st_shared_zero8(to);
-            }
-    }
-    const int q = tid & 15, col = 4 * q;
-    if (col < p.d)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int r = (tid >> 4) + 16 * k;
-            const uint32_t to = ptx::smem_u32(s.g) + (r * kDp + col) * 4;
-            if (t0 + r < count) cp_async_16(to, p.G + row + (size_t)(t0 + r) * stride + col);
-            else st_zero16(to);
-        }
-    cp_async_commit();
-}
+// The rows of a stretch of `count` tokens, 64 at a time: a thread's sources go on from chunk to
+// chunk.  Rows past the end are zero, as the columns past d stay.
+struct Loader {
+    const char *p1, *p2, *v, *g;
+    size_t half;    // bytes from a row to the thread's next one
+    size_t g_step;
+    size_t chunk;   // and from a chunk to the next
+    int row, g_row, col, g_col;
+    uint32_t dst, g_dst;
 
-// The warp's 8 tokens: S / |p1| and S / |p2|, eight lanes a token.
+    __device__ __forceinline__ Loader(const LinearPool& p, size_t first) {
+        const int tid = threadIdx.x;
+        const bool wide = (p.d & 7) == 0;  // else rows of 120 bytes, which start on 8
+        const size_t stride = (size_t)p.H * p.d;
+        row = wide ? tid >> 3 : tid >> 4;
+        col = wide ? 8 * (tid & 7) : 4 * (tid & 15);
+        g_row = tid >> 4, g_col = 4 * (tid & 15);
+        const size_t at = (first + row * stride + col) * 2;
+        p1 = static_cast<const char*>(p.P1) + at;
+        p2 = static_cast<const char*>(p.P2) + at;
+        v = static_cast<const char*>(p.I) + at;
+        g = reinterpret_cast<const char*>(p.G) + (first + g_row * stride + g_col) * 4;
+        half = stride * 2 * (wide ? 32 : 16);
+        g_step = stride * 4 * 16;
+        chunk = stride * 2 * kT;
+        dst = swz(row, col);
+        g_dst = (g_row * kDp + g_col) * 4;
+    }
+    // left: tokens from this chunk on.
+    __device__ __forceinline__ void chunk_into(ChunkStage& s, int d, int left) {
+        const char* src[3] = {p1, p2, v};
+        const uint32_t to[3] = {ptx::smem_u32(s.p1) + dst, ptx::smem_u32(s.p2) + dst, ptx::smem_u32(s.v) + dst};
+        if (col < d) {
+            if ((d & 7) == 0) {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        if (row + 32 * r < left) cp_async_16(to[k] + r * 32 * 128, src[k] + r * half);
+                        else st_zero16(to[k] + r * 32 * 128);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (row + 16 * r < left) cp_async_8(to[k] + r * 16 * 128, src[k] + r * half);
+                        else st_shared_zero8(to[k] + r * 16 * 128);
+            }
+        }
+        if (g_col < d)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const uint32_t at = ptx::smem_u32(s.g) + g_dst + r * 16 * kDp * 4;
+                if (g_row + 16 * r < left) cp_async_16(at, g + r * g_step);
+                else st_zero16(at);
+            }
+        cp_async_commit();
+        p1 += chunk, p2 += chunk, v += chunk, g += 2 * chunk;
+    }
+};
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return ptx::add2(a, b); }
+
+// The warp's 8 tokens: |p1|^2, |p2|^2 and p1 . p2 are the diagonals of three 8 x 8 products of the rows with
+// one another (a row's fragment is the same on both sides), then S / |p1| and S / |p2|.  Twelve products and
+// four fetches in place of some 150 multiply-adds and shuffles.
 __device__ __forceinline__ void row_scalars(ChunkSmem& sm, const ChunkStage& s, float zscale, int warp, int lane) {
+    float n1[4] = {}, n2[4] = {}, dt[4] = {};
+    const uint32_t at = 8 * warp * 128 + swz(lane & 7, 8 * (lane >> 3)), at2 = 8 * warp * 128 + swz(lane & 7, 32 + 8 * (lane >> 3));
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const int i = 8 * warp + 4 * k + (lane >> 3), col = 8 * (lane & 7);
-        const uint4 x = *reinterpret_cast<const uint4*>(s.p1 + swz(i, col));
-        const uint4 y = *reinterpret_cast<const uint4*>(s.p2 + swz(i, col));
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-        float n1 = 0.f, n2 = 0.f, dt = 0.f;
+        uint32_t x[4], y[4];
+        ldsm4(x, ptx::smem_u32(s.p1) + (k ? at2 : at));
+        ldsm4(y, ptx::smem_u32(s.p2) + (k ? at2 : at));
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            const float a0 = lo_f(xs[w]), a1 = hi_f(xs[w]), b0 = lo_f(ys[w]), b1 = hi_f(ys[w]);
-            n1 = fmaf(a0, a0, fmaf(a1, a1, n1));
-            n2 = fmaf(b0, b0, fmaf(b1, b1, n2));
-            dt = fmaf(a0, b0, fmaf(a1, b1, dt));
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t ax[4] = {x[2 * h], 0u, x[2 * h + 1], 0u}, ay[4] = {y[2 * h], 0u, y[2 * h + 1], 0u};
+            mma16816(n1, ax, x[2 * h], x[2 * h + 1]);
+            mma16816(dt, ax, y[2 * h], y[2 * h + 1]);
+            mma16816(n2, ay, y[2 * h], y[2 * h + 1]);
         }
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) {
-            n1 += __shfl_xor_sync(0xffffffffu, n1, o);
-            n2 += __shfl_xor_sync(0xffffffffu, n2, o);
-            dt += __shfl_xor_sync(0xffffffffu, dt, o);
-        }
-        if ((lane & 7) == 0) {
-            const float S = 1.f / (1.f + __expf(-dt * zscale));
-            sm.rs[i] = make_float2(n1 > 0.f ? S * rsqrtf(n1) : 0.f, n2 > 0.f ? S * rsqrtf(n2) : 0.f);
-        }
+    }
+    const int g = lane >> 2;
+    if ((lane & 3) == g >> 1) {  // the diagonal's entry of row g
+        const float a = g & 1 ? n1[1] : n1[0], b = g & 1 ? n2[1] : n2[0], x = g & 1 ? dt[1] : dt[0];
+        const float S = 1.f / (1.f + __expf(-x * zscale));
+        sm.rs[8 * warp + g] = make_float2(a > 0.f ? S * rsqrtf(a) : 0.f, b > 0.f ? S * rsqrtf(b) : 0.f);
     }
     __syncwarp();
 }
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
 
 // Entries (16 rt + lane / 4 (+ 8), 8 n + 2 (lane % 4) (+ 1)) of q k^T with the retention between
 // the two tokens, n < 2 rt + 2, for a chunk whose factors from one reference would leave
@@ -453,7 +470,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const size_t row = ((size_t)it.first * p.H + h) * p.d;
     const int chunks = (it.count + kT - 1) / kT;
     __syncthreads();
-    load_chunk(sm.st[0], p, row, 0, it.count);
+    Loader load(p, row);
+    load.chunk_into(sm.st[0], p.d, it.count);
 
     // The state C^T.
     const int g = lane >> 2, t = lane & 3, vt = 16 * (warp & 3), ct = 32 * (warp >> 2);
@@ -476,42 +494,47 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     const int rt = warp < 4 ? warp : 7 - warp, v0 = 32 * (warp >> 2);
     const int c2 = 2 * lane;
+    const uint32_t own = 8 * warp * 128 + ((c2 & 7) << 1);  // the lane's channels in its tokens' rows, see `at`
     const Gate gate = gate_of<kGate>(p, h, c2);
+    const size_t ystride = (size_t)p.H * p.d;
+    __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.Y) + row + (16 * rt + g) * ystride + v0 + 2 * t;
     float2 lost = make_float2(0.f, 0.f);  // log2 of the segment's retention
+    // The accumulators hold the state over 2^owed (per channel): the factor after a chunk's update and the one before
+    // the next are applied as one.
+    float2 owed = make_float2(0.f, 0.f);
     for (int n = 0; n < chunks; ++n) {
         ChunkStage& s = sm.st[n & 1];
+        const int left = it.count - n * kT;  // tokens from this chunk on
         cp_async_wait<0>();
         __syncthreads();  // the chunk is there, and nothing reads the one before any more
-        if (n + 1 < chunks) load_chunk(sm.st[(n + 1) & 1], p, row, (n + 1) * kT, it.count);
+        if (n + 1 < chunks) load.chunk_into(sm.st[(n + 1) & 1], p.d, left - kT);
         row_scalars(sm, s, p.zscale, warp, lane);
         // G inside the warp's 8 tokens.
-        const int left = it.count - n * kT - 8 * warp;  // tokens that are there
-        float2 G[8], sum = make_float2(0.f, 0.f), size = make_float2(0.f, 0.f);
+        float2 G[8], sum = make_float2(0.f, 0.f);
+        float most = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 x = *reinterpret_cast<const float2*>(s.g + (8 * warp + i) * kDp + c2);
-            float2 e = make_float2(0.f, 0.f);
-            if (i < left) e = log2_retention<kGate>(x, gate);
+            float2 e = log2_retention<kGate>(*reinterpret_cast<const float2*>(s.g + (8 * warp + i) * kDp + c2), gate);
+            if (kGate && 8 * warp + i >= left) e = make_float2(0.f, 0.f);  // (else the row is zero)
+            if (!kGate) most = ptx::max3(most, e.x, e.y);
             sum = add2(sum, e);
-            size = add2(size, make_float2(fabsf(e.x), fabsf(e.y)));
             G[i] = sum;
         }
         *reinterpret_cast<float2*>(&sm.tot[warp][c2]) = sum;
-        *reinterpret_cast<float2*>(&sm.size[warp][c2]) = size;
-        __syncthreads();
-        float2 base = make_float2(0.f, 0.f), mid = base, rest = base, after = base, size0 = base, size1 = base;
+        // A state that grows may do so at one token and fade at others: the sums of half a chunk say nothing then.
+        const bool grows = kGate ? (__syncthreads(), false) : __syncthreads_or(most > 0.f);
+        float2 base = make_float2(0.f, 0.f), mid = base, rest = base;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
             const float2 x = *reinterpret_cast<const float2*>(&sm.tot[w][c2]);
-            const float2 y = *reinterpret_cast<const float2*>(&sm.size[w][c2]);
-            if (w < warp) base = add2(base, x);
-            if (w > warp) after = add2(after, x);
-            if (w < 4) mid = add2(mid, x), size0 = add2(size0, y);
-            else rest = add2(rest, x), size1 = add2(size1, y);
+            if (w == warp) base = add2(mid, rest);
+            if (w < 4) mid = add2(mid, x);
+            else rest = add2(rest, x);
         }
-        lost = add2(lost, add2(mid, rest));
-        const float widest = fmaxf(fmaxf(size0.x, size0.y), fmaxf(size1.x, size1.y));
-        const bool strong = __any_sync(0xffffffffu, !(widest <= kRange));  // the same for every warp
+        const float2 all = add2(mid, rest);
+        lost = add2(lost, all);
+        const float least = fminf(fminf(mid.x, mid.y), fminf(rest.x, rest.y));
+        const bool strong = grows || __any_sync(0xffffffffu, !(least >= -kRange));  // the same for every warp
         float w[8][4];
         if (strong) {
             if (kOut) {
@@ -528,64 +551,81 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncthreads();  // before the rows are overwritten
             }
         }
-        // The operands, in the rows' places: a warp's own tokens, a lane's own channels.
+        // The operands, in the rows' places: a warp's own tokens, a lane's own channels.  Exponents: of a query
+        // G - mid and of a key its negative; in a strong chunk from the chunk's start, and to its end.
+        const float2 from = strong ? base : make_float2(base.x - mid.x, base.y - mid.y);
+        float2 to_end = sum;
+        if (strong)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (x > warp) to_end = add2(to_end, *reinterpret_cast<const float2*>(&sm.tot[x][c2]));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int r = 8 * warp + i;
-            const uint32_t at = swz(r, c2);
-            const float2 f = sm.rs[r];
-            float2 eq, ek;
-            if (strong) {  // from the chunk's start, and to its end
-                eq = add2(base, G[i]);
-                ek = add2(make_float2(sum.x - G[i].x, sum.y - G[i].y), after);
-            } else {
-                eq = make_float2(base.x + G[i].x - mid.x, base.y + G[i].y - mid.y);
-                ek = make_float2(-eq.x, -eq.y);
-            }
+            const uint32_t at = own + i * 128 + (((lane >> 2) ^ i) << 4);  // swz(8 warp + i, c2)
+            const float2 f = sm.rs[8 * warp + i], eq = add2(from, G[i]);
+            const float2 ek = strong ? make_float2(to_end.x - G[i].x, to_end.y - G[i].y) : make_float2(-eq.x, -eq.y);
             if (kOut) {
                 const uint32_t x = *reinterpret_cast<const uint32_t*>(s.p1 + at);
-                *reinterpret_cast<uint32_t*>(s.p1 + at) =
-                    pack2(lo_f(x) * f.x * ptx::ex2_approx(eq.x), hi_f(x) * f.x * ptx::ex2_approx(eq.y));
+                const float2 q = mul2(mul2(make_float2(lo_f(x), hi_f(x)), make_float2(f.x, f.x)),
+                                      make_float2(ptx::ex2_approx(eq.x), ptx::ex2_approx(eq.y)));
+                *reinterpret_cast<uint32_t*>(s.p1 + at) = pack2(q.x, q.y);
             }
             const uint32_t y = *reinterpret_cast<const uint32_t*>(s.p2 + at);
-            const float k0 = lo_f(y) * f.y * ptx::ex2_approx(ek.x), k1 = hi_f(y) * f.y * ptx::ex2_approx(ek.y);
-            const uint32_t hi = pack2(k0, k1);
+            const float2 k = mul2(mul2(make_float2(lo_f(y), hi_f(y)), make_float2(f.y, f.y)),
+                                  make_float2(ptx::ex2_approx(ek.x), ptx::ex2_approx(ek.y)));
+            const uint32_t hi = pack2(k.x, k.y);
             *reinterpret_cast<uint32_t*>(s.p2 + at) = hi;
-            *reinterpret_cast<uint32_t*>(sm.kl + at) = pack2(k0 - lo_f(hi), k1 - hi_f(hi));
+            const float2 lo = add2(k, make_float2(-lo_f(hi), -hi_f(hi)));
+            *reinterpret_cast<uint32_t*>(sm.kl + at) = pack2(lo.x, lo.y);
         }
+        // What is owed goes with 2^mid, or before it: always in a strong chunk, and where both together would be
+        // too small for a float32 factor, though the accumulators, which hold 2^-owed times the state, are not.
+        const float2 both = add2(owed, mid);
+        const bool apart = strong || __any_sync(0xffffffffu, !(fminf(both.x, both.y) >= -120.f));
         if (warp == 0) {
-            const float2 m = make_float2(ptx::ex2_approx(mid.x), ptx::ex2_approx(mid.y));
-            const float2 all = make_float2(ptx::ex2_approx(mid.x + rest.x), ptx::ex2_approx(mid.y + rest.y));
-            const float2 one = make_float2(1.f, 1.f);
-            *reinterpret_cast<float2*>(&sm.c_op[c2]) = strong ? one : m;
-            *reinterpret_cast<float2*>(&sm.c_pre[c2]) = strong ? all : m;
-            *reinterpret_cast<float2*>(&sm.c_post[c2]) =
-                strong ? one : make_float2(ptx::ex2_approx(rest.x), ptx::ex2_approx(rest.y));
+            const float2 to = strong ? all : apart ? mid : both;
+            *reinterpret_cast<float2*>(&sm.c_pre[c2]) = make_float2(ptx::ex2_approx(to.x), ptx::ex2_approx(to.y));
+            *reinterpret_cast<float2*>(&sm.c_op[c2]) = make_float2(ptx::ex2_approx(owed.x), ptx::ex2_approx(owed.y));
         }
+        owed = strong ? make_float2(0.f, 0.f) : rest;
         __syncthreads();
-        if (kOut) {
-            // The state as the output's operand.
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int c = ct + 8 * x + 2 * t;
-                const float2 f = *reinterpret_cast<const float2*>(&sm.c_op[c]);
-                *reinterpret_cast<uint32_t*>(sm.c + swz(vt + g, c)) = pack2(C[x][0] * f.x, C[x][1] * f.y);
-                *reinterpret_cast<uint32_t*>(sm.c + swz(vt + g + 8, c)) = pack2(C[x][2] * f.x, C[x][3] * f.y);
-            }
-        }
+        // The state as the output's operand (2^mid C; of a strong chunk C) and as the update finds it (the same; all's
+        // retention applied).
+        const uint32_t c_row = (vt + g) * 128;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const float2 f = *reinterpret_cast<const float2*>(&sm.c_pre[ct + 8 * x + 2 * t]);
-            C[x][0] *= f.x, C[x][1] *= f.y, C[x][2] *= f.x, C[x][3] *= f.y;
+            const int c = ct + 8 * x + 2 * t;
+            const uint32_t at = c_row + ((((c >> 3) ^ g) & 7) << 4) + 4 * t;  // rows vt + g and 8 further
+            float2 lo = make_float2(C[x][0], C[x][1]), hi = make_float2(C[x][2], C[x][3]);
+            if (apart) {
+                const float2 f = *reinterpret_cast<const float2*>(&sm.c_op[c]);
+                lo = mul2(lo, f), hi = mul2(hi, f);
+                if (kOut && strong) {
+                    *reinterpret_cast<uint32_t*>(sm.c + at) = pack2(lo.x, lo.y);
+                    *reinterpret_cast<uint32_t*>(sm.c + at + 8 * 128) = pack2(hi.x, hi.y);
+                }
+            }
+            const float2 f = *reinterpret_cast<const float2*>(&sm.c_pre[c]);
+            lo = mul2(lo, f), hi = mul2(hi, f);
+            C[x][0] = lo.x, C[x][1] = lo.y, C[x][2] = hi.x, C[x][3] = hi.y;
+            if (kOut && !strong) {
+                *reinterpret_cast<uint32_t*>(sm.c + at) = pack2(lo.x, lo.y);
+                *reinterpret_cast<uint32_t*>(sm.c + at + 8 * 128) = pack2(hi.x, hi.y);
+            }
         }
         if (kOut) {
             uint32_t aq[4][4];
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) ldsm4(aq[ks], addr_a(s.p1 + rt * 16 * 128, 16 * ks, lane));
-            if (!strong) {
+            float E[4][4];
 #pragma unroll
-                for (int kb = 0; kb < 4; ++kb) {
-                    if (kb > rt) break;
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) E[x][e] = 0.f;
+#pragma unroll
+            for (int kb = 0; kb < 4; ++kb) {
+                if (kb > rt) break;
+                if (!strong) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[2 * kb][e] = w[2 * kb + 1][e] = 0.f;
 #pragma unroll
@@ -596,15 +636,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                         mma16816(w[2 * kb + 1], aq[ks], b[2], b[3]);
                     }
                 }
-            }
-            float E[4][4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) E[x][e] = 0.f;
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                if (kb > rt) break;
                 if (kb == rt) {  // strictly earlier keys only
 #pragma unroll
                     for (int y = 0; y < 2; ++y)
@@ -632,20 +663,21 @@ __global__ void __launch_bounds__(kThreads, 2)
                     mma16816(E[2 * x], aq[ks], b[0], b[1]);
                     mma16816(E[2 * x + 1], aq[ks], b[2], b[3]);
                 }
-            __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.Y) + row;
+            const uint32_t v_at = (16 * rt + g) * 128 + 4 * t;
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const int i = 16 * rt + g + 8 * half;
-                if (n * kT + i >= it.count) continue;
+                if (16 * rt + g + 8 * half >= left) continue;
+                __nv_bfloat16* y = Y + 8 * half * ystride;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int v = v0 + 8 * x + 2 * t;
-                    if (v >= p.d) continue;
-                    const uint32_t own = *reinterpret_cast<const uint32_t*>(s.v + swz(i, v));
-                    *reinterpret_cast<uint32_t*>(Y + (size_t)(n * kT + i) * p.H * p.d + v) =
-                        pack2(lo_f(own) + E[x][2 * half], hi_f(own) + E[x][2 * half + 1]);
+                    if (v0 + 8 * x + 2 * t >= p.d) continue;
+                    const uint32_t i = *reinterpret_cast<const uint32_t*>(
+                        s.v + v_at + 8 * half * 128 + ((((v0 >> 3) + x) ^ g) << 4));  // swz(16 rt + g + 8 half, v)
+                    const float2 o = add2(make_float2(lo_f(i), hi_f(i)), make_float2(E[x][2 * half], E[x][2 * half + 1]));
+                    *reinterpret_cast<uint32_t*>(y + 8 * x) = pack2(o.x, o.y);
                 }
             }
+            Y += kT * ystride;
         }
         // C^T += I~^T k~.
 #pragma unroll
@@ -663,12 +695,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mma16816(C[2 * x + 1], a, b[2], b[3]);
             }
         }
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const float2 f = *reinterpret_cast<const float2*>(&sm.c_post[ct + 8 * x + 2 * t]);
-            C[x][0] *= f.x, C[x][1] *= f.y, C[x][2] *= f.x, C[x][3] *= f.y;
-        }
     }
+    if (warp == 0) *reinterpret_cast<float2*>(&sm.c_op[c2]) = make_float2(ptx::ex2_approx(owed.x), ptx::ex2_approx(owed.y));
+    __syncthreads();
     float* out = mine;
     int ld = kDp;
     if (kOut) {
@@ -683,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int v = vt + g + 8 * (e >> 1), c = ct + 8 * x + 2 * t + (e & 1);
-                if (v < ld && c < ld) out[(size_t)c * ld + v] = C[x][e];
+                if (v < ld && c < ld) out[(size_t)c * ld + v] = C[x][e] * sm.c_op[c];
             }
     }
     // (few calls: the whole chain ends with this kernel's end)
@@ -691,7 +720,8 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 // Every segment's entering state in the place of its own contribution, from the pool's
-// state on.  A thread has four columns of a row; the next segments' values are on their way.
+// state on.  A thread has one entry, the next 16 segments' on their way: what it takes are the rounds of
+// loads, not the bytes.
 constexpr int kScanThreads = 128;
 __global__ void __launch_bounds__(kScanThreads)
     linear_join_kernel(const __grid_constant__ LinearPool p, const Item* __restrict__ items, float* __restrict__ segments) {
@@ -700,32 +730,26 @@ __global__ void __launch_bounds__(kScanThreads)
     const Item it = items[blockIdx.x];
     const int seg = it.seg_segs & 0xffff, segs = it.seg_segs >> 16, h = blockIdx.y;
     if (seg != 0 || segs < 2) return;
-    const int e = (blockIdx.z * kScanThreads + threadIdx.x) * 4, c = e >> 6, v = e & 63;
+    const int e = blockIdx.z * kScanThreads + threadIdx.x, c = e >> 6, v = e & 63;
     const float* in = state_of(p, __ldg(p.slots_in + it.r), h);
-    float4 C = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (in != nullptr && c < p.d && v < p.d) C = *reinterpret_cast<const float4*>(in + (size_t)c * p.d + v);
+    float C = in != nullptr && c < p.d && v < p.d ? in[(size_t)c * p.d + v] : 0.f;
     const size_t step = (size_t)p.H * kSegFloats;
     float* H = segments + ((size_t)blockIdx.x * p.H + h) * kSegFloats;
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     for (int s0 = 0; s0 < segs; s0 += kAhead) {
-        float4 x[kAhead];
-        float a[kAhead];
+        float x[kAhead], a[kAhead];
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int s = s0 + k;
-            x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            a[k] = 0.f;
-            if (s + 1 < segs) {  // the last one leaves none
-                x[k] = *reinterpret_cast<const float4*>(H + s * step + e);
-                a[k] = H[s * step + kDp * kDp + c];
-            }
+            const bool there = s + 1 < segs;  // the last one leaves none
+            x[k] = there ? H[s * step + e] : 0.f;
+            a[k] = there ? H[s * step + kDp * kDp + c] : 0.f;
         }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int s = s0 + k;
-            if (s < segs) *reinterpret_cast<float4*>(H + s * step + e) = C;
-            const float f = exp2f(a[k]);
-            C = make_float4(fmaf(f, C.x, x[k].x), fmaf(f, C.y, x[k].y), fmaf(f, C.z, x[k].z), fmaf(f, C.w, x[k].w));
+            if (s < segs) H[s * step + e] = C;
+            C = fmaf(exp2f(a[k]), C, x[k]);
         }
     }
 }
@@ -794,7 +818,7 @@ cudaError_t launch_pool(const LinearPool& p, void* workspace, const Cut& cut, in
         *launches = 4;
         e = launch(linear_chunk_kernel<false, kGate>, grid, kThreads, smem, s, p, items, segments);
         if (e != cudaSuccess) return e;
-        e = launch(linear_join_kernel, dim3(grid.x, grid.y, kDp * kDp / 4 / kScanThreads), kScanThreads, 0, s, p, items,
+        e = launch(linear_join_kernel, dim3(grid.x, grid.y, kDp * kDp / kScanThreads), kScanThreads, 0, s, p, items,
                    segments);
         if (e != cudaSuccess) return e;
     } else {
