@@ -129,9 +129,10 @@ struct FewSmem {
     float part[2][8][kDp];
 };
 
-// Block 0 of a packed call with items: the list of the longer requests' segments.
-__device__ void make_items(const LinearPool& p, Item* items, int most, int seg_tokens) {
-    __shared__ int sums[kFewThreads / 32];
+// Block 0 of a packed call with items: the list of the longer requests' segments, and where those of more than one begin.
+__device__ void make_items(const LinearPool& p, Item* items, int most, int* joins, int most_joins, int seg_tokens) {
+    __shared__ int sums[kFewThreads / 32], many;
+    if (threadIdx.x == 0) many = 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int base = 0;
     for (int r0 = 0; r0 < p.R; r0 += kFewThreads) {
@@ -154,14 +155,20 @@ __device__ void make_items(const LinearPool& p, Item* items, int most, int seg_t
         }
         for (int k = 0; k < segs && at + k < most; ++k)
             items[at + k] = Item{r, sp.first + k * seg_tokens, min(seg_tokens, sp.count - k * seg_tokens), k | segs << 16};
+        if (segs > 1) {  // in any order
+            const int x = atomicAdd(&many, 1);
+            if (x < most_joins) joins[x] = at;
+        }
         __syncthreads();
     }
     for (int k = base + tid; k < most; k += kFewThreads) items[k] = Item{0, 0, 0, 0};
+    for (int k = many + tid; k < most_joins; k += kFewThreads) joins[k] = -1;
 }
 
 template <int D, bool kGate>
 __global__ void __launch_bounds__(kFewThreads)
-    linear_few_kernel(const __grid_constant__ LinearPool p, Item* items, int most_items, int seg_tokens) {
+    linear_few_kernel(const __grid_constant__ LinearPool p, Item* items, int most_items, int* joins, int most_joins,
+                      int seg_tokens) {
     __shared__ __align__(16) FewSmem sm;
     constexpr int kCols = D / 4, kRows = (D + 7) / 8;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -170,7 +177,7 @@ __global__ void __launch_bounds__(kFewThreads)
     int x = blockIdx.x;
     if (items != nullptr) {
         if (x == 0) {
-            make_items(p, items, most_items, seg_tokens);
+            make_items(p, items, most_items, joins, most_joins, seg_tokens);
             return;
         }
         --x;
@@ -263,7 +270,7 @@ __global__ void __launch_bounds__(kFewThreads)
 
 // ------------------------------------------------------------------- chunks
 constexpr int kT = 64;            // tokens of a chunk
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kBlocksPerSm = 2;
 constexpr float kRange = 100.f;   // log2 of what half a chunk may lose of a channel
 constexpr int kTile = kT * 128;   // a bf16 tile of 64 x 64
 constexpr int kSegFloats = kDp * kDp + kDp;  // of a segment in the workspace: its state, the log2 of its retention
@@ -272,75 +279,95 @@ struct ChunkStage {
     uint8_t p1[kTile];  // q~ in place of p1, the larger part of k~ in place of p2, once they are made
     uint8_t p2[kTile];
     uint8_t v[kTile];
-    float g[kT * kDp];
 };
 struct ChunkSmem {
     ChunkStage st[2];
-    uint8_t kl[kTile];    // what bf16 leaves of k~
-    uint8_t c[kTile];     // the state as an operand, [value channel][key channel]
-    float tot[8][kDp];    // a warp's 8 tokens: sum of log2 of their retentions
-    float c_op[kDp], c_pre[kDp];  // per channel: the state's factor as an operand and before the update
+    union {
+        struct {
+            uint8_t kl[kTile];  // what bf16 leaves of k~
+            uint8_t c[kTile];   // the state as an operand, [value channel][key channel]
+        };
+        float g[kT * kDp];  // (strong_chunk)
+        struct {
+            uint8_t below[kTile];
+            float tot[8][kDp];  // a warp's 8 tokens: sum of log2 of their retentions
+        };
+    };
+    uint8_t w[kTile];  // the weights inside the chunk, [query][key]
+    float c_op[kDp], c_all[kDp], c_rest[kDp];  // per channel: factors of the state as an operand and through the
+                                               // chunk, and of what the chunk adds
     float2 rs[kT];        // (S / |p1|, S / |p2|) of a token
+    uint64_t c_done, o_done, drain;
+    uint32_t tmem;
+    int abort_flag;
 };
+static_assert(sizeof(ChunkStage) % 1024 == 0, "tiles on swizzle atoms");
 
-// The rows of a stretch of `count` tokens, 64 at a time: a thread's sources go on from chunk to
-// chunk.  Rows past the end are zero, as the columns past d stay.
+// Accumulators of 64 rows lie in lanes 0-15 of each of the four warps' 32: row r in lane 32 (r / 16) + r % 16.
+constexpr uint32_t kColW = 0, kColO = 0, kColC = 64, kTmemCols = 128;  // O overwrites the scores once they are read
+
+// 16 rows x 32 columns of an accumulator as four fragments of m16n8: x[n][0, 1] row lane / 4, columns 8 n + 2 (lane % 4)
+// and the next, x[n][2, 3] the row 8 further.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, uint32_t (&x)[4][4]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(x[0][0]), "=r"(x[0][1]), "=r"(x[0][2]), "=r"(x[0][3]), "=r"(x[1][0]), "=r"(x[1][1]), "=r"(x[1][2]),
+          "=r"(x[1][3]), "=r"(x[2][0]), "=r"(x[2][1]), "=r"(x[2][2]), "=r"(x[2][3]), "=r"(x[3][0]), "=r"(x[3][1]),
+          "=r"(x[3][2]), "=r"(x[3][3])
+        : "r"(taddr));
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int n = 0; n < 4; ++n) ptx::pin_regs(x[n]);
+}
+// Four 8 x 8 blocks of bf16 pairs from such fragments into a tile.
+__device__ __forceinline__ void stsm4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+// A chunk's rows: those past the stretch's end are zero, as the columns past d stay.
 struct Loader {
-    const char *p1, *p2, *v, *g;
-    size_t half;    // bytes from a row to the thread's next one
-    size_t g_step;
-    size_t chunk;   // and from a chunk to the next
-    int row, g_row, col, g_col;
-    uint32_t dst, g_dst;
+    int row, col;
+    uint32_t dst;
 
-    __device__ __forceinline__ Loader(const LinearPool& p, size_t first) {
+    __device__ __forceinline__ explicit Loader(const LinearPool& p) {
         const int tid = threadIdx.x;
         const bool wide = (p.d & 7) == 0;  // else rows of 120 bytes, which start on 8
-        const size_t stride = (size_t)p.H * p.d;
         row = wide ? tid >> 3 : tid >> 4;
         col = wide ? 8 * (tid & 7) : 4 * (tid & 15);
-        g_row = tid >> 4, g_col = 4 * (tid & 15);
-        const size_t at = (first + row * stride + col) * 2;
-        p1 = static_cast<const char*>(p.P1) + at;
-        p2 = static_cast<const char*>(p.P2) + at;
-        v = static_cast<const char*>(p.I) + at;
-        g = reinterpret_cast<const char*>(p.G) + (first + g_row * stride + g_col) * 4;
-        half = stride * 2 * (wide ? 32 : 16);
-        g_step = stride * 4 * 16;
-        chunk = stride * 2 * kT;
         dst = swz(row, col);
-        g_dst = (g_row * kDp + g_col) * 4;
     }
-    // left: tokens from this chunk on.
-    __device__ __forceinline__ void chunk_into(ChunkStage& s, int d, int left) {
-        const char* src[3] = {p1, p2, v};
-        const uint32_t to[3] = {ptx::smem_u32(s.p1) + dst, ptx::smem_u32(s.p2) + dst, ptx::smem_u32(s.v) + dst};
-        if (col < d) {
-            if ((d & 7) == 0) {
+    // first: the element that the chunk's first row begins at; left: tokens from this chunk on.
+    template <bool kAll>
+    __device__ __forceinline__ void rows(const ChunkStage& s, const LinearPool& p, size_t first, int left) const {
+        const uint32_t stride = (uint32_t)(p.H * p.d);
+        const size_t at = (first + (size_t)row * stride + col) * 2;
+        const char* src[3] = {static_cast<const char*>(p.P1) + at, static_cast<const char*>(p.P2) + at,
+                              static_cast<const char*>(p.I) + at};
+        const uint32_t to = ptx::smem_u32(s.p1) + dst;
+        if ((p.d & 7) == 0) {
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
+            for (int k = 0; k < 3; ++k)
 #pragma unroll
-                    for (int r = 0; r < 2; ++r)
-                        if (row + 32 * r < left) cp_async_16(to[k] + r * 32 * 128, src[k] + r * half);
-                        else st_zero16(to[k] + r * 32 * 128);
-            } else {
+                for (int r = 0; r < 2; ++r)
+                    if (kAll || row + 32 * r < left) cp_async_16(to + k * kTile + r * 32 * 128, src[k] + (size_t)(r * 64 * stride));
+                    else st_zero16(to + k * kTile + r * 32 * 128);
+        } else {
 #pragma unroll
-                for (int k = 0; k < 3; ++k)
+            for (int k = 0; k < 3; ++k)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (row + 16 * r < left) cp_async_8(to[k] + r * 16 * 128, src[k] + r * half);
-                        else st_shared_zero8(to[k] + r * 16 * 128);
-            }
+                for (int r = 0; r < 4; ++r)
+                    if (kAll || row + 16 * r < left) cp_async_8(to + k * kTile + r * 16 * 128, src[k] + (size_t)(r * 32 * stride));
+                    else st_shared_zero8(to + k * kTile + r * 16 * 128);
         }
-        if (g_col < d)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const uint32_t at = ptx::smem_u32(s.g) + g_dst + r * 16 * kDp * 4;
-                if (g_row + 16 * r < left) cp_async_16(at, g + r * g_step);
-                else st_zero16(at);
-            }
+    }
+    __device__ __forceinline__ void chunk_into(const ChunkStage& s, const LinearPool& p, size_t first, int left) const {
+        if (col < p.d) {
+            if (left >= kT) rows<true>(s, p, first, left);
+            else rows<false>(s, p, first, left);
+        }
         cp_async_commit();
-        p1 += chunk, p2 += chunk, v += chunk, g += 2 * chunk;
     }
 };
 
@@ -374,83 +401,87 @@ __device__ __forceinline__ void row_scalars(ChunkSmem& sm, const ChunkStage& s, 
     __syncwarp();
 }
 
-// Entries (16 rt + lane / 4 (+ 8), 8 n + 2 (lane % 4) (+ 1)) of q k^T with the retention between
-// the two tokens, n < 2 rt + 2, for a chunk whose factors from one reference would leave
-// bf16's range: s.g holds G, s.p1 and s.p2 the rows as they came.  Keys before the 16 tokens
-// meet the queries at the block's first token, the block's first 8 keys its last 8 queries at the ninth:
-// all factors are retentions.  What is left are pairs inside 8 tokens, one by one.
-__device__ __noinline__ void strong_chunk(float (&w)[8][4], const ChunkSmem& sm, const ChunkStage& s, int rt, int lane) {
-    const int g = lane >> 2, t = lane & 3;
+// The weights (in sm.w) of rows 16 rt .. 16 rt + 15, q k^T with the retention between the two tokens, for a chunk whose
+// factors from one reference would leave bf16's range: sm.g holds G, s.p1 and s.p2 the rows as they came.  Keys before
+// the 16 tokens meet the queries at the block's first token, the block's first 8 keys its last 8 queries at the ninth:
+// all factors are retentions.  What is left are pairs inside 8 tokens, one by one.  16 keys at a time, so
+// that the call saves few of the caller's registers: chunks like this are rare, the others run past it.
+__device__ __noinline__ void strong_chunk(ChunkSmem& sm, const ChunkStage& s, int rt, int lane) {
+    const int g = lane >> 2, t = lane & 3, i0 = 16 * rt + g;
     const auto row_of = [](const uint8_t* tile, int r, int c) { return *reinterpret_cast<const uint32_t*>(tile + swz(r, c)); };
     // q (or k) of row r, columns c and c + 1, times 2^(+-(G_r - G_b)) as a bf16 pair; b < 0: from the chunk's start.
     const auto scaled = [&](bool query, int r, int b, int c) {
-        const float2 G = *reinterpret_cast<const float2*>(s.g + r * kDp + c);
-        const float2 B = b < 0 ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(s.g + b * kDp + c);
+        const float2 G = *reinterpret_cast<const float2*>(sm.g + r * kDp + c);
+        const float2 B = b < 0 ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(sm.g + b * kDp + c);
         const uint32_t x = row_of(query ? s.p1 : s.p2, r, c);
         const float f = query ? sm.rs[r].x : sm.rs[r].y;
         const float2 e = query ? make_float2(G.x - B.x, G.y - B.y) : make_float2(B.x - G.x, B.y - G.y);
         return pack2(lo_f(x) * f * ptx::ex2_approx(e.x), hi_f(x) * f * ptx::ex2_approx(e.y));
     };
-    const int i0 = 16 * rt + g;
-#pragma unroll
-    for (int n = 0; n < 8; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[n][e] = 0.f;
+    const auto put = [&](int n, const float (&w)[4]) {
+        *reinterpret_cast<uint32_t*>(sm.w + swz(i0, 8 * n + 2 * t)) = pack2(w[0], w[1]);
+        *reinterpret_cast<uint32_t*>(sm.w + swz(i0 + 8, 8 * n + 2 * t)) = pack2(w[2], w[3]);
+    };
 #pragma unroll 1
-    for (int c0 = 0; c0 < kDp; c0 += 16) {
-        const int c = c0 + 2 * t;
-        uint32_t a[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) a[x] = scaled(true, i0 + 8 * (x & 1), 16 * rt - 1, c + 8 * (x >> 1));
-#pragma unroll
-        for (int n = 0; n < 6; ++n)
-            if (n < 2 * rt) mma16816(w[n], a, scaled(false, 8 * n + g, 16 * rt - 1, c), scaled(false, 8 * n + g, 16 * rt - 1, c + 8));
-        a[0] = a[2] = 0u;
-        a[1] = scaled(true, i0 + 8, 16 * rt + 7, c);
-        a[3] = scaled(true, i0 + 8, 16 * rt + 7, c + 8);
-        const uint32_t b0 = scaled(false, i0, 16 * rt + 7, c), b1 = scaled(false, i0, 16 * rt + 7, c + 8);
-#pragma unroll
-        for (int n = 0; n < 8; n += 2)
-            if (n == 2 * rt) mma16816(w[n], a, b0, b1);
-    }
-    // Rows lane / 4 against columns 2 (lane % 4) of the two triangles on the diagonal.
+    for (int n = 0; n < 8; ++n) {
+        float w[4] = {0.f, 0.f, 0.f, 0.f};
+        const bool before = n < 2 * rt, last = n == 2 * rt;
+        if (before || last) {
+            const int b = before ? 16 * rt - 1 : 16 * rt + 7;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-        const int base = 16 * rt + 8 * half, i = base + g, j = base + 2 * t;
-        float x0 = 0.f, x1 = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < kDp; c += 2) {
-            const float2 Gi = *reinterpret_cast<const float2*>(s.g + i * kDp + c);
-            const float2 Gj = *reinterpret_cast<const float2*>(s.g + j * kDp + c);
-            const float2 Gk = *reinterpret_cast<const float2*>(s.g + (j + 1) * kDp + c);
-            const uint32_t q = row_of(s.p1, i, c), k0 = row_of(s.p2, j, c), k1 = row_of(s.p2, j + 1, c);
-            if (j < i)
-                x0 += lo_f(q) * lo_f(k0) * ptx::ex2_approx(Gi.x - Gj.x) + hi_f(q) * hi_f(k0) * ptx::ex2_approx(Gi.y - Gj.y);
-            if (j + 1 < i)
-                x1 += lo_f(q) * lo_f(k1) * ptx::ex2_approx(Gi.x - Gk.x) + hi_f(q) * hi_f(k1) * ptx::ex2_approx(Gi.y - Gk.y);
+            for (int c = 2 * t; c < kDp; c += 16) {
+                const uint32_t a[4] = {before ? scaled(true, i0, b, c) : 0u, scaled(true, i0 + 8, b, c),
+                                       before ? scaled(true, i0, b, c + 8) : 0u, scaled(true, i0 + 8, b, c + 8)};
+                mma16816(w, a, scaled(false, 8 * n + g, b, c), scaled(false, 8 * n + g, b, c + 8));
+            }
         }
-        x0 *= sm.rs[i].x * sm.rs[j].y;
-        x1 *= sm.rs[i].x * sm.rs[j + 1].y;
-#pragma unroll
-        for (int n = 0; n < 8; ++n)
-            if (n == 2 * rt + half) w[n][2 * half] = x0, w[n][2 * half + 1] = x1;
+        if (n == 2 * rt || n == 2 * rt + 1) {
+            // Row lane / 4 against columns 2 (lane % 4) and the next of the triangle on the diagonal.
+            const int base = 8 * n, i = base + g, j = base + 2 * t;
+            float x0 = 0.f, x1 = 0.f;
+#pragma unroll 1
+            for (int c = 0; c < kDp; c += 2) {
+                const float2 Gi = *reinterpret_cast<const float2*>(sm.g + i * kDp + c);
+                const float2 Gj = *reinterpret_cast<const float2*>(sm.g + j * kDp + c);
+                const float2 Gk = *reinterpret_cast<const float2*>(sm.g + (j + 1) * kDp + c);
+                const uint32_t q = row_of(s.p1, i, c), k0 = row_of(s.p2, j, c), k1 = row_of(s.p2, j + 1, c);
+                if (j < i)
+                    x0 += lo_f(q) * lo_f(k0) * ptx::ex2_approx(Gi.x - Gj.x) + hi_f(q) * hi_f(k0) * ptx::ex2_approx(Gi.y - Gj.y);
+                if (j + 1 < i)
+                    x1 += lo_f(q) * lo_f(k1) * ptx::ex2_approx(Gi.x - Gk.x) + hi_f(q) * hi_f(k1) * ptx::ex2_approx(Gi.y - Gk.y);
+            }
+            x0 *= sm.rs[i].x * sm.rs[j].y;
+            x1 *= sm.rs[i].x * sm.rs[j + 1].y;
+            if (last) w[0] = x0, w[1] = x1;
+            else w[2] = x0, w[3] = x1;
+        }
+        put(n, w);
     }
 }
 
 // One block a segment of a request and head: the output pass (kOut) from the state that
 // enters it, or the state pass, which leaves the segment's own contribution and retention.
-// Warps 0-3 have the query rows 16 w and value channels 0-31, warps 4-7 the rows
-// 16 (7 - w), so that a scheduler's two warps have five of the eight triangle's parts, and
-// channels 32-63; of the state C^T, warp w has rows (value channels) 16 (w % 4) and columns (key
-// channels) 32 (w / 4), as accumulators, from chunk to chunk.
+//
+// The chunk's elements are the threads' (warp w has tokens 8 w .. 8 w + 7, a lane two channels; the retention comes
+// straight to their registers, a chunk ahead), its four products tcgen05's: scores q~ k~^T and the state's addition
+// I~^T k~ as soon as the operands are there, then O = w I~ + q~ C into the scores' columns once those are read.  Of the
+// accumulators' 64 rows, a warp reads the 16 of its quarter (w % 4), columns 32 (w / 4) and on, as fragments of
+// m16n8: of the weights, of O and of the state's addition, whose rows are value channels and whose columns key
+// channels; the state itself stays in such fragments, from chunk to chunk.
 template <bool kOut, bool kGate>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     linear_chunk_kernel(const __grid_constant__ LinearPool p, const Item* __restrict__ items, float* __restrict__ segments) {
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    ChunkSmem& sm = *reinterpret_cast<ChunkSmem*>(smem_raw);
+    extern __shared__ uint8_t smem_raw[];
+    ChunkSmem& sm =
+        *reinterpret_cast<ChunkSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
     for (int k = tid; k < (int)(sizeof(sm.st) / 16); k += kThreads)
         reinterpret_cast<uint4*>(sm.st)[k] = make_uint4(0, 0, 0, 0);
+    if (tid == 0) {
+        for (uint64_t* bar : {&sm.c_done, &sm.o_done, &sm.drain}) ptx::mbar_init(bar, 1);
+        sm.abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
     // The kernel before waited for what ran before it, and leaves the items.
     if (items != nullptr) dependency_wait();
     dependency_release();
@@ -467,15 +498,40 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (items == nullptr && tid == 0) dependency_wait();
         return;
     }
+    if (warp == 0) {
+        ptx::tmem_alloc(&sm.tmem, kTmemCols);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem;
     const size_t row = ((size_t)it.first * p.H + h) * p.d;
     const int chunks = (it.count + kT - 1) / kT;
-    __syncthreads();
-    Loader load(p, row);
-    load.chunk_into(sm.st[0], p.d, it.count);
+    const uint32_t stride = (uint32_t)(p.H * p.d);
+    const Loader load(p);
+    load.chunk_into(sm.st[0], p, row, it.count);
+    // The lane's channels of the warp's 8 tokens: what G holds of them, then its running sums.
+    const int c2 = 2 * lane;
+    float2 G[8];
+    auto load_g = [&](size_t first, int left) {
+        const float* src = p.G + first + (size_t)(8 * warp) * stride + c2;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            G[i] = make_float2(0.f, 0.f);
+            if (c2 < p.d && 8 * warp + i < left)
+                asm volatile("ld.global.nc.v2.f32 {%0, %1}, [%2];" : "=f"(G[i].x), "=f"(G[i].y) : "l"(src + i * stride));
+        }
+    };
+    load_g(row, it.count);
 
-    // The state C^T.
-    const int g = lane >> 2, t = lane & 3, vt = 16 * (warp & 3), ct = 32 * (warp >> 2);
-    float C[4][4];
+    const int g = lane >> 2, t = lane & 3, quarter = warp & 3, r0 = 16 * quarter + g, col0 = 32 * (warp >> 2);
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * quarter) << 16) + col0;
+    // Where a lane's row of stsm4's (and ldsm4's) four blocks begins: rows 16 quarter .. + 15, columns col0 .. + 15; the
+    // next 16 columns are two chunks further, which the permutation turns into an exclusive-or.
+    const uint32_t frag_at = swz(16 * quarter + (lane & 15), col0 + 8 * (lane >> 4)), frag_next = frag_at ^ 32;
+    // Rows r0, r0 + 8 of the state C^T, columns col0 + 8 n + 2 t and the next.
+    float2 C[4][2];
     float* mine = segments == nullptr ? nullptr : segments + ((size_t)blockIdx.x * p.H + h) * kSegFloats;
     {
         const float* in = nullptr;
@@ -487,35 +543,49 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int v = vt + g + 8 * (e >> 1), c = ct + 8 * n + 2 * t + (e & 1);
-                C[n][e] = in != nullptr && v < ld && c < ld ? in[(size_t)c * ld + v] : 0.f;
+            for (int e = 0; e < 2; ++e) {
+                const int v = r0 + 8 * e, c = col0 + 8 * n + 2 * t;  // (widths are even)
+                C[n][e] = in != nullptr && v < ld && c < ld ? make_float2(in[(size_t)c * ld + v], in[(size_t)(c + 1) * ld + v])
+                                                            : make_float2(0.f, 0.f);
             }
     }
-    const int rt = warp < 4 ? warp : 7 - warp, v0 = 32 * (warp >> 2);
-    const int c2 = 2 * lane;
     const uint32_t own = 8 * warp * 128 + ((c2 & 7) << 1);  // the lane's channels in its tokens' rows, see `at`
     const Gate gate = gate_of<kGate>(p, h, c2);
-    const size_t ystride = (size_t)p.H * p.d;
-    __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.Y) + row + (16 * rt + g) * ystride + v0 + 2 * t;
     float2 lost = make_float2(0.f, 0.f);  // log2 of the segment's retention
-    // The accumulators hold the state over 2^owed (per channel): the factor after a chunk's update and the one before
-    // the next are applied as one.
-    float2 owed = make_float2(0.f, 0.f);
+    // Operands along a row (K) or across rows (M).
+    constexpr uint32_t kKK = ptx::idesc_bf16(64, 64, false, false), kKM = ptx::idesc_bf16(64, 64, false, true),
+                       kMM = ptx::idesc_bf16(64, 64, true, true);
+    constexpr uint32_t kStepK = 32 >> 4, kStepM = 2048 >> 4;  // 16 columns, 16 rows
+    const uint64_t desc0 = ptx::smem_desc(0, kTile, 1024, ptx::kSwizzle128B);
+    const uint32_t desc_high = ptx::desc_hi(desc0);
+    auto desc = [&](const uint8_t* tile) { return ptx::desc_lo(desc0) | ((ptx::smem_u32(tile) & 0x3FFFFu) >> 4); };
+    volatile int* abort_flag = &sm.abort_flag;
+    bool ok = true;
+    // One warp asks for the products' end, the others wait for that warp: eight that ask took two fifths of the
+    // instructions.
+    auto wait = [&](uint64_t* bar, int n) {
+        if (warp == 0 && ok) ok = ptx::mbar_wait_warp(bar, n & 1, abort_flag, p.status, kDevTimeoutMma);
+        __syncthreads();
+        ptx::tc_fence_after();
+    };
     for (int n = 0; n < chunks; ++n) {
         ChunkStage& s = sm.st[n & 1];
         const int left = it.count - n * kT;  // tokens from this chunk on
         cp_async_wait<0>();
-        __syncthreads();  // the chunk is there, and nothing reads the one before any more
-        if (n + 1 < chunks) load.chunk_into(sm.st[(n + 1) & 1], p.d, left - kT);
+        // The chunk is there, and nothing reads the one before any more.
+        if (!__syncthreads_and(ok)) {
+            ok = false;
+            break;
+        }
+        if (n + 1 < chunks) load.chunk_into(sm.st[(n + 1) & 1], p, row + (size_t)(n + 1) * kT * stride, left - kT);
         row_scalars(sm, s, p.zscale, warp, lane);
-        // G inside the warp's 8 tokens.
-        float2 G[8], sum = make_float2(0.f, 0.f);
+        // The running sums inside the warp's 8 tokens.
+        float2 sum = make_float2(0.f, 0.f);
         float most = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float2 e = log2_retention<kGate>(*reinterpret_cast<const float2*>(s.g + (8 * warp + i) * kDp + c2), gate);
-            if (kGate && 8 * warp + i >= left) e = make_float2(0.f, 0.f);  // (else the row is zero)
+            float2 e = log2_retention<kGate>(G[i], gate);
+            if (kGate && (8 * warp + i >= left || c2 >= p.d)) e = make_float2(0.f, 0.f);  // (a gate opens at zero)
             if (!kGate) most = ptx::max3(most, e.x, e.y);
             sum = add2(sum, e);
             G[i] = sum;
@@ -535,30 +605,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         lost = add2(lost, all);
         const float least = fminf(fminf(mid.x, mid.y), fminf(rest.x, rest.y));
         const bool strong = grows || __any_sync(0xffffffffu, !(least >= -kRange));  // the same for every warp
-        float w[8][4];
-        if (strong) {
+        float2 to_end = sum;
+        if (__builtin_expect(strong, 0)) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (x > warp) to_end = add2(to_end, *reinterpret_cast<const float2*>(&sm.tot[x][c2]));
             if (kOut) {
+                __syncthreads();  // before the sums are overwritten
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<float2*>(s.g + (8 * warp + i) * kDp + c2) = add2(base, G[i]);
+                    *reinterpret_cast<float2*>(sm.g + (8 * warp + i) * kDp + c2) = add2(base, G[i]);
                 __syncthreads();
-                float there[8][4];
-                strong_chunk(there, sm, s, rt, lane);
-#pragma unroll
-                for (int x = 0; x < 8; ++x)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[x][e] = there[x][e];
+                if (warp < 4) strong_chunk(sm, s, warp, lane);
                 __syncthreads();  // before the rows are overwritten
             }
         }
         // The operands, in the rows' places: a warp's own tokens, a lane's own channels.  Exponents: of a query
         // G - mid and of a key its negative; in a strong chunk from the chunk's start, and to its end.
         const float2 from = strong ? base : make_float2(base.x - mid.x, base.y - mid.y);
-        float2 to_end = sum;
-        if (strong)
-#pragma unroll
-            for (int x = 0; x < 8; ++x)
-                if (x > warp) to_end = add2(to_end, *reinterpret_cast<const float2*>(&sm.tot[x][c2]));
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t at = own + i * 128 + (((lane >> 2) ^ i) << 4);  // swz(8 warp + i, c2)
@@ -578,126 +642,134 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float2 lo = add2(k, make_float2(-lo_f(hi), -hi_f(hi)));
             *reinterpret_cast<uint32_t*>(sm.kl + at) = pack2(lo.x, lo.y);
         }
-        // What is owed goes with 2^mid, or before it: always in a strong chunk, and where both together would be
-        // too small for a float32 factor, though the accumulators, which hold 2^-owed times the state, are not.
-        const float2 both = add2(owed, mid);
-        const bool apart = strong || __any_sync(0xffffffffu, !(fminf(both.x, both.y) >= -120.f));
-        if (warp == 0) {
-            const float2 to = strong ? all : apart ? mid : both;
-            *reinterpret_cast<float2*>(&sm.c_pre[c2]) = make_float2(ptx::ex2_approx(to.x), ptx::ex2_approx(to.y));
-            *reinterpret_cast<float2*>(&sm.c_op[c2]) = make_float2(ptx::ex2_approx(owed.x), ptx::ex2_approx(owed.y));
+        if (warp == 1) {
+            const float2 one = make_float2(1.f, 1.f);
+            *reinterpret_cast<float2*>(&sm.c_all[c2]) = make_float2(ptx::ex2_approx(all.x), ptx::ex2_approx(all.y));
+            *reinterpret_cast<float2*>(&sm.c_op[c2]) =
+                strong ? one : make_float2(ptx::ex2_approx(mid.x), ptx::ex2_approx(mid.y));
+            *reinterpret_cast<float2*>(&sm.c_rest[c2]) =
+                strong ? one : make_float2(ptx::ex2_approx(rest.x), ptx::ex2_approx(rest.y));
         }
-        owed = strong ? make_float2(0.f, 0.f) : rest;
+        load_g(row + (size_t)(n + 1) * kT * stride, left - kT);  // the next chunk's
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
         __syncthreads();
-        // The state as the output's operand (2^mid C; of a strong chunk C) and as the update finds it (the same; all's
-        // retention applied).
-        const uint32_t c_row = (vt + g) * 128;
+        if (warp == 0) {
+            ptx::tc_fence_after();
+            const uint32_t q = desc(s.p1), kh = desc(s.p2), kl = desc(sm.kl), v = desc(s.v);
+            if (kOut) {  // (a strong chunk's are not used)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int c = ct + 8 * x + 2 * t;
-            const uint32_t at = c_row + ((((c >> 3) ^ g) & 7) << 4) + 4 * t;  // rows vt + g and 8 further
-            float2 lo = make_float2(C[x][0], C[x][1]), hi = make_float2(C[x][2], C[x][3]);
-            if (apart) {
-                const float2 f = *reinterpret_cast<const float2*>(&sm.c_op[c]);
-                lo = mul2(lo, f), hi = mul2(hi, f);
-                if (kOut && strong) {
-                    *reinterpret_cast<uint32_t*>(sm.c + at) = pack2(lo.x, lo.y);
-                    *reinterpret_cast<uint32_t*>(sm.c + at + 8 * 128) = pack2(hi.x, hi.y);
+                for (int ks = 0; ks < 4; ++ks)
+                    ptx::mma_ss_elect(tmem + kColW, q + ks * kStepK, desc_high, kh + ks * kStepK, desc_high, kKK, ks > 0);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                ptx::mma_ss_elect(tmem + kColC, v + (ks & 3) * kStepM, desc_high, (ks < 4 ? kh : kl) + (ks & 3) * kStepM,
+                                  desc_high, kMM, ks > 0);
+            ptx::mma_commit_elect(&sm.c_done);
+        }
+        if (kOut) {
+            // The state as an operand: 2^mid C, and C itself in a strong chunk.
+            uint32_t w[4][2];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const float2 f = *reinterpret_cast<const float2*>(&sm.c_op[col0 + 8 * x + 2 * t]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float2 a = mul2(C[x][e], f);
+                    w[x][e] = pack2(a.x, a.y);
                 }
             }
-            const float2 f = *reinterpret_cast<const float2*>(&sm.c_pre[c]);
-            lo = mul2(lo, f), hi = mul2(hi, f);
-            C[x][0] = lo.x, C[x][1] = lo.y, C[x][2] = hi.x, C[x][3] = hi.y;
-            if (kOut && !strong) {
-                *reinterpret_cast<uint32_t*>(sm.c + at) = pack2(lo.x, lo.y);
-                *reinterpret_cast<uint32_t*>(sm.c + at + 8 * 128) = pack2(hi.x, hi.y);
+            stsm4(ptx::smem_u32(sm.c) + frag_at, w[0][0], w[0][1], w[1][0], w[1][1]);
+            stsm4(ptx::smem_u32(sm.c) + frag_next, w[2][0], w[2][1], w[3][0], w[3][1]);
+        }
+        wait(&sm.c_done, n);
+        if (kOut) {
+            // The weights, in a strong chunk there already.
+            if (!strong) {
+                uint32_t x[4][4];
+                tmem_ld_frag(lane_addr + kColW, x);
+                uint32_t w[4][2];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int first = col0 + 8 * c - 16 * quarter;  // key 0 of the block from the warp's first row
+                    if (first > -8) {                               // strictly earlier keys only
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (first + 2 * t + (e & 1) >= g + 8 * (e >> 1)) x[c][e] = 0u;
+                    }
+                    w[c][0] = pack2(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+                    w[c][1] = pack2(__uint_as_float(x[c][2]), __uint_as_float(x[c][3]));
+                }
+                stsm4(ptx::smem_u32(sm.w) + frag_at, w[0][0], w[0][1], w[1][0], w[1][1]);
+                stsm4(ptx::smem_u32(sm.w) + frag_next, w[2][0], w[2][1], w[3][0], w[3][1]);
+            }
+            ptx::fence_proxy_async_smem();
+            ptx::tc_fence_before();
+            __syncthreads();
+            if (warp == 0) {
+                ptx::tc_fence_after();
+                const uint32_t q = desc(s.p1), v = desc(s.v), w = desc(sm.w), c = desc(sm.c);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    ptx::mma_ss_elect(tmem + kColO, q + ks * kStepK, desc_high, c + ks * kStepK, desc_high, kKK, ks > 0);
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    ptx::mma_ss_elect(tmem + kColO, w + ks * kStepK, desc_high, v + ks * kStepM, desc_high, kKM, 1);
+                ptx::mma_commit_elect(&sm.o_done);
+            }
+        }
+        // The state through the chunk.
+        {
+            uint32_t x[4][4];
+            tmem_ld_frag(lane_addr + kColC, x);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float2 a = *reinterpret_cast<const float2*>(&sm.c_all[col0 + 8 * c + 2 * t]);
+                const float2 f = *reinterpret_cast<const float2*>(&sm.c_rest[col0 + 8 * c + 2 * t]);
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    C[c][e] = fma2(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), f,
+                                   mul2(C[c][e], a));
             }
         }
         if (kOut) {
-            uint32_t aq[4][4];
-#pragma unroll
-            for (int ks = 0; ks < 4; ++ks) ldsm4(aq[ks], addr_a(s.p1 + rt * 16 * 128, 16 * ks, lane));
-            float E[4][4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) E[x][e] = 0.f;
-#pragma unroll
-            for (int kb = 0; kb < 4; ++kb) {
-                if (kb > rt) break;
-                if (!strong) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[2 * kb][e] = w[2 * kb + 1][e] = 0.f;
-#pragma unroll
-                    for (int ks = 0; ks < 4; ++ks) {
-                        uint32_t b[4];  // (keys 0-7, k 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15)
-                        ldsm4(b, addr_at(s.p2 + kb * 16 * 128, 16 * ks, lane));
-                        mma16816(w[2 * kb], aq[ks], b[0], b[1]);
-                        mma16816(w[2 * kb + 1], aq[ks], b[2], b[3]);
-                    }
-                }
-                if (kb == rt) {  // strictly earlier keys only
-#pragma unroll
-                    for (int y = 0; y < 2; ++y)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (8 * y + 2 * t + (e & 1) >= g + 8 * (e >> 1)) w[2 * kb + y][e] = 0.f;
-                }
-                const uint32_t a[4] = {pack2(w[2 * kb][0], w[2 * kb][1]), pack2(w[2 * kb][2], w[2 * kb][3]),
-                                       pack2(w[2 * kb + 1][0], w[2 * kb + 1][1]), pack2(w[2 * kb + 1][2], w[2 * kb + 1][3])};
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t b[4];
-                    ldsm4t(b, addr_bt(s.v + kb * 16 * 128, v0 + 16 * x, lane));
-                    mma16816(E[2 * x], a, b[0], b[1]);
-                    mma16816(E[2 * x + 1], a, b[2], b[3]);
-                }
+            uint32_t v[4][2];  // the tokens' own states, as fragments
+            {
+                uint32_t x[4];
+                ldsm4(x, ptx::smem_u32(s.v) + frag_at);
+                v[0][0] = x[0], v[0][1] = x[1], v[1][0] = x[2], v[1][1] = x[3];
+                ldsm4(x, ptx::smem_u32(s.v) + frag_next);
+                v[2][0] = x[0], v[2][1] = x[1], v[3][0] = x[2], v[3][1] = x[3];
             }
-            __syncthreads();  // the state's operand is there
+            wait(&sm.o_done, n);
+            uint32_t x[4][4];
+            tmem_ld_frag(lane_addr + kColO, x);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
+            for (int e = 0; e < 2; ++e) {
+                if (r0 + 8 * e >= left || !ok) continue;
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.Y) + row + ((size_t)n * kT + r0 + 8 * e) * stride + col0 + 2 * t;
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t b[4];
-                    ldsm4(b, addr_at(sm.c + (v0 + 16 * x) * 128, 16 * ks, lane));
-                    mma16816(E[2 * x], aq[ks], b[0], b[1]);
-                    mma16816(E[2 * x + 1], aq[ks], b[2], b[3]);
+                for (int c = 0; c < 4; ++c) {
+                    const float2 o = add2(make_float2(lo_f(v[c][e]), hi_f(v[c][e])),
+                                          make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])));
+                    if (col0 + 8 * c + 2 * t < p.d) *reinterpret_cast<uint32_t*>(y + 8 * c) = pack2(o.x, o.y);
                 }
-            const uint32_t v_at = (16 * rt + g) * 128 + 4 * t;
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                if (16 * rt + g + 8 * half >= left) continue;
-                __nv_bfloat16* y = Y + 8 * half * ystride;
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    if (v0 + 8 * x + 2 * t >= p.d) continue;
-                    const uint32_t i = *reinterpret_cast<const uint32_t*>(
-                        s.v + v_at + 8 * half * 128 + ((((v0 >> 3) + x) ^ g) << 4));  // swz(16 rt + g + 8 half, v)
-                    const float2 o = add2(make_float2(lo_f(i), hi_f(i)), make_float2(E[x][2 * half], E[x][2 * half + 1]));
-                    *reinterpret_cast<uint32_t*>(y + 8 * x) = pack2(o.x, o.y);
-                }
-            }
-            Y += kT * ystride;
-        }
-        // C^T += I~^T k~.
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t a[4];
-            ldsm4t(a, addr_at(s.v + ks * 16 * 128, vt, lane));
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                uint32_t b[4];
-                ldsm4t(b, addr_bt(s.p2 + ks * 16 * 128, ct + 16 * x, lane));
-                mma16816(C[2 * x], a, b[0], b[1]);
-                mma16816(C[2 * x + 1], a, b[2], b[3]);
-                ldsm4t(b, addr_bt(sm.kl + ks * 16 * 128, ct + 16 * x, lane));
-                mma16816(C[2 * x], a, b[0], b[1]);
-                mma16816(C[2 * x + 1], a, b[2], b[3]);
             }
         }
+        ptx::tc_fence_before();
     }
-    if (warp == 0) *reinterpret_cast<float2*>(&sm.c_op[c2]) = make_float2(ptx::ex2_approx(owed.x), ptx::ex2_approx(owed.y));
+    if (warp == 0 && *abort_flag) {  // let what is in flight end before its memory goes
+        ptx::mma_commit_elect(&sm.drain);
+        ptx::mbar_drain(&sm.drain, 0, p.status);
+    }
+    cp_async_wait<0>();
+    ptx::tc_fence_before();
     __syncthreads();
+    if (warp == 0) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, kTmemCols);
+    }
     float* out = mine;
     int ld = kDp;
     if (kOut) {
@@ -708,11 +780,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (out != nullptr) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
+        for (int n = 0; n < 4; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int v = vt + g + 8 * (e >> 1), c = ct + 8 * x + 2 * t + (e & 1);
-                if (v < ld && c < ld) out[(size_t)c * ld + v] = C[x][e] * sm.c_op[c];
+            for (int e = 0; e < 2; ++e) {
+                const int v = r0 + 8 * e, c = col0 + 8 * n + 2 * t;
+                if (v < ld && c < ld) out[(size_t)c * ld + v] = C[n][e].x, out[(size_t)(c + 1) * ld + v] = C[n][e].y;
             }
     }
     // (few calls: the whole chain ends with this kernel's end)
@@ -724,17 +796,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 // loads, not the bytes.
 constexpr int kScanThreads = 128;
 __global__ void __launch_bounds__(kScanThreads)
-    linear_join_kernel(const __grid_constant__ LinearPool p, const Item* __restrict__ items, float* __restrict__ segments) {
+    linear_join_kernel(const __grid_constant__ LinearPool p, const Item* __restrict__ items, const int* __restrict__ joins,
+                       float* __restrict__ segments) {
     dependency_wait();
     dependency_release();
-    const Item it = items[blockIdx.x];
-    const int seg = it.seg_segs & 0xffff, segs = it.seg_segs >> 16, h = blockIdx.y;
-    if (seg != 0 || segs < 2) return;
+    const int at = joins[blockIdx.x];
+    if (at < 0) return;
+    const Item it = items[at];
+    const int segs = it.seg_segs >> 16, h = blockIdx.y;
     const int e = blockIdx.z * kScanThreads + threadIdx.x, c = e >> 6, v = e & 63;
     const float* in = state_of(p, __ldg(p.slots_in + it.r), h);
     float C = in != nullptr && c < p.d && v < p.d ? in[(size_t)c * p.d + v] : 0.f;
     const size_t step = (size_t)p.H * kSegFloats;
-    float* H = segments + ((size_t)blockIdx.x * p.H + h) * kSegFloats;
+    float* H = segments + ((size_t)at * p.H + h) * kSegFloats;
     constexpr int kAhead = 16;
     for (int s0 = 0; s0 < segs; s0 += kAhead) {
         float x[kAhead], a[kAhead];
@@ -759,6 +833,7 @@ struct Cut {
     bool chunked;     // a request may have more than kFewTokens new tokens
     bool segmented;   // and more than seg_tokens
     int seg_tokens, items;
+    int joins;        // requests of more than one segment
 };
 Cut cut_of(int R, int N, int H, int max_fresh, int num_sms) {
     Cut c{};
@@ -766,15 +841,17 @@ Cut cut_of(int R, int N, int H, int max_fresh, int num_sms) {
     if (!c.chunked) return c;
     // A segment as long as a block's equal share of all tokens, 256 at least: shorter ones cost more
     // in the state pass and the join than they spread.
-    const int64_t share = ((int64_t)N * H / (2 * num_sms) + kT - 1) / kT * kT;
+    const int64_t share = ((int64_t)N * H / (kBlocksPerSm * num_sms) + kT - 1) / kT * kT;
     int64_t seg = std::max<int64_t>(256, share);
     seg = std::max<int64_t>(seg, ((int64_t)max_fresh / (kMaxSegs - 1) + kT) / kT * kT);
     c.seg_tokens = (int)std::min<int64_t>(seg, (INT32_MAX - kT) / kT * kT);
     c.segmented = max_fresh > c.seg_tokens;
     c.items = c.segmented ? (int)std::min<int64_t>((int64_t)N / c.seg_tokens + std::min(R, N / (kFewTokens + 1)), INT32_MAX) : R;
+    c.joins = std::min(R, N / (c.seg_tokens + 1));
     return c;
 }
-size_t items_bytes(const Cut& c) { return ((size_t)c.items * sizeof(Item) + 255) / 256 * 256; }
+// The list of segments, then the list of joins.
+size_t items_bytes(const Cut& c) { return ((size_t)c.items * sizeof(Item) + (size_t)c.joins * sizeof(int) + 255) / 256 * 256; }
 
 template <typename... P, typename... A>
 cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
@@ -792,12 +869,12 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cuda
 }
 
 template <bool kGate>
-cudaError_t launch_few(const LinearPool& p, Item* items, const Cut& cut, cudaStream_t s) {
+cudaError_t launch_few(const LinearPool& p, Item* items, int* joins, const Cut& cut, cudaStream_t s) {
     const dim3 grid((unsigned)((int64_t)p.R * p.H + (items != nullptr)));
     switch (p.d) {
-        case 48: return launch(linear_few_kernel<48, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, cut.seg_tokens);
-        case 60: return launch(linear_few_kernel<60, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, cut.seg_tokens);
-        case 64: return launch(linear_few_kernel<64, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, cut.seg_tokens);
+        case 48: return launch(linear_few_kernel<48, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, joins, cut.joins, cut.seg_tokens);
+        case 60: return launch(linear_few_kernel<60, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, joins, cut.joins, cut.seg_tokens);
+        case 64: return launch(linear_few_kernel<64, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, joins, cut.joins, cut.seg_tokens);
     }
     return cudaErrorInvalidValue;
 }
@@ -806,10 +883,11 @@ template <bool kGate>
 cudaError_t launch_pool(const LinearPool& p, void* workspace, const Cut& cut, int* launches, cudaStream_t s) {
     Item* items = cut.segmented ? static_cast<Item*>(workspace) : nullptr;
     float* segments = cut.segmented ? reinterpret_cast<float*>(static_cast<char*>(workspace) + items_bytes(cut)) : nullptr;
-    cudaError_t e = launch_few<kGate>(p, items, cut, s);
+    int* joins = cut.segmented ? reinterpret_cast<int*>(items + cut.items) : nullptr;
+    cudaError_t e = launch_few<kGate>(p, items, joins, cut, s);
     *launches = 1;
     if (e != cudaSuccess || !cut.chunked) return e;
-    constexpr int smem = (int)sizeof(ChunkSmem);
+    constexpr int smem = (int)sizeof(ChunkSmem) + 1024;
     static OncePerDevice once_out, once_state;
     if ((e = allow_dynamic_smem(once_out, linear_chunk_kernel<true, kGate>, smem)) != cudaSuccess) return e;
     if ((e = allow_dynamic_smem(once_state, linear_chunk_kernel<false, kGate>, smem)) != cudaSuccess) return e;
@@ -818,8 +896,8 @@ cudaError_t launch_pool(const LinearPool& p, void* workspace, const Cut& cut, in
         *launches = 4;
         e = launch(linear_chunk_kernel<false, kGate>, grid, kThreads, smem, s, p, items, segments);
         if (e != cudaSuccess) return e;
-        e = launch(linear_join_kernel, dim3(grid.x, grid.y, kDp * kDp / kScanThreads), kScanThreads, 0, s, p, items,
-                   segments);
+        e = launch(linear_join_kernel, dim3((unsigned)cut.joins, grid.y, kDp * kDp / kScanThreads), kScanThreads, 0, s, p,
+                   items, joins, segments);
         if (e != cudaSuccess) return e;
     } else {
         *launches = 2;

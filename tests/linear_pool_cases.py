@@ -64,7 +64,7 @@ def check(x, Y, states, chunked=True):
     rows = ~np.isnan(Yr)
     got = Y.double().cpu().numpy()
     tol = 2.0 ** -8 * np.abs(Yr) + (3 * 2.0 ** -8 if chunked else 2.0 ** -18) * 1.01 * Ya + 2.0 ** -20
-    bad = np.abs(got - Yr)[rows] > tol[rows]
+    bad = ~(np.abs(got - Yr)[rows] <= tol[rows])  # (a NaN is no smaller than anything)
     assert not bad.any(), (int(bad.sum()), float((np.abs(got - Yr)[rows] / tol[rows]).max()))
     tol = 2.0 ** -14 * Sa + 2.0 ** -20 * max(1.0, float(Sa.max()))
     off = np.abs(states.double().cpu().numpy() - Sr)
