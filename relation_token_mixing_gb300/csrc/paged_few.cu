@@ -28,6 +28,7 @@
 // the bf16 output; the weights are rounded to bf16 for the second product (as the
 // operands are), their sum is not.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
@@ -85,8 +86,10 @@ struct FewCfg {
     static constexpr int kPanels = DK > 4 ? 2 : 1;  // 64-column panels
     // Workers of a block and stages of each: 192 KB in all.  128 columns and 8 rows: 4 x 3
     // (decode 32 x 32k: 268 us, 6 x 2: 278 us); 16 rows, more work a key: 6 x 2 (a mixed step
-    // of 80-wide heads: 84 us, 4 x 3: 89 us).
-    static constexpr int kWarps = Q8 ? (kPanels == 1 ? 12 : NT == 1 ? 10 : 8) : kPanels == 1 ? 12 : NT == 1 ? 4 : 6;
+    // of 80-wide heads: 84 us, 4 x 3: 89 us).  8-bit pages, half the bytes and more work for each, want workers:
+    // 128 columns and 8 rows 11 x 2 (decode 32 x 32k: 180 us, 10 x 2: 195, 8 x 2: 207); 64 columns 12 x 3 (drafted
+    // tokens: 45 us, 8 x 5: 51).
+    static constexpr int kWarps = Q8 ? (kPanels == 1 ? 12 : NT == 1 ? 11 : 8) : kPanels == 1 ? 12 : NT == 1 ? 4 : 6;
     static constexpr int kStages = Q8 ? (kPanels == 1 ? 3 : 2) : kPanels == 2 && NT == 1 ? 3 : 2;
     static constexpr int kThreads = kWarps * 32;
     // A copy's rows: a panel's 128 bytes, or (Q8) all of a row's 64 or 128.
@@ -141,12 +144,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Bytes 0 and 2 of four whole numbers as a pair of f16, exactly: with the sign flipped a byte is b + 128, and
-// under f16's exponent of 1024 its low bits stand for 1024 + 128 + b.
+// Bytes 0 and 2 of four whole numbers b as a pair of f16, each b + 1152: with the sign flipped a byte is b + 128, and
+// under f16's exponent of 1024 its low bits stand for themselves.
+constexpr float kByteBias = 1152.f;
+__device__ __forceinline__ uint32_t biased_f16(uint32_t w) { return (w & 0x00ff00ffu) ^ 0x64806480u; }
+// The same without the bias, exactly.
 __device__ __forceinline__ uint32_t even_bytes_f16(uint32_t w) {
-    const uint32_t x = (w & 0x00ff00ffu) ^ 0x64806480u;
     uint32_t r;
-    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(0xe480e480u));  // - 1152
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(biased_f16(w)), "r"(0xe480e480u));
     return r;
 }
 __device__ __forceinline__ uint32_t odd_bytes_f16(uint32_t w) { return even_bytes_f16(w >> 8); }
@@ -196,7 +201,8 @@ constexpr float kLeastScale = -64.f;
 // A unit has all of a request's packed rows of one cache head.
 //
 // 8-bit pages (Q8).  The whole numbers go to the products as f16, which holds them exactly, so
-// the work a byte is a fetch by ldmatrix (of byte pairs), a masked exclusive-or and an f16 add for two.
+// the work a byte is a fetch by ldmatrix (of byte pairs), a masked exclusive-or and, for I~, an f16 add for two; P2's
+// numbers keep the bias that the exclusive-or gives them, and the scores begin at minus what it adds.
 // The bytes of a 16-bit unit are neighbours in a row, so the columns (of P2) or channels (of I~) come in
 // another order, which P1's fragments and the output's columns follow.  P2's scale multiplies
 // the score; P1's rows are f16 under a power of two of their own.  I~'s scale s multiplies the weight
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
     int j_begin = u.j, len = 0, nt_used = NT;
     // A lane holds packed rows 8 n + 2 (lane % 4) and the next one, of keys lane / 4 (+ 8).
     uint32_t qf[NT][DK][2];
-    float o[NT][DK][4], m[NT][2], l[NT][2], corr[NT][2], row_scale[NT][2];
+    float o[NT][DK][4], m[NT][2], l[NT][2], corr[NT][2], row_scale[NT][2], row_bias[NT][2];
     int pos[NT][2];
     const int key0 = lane >> 2, col0 = 2 * (lane & 3);
     const float c_half = 0.5f * pp.inv_sqrt_d, c_self = c_half / pp.tau_S, inv_tau = 1.f / pp.tau_S;
@@ -341,9 +347,22 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
                     qf[n][ks][1] =
                         pack_f16x2(__uint_as_float(w0 & 0xffff0000u) * inv, __uint_as_float(w1 & 0xffff0000u) * inv);
                 }
+                // What the bias of P2's bytes adds to the row's products, taken off before.
+                float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int ks = 0; ks < DK; ++ks)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&qf[n][ks][e]));
+                        sum += x.x + x.y;
+                    }
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
                     row_scale[n][e] = __uint_as_float(__shfl_sync(0xffffffffu, ex, 4 * (col0 + e)) << 23) * c_half;
+                    row_bias[n][e] = -kByteBias * __shfl_sync(0xffffffffu, sum, 4 * (col0 + e));
+                }
             } else {
 #pragma unroll
                 for (int ks = 0; ks < DK; ++ks)
@@ -471,6 +490,12 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
         float sc[NT][2][4] = {};
         if constexpr (Q8) {
 #pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[n][mt][e] = row_bias[n][e & 1];
+#pragma unroll
             for (int k2 = 0; k2 < DK; k2 += 2)
 #pragma unroll
                 for (int mt = 0; mt < 2; ++mt) {
@@ -479,8 +504,8 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
                         if (k2 + x >= DK) break;
-                        const uint32_t a[4] = {even_bytes_f16(w[2 * x]), even_bytes_f16(w[2 * x + 1]),
-                                               odd_bytes_f16(w[2 * x]), odd_bytes_f16(w[2 * x + 1])};
+                        const uint32_t a[4] = {biased_f16(w[2 * x]), biased_f16(w[2 * x + 1]), biased_f16(w[2 * x] >> 8),
+                                               biased_f16(w[2 * x + 1] >> 8)};
 #pragma unroll
                         for (int n = 0; n < NT; ++n)
                             if (n < nt_used) mma16816_f16(sc[n][mt], a, qf[n][k2 + x][0], qf[n][k2 + x][1]);
@@ -504,23 +529,51 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
         for (int n = 0; n < NT; ++n) {
             if (n >= nt_used) break;
             mt_[n][0] = mt_[n][1] = -INFINITY;
+            if constexpr (Q8) {
 #pragma unroll
-            for (int mt = 0; mt < 2; ++mt)
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {  // the lane's two rows of one key
+                        float2 x = make_float2(sc[n][mt][2 * k], sc[n][mt][2 * k + 1]);
+                        const float f = key_scale[mt][k], up = val_log[mt][k];
+                        const float2 h = ptx::mul2(ptx::mul2(x, make_float2(f, f)), make_float2(row_scale[n][0], row_scale[n][1]));
+                        x = ptx::mul2(ptx::fma2(h, make_float2(ptx::tanh_approx(h.x), ptx::tanh_approx(h.y)), h),
+                                      make_float2(kLog2e, kLog2e));
+                        if (edge) {
+                            const int j = tok + mt * 16 + key0 + k * 8;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float& r = e ? x.y : x.x;
+                                if (j == pos[n][e])
+                                    r = fmaf(0.5f * kLog2e, ptx::tanh_approx((e ? h.y : h.x) * inv_tau), 0.5f * kLog2e) +
+                                        corr[n][e];
+                                else if (j > pos[n][e])
+                                    r = -INFINITY;
+                            }
+                        }
+                        sc[n][mt][2 * k] = x.x, sc[n][mt][2 * k + 1] = x.y;
+                        const float2 y = ptx::add2(x, make_float2(up, up));
+                        mt_[n][0] = fmaxf(mt_[n][0], y.x);
+                        mt_[n][1] = fmaxf(mt_[n][1], y.y);
+                    }
+            }
+#pragma unroll
+            for (int mt = 0; mt < (Q8 ? 0 : 2); ++mt)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float x = sc[n][mt][e];
-                    const float h = Q8 ? x * key_scale[mt][e >> 1] * row_scale[n][e & 1] : x * c_half;
+                    const float h = x * c_half;
                     float r = fmaf(h, ptx::tanh_approx(h), h) * kLog2e;  // SiLU(U) = (U/2)(1 + tanh(U/2))
                     if (edge) {
                         const int j = tok + mt * 16 + key0 + (e >> 1) * 8;
                         if (j == pos[n][e & 1])
-                            r = fmaf(0.5f * kLog2e, ptx::tanh_approx(Q8 ? h * inv_tau : x * c_self), 0.5f * kLog2e) +
+                            r = fmaf(0.5f * kLog2e, ptx::tanh_approx(x * c_self), 0.5f * kLog2e) +
                                 corr[n][e & 1];
                         else if (j > pos[n][e & 1])
                             r = -INFINITY;
                     }
                     sc[n][mt][e] = r;
-                    mt_[n][e & 1] = fmaxf(mt_[n][e & 1], Q8 ? r + val_log[mt][e >> 1] : r);
+                    mt_[n][e & 1] = fmaxf(mt_[n][e & 1], r);
                 }
             raise |= mt_[n][0] > m[n][0] + kRaise || mt_[n][1] > m[n][1] + kRaise;
         }
@@ -552,12 +605,20 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
+                    if constexpr (Q8) {
+                        const float2 y = ptx::add2(make_float2(sc[n][mt][2 * h], sc[n][mt][2 * h + 1]), make_float2(-b0, -b1));
+                        const float2 w = make_float2(ptx::ex2_approx(y.x), ptx::ex2_approx(y.y));
+                        const float2 sum = ptx::add2(make_float2(l[n][0], l[n][1]), w);
+                        l[n][0] = sum.x, l[n][1] = sum.y;
+                        const float2 v = ptx::mul2(w, make_float2(val_scale[mt][h], val_scale[mt][h]));
+                        pb[n][mt][h] = turn8(pack_f16x2(v.x, v.y));
+                        continue;
+                    }
                     const float p0 = ptx::ex2_approx(sc[n][mt][2 * h] - b0);
                     const float p1 = ptx::ex2_approx(sc[n][mt][2 * h + 1] - b1);
                     l[n][0] += p0;
                     l[n][1] += p1;
-                    pb[n][mt][h] = turn8(Q8 ? pack_f16x2(p0 * val_scale[mt][h], p1 * val_scale[mt][h])
-                                            : ptx::pack_bf16x2(p0, p1));
+                    pb[n][mt][h] = turn8(ptx::pack_bf16x2(p0, p1));
                 }
         }
         if constexpr (Q8) {
