@@ -14,7 +14,9 @@
 //
 // One pass, as paged_store.cu: every element is read once and written once.  4, 8 or 16 lanes have a
 // row (columns c and c + d/2 together, as RoPE turns them) and find its largest value among
-// themselves, so a row never leaves its registers between the prologue and its pages.
+// themselves, so a row never leaves its registers between the prologue and its pages.  Both kernels
+// move bytes.  Measured, 16384 tokens, 32 heads over 8 of 128: the store 77 us (370 MB, 4.8 TB/s), the rows
+// read back right after it 15 us (101 MB, 6.6 TB/s, the pages still in L2); 4999 tokens, 8 heads of 60: 14.7 and 4.5 us.
 #include <math.h>
 
 #include <algorithm>
@@ -27,7 +29,9 @@ namespace relation {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTokens = 4;  // of one block
+// Tokens of one block: the angles of the next block's are computed while this one moves rows.  16384 tokens, 32 heads over
+// 8 of 128: 2: 81 us, 4: 77, 8: 75; 4999 tokens, 8 heads of 60: 15.3, 14.7, 16.5.
+constexpr int kMaxTokens = 4;
 
 // The scale's bits as a float: of the bits of max |x|, m 2^e, it takes the exponent e - 6, or e - 5
 // where m is above 127 / 64.
@@ -61,9 +65,12 @@ __global__ void __launch_bounds__(kThreads)
                           const __grid_constant__ RopeTable tab, const int* __restrict__ positions,
                           const int64_t* __restrict__ slots, __nv_bfloat16* __restrict__ P1, int8_t* __restrict__ P2_pages,
                           int8_t* __restrict__ I_pages, __nv_bfloat16* __restrict__ scales, unsigned int* status,
-                          int tokens) {
+                          int tokens, FastDiv by_rows) {
     constexpr int D = 2 * HALF, PER = HALF / VC;
-    extern __shared__ float2 sh[];  // (cos, sin) [tokens][HALF], then [G/2] of the head pairs
+    // Rows of a thread on their way at once: one of 32 bytes, or two of 8.  Two of 32 bytes take 98 registers, and 16 warps
+    // of an SM move less than 32 do (d = 128: 110 us against 77); one of 8 bytes leaves a warp waiting (d = 60: 17 against 14.7).
+    constexpr int FLY = VC == 2 ? 2 : 1;
+    extern __shared__ float2 sh[];  // (cos, sin) [tokens][VC][PER]: a row's lanes side by side, then [G/2] of the head pairs
     __shared__ int64_t s_row[kMaxTokens];  // the token's row of cache head 0, counted in rows, or -1
     float2* turn = sh;
     float2* mix = sh + kMaxTokens * HALF;
@@ -79,7 +86,7 @@ __global__ void __launch_bounds__(kThreads)
         const int t = k / HALF, c = k - t * HALF;
         float sn = 0.f, cs = 1.f;
         if (tab.enabled) position_sincos(positions[n0 + t], tab.hi[c], tab.lo[c], &sn, &cs);
-        turn[k] = make_float2(cs, sn);
+        turn[t * HALF + c % VC * PER + c / VC] = make_float2(cs, sn);
     }
     if (theta != nullptr)
         for (int k = threadIdx.x; k < pp.G / 2; k += kThreads) {
@@ -90,62 +97,67 @@ __global__ void __launch_bounds__(kThreads)
     __syncthreads();
     const int64_t head = (int64_t)page_row_index(pp, 0, 0, 1);  // rows from one cache head to the next
     const int lane = threadIdx.x % LANES, c = lane * VC;
-    const int rows = pp.H + 2 * pp.G;
     // The block's rows of all its tokens, one after another: H of X1, G of X2, G of I.
-    const int total = rows * count;
-    for (int k0 = threadIdx.x / 32 * (32 / LANES); k0 < total; k0 += kThreads / LANES) {
-        const int k = k0 + (int)(threadIdx.x % 32) / LANES;
-        const bool in = k < total && lane < PER;
-        const int t = in ? k / rows : 0, j = in ? k - t * rows : 0, n = n0 + t;
+    const int rows = pp.H + 2 * pp.G, total = rows * count;
+    struct Row {
+        Vec<__nv_bfloat16, VC> a, b, mate_a, mate_b;  // columns c and c + d/2 (and of a mixed row its partner's)
+        int t, j;                                     // token, row of it; j < 0: none
+        float2 mix;                                   // the row is mix.x times itself and mix.y times its partner
+    };
+    auto fetch = [&](int k, Row& r) {
+        r.t = by_rows.div(k);
+        r.j = k < total && lane < PER ? k - r.t * rows : -1;
+        if (r.j < 0) return;
+        const int n = n0 + r.t, g = r.j < pp.H + pp.G ? r.j - pp.H : r.j - pp.H - pp.G;
+        const __nv_bfloat16* src = (r.j < pp.H ? X1 + ((size_t)n * pp.H + r.j) * D
+                                               : (r.j < pp.H + pp.G ? X2 : I) + ((size_t)n * pp.G + g) * D) + c;
+        r.a.load(src);
+        r.b.load(src + HALF);
+        if (theta != nullptr && r.j >= pp.H + pp.G) {  // the first of a pair: cos a - sin b, the second: sin a + cos b
+            int pair;
+            bool first;
+            const int other = givens_partner(g, pp.G, pairing, &pair, &first);
+            const float2 w = mix[pair];
+            r.mix = make_float2(w.x, first ? -w.y : w.y);
+            const __nv_bfloat16* mate = I + ((size_t)n * pp.G + other) * D + c;
+            r.mate_a.load(mate);
+            r.mate_b.load(mate + HALF);
+        }
+    };
+    auto finish = [&](Row& r) {
         float a[VC], b[VC];
-        Vec<__nv_bfloat16, VC> va, vb;
         uint32_t top = 0;
+        const bool in = r.j >= 0, key = r.j < pp.H + pp.G;
         if (in) {
-            const int g = j < pp.H + pp.G ? j - pp.H : j - pp.H - pp.G;
-            if (j < pp.H + pp.G) {
-                const __nv_bfloat16* src = (j < pp.H ? X1 + ((size_t)n * pp.H + j) * D : X2 + ((size_t)n * pp.G + g) * D) + c;
-                va.load(src);
-                vb.load(src + HALF);
-                float x[VC], y[VC];
-                va.unpack(x);
-                vb.unpack(y);
+            float x[VC], y[VC];
+            r.a.unpack(x);
+            r.b.unpack(y);
+            if (key) {
 #pragma unroll
                 for (int e = 0; e < VC; ++e) {
-                    const float2 w = turn[t * HALF + c + e];
+                    const float2 w = turn[r.t * HALF + e * PER + lane];
                     a[e] = w.x * x[e] - w.y * y[e];
                     b[e] = w.y * x[e] + w.x * y[e];
                 }
             } else {
-                const __nv_bfloat16* src = I + ((size_t)n * pp.G + g) * D + c;
-                va.load(src);
-                vb.load(src + HALF);
-                va.unpack(a);
-                vb.unpack(b);
-                if (theta != nullptr) {  // the first of a pair: cos a - sin b, the second: sin a + cos b
-                    int pair;
-                    bool first;
-                    const int other = givens_partner(g, pp.G, pairing, &pair, &first);
-                    const float2 w = mix[pair];
-                    const float sn = first ? -w.y : w.y;
-                    const __nv_bfloat16* mate = I + ((size_t)n * pp.G + other) * D + c;
-                    va.load(mate);
-                    vb.load(mate + HALF);
-                    float x[VC], y[VC];
-                    va.unpack(x);
-                    vb.unpack(y);
+#pragma unroll
+                for (int e = 0; e < VC; ++e) a[e] = x[e], b[e] = y[e];
+                if (theta != nullptr) {
+                    r.mate_a.unpack(x);
+                    r.mate_b.unpack(y);
 #pragma unroll
                     for (int e = 0; e < VC; ++e) {
-                        a[e] = w.x * a[e] + sn * x[e];
-                        b[e] = w.x * b[e] + sn * y[e];
+                        a[e] = r.mix.x * a[e] + r.mix.y * x[e];
+                        b[e] = r.mix.x * b[e] + r.mix.y * y[e];
                     }
                 }
             }
-            if (j < pp.H) {
-                va.pack(a);
-                vb.pack(b);
-                __nv_bfloat16* dst = P1 + ((size_t)n * pp.H + j) * D + c;
-                va.store(dst);
-                vb.store(dst + HALF);
+            if (r.j < pp.H) {
+                r.a.pack(a);
+                r.b.pack(b);
+                __nv_bfloat16* dst = P1 + ((size_t)(n0 + r.t) * pp.H + r.j) * D + c;
+                r.a.store(dst);
+                r.b.store(dst + HALF);
             } else {
 #pragma unroll
                 for (int e = 0; e < VC; ++e)  // as whole numbers, so that a NaN is above all
@@ -154,11 +166,11 @@ __global__ void __launch_bounds__(kThreads)
         }
 #pragma unroll
         for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (!in || j < pp.H || s_row[t] < 0) continue;
-        const bool finite = top < 0x7f800000u, key = j < pp.H + pp.G;
+        if (!in || r.j < pp.H || s_row[r.t] < 0) return;
+        const bool finite = top < 0x7f800000u;
         const uint32_t ex = scale_exponent(top);
         const float inv = finite ? __uint_as_float((254u - ex) << 23) : 0.f;
-        const int64_t row = s_row[t] + (key ? j - pp.H : j - pp.H - pp.G) * head;
+        const int64_t row = s_row[r.t] + (key ? r.j - pp.H : r.j - pp.H - pp.G) * head;
         int8_t* dst = (key ? P2_pages : I_pages) + (size_t)row * pp.row + c;
         if (!finite)
 #pragma unroll
@@ -167,19 +179,28 @@ __global__ void __launch_bounds__(kThreads)
         store_q8<VC>(dst + HALF, b, inv);
         if (lane == 0)
             scales[2 * row + (key ? 0 : 1)] = __ushort_as_bfloat16(finite ? (unsigned short)(ex << 7) : (unsigned short)0x7fc0);
+    };
+    constexpr int kStep = kThreads / LANES;
+    for (int k0 = threadIdx.x / 32 * (32 / LANES); k0 < total; k0 += FLY * kStep) {
+        const int k = k0 + (int)(threadIdx.x % 32) / LANES;
+        Row r[FLY];
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) fetch(k + f * kStep, r[f]);
+#pragma unroll
+        for (int f = 0; f < FLY; ++f) finish(r[f]);
     }
 }
 
-// Rows [N, G, d] of some slots, as the values they stand for (exact in bf16): VC columns a thread.
-template <int VC>
+// Rows [N, G, d] of some slots, as the values they stand for (exact in bf16): VC columns a thread, PER = d / VC threads
+// a row, `tokens` tokens a block.
+template <int VC, int PER>
 __global__ void __launch_bounds__(kThreads)
     paged_read_q8_kernel(PagedProblem pp, const int64_t* __restrict__ slots, const int8_t* __restrict__ P2_pages,
                          const int8_t* __restrict__ I_pages, const __nv_bfloat16* __restrict__ scales,
-                         __nv_bfloat16* __restrict__ P2, __nv_bfloat16* __restrict__ I, unsigned int* status, int64_t total) {
-    const int per = pp.d / VC;
-    for (int64_t k = (int64_t)blockIdx.x * kThreads + threadIdx.x; k < total; k += (int64_t)gridDim.x * kThreads) {
-        const int64_t ng = k / per;  // token and cache head
-        const int c = (int)(k - ng * per) * VC, n = (int)(ng / pp.G), g = (int)(ng - (int64_t)n * pp.G);
+                         __nv_bfloat16* __restrict__ P2, __nv_bfloat16* __restrict__ I, unsigned int* status, int tokens) {
+    const int n0 = blockIdx.x * tokens, count = min(tokens, pp.N - n0), items = count * pp.G * PER;
+    for (int k = threadIdx.x; k < items; k += kThreads) {
+        const int row_of = k / PER, c = (k - row_of * PER) * VC, t = pp.by_G.div(row_of), g = row_of - t * pp.G, n = n0 + t;
         const int64_t slot = slots[n];
         const bool in = slot >= 0 && slot < ((int64_t)pp.pages << pp.page_shift);
         if (slot >= 0 && !in) record_status(status, kDevBadPosition);
@@ -189,8 +210,8 @@ __global__ void __launch_bounds__(kThreads)
         if (in) {
 #pragma unroll
             for (int w = 0; w < VC / 4; ++w) {
-                x[0][w] = *reinterpret_cast<const uint32_t*>(P2_pages + row * pp.row + c + 4 * w);
-                x[1][w] = *reinterpret_cast<const uint32_t*>(I_pages + row * pp.row + c + 4 * w);
+                x[0][w] = __ldg(reinterpret_cast<const uint32_t*>(P2_pages + row * pp.row + c + 4 * w));
+                x[1][w] = __ldg(reinterpret_cast<const uint32_t*>(I_pages + row * pp.row + c + 4 * w));
             }
         }
 #pragma unroll
@@ -201,7 +222,7 @@ __global__ void __launch_bounds__(kThreads)
             for (int e = 0; e < VC; ++e) v[e] = s * (float)(int8_t)(x[which][e / 4] >> (8 * (e % 4)));
             Vec<__nv_bfloat16, VC> out;
             out.pack(v);
-            out.store((which ? I : P2) + (size_t)ng * pp.d + c);
+            out.store((which ? I : P2) + ((size_t)n * pp.G + g) * pp.d + c);
         }
     }
 }
@@ -220,7 +241,7 @@ cudaError_t launch_paged_store_q8(const PagedProblem& pp, const void* X1, const 
 #define STORE(HALF, VC, LANES)                                                                                      \
     paged_store_q8_kernel<HALF, VC, LANES><<<blocks, kThreads, sh, s>>>(                                             \
         pp, (const B*)X1, (const B*)X2, (const B*)I, theta, pairing, tab, positions, slots, (B*)P1, (int8_t*)P2_pages, \
-        (int8_t*)I_pages, (B*)scales, status, tokens);                                                               \
+        (int8_t*)I_pages, (B*)scales, status, tokens, FastDiv((uint32_t)(pp.H + 2 * pp.G)));                          \
     return cudaGetLastError()
     switch (pp.d) {  // the widest access that d/2 columns and the rows' alignment allow
         case 48: STORE(24, 8, 4);
@@ -237,15 +258,23 @@ cudaError_t launch_paged_read_q8(const PagedProblem& pp, const int64_t* slots, c
                                  const void* scales, void* P2, void* I, unsigned int* status, int num_sms,
                                  cudaStream_t s) {
     using B = __nv_bfloat16;
-    const int vc = pp.d % 8 == 0 ? 8 : 4;
-    const int64_t total = (int64_t)pp.N * pp.G * (pp.d / vc);
-    const unsigned blocks = (unsigned)std::min<int64_t>((total + kThreads - 1) / kThreads, (int64_t)num_sms * 64);
+    // Two rounds of a block's threads, as long as that leaves some blocks for every SM.
+    const int vc = pp.d % 8 == 0 ? 8 : 4, per_token = pp.G * (pp.d / vc);
+    const int tokens = (int)std::max<int64_t>(1, std::min<int64_t>(2 * kThreads / per_token, (int64_t)pp.N / (4 * num_sms)));
+    const unsigned blocks = (unsigned)(((int64_t)pp.N + tokens - 1) / tokens);
     auto run = [&](auto kern) {
         kern<<<blocks, kThreads, 0, s>>>(pp, slots, (const int8_t*)P2_pages, (const int8_t*)I_pages, (const B*)scales,
-                                         (B*)P2, (B*)I, status, total);
+                                         (B*)P2, (B*)I, status, tokens);
         return cudaGetLastError();
     };
-    return vc == 8 ? run(paged_read_q8_kernel<8>) : run(paged_read_q8_kernel<4>);
+    switch (pp.d) {
+        case 48: return run(paged_read_q8_kernel<8, 6>);
+        case 60: return run(paged_read_q8_kernel<4, 15>);
+        case 64: return run(paged_read_q8_kernel<8, 8>);
+        case 80: return run(paged_read_q8_kernel<8, 10>);
+        case 128: return run(paged_read_q8_kernel<8, 16>);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace relation
