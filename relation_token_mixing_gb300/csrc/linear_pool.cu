@@ -30,6 +30,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "linear_common.cuh"
@@ -43,6 +44,9 @@ namespace lin {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+// Tokens that the recurrence takes one by one. 64 requests, 16 heads of 64, of 16 tokens each: 18.6 us so, 28.8 as a
+// chunk; of 24: 25 and 28.8, but room for 24 tokens' vectors leaves the long requests' kernels beside it less of an
+// SM's memory (prompts of up to 2048 tokens, 8 heads of 60: 139 us against 130).
 constexpr int kFewTokens = 16;
 
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -116,6 +120,13 @@ struct Item {
     int seg_segs;  // seg | segs << 16 (segs = 0: no such item)
 };
 constexpr int kMaxSegs = 1 << 15;
+constexpr int kChunk = 64;  // tokens
+// What block 0 of the first kernel leaves for the others (items = nullptr: every request is one segment).
+struct Plan {
+    Item* items;
+    int *order, *joins;
+    int most_items, most_joins, seg_tokens;
+};
 
 // ------------------------------------------------------------ the recurrence
 // One block per request and head: thread (rg, cg) has rows rg + 8 i and columns 4 cg ..
@@ -124,22 +135,31 @@ constexpr int kMaxSegs = 1 << 15;
 // vectors are made by the warps in turn while the state is on its way.
 constexpr int kFewThreads = 128;
 
-struct FewSmem {
-    float a[kFewTokens][kDp], q[kFewTokens][kDp], k[kFewTokens][kDp], v[kFewTokens][kDp];
-    float part[2][8][kDp];
-};
+// A token's vectors in shared memory, of as many tokens as a request may have.
+constexpr int few_smem(int max_fresh) { return std::min(max_fresh, kFewTokens) * 4 * kDp * (int)sizeof(float); }
 
-// Block 0 of a packed call with items: the list of the longer requests' segments, and where those of more than one begin.
-__device__ void make_items(const LinearPool& p, Item* items, int most, int* joins, int most_joins, int seg_tokens) {
-    __shared__ int sums[kFewThreads / 32], many;
-    if (threadIdx.x == 0) many = 0;
+// Block 0 of a packed call with items: the longer requests' segments, a request's side by side and equal but for whole
+// chunks; where the requests of more than one begin; and the order in which blocks take the segments, the longest
+// first (those of one length in any order), so that the last to start are short.
+__device__ void make_items(const LinearPool& p, const Plan& plan) {
+    constexpr int kBins = 64;  // of segments by their chunks, 63 and more together
+    __shared__ int sums[kFewThreads / 32], many, bins[kBins];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const auto bin_of = [](int tokens) { return kBins - 1 - min((tokens + kChunk - 1) / kChunk, kBins - 1); };
+    if (tid == 0) many = 0;
+    for (int k = tid; k < kBins; k += kFewThreads) bins[k] = 0;
     int base = 0;
     for (int r0 = 0; r0 < p.R; r0 += kFewThreads) {
         const int r = r0 + tid;
         Span sp{0, 0};
         if (r < p.R) sp = span_of(p, r);
-        const int segs = sp.count > kFewTokens ? (sp.count + seg_tokens - 1) / seg_tokens : 0;
+        int segs = 0, each = 0;  // tokens of one
+        if (sp.count > kFewTokens) {
+            const int chunks = (sp.count + kChunk - 1) / kChunk;
+            segs = (sp.count + plan.seg_tokens - 1) / plan.seg_tokens;
+            const int per = (chunks + segs - 1) / segs;
+            segs = (chunks + per - 1) / per, each = per * kChunk;
+        }
         int x = segs;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -153,31 +173,52 @@ __device__ void make_items(const LinearPool& p, Item* items, int most, int* join
             if (w < warp) at += sums[w];
             base += sums[w];
         }
-        for (int k = 0; k < segs && at + k < most; ++k)
-            items[at + k] = Item{r, sp.first + k * seg_tokens, min(seg_tokens, sp.count - k * seg_tokens), k | segs << 16};
+        for (int k = 0; k < segs && at + k < plan.most_items; ++k) {
+            const int count = min(each, sp.count - k * each);
+            plan.items[at + k] = Item{r, sp.first + k * each, count, k | segs << 16};
+            atomicAdd(&bins[bin_of(count)], 1);
+        }
         if (segs > 1) {  // in any order
             const int x = atomicAdd(&many, 1);
-            if (x < most_joins) joins[x] = at;
+            if (x < plan.most_joins) plan.joins[x] = at;
         }
         __syncthreads();
     }
-    for (int k = base + tid; k < most; k += kFewThreads) items[k] = Item{0, 0, 0, 0};
-    for (int k = many + tid; k < most_joins; k += kFewThreads) joins[k] = -1;
+    base = min(base, plan.most_items);
+    for (int k = many + tid; k < plan.most_joins; k += kFewThreads) plan.joins[k] = -1;
+    if (warp == 0) {  // where each length's begin
+        const int a = bins[2 * lane], b = bins[2 * lane + 1];
+        int x = a + b;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        bins[2 * lane] = x - a - b, bins[2 * lane + 1] = x - b;
+    }
+    __syncthreads();
+    for (int k = tid; k < plan.most_items; k += kFewThreads) {
+        if (k < base) plan.order[atomicAdd(&bins[bin_of(plan.items[k].count)], 1)] = k;
+        else plan.order[k] = -1;
+    }
 }
 
 template <int D, bool kGate>
 __global__ void __launch_bounds__(kFewThreads)
-    linear_few_kernel(const __grid_constant__ LinearPool p, Item* items, int most_items, int* joins, int most_joins,
-                      int seg_tokens) {
-    __shared__ __align__(16) FewSmem sm;
+    linear_few_kernel(const __grid_constant__ LinearPool p, const __grid_constant__ Plan plan) {
+    extern __shared__ __align__(16) float few[];
+    __shared__ __align__(16) float part[2][8][kDp];
+    const int most = min(p.max_fresh, kFewTokens);
+    float (*const sa)[kDp] = reinterpret_cast<float (*)[kDp]>(few), (*const sq)[kDp] = sa + most, (*const sk)[kDp] = sq + most,
+          (*const sv)[kDp] = sk + most;
     constexpr int kCols = D / 4, kRows = (D + 7) / 8;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     dependency_wait();
     dependency_release();
     int x = blockIdx.x;
-    if (items != nullptr) {
+    if (plan.items != nullptr) {
         if (x == 0) {
-            make_items(p, items, most_items, joins, most_joins, seg_tokens);
+            make_items(p, plan);
             return;
         }
         --x;
@@ -224,36 +265,36 @@ __global__ void __launch_bounds__(kFewThreads)
             const float S = 1.f / (1.f + __expf(-dt * p.zscale));
             const float s1 = n1 > 0.f ? S * rsqrtf(n1) : 0.f, s2 = n2 > 0.f ? S * rsqrtf(n2) : 0.f;
             const float2 e = log2_retention<kGate>(g, gate);
-            *reinterpret_cast<float2*>(&sm.a[t][c]) = make_float2(exp2f(e.x), exp2f(e.y));
-            *reinterpret_cast<float2*>(&sm.q[t][c]) = make_float2(lo_f(w1) * s1, hi_f(w1) * s1);
-            *reinterpret_cast<float2*>(&sm.k[t][c]) = make_float2(lo_f(w2) * s2, hi_f(w2) * s2);
-            *reinterpret_cast<float2*>(&sm.v[t][c]) = make_float2(lo_f(wv), hi_f(wv));
+            *reinterpret_cast<float2*>(&sa[t][c]) = make_float2(exp2f(e.x), exp2f(e.y));
+            *reinterpret_cast<float2*>(&sq[t][c]) = make_float2(lo_f(w1) * s1, hi_f(w1) * s1);
+            *reinterpret_cast<float2*>(&sk[t][c]) = make_float2(lo_f(w2) * s2, hi_f(w2) * s2);
+            *reinterpret_cast<float2*>(&sv[t][c]) = make_float2(lo_f(wv), hi_f(wv));
         }
     }
     __syncthreads();
     __nv_bfloat16* Y = static_cast<__nv_bfloat16*>(p.Y);
     for (int t = 0; t < sp.count; ++t) {
         if (active) {
-            const float4 v = *reinterpret_cast<const float4*>(&sm.v[t][4 * cg]);
+            const float4 v = *reinterpret_cast<const float4*>(&sv[t][4 * cg]);
             float4 e = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
                 const int c = rg + 8 * i;
                 if (c >= D) break;
-                const float a = sm.a[t][c], q = sm.q[t][c], k = sm.k[t][c];
+                const float a = sa[t][c], q = sq[t][c], k = sk[t][c];
                 C[i] = make_float4(C[i].x * a, C[i].y * a, C[i].z * a, C[i].w * a);
                 e = make_float4(fmaf(q, C[i].x, e.x), fmaf(q, C[i].y, e.y), fmaf(q, C[i].z, e.z), fmaf(q, C[i].w, e.w));
                 C[i] = make_float4(fmaf(k, v.x, C[i].x), fmaf(k, v.y, C[i].y), fmaf(k, v.z, C[i].z),
                                    fmaf(k, v.w, C[i].w));
             }
-            *reinterpret_cast<float4*>(&sm.part[t & 1][rg][4 * cg]) = e;
+            *reinterpret_cast<float4*>(&part[t & 1][rg][4 * cg]) = e;
         }
         __syncthreads();  // the other buffer's readers are a token behind: past the next barrier
         if (tid < D / 2) {
-            float2 y = *reinterpret_cast<const float2*>(&sm.v[t][2 * tid]);
+            float2 y = *reinterpret_cast<const float2*>(&sv[t][2 * tid]);
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
-                const float2 e = *reinterpret_cast<const float2*>(&sm.part[t & 1][g][2 * tid]);
+                const float2 e = *reinterpret_cast<const float2*>(&part[t & 1][g][2 * tid]);
                 y.x += e.x, y.y += e.y;
             }
             *reinterpret_cast<uint32_t*>(Y + ((size_t)(sp.first + t) * p.H + h) * D + 2 * tid) = pack2(y.x, y.y);
@@ -269,10 +310,11 @@ __global__ void __launch_bounds__(kFewThreads)
 }
 
 // ------------------------------------------------------------------- chunks
-constexpr int kT = 64;            // tokens of a chunk
+constexpr int kT = kChunk;
 constexpr int kThreads = 256, kBlocksPerSm = 2;
 constexpr float kRange = 100.f;   // log2 of what half a chunk may lose of a channel
 constexpr int kTile = kT * 128;   // a bf16 tile of 64 x 64
+constexpr int kGp = kDp + 8;      // of a row of sums: eight rows' same columns on different banks
 constexpr int kSegFloats = kDp * kDp + kDp;  // of a segment in the workspace: its state, the log2 of its retention
 
 struct ChunkStage {
@@ -287,7 +329,7 @@ struct ChunkSmem {
             uint8_t kl[kTile];  // what bf16 leaves of k~
             uint8_t c[kTile];   // the state as an operand, [value channel][key channel]
         };
-        float g[kT * kDp];  // (strong_chunk)
+        float g[kT * kGp];  // (strong_chunk)
         struct {
             uint8_t below[kTile];
             float tot[8][kDp];  // a warp's 8 tokens: sum of log2 of their retentions
@@ -401,61 +443,76 @@ __device__ __forceinline__ void row_scalars(ChunkSmem& sm, const ChunkStage& s, 
     __syncwarp();
 }
 
-// The weights (in sm.w) of rows 16 rt .. 16 rt + 15, q k^T with the retention between the two tokens, for a chunk whose
-// factors from one reference would leave bf16's range: sm.g holds G, s.p1 and s.p2 the rows as they came.  Keys before
-// the 16 tokens meet the queries at the block's first token, the block's first 8 keys its last 8 queries at the ninth:
-// all factors are retentions.  What is left are pairs inside 8 tokens, one by one.  16 keys at a time, so
-// that the call saves few of the caller's registers: chunks like this are rare, the others run past it.
-__device__ __noinline__ void strong_chunk(ChunkSmem& sm, const ChunkStage& s, int rt, int lane) {
-    const int g = lane >> 2, t = lane & 3, i0 = 16 * rt + g;
+// The weights (in sm.w), q k^T with the retention between the two tokens, for a chunk whose factors from one
+// reference would leave bf16's range: sm.g holds G, s.p1 and s.p2 the rows as they came.  Of each 16 queries, keys
+// before them meet the queries at the block's first token, the block's first 8 keys its last 8 queries at the ninth:
+// all factors are retentions.  What is left are pairs inside 8 tokens, a lane a pair.  Warps w and w + 4 share 16
+// queries, 8 keys in turn.  Chunks like this are rare; one costs its block some 9 us (others: 4), most of it code that
+// no other block has fetched.
+__device__ __noinline__ void strong_chunk(ChunkSmem& sm, const ChunkStage& s, int warp, int lane) {
+    const int g = lane >> 2, t = lane & 3, rt = warp & 3, half = warp >> 2, i0 = 16 * rt + g;
     const auto row_of = [](const uint8_t* tile, int r, int c) { return *reinterpret_cast<const uint32_t*>(tile + swz(r, c)); };
-    // q (or k) of row r, columns c and c + 1, times 2^(+-(G_r - G_b)) as a bf16 pair; b < 0: from the chunk's start.
-    const auto scaled = [&](bool query, int r, int b, int c) {
-        const float2 G = *reinterpret_cast<const float2*>(sm.g + r * kDp + c);
-        const float2 B = b < 0 ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2*>(sm.g + b * kDp + c);
+    const auto sum_of = [&](int r, int c) { return *reinterpret_cast<const float2*>(sm.g + r * kGp + c); };
+    // q (or k) of row r, columns c and c + 1, times 2^(+-(G_r - B)) as a bf16 pair.
+    const auto scaled = [&](bool query, int r, float2 B, int c) {
+        const float2 G = sum_of(r, c);
         const uint32_t x = row_of(query ? s.p1 : s.p2, r, c);
         const float f = query ? sm.rs[r].x : sm.rs[r].y;
         const float2 e = query ? make_float2(G.x - B.x, G.y - B.y) : make_float2(B.x - G.x, B.y - G.y);
         return pack2(lo_f(x) * f * ptx::ex2_approx(e.x), hi_f(x) * f * ptx::ex2_approx(e.y));
     };
-    const auto put = [&](int n, const float (&w)[4]) {
-        *reinterpret_cast<uint32_t*>(sm.w + swz(i0, 8 * n + 2 * t)) = pack2(w[0], w[1]);
-        *reinterpret_cast<uint32_t*>(sm.w + swz(i0 + 8, 8 * n + 2 * t)) = pack2(w[2], w[3]);
+    const auto put = [&](int row, int n, float a, float b) {
+        *reinterpret_cast<uint32_t*>(sm.w + swz(row, 8 * n + 2 * t)) = pack2(a, b);
     };
+    float w[3][4] = {}, last[4] = {};
 #pragma unroll 1
-    for (int n = 0; n < 8; ++n) {
-        float w[4] = {0.f, 0.f, 0.f, 0.f};
-        const bool before = n < 2 * rt, last = n == 2 * rt;
-        if (before || last) {
-            const int b = before ? 16 * rt - 1 : 16 * rt + 7;
-#pragma unroll 1
-            for (int c = 2 * t; c < kDp; c += 16) {
-                const uint32_t a[4] = {before ? scaled(true, i0, b, c) : 0u, scaled(true, i0 + 8, b, c),
-                                       before ? scaled(true, i0, b, c + 8) : 0u, scaled(true, i0 + 8, b, c + 8)};
-                mma16816(w, a, scaled(false, 8 * n + g, b, c), scaled(false, 8 * n + g, b, c + 8));
-            }
+    for (int c = 2 * t; c < kDp; c += 16) {
+        if (rt > 0) {
+            const float2 B0 = sum_of(16 * rt - 1, c), B1 = sum_of(16 * rt - 1, c + 8);
+            const uint32_t a[4] = {scaled(true, i0, B0, c), scaled(true, i0 + 8, B0, c), scaled(true, i0, B1, c + 8),
+                                   scaled(true, i0 + 8, B1, c + 8)};
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+                if (k < rt) {
+                    const int j = 8 * (2 * k + half) + g;
+                    mma16816(w[k], a, scaled(false, j, B0, c), scaled(false, j, B1, c + 8));
+                }
         }
-        if (n == 2 * rt || n == 2 * rt + 1) {
-            // Row lane / 4 against columns 2 (lane % 4) and the next of the triangle on the diagonal.
-            const int base = 8 * n, i = base + g, j = base + 2 * t;
-            float x0 = 0.f, x1 = 0.f;
-#pragma unroll 1
-            for (int c = 0; c < kDp; c += 2) {
-                const float2 Gi = *reinterpret_cast<const float2*>(sm.g + i * kDp + c);
-                const float2 Gj = *reinterpret_cast<const float2*>(sm.g + j * kDp + c);
-                const float2 Gk = *reinterpret_cast<const float2*>(sm.g + (j + 1) * kDp + c);
-                const uint32_t q = row_of(s.p1, i, c), k0 = row_of(s.p2, j, c), k1 = row_of(s.p2, j + 1, c);
-                if (j < i)
-                    x0 += lo_f(q) * lo_f(k0) * ptx::ex2_approx(Gi.x - Gj.x) + hi_f(q) * hi_f(k0) * ptx::ex2_approx(Gi.y - Gj.y);
-                if (j + 1 < i)
-                    x1 += lo_f(q) * lo_f(k1) * ptx::ex2_approx(Gi.x - Gk.x) + hi_f(q) * hi_f(k1) * ptx::ex2_approx(Gi.y - Gk.y);
-            }
-            x0 *= sm.rs[i].x * sm.rs[j].y;
-            x1 *= sm.rs[i].x * sm.rs[j + 1].y;
-            if (last) w[0] = x0, w[1] = x1;
-            else w[2] = x0, w[3] = x1;
+        if (half == 0) {
+            const float2 B0 = sum_of(16 * rt + 7, c), B1 = sum_of(16 * rt + 7, c + 8);
+            const uint32_t a[4] = {0u, scaled(true, i0 + 8, B0, c), 0u, scaled(true, i0 + 8, B1, c + 8)};
+            mma16816(last, a, scaled(false, i0, B0, c), scaled(false, i0, B1, c + 8));
         }
-        put(n, w);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int n = 2 * k + half;
+        if (k != rt) {
+            const bool before = k < rt;
+            put(i0, n, before ? w[k < 3 ? k : 0][0] : 0.f, before ? w[k < 3 ? k : 0][1] : 0.f);
+            put(i0 + 8, n, before ? w[k < 3 ? k : 0][2] : 0.f, before ? w[k < 3 ? k : 0][3] : 0.f);
+        } else if (half == 0) {
+            put(i0 + 8, n, last[2], last[3]);
+        } else {
+            put(i0, n, 0.f, 0.f);
+        }
+    }
+    // The 28 pairs of the warp's own 8 tokens; zeros on and above the diagonal.
+    put(8 * warp + g, warp, 0.f, 0.f);
+    __syncwarp();
+    if (lane < 28) {
+        int i = 1, j = lane;
+        while (j >= i) j -= i++;
+        i += 8 * warp, j += 8 * warp;
+        float2 x = make_float2(0.f, 0.f);
+#pragma unroll 2
+        for (int c = 0; c < kDp; c += 2) {
+            const float2 Gi = sum_of(i, c), Gj = sum_of(j, c);
+            const uint32_t q = row_of(s.p1, i, c), k = row_of(s.p2, j, c);
+            x.x += lo_f(q) * lo_f(k) * ptx::ex2_approx(Gi.x - Gj.x);
+            x.y += hi_f(q) * hi_f(k) * ptx::ex2_approx(Gi.y - Gj.y);
+        }
+        *reinterpret_cast<__nv_bfloat16*>(sm.w + swz(i, j)) = __float2bfloat16_rn((x.x + x.y) * (sm.rs[i].x * sm.rs[j].y));
     }
 }
 
@@ -470,34 +527,41 @@ __device__ __noinline__ void strong_chunk(ChunkSmem& sm, const ChunkStage& s, in
 // channels; the state itself stays in such fragments, from chunk to chunk.
 template <bool kOut, bool kGate>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
-    linear_chunk_kernel(const __grid_constant__ LinearPool p, const Item* __restrict__ items, float* __restrict__ segments) {
+    linear_chunk_kernel(const __grid_constant__ LinearPool p, const __grid_constant__ Plan plan, float* __restrict__ segments) {
     extern __shared__ uint8_t smem_raw[];
     ChunkSmem& sm =
         *reinterpret_cast<ChunkSmem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, h = blockIdx.y;
-    for (int k = tid; k < (int)(sizeof(sm.st) / 16); k += kThreads)
-        reinterpret_cast<uint4*>(sm.st)[k] = make_uint4(0, 0, 0, 0);
-    if (tid == 0) {
-        for (uint64_t* bar : {&sm.c_done, &sm.o_done, &sm.drain}) ptx::mbar_init(bar, 1);
-        sm.abort_flag = 0;
-        ptx::fence_barrier_init();
-    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int x = blockIdx.x / p.H;
+    const int h = blockIdx.x - x * p.H;
     // The kernel before waited for what ran before it, and leaves the items.
-    if (items != nullptr) dependency_wait();
+    if (plan.items != nullptr) dependency_wait();
     dependency_release();
-    Item it{(int)blockIdx.x, 0, 0, 1 << 16};
-    if (items != nullptr) {
-        it = items[blockIdx.x];
+    Item it{x, 0, 0, 1 << 16};
+    if (plan.items != nullptr) {
+        x = plan.order[x];
+        if (x < 0) return;
+        it = plan.items[x];
     } else {
         const Span sp = span_of(p, it.r);
         it.first = sp.first, it.count = sp.count;
     }
     const int seg = it.seg_segs & 0xffff, segs = it.seg_segs >> 16;
-    const bool none = segs == 0 || it.count <= (segs > 1 ? 0 : kFewTokens) || (!kOut && seg + 1 >= segs);
-    if (none) {
-        if (items == nullptr && tid == 0) dependency_wait();
+    if (it.count <= (segs > 1 ? 0 : kFewTokens) || (!kOut && seg + 1 == segs)) {
+        if (plan.items == nullptr && tid == 0) dependency_wait();
         return;
     }
+    if (tid == 0) {
+        for (uint64_t* bar : {&sm.c_done, &sm.o_done, &sm.drain}) ptx::mbar_init(bar, 1);
+        sm.abort_flag = 0;
+        ptx::fence_barrier_init();
+    }
+    // Zeros for the columns past d, which no copy writes.
+    if (p.d < kDp)
+        for (int k = tid; k < 6 * kT; k += kThreads) {
+            uint8_t* tile = sm.st[k / (3 * kT)].p1 + k / kT % 3 * kTile;
+            for (int c = p.d & ~7; c < kDp; c += 8) *reinterpret_cast<uint4*>(tile + swz(k % kT, c)) = make_uint4(0, 0, 0, 0);
+        }
     if (warp == 0) {
         ptx::tmem_alloc(&sm.tmem, kTmemCols);
         ptx::tmem_relinquish();
@@ -532,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const uint32_t frag_at = swz(16 * quarter + (lane & 15), col0 + 8 * (lane >> 4)), frag_next = frag_at ^ 32;
     // Rows r0, r0 + 8 of the state C^T, columns col0 + 8 n + 2 t and the next.
     float2 C[4][2];
-    float* mine = segments == nullptr ? nullptr : segments + ((size_t)blockIdx.x * p.H + h) * kSegFloats;
+    float* mine = segments == nullptr ? nullptr : segments + ((size_t)x * p.H + h) * kSegFloats;
     {
         const float* in = nullptr;
         int ld = p.d;
@@ -568,14 +632,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         __syncthreads();
         ptx::tc_fence_after();
     };
-    for (int n = 0; n < chunks; ++n) {
+    // The same code twice: without the strong chunks' way, and with it for the chunks that turn out to need it, which
+    // start over. In one, what that way needs takes registers from every chunk (mixed step of 64 requests, 16 heads of
+    // 64: 46 us against 42).
+    enum { kNext, kStop };
+    auto chunk = [&](int n, auto rare) {
+        constexpr bool kRare = decltype(rare)::value;
         ChunkStage& s = sm.st[n & 1];
         const int left = it.count - n * kT;  // tokens from this chunk on
         cp_async_wait<0>();
         // The chunk is there, and nothing reads the one before any more.
         if (!__syncthreads_and(ok)) {
             ok = false;
-            break;
+            return kStop;
         }
         if (n + 1 < chunks) load.chunk_into(sm.st[(n + 1) & 1], p, row + (size_t)(n + 1) * kT * stride, left - kT);
         row_scalars(sm, s, p.zscale, warp, lane);
@@ -602,11 +671,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             else rest = add2(rest, x);
         }
         const float2 all = add2(mid, rest);
-        lost = add2(lost, all);
         const float least = fminf(fminf(mid.x, mid.y), fminf(rest.x, rest.y));
-        const bool strong = grows || __any_sync(0xffffffffu, !(least >= -kRange));  // the same for every warp
+        const bool is_strong = grows || __any_sync(0xffffffffu, !(least >= -kRange));  // the same for every warp
+        if (!kRare && is_strong) return kStop;
+        const bool strong = kRare && is_strong;
+        lost = add2(lost, all);
         float2 to_end = sum;
-        if (__builtin_expect(strong, 0)) {
+        if (strong) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
                 if (x > warp) to_end = add2(to_end, *reinterpret_cast<const float2*>(&sm.tot[x][c2]));
@@ -614,9 +685,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 __syncthreads();  // before the sums are overwritten
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    *reinterpret_cast<float2*>(sm.g + (8 * warp + i) * kDp + c2) = add2(base, G[i]);
+                    *reinterpret_cast<float2*>(sm.g + (8 * warp + i) * kGp + c2) = add2(base, G[i]);
                 __syncthreads();
-                if (warp < 4) strong_chunk(sm, s, warp, lane);
+                strong_chunk(sm, s, warp, lane);
                 __syncthreads();  // before the rows are overwritten
             }
         }
@@ -758,6 +829,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             }
         }
         ptx::tc_fence_before();
+        return kNext;
+    };
+    for (int n = 0; n < chunks && ok; ++n) {
+        if (kOut) {
+            if (chunk(n, std::false_type()) == kNext) continue;
+            if (!ok) break;
+            load_g(row + (size_t)n * kT * stride, it.count - n * kT);
+        }
+        chunk(n, std::true_type());
     }
     if (warp == 0 && *abort_flag) {  // let what is in flight end before its memory goes
         ptx::mma_commit_elect(&sm.drain);
@@ -788,7 +868,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             }
     }
     // (few calls: the whole chain ends with this kernel's end)
-    if (items == nullptr && tid == 0) dependency_wait();
+    if (plan.items == nullptr && tid == 0) dependency_wait();
 }
 
 // Every segment's entering state in the place of its own contribution, from the pool's
@@ -796,13 +876,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // loads, not the bytes.
 constexpr int kScanThreads = 128;
 __global__ void __launch_bounds__(kScanThreads)
-    linear_join_kernel(const __grid_constant__ LinearPool p, const Item* __restrict__ items, const int* __restrict__ joins,
-                       float* __restrict__ segments) {
+    linear_join_kernel(const __grid_constant__ LinearPool p, const __grid_constant__ Plan plan, float* __restrict__ segments) {
     dependency_wait();
     dependency_release();
-    const int at = joins[blockIdx.x];
+    const int at = plan.joins[blockIdx.x];
     if (at < 0) return;
-    const Item it = items[at];
+    const Item it = plan.items[at];
     const int segs = it.seg_segs >> 16, h = blockIdx.y;
     const int e = blockIdx.z * kScanThreads + threadIdx.x, c = e >> 6, v = e & 63;
     const float* in = state_of(p, __ldg(p.slots_in + it.r), h);
@@ -828,10 +907,11 @@ __global__ void __launch_bounds__(kScanThreads)
     }
 }
 
-// How a packed call is cut: requests longer than `seg_tokens` in segments of that many.
+constexpr int kLeastCut = 256, kUncut = 640;
+// How a packed call is cut: requests longer than `seg_tokens` in equal segments of that many at most.
 struct Cut {
     bool chunked;     // a request may have more than kFewTokens new tokens
-    bool segmented;   // and more than seg_tokens
+    bool segmented;   // and is worth cutting
     int seg_tokens, items;
     int joins;        // requests of more than one segment
 };
@@ -839,19 +919,24 @@ Cut cut_of(int R, int N, int H, int max_fresh, int num_sms) {
     Cut c{};
     c.chunked = max_fresh > kFewTokens;
     if (!c.chunked) return c;
-    // A segment as long as a block's equal share of all tokens, 256 at least: shorter ones cost more
-    // in the state pass and the join than they spread.
-    const int64_t share = ((int64_t)N * H / (kBlocksPerSm * num_sms) + kT - 1) / kT * kT;
-    int64_t seg = std::max<int64_t>(256, share);
+    // share: a block's equal share of all tokens. A request of up to 1.5 of it, or of up to kUncut tokens, is left whole:
+    // cutting costs the state pass (0.6 of the output pass), the join and two more launches (4 requests, 16 heads
+    // of 64: 512 tokens each 28 us whole and 35 cut, 640: 33 and 35, 768: 39 and 35, 1536: 74 and 48).
+    // One request is cut in equal shares; several in halves of one, kLeastCut at least, as their blocks are evened out by
+    // the order (prompts of up to 2048, 8 heads of 60: 131 us, in whole shares 142, in 512 at least 137, uncut 167).
+    const int64_t share = (int64_t)N * H / (kBlocksPerSm * num_sms);
+    int64_t seg = std::max<int64_t>(kLeastCut, ((R > 1 ? share / 2 : share) + kT - 1) / kT * kT);
     seg = std::max<int64_t>(seg, ((int64_t)max_fresh / (kMaxSegs - 1) + kT) / kT * kT);
     c.seg_tokens = (int)std::min<int64_t>(seg, (INT32_MAX - kT) / kT * kT);
-    c.segmented = max_fresh > c.seg_tokens;
+    c.segmented = max_fresh > std::max<int64_t>({kUncut, share + share / 2, c.seg_tokens});
     c.items = c.segmented ? (int)std::min<int64_t>((int64_t)N / c.seg_tokens + std::min(R, N / (kFewTokens + 1)), INT32_MAX) : R;
     c.joins = std::min(R, N / (c.seg_tokens + 1));
     return c;
 }
-// The list of segments, then the list of joins.
-size_t items_bytes(const Cut& c) { return ((size_t)c.items * sizeof(Item) + (size_t)c.joins * sizeof(int) + 255) / 256 * 256; }
+// The list of segments, their order, the list of joins.
+size_t items_bytes(const Cut& c) {
+    return ((size_t)c.items * (sizeof(Item) + sizeof(int)) + (size_t)c.joins * sizeof(int) + 255) / 256 * 256;
+}
 
 template <typename... P, typename... A>
 cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, A... args) {
@@ -869,40 +954,48 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cuda
 }
 
 template <bool kGate>
-cudaError_t launch_few(const LinearPool& p, Item* items, int* joins, const Cut& cut, cudaStream_t s) {
-    const dim3 grid((unsigned)((int64_t)p.R * p.H + (items != nullptr)));
+cudaError_t launch_few(const LinearPool& p, const Plan& plan, cudaStream_t s) {
+    const dim3 grid((unsigned)((int64_t)p.R * p.H + (plan.items != nullptr)));
     switch (p.d) {
-        case 48: return launch(linear_few_kernel<48, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, joins, cut.joins, cut.seg_tokens);
-        case 60: return launch(linear_few_kernel<60, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, joins, cut.joins, cut.seg_tokens);
-        case 64: return launch(linear_few_kernel<64, kGate>, grid, kFewThreads, 0, s, p, items, cut.items, joins, cut.joins, cut.seg_tokens);
+        case 48: return launch(linear_few_kernel<48, kGate>, grid, kFewThreads, few_smem(p.max_fresh), s, p, plan);
+        case 60: return launch(linear_few_kernel<60, kGate>, grid, kFewThreads, few_smem(p.max_fresh), s, p, plan);
+        case 64: return launch(linear_few_kernel<64, kGate>, grid, kFewThreads, few_smem(p.max_fresh), s, p, plan);
     }
     return cudaErrorInvalidValue;
 }
 
 template <bool kGate>
 cudaError_t launch_pool(const LinearPool& p, void* workspace, const Cut& cut, int* launches, cudaStream_t s) {
-    Item* items = cut.segmented ? static_cast<Item*>(workspace) : nullptr;
-    float* segments = cut.segmented ? reinterpret_cast<float*>(static_cast<char*>(workspace) + items_bytes(cut)) : nullptr;
-    int* joins = cut.segmented ? reinterpret_cast<int*>(items + cut.items) : nullptr;
-    cudaError_t e = launch_few<kGate>(p, items, joins, cut, s);
+    Plan plan{};
+    float* segments = nullptr;
+    if (cut.segmented) {
+        plan.items = static_cast<Item*>(workspace);
+        plan.order = reinterpret_cast<int*>(plan.items + cut.items);
+        plan.joins = plan.order + cut.items;
+        plan.most_items = cut.items, plan.most_joins = cut.joins, plan.seg_tokens = cut.seg_tokens;
+        segments = reinterpret_cast<float*>(static_cast<char*>(workspace) + items_bytes(cut));
+    }
+    cudaError_t e = launch_few<kGate>(p, plan, s);
     *launches = 1;
     if (e != cudaSuccess || !cut.chunked) return e;
     constexpr int smem = (int)sizeof(ChunkSmem) + 1024;
-    static OncePerDevice once_out, once_state;
+    static OncePerDevice once_out, once_state, split_out, split_state;
+    if ((e = prefer_shared(split_out, linear_chunk_kernel<true, kGate>, kBlocksPerSm, smem)) != cudaSuccess) return e;
+    if ((e = prefer_shared(split_state, linear_chunk_kernel<false, kGate>, kBlocksPerSm, smem)) != cudaSuccess) return e;
     if ((e = allow_dynamic_smem(once_out, linear_chunk_kernel<true, kGate>, smem)) != cudaSuccess) return e;
     if ((e = allow_dynamic_smem(once_state, linear_chunk_kernel<false, kGate>, smem)) != cudaSuccess) return e;
-    const dim3 grid((unsigned)cut.items, (unsigned)p.H);
+    const dim3 grid((unsigned)((int64_t)cut.items * p.H));
     if (cut.segmented) {
         *launches = 4;
-        e = launch(linear_chunk_kernel<false, kGate>, grid, kThreads, smem, s, p, items, segments);
+        e = launch(linear_chunk_kernel<false, kGate>, grid, kThreads, smem, s, p, plan, segments);
         if (e != cudaSuccess) return e;
-        e = launch(linear_join_kernel, dim3((unsigned)cut.joins, grid.y, kDp * kDp / kScanThreads), kScanThreads, 0, s, p,
-                   items, joins, segments);
+        e = launch(linear_join_kernel, dim3((unsigned)cut.joins, (unsigned)p.H, kDp * kDp / kScanThreads), kScanThreads, 0,
+                   s, p, plan, segments);
         if (e != cudaSuccess) return e;
     } else {
         *launches = 2;
     }
-    return launch(linear_chunk_kernel<true, kGate>, grid, kThreads, smem, s, p, items, segments);
+    return launch(linear_chunk_kernel<true, kGate>, grid, kThreads, smem, s, p, plan, segments);
 }
 
 }  // namespace

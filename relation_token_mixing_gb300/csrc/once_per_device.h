@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -36,6 +37,20 @@ cudaError_t allow_dynamic_smem(OncePerDevice& once, Kernel* kern, int bytes) {
     if (e != cudaSuccess) return e;
     return once.run(device,
                     [&] { return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes); });
+}
+
+// Splits an SM between shared memory and L1 so that `blocks` of kern's blocks, of `bytes` each, fit on the current
+// device, and no further; once: the kernel's own. Left alone, an SM keeps the split of the kernel before.
+template <typename Kernel>
+cudaError_t prefer_shared(OncePerDevice& once, Kernel* kern, int blocks, int bytes) {
+    int device = 0, most = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return once.run(device, [&] {
+        if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerMultiprocessor, device)) != cudaSuccess) return e;
+        const int percent = std::min(100, (100 * blocks * (bytes + 1024) + most - 1) / most);  // (1 KB is the system's)
+        return cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, percent);
+    });
 }
 
 }  // namespace relation

@@ -40,29 +40,31 @@ def test_few_tokens(H, d, gate):
 
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("H,d", [(1, 64), (3, 60), (2, 48)])
-@pytest.mark.parametrize("lengths", [[17], [64], [65, 63], [1, 0, 17, 128, 5, 200, 64, 2], [33, 16, 250, 31]])
+@pytest.mark.parametrize("lengths", [[17], [24], [25], [64], [65, 63], [1, 0, 17, 128, 5, 200, 64, 2], [33, 16, 250, 31, 24, 25]])
 def test_requests_of_one_stretch(lengths, H, d, gate):
     x = inputs(lengths, H, d, gate, seed=len(lengths))
     c = on_gpu(x)
     Y = packed(c, max_fresh=max(lengths))
     _ok()
-    assert rb.relation_last_launch_count() == 2
+    assert rb.relation_last_launch_count() == (2 if max(lengths) > 16 else 1)  # up to 16 tokens one by one
     check(x, Y, c["states"])
 
 
 @pytest.mark.parametrize("gate", [False, True])
 @pytest.mark.parametrize("H,d", [(2, 64), (3, 60), (1, 48)])
-@pytest.mark.parametrize("lengths,bound", [([257], 257), ([1100, 17, 300, 1, 0, 256], 0), ([3, 512, 513, 255, 70], 1000)])
+@pytest.mark.parametrize("lengths,bound", [([257], 257), ([1100, 17, 300, 1, 0, 256], 0), ([3, 512, 513, 255, 70], 1000),
+                                           ([257], 800), ([770], 770), ([64, 2000, 769, 830, 1], 2000)])
 def test_requests_of_many_segments(lengths, bound, H, d, gate):
     x = inputs(lengths, H, d, gate, seed=11)
     c = on_gpu(x)
     Y = packed(c, max_fresh=bound)
     _ok()
-    assert rb.relation_last_launch_count() == 4
+    # Cut, if some request may be longer than 640.
+    assert rb.relation_last_launch_count() == (4 if min(bound or sum(lengths), sum(lengths)) > 640 else 2)
     check(x, Y, c["states"])
 
 
-@pytest.mark.parametrize("lengths", [[40, 100, 64], [300, 20, 64]])
+@pytest.mark.parametrize("lengths", [[40, 100, 64], [300, 20, 64], [900, 20, 64]])
 @pytest.mark.parametrize("kind", ["strong", "one_channel", "resets", "none", "growing", "lowest", "ragged"])
 def test_retention(kind, lengths):
     """Factors that leave the range of a chunk with one reference, retention of nothing and of everything."""
