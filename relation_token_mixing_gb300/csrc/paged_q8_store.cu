@@ -15,8 +15,8 @@
 // One pass, as paged_store.cu: every element is read once and written once.  4, 8 or 16 lanes have a
 // row (columns c and c + d/2 together, as RoPE turns them) and find its largest value among
 // themselves, so a row never leaves its registers between the prologue and its pages.  Both kernels
-// move bytes.  Measured, 16384 tokens, 32 heads over 8 of 128: the store 77 us (370 MB, 4.8 TB/s), the rows
-// read back right after it 15 us (101 MB, 6.6 TB/s, the pages still in L2); 4999 tokens, 8 heads of 60: 14.7 and 4.5 us.
+// move bytes.  Measured, 16384 tokens, 32 heads over 8 of 128: the store 70 us (370 MB, 5.3 TB/s), the rows
+// read back right after it 15 us (101 MB, 6.6 TB/s, the pages still in L2); 4999 tokens, 8 heads of 60: 14 and 4.5 us.
 #include <math.h>
 
 #include <algorithm>
@@ -29,8 +29,8 @@ namespace relation {
 namespace {
 
 constexpr int kThreads = 256;
-// Tokens of one block: the angles of the next block's are computed while this one moves rows.  16384 tokens, 32 heads over
-// 8 of 128: 2: 81 us, 4: 77, 8: 75; 4999 tokens, 8 heads of 60: 15.3, 14.7, 16.5.
+// Tokens of one block (16384 tokens, 32 heads over 8 of 128: 2: 81 us, 4: 77, 8: 75; 4999 tokens, 8 heads of 60: 15.3,
+// 14.7, 16.5).
 constexpr int kMaxTokens = 4;
 
 // The scale's bits as a float: of the bits of max |x|, m 2^e, it takes the exponent e - 6, or e - 5
@@ -67,9 +67,6 @@ __global__ void __launch_bounds__(kThreads)
                           int8_t* __restrict__ I_pages, __nv_bfloat16* __restrict__ scales, unsigned int* status,
                           int tokens, FastDiv by_rows) {
     constexpr int D = 2 * HALF, PER = HALF / VC;
-    // Rows of a thread on their way at once: one of 32 bytes, or two of 8.  Two of 32 bytes take 98 registers, and 16 warps
-    // of an SM move less than 32 do (d = 128: 110 us against 77); one of 8 bytes leaves a warp waiting (d = 60: 17 against 14.7).
-    constexpr int FLY = VC == 2 ? 2 : 1;
     extern __shared__ float2 sh[];  // (cos, sin) [tokens][VC][PER]: a row's lanes side by side, then [G/2] of the head pairs
     __shared__ int64_t s_row[kMaxTokens];  // the token's row of cache head 0, counted in rows, or -1
     float2* turn = sh;
@@ -99,65 +96,55 @@ __global__ void __launch_bounds__(kThreads)
     const int lane = threadIdx.x % LANES, c = lane * VC;
     // The block's rows of all its tokens, one after another: H of X1, G of X2, G of I.
     const int rows = pp.H + 2 * pp.G, total = rows * count;
-    struct Row {
-        Vec<__nv_bfloat16, VC> a, b, mate_a, mate_b;  // columns c and c + d/2 (and of a mixed row its partner's)
-        int t, j;                                     // token, row of it; j < 0: none
-        float2 mix;                                   // the row is mix.x times itself and mix.y times its partner
-    };
-    auto fetch = [&](int k, Row& r) {
-        r.t = by_rows.div(k);
-        r.j = k < total && lane < PER ? k - r.t * rows : -1;
-        if (r.j < 0) return;
-        const int n = n0 + r.t, g = r.j < pp.H + pp.G ? r.j - pp.H : r.j - pp.H - pp.G;
-        const __nv_bfloat16* src = (r.j < pp.H ? X1 + ((size_t)n * pp.H + r.j) * D
-                                               : (r.j < pp.H + pp.G ? X2 : I) + ((size_t)n * pp.G + g) * D) + c;
-        r.a.load(src);
-        r.b.load(src + HALF);
-        if (theta != nullptr && r.j >= pp.H + pp.G) {  // the first of a pair: cos a - sin b, the second: sin a + cos b
-            int pair;
-            bool first;
-            const int other = givens_partner(g, pp.G, pairing, &pair, &first);
-            const float2 w = mix[pair];
-            r.mix = make_float2(w.x, first ? -w.y : w.y);
-            const __nv_bfloat16* mate = I + ((size_t)n * pp.G + other) * D + c;
-            r.mate_a.load(mate);
-            r.mate_b.load(mate + HALF);
-        }
-    };
-    auto finish = [&](Row& r) {
-        float a[VC], b[VC];
+    for (int k0 = threadIdx.x / 32 * (32 / LANES); k0 < total; k0 += kThreads / LANES) {
+        const int k = k0 + (int)(threadIdx.x % 32) / LANES, t = by_rows.div(k), j = k - t * rows, n = n0 + t;
+        const bool in = k < total && lane < PER, key = j < pp.H + pp.G;
+        const int g = key ? j - pp.H : j - pp.H - pp.G;  // (of a row of X2 or I)
+        float a[VC], b[VC];  // columns c and c + d/2
         uint32_t top = 0;
-        const bool in = r.j >= 0, key = r.j < pp.H + pp.G;
         if (in) {
-            float x[VC], y[VC];
-            r.a.unpack(x);
-            r.b.unpack(y);
+            Vec<__nv_bfloat16, VC> va, vb;
+            const __nv_bfloat16* src = (j < pp.H ? X1 + ((size_t)n * pp.H + j) * D : (key ? X2 : I) + ((size_t)n * pp.G + g) * D) + c;
+            va.load(src);
+            vb.load(src + HALF);
             if (key) {
+                float x[VC], y[VC];
+                va.unpack(x);
+                vb.unpack(y);
 #pragma unroll
                 for (int e = 0; e < VC; ++e) {
-                    const float2 w = turn[r.t * HALF + e * PER + lane];
+                    const float2 w = turn[t * HALF + e * PER + lane];
                     a[e] = w.x * x[e] - w.y * y[e];
                     b[e] = w.y * x[e] + w.x * y[e];
                 }
             } else {
-#pragma unroll
-                for (int e = 0; e < VC; ++e) a[e] = x[e], b[e] = y[e];
-                if (theta != nullptr) {
-                    r.mate_a.unpack(x);
-                    r.mate_b.unpack(y);
+                va.unpack(a);
+                vb.unpack(b);
+                if (theta != nullptr) {  // the first of a pair: cos a - sin b, the second: sin a + cos b
+                    int pair;
+                    bool first;
+                    const int other = givens_partner(g, pp.G, pairing, &pair, &first);
+                    const float2 w = mix[pair];
+                    const float sn = first ? -w.y : w.y;
+                    const __nv_bfloat16* mate = I + ((size_t)n * pp.G + other) * D + c;
+                    va.load(mate);
+                    vb.load(mate + HALF);
+                    float x[VC], y[VC];
+                    va.unpack(x);
+                    vb.unpack(y);
 #pragma unroll
                     for (int e = 0; e < VC; ++e) {
-                        a[e] = r.mix.x * a[e] + r.mix.y * x[e];
-                        b[e] = r.mix.x * b[e] + r.mix.y * y[e];
+                        a[e] = w.x * a[e] + sn * x[e];
+                        b[e] = w.x * b[e] + sn * y[e];
                     }
                 }
             }
-            if (r.j < pp.H) {
-                r.a.pack(a);
-                r.b.pack(b);
-                __nv_bfloat16* dst = P1 + ((size_t)(n0 + r.t) * pp.H + r.j) * D + c;
-                r.a.store(dst);
-                r.b.store(dst + HALF);
+            if (j < pp.H) {
+                va.pack(a);
+                vb.pack(b);
+                __nv_bfloat16* dst = P1 + ((size_t)n * pp.H + j) * D + c;
+                va.store(dst);
+                vb.store(dst + HALF);
             } else {
 #pragma unroll
                 for (int e = 0; e < VC; ++e)  // as whole numbers, so that a NaN is above all
@@ -166,11 +153,11 @@ __global__ void __launch_bounds__(kThreads)
         }
 #pragma unroll
         for (int o = 1; o < LANES; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (!in || r.j < pp.H || s_row[r.t] < 0) return;
+        if (!in || j < pp.H || s_row[t] < 0) continue;
         const bool finite = top < 0x7f800000u;
         const uint32_t ex = scale_exponent(top);
         const float inv = finite ? __uint_as_float((254u - ex) << 23) : 0.f;
-        const int64_t row = s_row[r.t] + (key ? r.j - pp.H : r.j - pp.H - pp.G) * head;
+        const int64_t row = s_row[t] + g * head;
         int8_t* dst = (key ? P2_pages : I_pages) + (size_t)row * pp.row + c;
         if (!finite)
 #pragma unroll
@@ -179,15 +166,6 @@ __global__ void __launch_bounds__(kThreads)
         store_q8<VC>(dst + HALF, b, inv);
         if (lane == 0)
             scales[2 * row + (key ? 0 : 1)] = __ushort_as_bfloat16(finite ? (unsigned short)(ex << 7) : (unsigned short)0x7fc0);
-    };
-    constexpr int kStep = kThreads / LANES;
-    for (int k0 = threadIdx.x / 32 * (32 / LANES); k0 < total; k0 += FLY * kStep) {
-        const int k = k0 + (int)(threadIdx.x % 32) / LANES;
-        Row r[FLY];
-#pragma unroll
-        for (int f = 0; f < FLY; ++f) fetch(k + f * kStep, r[f]);
-#pragma unroll
-        for (int f = 0; f < FLY; ++f) finish(r[f]);
     }
 }
 
