@@ -57,7 +57,7 @@ def check(x, Y, states, chunked=True):
     Y is rounded once to bf16, 2^-8 of itself.  In chunks a weight's two factors and the weight are rounded to bf16, or
     the query's factor and the state, so the sum of magnitudes gives 3 2^-8 of itself; the recurrence rounds in float32:
     with some 8 roundings a token, 2^-18 for the 16 tokens that run in it.
-    The state: the key's factor is kept to 2^-16; the sums of log2-retentions, up to 100 in a half chunk, have up to
+    The state: the key's factor is kept to 2^-24, to 2^-16 in a strongly fading chunk; the sums of log2-retentions, up to 100 in a half chunk, have up to
     16 roundings of 2^-18 each, ln 2 of which is the relative error; together below 2^-14 of the sum of magnitudes.
     A sum's own rounding, and that of small exponentials, stays below 2^-20 of the largest."""
     (Yr, Sr), (Ya, Sa) = reference(x)
