@@ -23,7 +23,8 @@
 // Measured: decoding 32 requests of 1000 to 32767, 32 heads over 8 of 128: 0.264 to 0.270 ms,
 // 6.7 to 6.8 TB/s, the copy rate; 8 requests of up to 4095, 16 heads of 64: 22 us, of which 3.3 until the first
 // bytes and 4 for the merge; 48 requests of up to 8192 with 0 to 5 new tokens, 10 heads over 5 of
-// 64: 46 us, 4.5 TB/s.
+// 64: 46 us, 4.5 TB/s.  Over 8-bit pages (below): the 32 requests 179 us, 5.5 TB/s of half the bytes; the 8 requests 18 us;
+// the 48 requests 46 us: at 64 columns a key's instructions, not its bytes, are what a worker spends its time on.
 // The sigmoid is (1 + tanh)/2 by the hardware's tanh (2^-11), below the rounding of
 // the bf16 output; the weights are rounded to bf16 for the second product (as the
 // operands are), their sum is not.
