@@ -443,6 +443,9 @@ relation_status_t relation_linear_bwd_gate(const relation_problem_t* p, const vo
  * skipped (a slot past the pool counts as negative) and
  * relation_check_device_status() reports RELATION_ERR_INVALID_ARGUMENT.
  * Outputs must not overlap inputs or each other.
+ * A non-finite value of a token makes its request's head non-finite from that token
+ * on, the state included, and may reach the up to 63 tokens of the same call before
+ * it; other requests and heads are not touched.
  *
  * relation_linear_step: one new token a request (row r is request r's; N >= R, rows
  *   from R on are left unwritten); one launch.

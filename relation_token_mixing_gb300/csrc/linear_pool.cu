@@ -90,12 +90,18 @@ __device__ __forceinline__ Gate gate_of(const LinearPool& p, int h, int c) {
     }
     return g;
 }
+// The larger of two, NaN if one is (fmaxf gives the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 // At least -280: 2^-280 of any float32 is 0, and sums of a chunk's terms keep their fractions.
 template <bool kGate>
 __device__ __forceinline__ float2 log2_retention(float2 x, const Gate& g) {
     const float2 e = kGate ? make_float2(g.na.x * softplus_rel(x.x + g.db.x), g.na.y * softplus_rel(x.y + g.db.y))
                            : make_float2(x.x * g.na.x, x.y * g.na.y);
-    return make_float2(fmaxf(e.x, -280.f), fmaxf(e.y, -280.f));
+    return make_float2(max_nan(e.x, -280.f), max_nan(e.y, -280.f));
 }
 
 // A request's tokens; ones that cannot be followed give count = -1 and are reported.

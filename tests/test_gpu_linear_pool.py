@@ -161,17 +161,18 @@ def test_same_results_from_run_to_run():
     _ok()
 
 
-def test_captured_and_replayed_with_other_lengths():
-    lengths = [[300, 17, 1], [5, 290, 23], [0, 16, 302]]
+@pytest.mark.parametrize("longer", [0, 500])
+def test_captured_and_replayed_with_other_lengths(longer):
+    lengths = [[300 + longer, 17, 1], [5, 290 + longer, 23], [0, 16, 302 + longer]]
     xs = [inputs(n, 2, 64, slots=([0, 1, 2], [0, 1, 2]), seed=20 + k) for k, n in enumerate(lengths)]
     c = on_gpu(xs[0])
     Y = torch.empty_like(c["P1"])
     ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
-    packed(c, max_fresh=310, Y=Y, workspace=ws)  # loads the kernels
+    packed(c, max_fresh=310 + longer, Y=Y, workspace=ws)  # loads the kernels
     torch.cuda.synchronize()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        packed(c, max_fresh=310, Y=Y, workspace=ws)
+        packed(c, max_fresh=310 + longer, Y=Y, workspace=ws)
     for x in xs:
         for k, t in x.items():
             if t is not None:
@@ -181,8 +182,53 @@ def test_captured_and_replayed_with_other_lengths():
         check(x, Y, c["states"])
 
 
-def test_on_another_stream():
-    x = inputs([300, 2, 40], 2, 64, seed=6)
+def test_two_captured_graphs_over_one_workspace():
+    xs = [inputs([900, 3, 70], 2, 64, seed=30), inputs([20, 700, 800, 1], 2, 64, True, seed=31)]
+    cs = [on_gpu(x) for x in xs]
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
+    ys, graphs = [torch.empty_like(c["P1"]) for c in cs], []
+    for c, Y in zip(cs, ys):
+        packed(c, Y=Y, workspace=ws)  # loads the kernels
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            packed(c, Y=Y, workspace=ws)
+    for k in (0, 1, 1, 0):
+        cs[k]["states"].copy_(xs[k]["states"])
+        ys[k].zero_()
+        graphs[k].replay()
+    _ok()
+    for x, c, Y in zip(xs, cs, ys):
+        check(x, Y, c["states"])
+
+
+@pytest.mark.parametrize("lengths", [[90, 130, 5, 40], [90, 900, 5, 40]])
+@pytest.mark.parametrize("which", ["P1", "P2", "I", "G"])
+def test_a_value_that_is_not_finite_stays_with_its_head(which, lengths):
+    """NaN in one head of one token: that head from that token on, at most 63 rows before it, and its state; no other."""
+    x = inputs(lengths, 2, 64, seed=16)
+    c = on_gpu(x)
+    at = lengths[0] + 100
+    c[which][at, 1, 5] = float("nan")
+    Y = packed(c)
+    _ok()
+    end = lengths[0] + lengths[1]
+    assert torch.isnan(Y[at: end, 1].float()).any(-1).all()
+    assert torch.isnan(c["states"][int(c["slots_out"][1]), 1]).any()
+    # The rest as if it had not been.
+    want, pool = packed(dict(on_gpu(x), states=(clean := x["states"].cuda()))), clean
+    keep = torch.ones(Y.shape[:2], dtype=torch.bool, device="cuda")
+    keep[at - 63: end, 1] = False
+    assert torch.equal(Y[keep], want[keep])
+    mine = torch.ones(pool.shape[:2], dtype=torch.bool, device="cuda")
+    mine[int(c["slots_out"][1]), 1] = False
+    assert torch.equal(c["states"][mine], pool[mine])
+    check(x, want, pool)
+
+
+@pytest.mark.parametrize("longest", [300, 900])
+def test_on_another_stream(longest):
+    x = inputs([longest, 2, 40], 2, 64, seed=6)
     c = on_gpu(x)
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
@@ -192,9 +238,10 @@ def test_on_another_stream():
     check(x, Y, c["states"])
 
 
-def test_calls_in_flight_over_one_workspace():
+@pytest.mark.parametrize("longest", [280, 900])
+def test_calls_in_flight_over_one_workspace(longest):
     """Steps queued one after another, each going on from the state of the one before."""
-    x = inputs([280, 30, 1], 2, 64, slots=([0, 1, 2], [0, 1, 2]), seed=12)
+    x = inputs([longest, 30, 1], 2, 64, slots=([0, 1, 2], [0, 1, 2]), seed=12)
     c = on_gpu(x)
     ws = torch.empty(64 << 20, dtype=torch.uint8, device="cuda")
     ys = [packed(c, workspace=ws) for _ in range(5)]
