@@ -11,8 +11,8 @@
 // (linear_chunk_kernel).  Single tokens are bound by the states' bytes; chunks by the instructions and latencies of
 // forming their operands (a channel of a token: two exponentials, two scales, three roundings), far above the bytes.
 // Measured: one token each of 512 requests, 16 heads of 64: 44 us, 6.2 TB/s; of 16 requests, 8 heads of 60: 3.0 us, one
-// launch's latency; one request of 32768 tokens, 8 heads of 60: 128 us, 1.5 TB/s;
-// 24 prompts of up to 2048, 25198 tokens: 137 us; 60 single tokens and 4 chunks of 250 to 500, 16 heads of 64: 44 us.
+// launch's latency; one request of 32768 tokens, 8 heads of 60: 129 us, 1.5 TB/s;
+// 24 prompts of up to 2048, 25198 tokens: 135 us; 60 single tokens and 4 chunks of 250 to 500, 16 heads of 64: 43 us.
 //
 // A chunk.  With q = S p^1, k = S p^2 and the running sum of the log-retentions
 // G_t (from the chunk's start, in units of log2), the retention between tokens j
@@ -59,18 +59,18 @@ __device__ __forceinline__ void dependency_release() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
-// softplus to a relative 3e-7 (softplus_f is exact to 1e-7 absolute, which a float32 state of
-// weak retention would show): log(1 + y) = 2 artanh(y / (2 + y)), y <= 1, by its Taylor series
-// up to the 13th power of an argument of at most 1/3.
-__device__ __forceinline__ float softplus_rel(float x) {
-    const float y = __expf(-fabsf(x)), s = __fdividef(y, 2.f + y), z = s * s;
-    float t = fmaf(z, 1.f / 13.f, 1.f / 11.f);
-    t = fmaf(z, t, 1.f / 9.f);
-    t = fmaf(z, t, 1.f / 7.f);
-    t = fmaf(z, t, 1.f / 5.f);
-    t = fmaf(z, t, 1.f / 3.f);
-    t = fmaf(z, t, 1.f);
-    return fmaf(2.f * s, t, fmaxf(x, 0.f));
+// softplus of two to a relative 2e-7 (softplus_f is exact to 1e-7 absolute, which a float32 state of
+// weak retention would show): log(1 + y) = 2 artanh(s), s = y / (2 + y), y <= 1, with artanh(s) / s by a polynomial of
+// degree 4 in s^2 <= 1/9 (fitted at Chebyshev nodes: 4e-9).
+__device__ __forceinline__ float2 softplus_rel(float2 x) {
+    const auto two = [](float c) { return make_float2(c, c); };
+    const float2 y = make_float2(__expf(-fabsf(x.x)), __expf(-fabsf(x.y))), d = ptx::add2(y, two(2.f));
+    const float2 s = make_float2(__fdividef(y.x, d.x), __fdividef(y.y, d.y)), z = ptx::mul2(s, s);
+    float2 t = ptx::fma2(z, two(0.140873283f), two(0.139807090f));
+    t = ptx::fma2(z, t, two(0.200124264f));
+    t = ptx::fma2(z, t, two(0.333331585f));
+    t = ptx::fma2(z, t, two(1.f));
+    return ptx::fma2(ptx::add2(s, s), t, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
 }
 
 // log2 of the retention of one thread's channels c, c + 1 of head h from what G holds.
@@ -99,8 +99,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // At least -280: 2^-280 of any float32 is 0, and sums of a chunk's terms keep their fractions.
 template <bool kGate>
 __device__ __forceinline__ float2 log2_retention(float2 x, const Gate& g) {
-    const float2 e = kGate ? make_float2(g.na.x * softplus_rel(x.x + g.db.x), g.na.y * softplus_rel(x.y + g.db.y))
-                           : make_float2(x.x * g.na.x, x.y * g.na.y);
+    const float2 e = ptx::mul2(kGate ? softplus_rel(ptx::add2(x, g.db)) : x, g.na);
     return make_float2(max_nan(e.x, -280.f), max_nan(e.y, -280.f));
 }
 
