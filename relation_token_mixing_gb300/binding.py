@@ -670,10 +670,11 @@ def _on_current_device(*tensors) -> None:
 
 def _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias):
     _on_current_device(P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias)
-    if P2.shape != P1.shape or I.shape != P1.shape or G.shape != P1.shape:
+    shape, dtype = P1.shape, P1.dtype
+    if P2.shape != shape or I.shape != shape or G.shape != shape:
         raise ValueError("P1, P2, I and G are [N, H, d_h]")
-    if P2.dtype is not P1.dtype or I.dtype is not P1.dtype or G.dtype is not torch.float32:
-        raise ValueError(f"P2 and I are {P1.dtype}, as P1, and G is torch.float32")
+    if P2.dtype is not dtype or I.dtype is not dtype or G.dtype is not torch.float32:
+        raise ValueError(f"P2 and I are {dtype}, as P1, and G is torch.float32")
     if not (slots_in.dtype is slots_out.dtype is _I32) or slots_in.numel() != prob.R or slots_out.numel() != prob.R:
         raise ValueError("slots_in and slots_out are [R] of torch.int32")
     if (A_log is None) != (dt_bias is None):
@@ -686,10 +687,11 @@ def _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log,
 def _like_on(x, Y, stream):
     """Y, or a tensor like x from the stream that the kernels run on, marked as used by the caller's stream."""
     if Y is None:
-        with torch.cuda.stream(stream):  # None: the current one
+        if stream is None:  # the current one
+            return torch.empty_like(x)
+        with torch.cuda.stream(stream):
             Y = torch.empty_like(x)
-        if stream is not None:
-            Y.record_stream(torch.cuda.current_stream())
+        Y.record_stream(torch.cuda.current_stream())
     elif Y.shape != x.shape or Y.dtype is not x.dtype:
         raise ValueError("Y is like P1")
     return Y
