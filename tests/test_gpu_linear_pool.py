@@ -28,7 +28,7 @@ def test_single_tokens(H, d, gate):
 
 
 @pytest.mark.parametrize("gate", [False, True])
-@pytest.mark.parametrize("H,d", [(1, 64), (3, 60), (2, 48)])
+@pytest.mark.parametrize("H,d", [(1, 64), (3, 60), (2, 48), (4, 60)])
 def test_few_tokens(H, d, gate):
     x = inputs([0, 1, 2, 5, 16, 15, 3, 0], H, d, gate, seed=7)
     c = on_gpu(x)
@@ -39,7 +39,7 @@ def test_few_tokens(H, d, gate):
 
 
 @pytest.mark.parametrize("gate", [False, True])
-@pytest.mark.parametrize("H,d", [(1, 64), (3, 60), (2, 48)])
+@pytest.mark.parametrize("H,d", [(1, 64), (3, 60), (2, 48), (4, 60)])
 @pytest.mark.parametrize("lengths", [[17], [24], [25], [64], [65, 63], [1, 0, 17, 128, 5, 200, 64, 2], [33, 16, 250, 31, 24, 25]])
 def test_requests_of_one_stretch(lengths, H, d, gate):
     x = inputs(lengths, H, d, gate, seed=len(lengths))
@@ -51,7 +51,7 @@ def test_requests_of_one_stretch(lengths, H, d, gate):
 
 
 @pytest.mark.parametrize("gate", [False, True])
-@pytest.mark.parametrize("H,d", [(2, 64), (3, 60), (1, 48)])
+@pytest.mark.parametrize("H,d", [(2, 64), (3, 60), (1, 48), (2, 60)])
 @pytest.mark.parametrize("lengths,bound", [([257], 257), ([1100, 17, 300, 1, 0, 256], 0), ([3, 512, 513, 255, 70], 1000),
                                            ([257], 800), ([770], 770), ([64, 2000, 769, 830, 1], 2000)])
 def test_requests_of_many_segments(lengths, bound, H, d, gate):
@@ -66,9 +66,10 @@ def test_requests_of_many_segments(lengths, bound, H, d, gate):
 
 @pytest.mark.parametrize("lengths", [[40, 100, 64], [300, 20, 64], [900, 20, 64]])
 @pytest.mark.parametrize("kind", ["strong", "one_channel", "resets", "none", "growing", "lowest", "ragged"])
-def test_retention(kind, lengths):
+@pytest.mark.parametrize("d", [64, 60])
+def test_retention(kind, lengths, d):
     """Factors that leave the range of a chunk with one reference, retention of nothing and of everything."""
-    x = inputs(lengths, 2, 64, seed=5)
+    x = inputs(lengths, 2, d, seed=5)
     N = x["G"].shape[0]
     if kind == "strong":
         x["G"] *= 20.0 / x["G"].abs().mean()
