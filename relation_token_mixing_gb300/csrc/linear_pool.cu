@@ -11,8 +11,8 @@
 // (linear_chunk_kernel).  Single tokens are bound by the states' bytes; chunks by the instructions and latencies of
 // forming their operands (a channel of a token: two exponentials, two scales, three roundings), far above the bytes.
 // Measured: one token each of 512 requests, 16 heads of 64: 44 us, 6.2 TB/s; of 16 requests, 8 heads of 60: 3.0 us, one
-// launch's latency; one request of 32768 tokens, 8 heads of 60: 129 us, 1.5 TB/s;
-// 24 prompts of up to 2048, 25198 tokens: 135 us; 60 single tokens and 4 chunks of 250 to 500, 16 heads of 64: 43 us.
+// launch's latency; one request of 32768 tokens, 8 heads of 60: 123 us, 1.5 TB/s;
+// 24 prompts of up to 2048, 25198 tokens: 122 us; 60 single tokens and 4 chunks of 250 to 500, 16 heads of 64: 43 us.
 //
 // A chunk.  With q = S p^1, k = S p^2 and the running sum of the log-retentions
 // G_t (from the chunk's start, in units of log2), the retention between tokens j
@@ -21,7 +21,7 @@
 //     Y = I~ + strictly-lower(q~ k~^T) I~ + q~ (2^m C),
 //     C <- 2^(G_end - m) (2^m C + k~^T I~)
 // is the recurrence in four products of 64 x 64 x 64, all from the same two operands.
-// m is the sum at the chunk's middle: half a chunk may then lose up to 2^kRange of
+// m is half of what the chunk loses, G_end / 2: a chunk may then lose up to 2^(2 kRange) of
 // a channel before a factor leaves the range of bf16.  A chunk that loses more in some
 // channel takes another way to the same sums (strong_chunk below) whose factors
 // are all retentions between two of its own tokens.
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kFewThreads)
 // ------------------------------------------------------------------- chunks
 constexpr int kT = kChunk;
 constexpr int kThreads = 256, kBlocksPerSm = 2;
-constexpr float kRange = 100.f;   // log2 of what half a chunk may lose of a channel
+constexpr float kRange = 100.f;   // log2 of half of what a chunk may lose of a channel
 constexpr int kTile = kT * 128;   // a bf16 tile of 64 x 64
 constexpr int kGp = kDp + 8;      // of a row of sums: eight rows' same columns on different banks
 constexpr int kSegFloats = kDp * kDp + kDp;  // of a segment in the workspace: its state, the log2 of its retention
@@ -346,8 +346,8 @@ struct ChunkSmem {
         };
     };
     uint8_t w[kTile];  // the weights inside the chunk, [query][key]; before, what two bf16 leave of k~
-    float c_op[kDp], c_all[kDp], c_rest[kDp];  // per channel: factors of the state as an operand and through the
-                                               // chunk, and of what the chunk adds
+    float c_half[kDp], c_all[kDp];  // per channel: factor of the state as an operand and of what the chunk adds; of the
+                                    // state through the chunk
     float2 rs[kT];        // (S / |p1|, S / |p2|) of a token
     uint64_t c_done, o_done, drain;
     uint32_t tmem;
@@ -670,19 +670,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             G[i] = sum;
         }
         *reinterpret_cast<float2*>(&sm.tot[warp][c2]) = sum;
-        // A state that grows may do so at one token and fade at others: the sums of half a chunk say nothing then.
+        // A state that grows may do so at one token and fade at others: the sums say nothing then.
         const bool grows = kGate ? (__syncthreads(), false) : __syncthreads_or(most > 0.f);
-        float2 base = make_float2(0.f, 0.f), mid = base, rest = base;
+        float2 base = make_float2(0.f, 0.f), all = base;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
-            const float2 x = *reinterpret_cast<const float2*>(&sm.tot[w][c2]);
-            if (w == warp) base = add2(mid, rest);
-            if (w < 4) mid = add2(mid, x);
-            else rest = add2(rest, x);
+            if (w == warp) base = all;
+            all = add2(all, *reinterpret_cast<const float2*>(&sm.tot[w][c2]));
         }
-        const float2 all = add2(mid, rest);
-        const float least = fminf(fminf(mid.x, mid.y), fminf(rest.x, rest.y));
-        const bool is_strong = grows || __any_sync(0xffffffffu, !(least >= -kRange));  // the same for every warp
+        const float2 half = mul2(all, make_float2(0.5f, 0.5f));
+        // The same for every warp.
+        const bool is_strong = grows || __any_sync(0xffffffffu, !(fminf(half.x, half.y) >= -kRange));
         if (!kRare && is_strong) return kStop;
         const bool strong = kRare && is_strong;
         lost = add2(lost, all);
@@ -702,9 +700,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             }
         }
         // The operands, in the rows' places: a warp's own tokens, a lane's own channels.  Exponents: of a query
-        // G - mid and of a key its negative; in a strong chunk from the chunk's start, and to its end.
+        // G - m and of a key its negative; in a strong chunk from the chunk's start, and to its end.
         const bool third = !kOut || !strong;  // of k~, in the weights' place until those are there
-        const float2 from = strong ? base : make_float2(base.x - mid.x, base.y - mid.y);
+        const float2 from = strong ? base : make_float2(base.x - half.x, base.y - half.y);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint32_t at = own + i * 128 + (((lane >> 2) ^ i) << 4);  // swz(8 warp + i, c2)
@@ -732,10 +730,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (warp == 1) {
             const float2 one = make_float2(1.f, 1.f);
             *reinterpret_cast<float2*>(&sm.c_all[c2]) = make_float2(ptx::ex2_approx(all.x), ptx::ex2_approx(all.y));
-            *reinterpret_cast<float2*>(&sm.c_op[c2]) =
-                strong ? one : make_float2(ptx::ex2_approx(mid.x), ptx::ex2_approx(mid.y));
-            *reinterpret_cast<float2*>(&sm.c_rest[c2]) =
-                strong ? one : make_float2(ptx::ex2_approx(rest.x), ptx::ex2_approx(rest.y));
+            *reinterpret_cast<float2*>(&sm.c_half[c2]) =
+                strong ? one : make_float2(ptx::ex2_approx(half.x), ptx::ex2_approx(half.y));
         }
         load_g(row + (size_t)(n + 1) * kT * stride, left - kT);  // the next chunk's
         ptx::fence_proxy_async_smem();
@@ -762,11 +758,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             ptx::mma_commit_elect(&sm.c_done);
         }
         if (kOut) {
-            // The state as an operand: 2^mid C, and C itself in a strong chunk.
+            // The state as an operand: 2^m C, and C itself in a strong chunk.
             uint32_t w[4][2];
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const float2 f = *reinterpret_cast<const float2*>(&sm.c_op[col0 + 8 * x + 2 * t]);
+                const float2 f = *reinterpret_cast<const float2*>(&sm.c_half[col0 + 8 * x + 2 * t]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const float2 a = mul2(C[x][e], f);
@@ -819,7 +815,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 const float2 a = *reinterpret_cast<const float2*>(&sm.c_all[col0 + 8 * c + 2 * t]);
-                const float2 f = *reinterpret_cast<const float2*>(&sm.c_rest[col0 + 8 * c + 2 * t]);
+                const float2 f = *reinterpret_cast<const float2*>(&sm.c_half[col0 + 8 * c + 2 * t]);
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     C[c][e] = fma2(make_float2(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), f,
