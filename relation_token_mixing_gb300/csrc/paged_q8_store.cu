@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads)
     for (int k = threadIdx.x; k < count * HALF; k += kThreads) {
         const int t = k / HALF, c = k - t * HALF;
         float sn = 0.f, cs = 1.f;
-        if (tab.enabled) position_sincos(positions[n0 + t], tab.hi[c], tab.lo[c], &sn, &cs);
+        if (tab.enabled) position_sincos_fine(positions[n0 + t], tab.hi[c], tab.lo[c], &sn, &cs);
         turn[t * HALF + c % VC * PER + c / VC] = make_float2(cs, sn);
     }
     if (theta != nullptr)

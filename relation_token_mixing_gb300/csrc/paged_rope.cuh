@@ -24,4 +24,30 @@ __device__ __forceinline__ void position_sincos(int pos, float hi, float lo, flo
     sincospif(2.f * (turns - rintf(turns)), s, c);
 }
 
+// The same to 1e-7, for rows that are rounded to fewer bits than a float of angle error would let stand: the turns are
+// summed with what each addition loses, and that turns the pair by a little more.
+__device__ __forceinline__ void position_sincos_fine(int pos, float hi, float lo, float* s, float* c) {
+    float turns = 0.f, lost = 0.f;
+    auto add = [&](float x) {
+        const float t = turns + x, z = t - turns;
+        lost += (turns - (t - z)) + (x - z);
+        turns = t;
+    };
+    auto part = [&](float p) {
+        for (const float f : {hi, lo}) {
+            const float whole = p * f, err = fmaf(p, f, -whole);
+            add(whole - rintf(whole));
+            add(err - rintf(err));
+        }
+    };
+    const int rest = pos % (1 << 24);
+    part((float)rest);
+    if (rest != pos) part((float)(pos - rest));
+    float sn, cs;
+    sincospif(2.f * (turns - rintf(turns)), &sn, &cs);
+    const float more = 6.2831853f * lost;
+    *s = fmaf(cs, more, sn);
+    *c = fmaf(-sn, more, cs);
+}
+
 }  // namespace relation
