@@ -316,3 +316,45 @@ def test_agrees_with_the_dense_forward():
     scale = float(Yd.float().abs().max())
     assert float((Y.view(B, T, H, d).float() - Yd.float()).abs().max()) <= 2e-2 * scale  # both within 1e-2
     assert float((c["states"] - state).abs().max()) <= 2e-2 * float(np.abs(state.cpu().numpy()).max())
+
+
+def test_slots_past_32_bits():
+    """A pool of more than 2^32 floats: its last slots against the same states in a small pool."""
+    H, d, slots = 8, 64, 132000
+    big = rb.linear_states(slots, H, d)
+    assert big.numel() > 1 << 32
+    x = inputs([70, 1, 5, 900], H, d, slots=([4, 5, -1, 6], [0, 5, 1, 2]), seed=17)
+    small = on_gpu(x)
+    n = small["states"].shape[0]
+    big[-n:] = small["states"]
+    Y = packed(small)
+    up = lambda s: torch.where(s < 0, s, s + slots - n)  # noqa: E731
+    Yb = packed(dict(small, states=big, slots_in=up(small["slots_in"]), slots_out=up(small["slots_out"])))
+    _ok()
+    assert torch.equal(Y, Yb) and torch.equal(big[-n:], small["states"])
+    assert (big[:-n] == 0).all()
+
+
+@pytest.mark.parametrize("max_fresh", [0, 1])
+def test_rows_past_32_bits(max_fresh):
+    """Packed tensors of more than 2^31 values: the last request's heads against a call of their own."""
+    H, d = 1024, 64
+    lengths = [33000, 17, 1] if max_fresh == 0 else [1] * 33018
+    N, gen = sum(lengths), torch.Generator("cuda").manual_seed(18)
+    assert N * H * d > 1 << 31
+    P1, P2, I = (torch.randn(N, H, d, generator=gen, device="cuda", dtype=torch.bfloat16) for _ in range(3))
+    G = -0.1 * torch.rand(N, H, d, generator=gen, device="cuda")
+    starts = torch.tensor([0] + lengths, device="cuda").cumsum(0).int()
+    R, last = len(lengths), 3
+    keep = torch.full((R,), -1, dtype=torch.int32, device="cuda")
+    keep[-last:] = torch.arange(last, device="cuda", dtype=torch.int32)
+    states = rb.linear_states(last, H, d)
+    Y = rb.linear_packed_fwd(P1, P2, I, G, starts, states, torch.full_like(keep, -1), keep, max_fresh, TAU)
+    _ok()
+    n = sum(lengths[-2:])  # the last two requests, first and last head
+    for h in (0, H - 1):
+        x = dict(P1=P1, P2=P2, I=I, G=G)
+        x = {k: t[-n:, h: h + 1].contiguous().cpu() for k, t in x.items()}
+        x |= dict(A_log=None, dt_bias=None, starts=torch.tensor([0, lengths[-2], n]), states=torch.zeros(2, 1, d, d),
+                  slots_in=torch.tensor([-1, -1]), slots_out=torch.tensor([0, 1]))
+        check(x, Y[-n:, h: h + 1].cpu(), states[-2:, h: h + 1].cpu())
