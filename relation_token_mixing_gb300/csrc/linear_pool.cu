@@ -12,7 +12,7 @@
 // forming their operands (a channel of a token: two exponentials, two scales, three roundings), far above the bytes.
 // Measured: one token each of 512 requests, 16 heads of 64: 44 us, 6.2 TB/s; of 16 requests, 8 heads of 60: 3.0 us, one
 // launch's latency; one request of 32768 tokens, 8 heads of 60: 123 us, 1.5 TB/s;
-// 24 prompts of up to 2048, 25198 tokens: 122 us; 60 single tokens and 4 chunks of 250 to 500, 16 heads of 64: 43 us.
+// 24 prompts of up to 2048, 25198 tokens: 122 us; 60 single tokens and 4 chunks of 250 to 500, 16 heads of 64: 40 us.
 //
 // A chunk.  With q = S p^1, k = S p^2 and the running sum of the log-retentions
 // G_t (from the chunk's start, in units of log2), the retention between tokens j
@@ -136,6 +136,7 @@ struct Plan {
     Item* items;
     int *order, *joins;
     int most_items, most_joins, seg_tokens;
+    bool beside;  // the requests of few tokens run beside the others, which were launched before them
 };
 
 // ------------------------------------------------------------ the recurrence
@@ -223,8 +224,13 @@ __global__ void __launch_bounds__(kFewThreads)
           (*const sv)[kDp] = sk + most;
     constexpr int kCols = D / 4, kRows = (D + 7) / 8;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    dependency_wait();
+    // Beside the chunks' kernel, which waited for what ran before it, only the grid's end has to wait for that kernel's.
+    if (!plan.beside) dependency_wait();
     dependency_release();
+    if (plan.beside && blockIdx.x == gridDim.x - 1) {
+        dependency_wait();
+        return;
+    }
     int x = blockIdx.x;
     if (plan.items != nullptr) {
         if (x == 0) {
@@ -544,8 +550,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     int x = blockIdx.x / p.H;
     const int h = blockIdx.x - x * p.H;
-    // The kernel before waited for what ran before it, and leaves the items.
-    if (plan.items != nullptr) dependency_wait();
+    dependency_wait();
     dependency_release();
     Item it{x, 0, 0, 1 << 16};
     if (plan.items != nullptr) {
@@ -557,10 +562,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         it.first = sp.first, it.count = sp.count;
     }
     const int seg = it.seg_segs & 0xffff, segs = it.seg_segs >> 16;
-    if (it.count <= (segs > 1 ? 0 : kFewTokens) || (!kOut && seg + 1 == segs)) {
-        if (plan.items == nullptr && tid == 0) dependency_wait();
-        return;
-    }
+    if (it.count <= (segs > 1 ? 0 : kFewTokens) || (!kOut && seg + 1 == segs)) return;
     if (tid == 0) {
         for (uint64_t* bar : {&sm.c_done, &sm.o_done, &sm.drain}) ptx::mbar_init(bar, 1);
         sm.abort_flag = 0;
@@ -885,8 +887,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
                 if (v < ld && c < ld) out[(size_t)c * ld + v] = C[n][e].x, out[(size_t)(c + 1) * ld + v] = C[n][e].y;
             }
     }
-    // (few calls: the whole chain ends with this kernel's end)
-    if (plan.items == nullptr && tid == 0) dependency_wait();
 }
 
 // Every segment's entering state in the place of its own contribution, from the pool's
@@ -973,7 +973,7 @@ cudaError_t launch(void (*kern)(P...), dim3 grid, int threads, size_t smem, cuda
 
 template <bool kGate>
 cudaError_t launch_few(const LinearPool& p, const Plan& plan, cudaStream_t s) {
-    const dim3 grid((unsigned)((int64_t)p.R * p.H + (plan.items != nullptr)));
+    const dim3 grid((unsigned)((int64_t)p.R * p.H + (plan.items != nullptr || plan.beside)));
     switch (p.d) {
         case 48: return launch(linear_few_kernel<48, kGate>, grid, kFewThreads, few_smem(p.max_fresh), s, p, plan);
         case 60: return launch(linear_few_kernel<60, kGate>, grid, kFewThreads, few_smem(p.max_fresh), s, p, plan);
@@ -993,9 +993,11 @@ cudaError_t launch_pool(const LinearPool& p, void* workspace, const Cut& cut, in
         plan.most_items = cut.items, plan.most_joins = cut.joins, plan.seg_tokens = cut.seg_tokens;
         segments = reinterpret_cast<float*>(static_cast<char*>(workspace) + items_bytes(cut));
     }
-    cudaError_t e = launch_few<kGate>(p, plan, s);
-    *launches = 1;
-    if (e != cudaSuccess || !cut.chunked) return e;
+    cudaError_t e;
+    if (!cut.chunked) {
+        *launches = 1;
+        return launch_few<kGate>(p, plan, s);
+    }
     constexpr int smem = (int)sizeof(ChunkSmem) + 1024;
     static OncePerDevice once_out, once_state, split_out, split_state;
     if ((e = prefer_shared(split_out, linear_chunk_kernel<true, kGate>, kBlocksPerSm, smem)) != cudaSuccess) return e;
@@ -1003,16 +1005,20 @@ cudaError_t launch_pool(const LinearPool& p, void* workspace, const Cut& cut, in
     if ((e = allow_dynamic_smem(once_out, linear_chunk_kernel<true, kGate>, smem)) != cudaSuccess) return e;
     if ((e = allow_dynamic_smem(once_state, linear_chunk_kernel<false, kGate>, smem)) != cudaSuccess) return e;
     const dim3 grid((unsigned)((int64_t)cut.items * p.H));
-    if (cut.segmented) {
-        *launches = 4;
-        e = launch(linear_chunk_kernel<false, kGate>, grid, kThreads, smem, s, p, plan, segments);
-        if (e != cudaSuccess) return e;
-        e = launch(linear_join_kernel, dim3((unsigned)cut.joins, (unsigned)p.H, kDp * kDp / kScanThreads), kScanThreads, 0,
-                   s, p, plan, segments);
-        if (e != cudaSuccess) return e;
-    } else {
+    if (!cut.segmented) {
+        // The longer requests first, the others in the room beside them (60 single tokens and 4 chunks of 250 to 500,
+        // 16 heads of 64: 40 us; the other way round 43).
         *launches = 2;
+        plan.beside = true;
+        e = launch(linear_chunk_kernel<true, kGate>, grid, kThreads, smem, s, p, plan, segments);
+        return e != cudaSuccess ? e : launch_few<kGate>(p, plan, s);
     }
+    *launches = 4;
+    if ((e = launch_few<kGate>(p, plan, s)) != cudaSuccess) return e;
+    if ((e = launch(linear_chunk_kernel<false, kGate>, grid, kThreads, smem, s, p, plan, segments)) != cudaSuccess) return e;
+    e = launch(linear_join_kernel, dim3((unsigned)cut.joins, (unsigned)p.H, kDp * kDp / kScanThreads), kScanThreads, 0, s, p,
+               plan, segments);
+    if (e != cudaSuccess) return e;
     return launch(linear_chunk_kernel<true, kGate>, grid, kThreads, smem, s, p, plan, segments);
 }
 
