@@ -441,7 +441,9 @@ relation_status_t relation_linear_bwd_gate(const relation_problem_t* p, const vo
  * A slot past the pool, packed offsets that do not ascend or pass N, or more new
  * tokens than max_fresh are never followed: such a request's rows or state are
  * skipped (a slot past the pool counts as negative) and
- * relation_check_device_status() reports RELATION_ERR_INVALID_ARGUMENT.
+ * relation_check_device_status() reports RELATION_ERR_INVALID_ARGUMENT.  Where
+ * offsets descend, a later request can have rows of an earlier one: it may be
+ * skipped too, and the rows that it shares hold the outputs of either.
  * Outputs must not overlap inputs or each other.
  * A non-finite value of a token makes its request's head non-finite from that token
  * on, the state included, and may reach the up to 63 tokens of the same call before

@@ -39,6 +39,7 @@
 
 #include "common.cuh"
 #include "linear_common.cuh"
+#include "linear_cut.h"
 #include "linear_pool.h"
 #include "once_per_device.h"
 #include "ptx_sm100.cuh"
@@ -49,11 +50,6 @@ namespace lin {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-// Tokens that the recurrence takes one by one. 64 requests, 16 heads of 64, of 16 tokens each: 18.6 us so, 28.8 as a
-// chunk; of 24: 25 and 28.8, but room for 24 tokens' vectors leaves the long requests' kernels beside it less of an
-// SM's memory (prompts of up to 2048 tokens, 8 heads of 60: 139 us against 130).
-constexpr int kFewTokens = 16;
-
 __device__ __forceinline__ void dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dependency_release() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -104,18 +100,11 @@ __device__ __forceinline__ float2 log2_retention(float2 x, const Gate& g) {
 }
 
 // A request's tokens; ones that cannot be followed give count = -1 and are reported.
-struct Span {
-    int first, count;
-};
 __device__ __forceinline__ Span span_of(const LinearPool& p, int r) {
     if (p.starts == nullptr) return Span{r, 1};
-    const int first = __ldg(p.starts + r);
-    const int64_t n = (int64_t)__ldg(p.starts + r + 1) - first;
-    if (first < 0 || n < 0 || first + n > p.N || n > p.max_fresh) {
-        record_status(p.status, kDevBadPosition);
-        return Span{0, -1};
-    }
-    return Span{first, (int)n};
+    const Span sp = span_between(__ldg(p.starts + r), __ldg(p.starts + r + 1), p.N, p.max_fresh);
+    if (sp.count < 0) record_status(p.status, kDevBadPosition);
+    return sp;
 }
 // The state a slot names, or nullptr (negative: none; past the pool: reported).
 __device__ __forceinline__ float* state_of(const LinearPool& p, int slot, int h) {
@@ -129,8 +118,6 @@ struct Item {
     int r, first, count;
     int seg_segs;  // seg | segs << 16 (segs = 0: no such item)
 };
-constexpr int kMaxSegs = 1 << 15;
-constexpr int kChunk = 64;  // tokens
 // What block 0 of the first kernel leaves for the others (items = nullptr: every request is one segment).
 struct Plan {
     Item* items;
@@ -151,27 +138,37 @@ constexpr int few_smem(int max_fresh) { return std::min(max_fresh, kFewTokens) *
 
 // Block 0 of a packed call with items: the longer requests' segments, a request's side by side and equal but for whole
 // chunks; where the requests of more than one begin; and the order in which blocks take the segments, the longest
-// first (those of one length in any order), so that the last to start are short.
+// first (those of one length in any order), so that the last to start are short. A request with rows before the end
+// of an earlier one is reported and has none: the list has places for each row once.
 __device__ void make_items(const LinearPool& p, const Plan& plan) {
     constexpr int kBins = 64;  // of segments by their chunks, 63 and more together
-    __shared__ int sums[kFewThreads / 32], many, bins[kBins];
+    __shared__ int sums[kFewThreads / 32], ends[kFewThreads / 32], many, bins[kBins];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const auto bin_of = [](int tokens) { return kBins - 1 - min((tokens + kChunk - 1) / kChunk, kBins - 1); };
     if (tid == 0) many = 0;
     for (int k = tid; k < kBins; k += kFewThreads) bins[k] = 0;
-    int base = 0;
+    int base = 0, end = 0;  // segments of the requests before, and the end of their rows
     for (int r0 = 0; r0 < p.R; r0 += kFewThreads) {
         const int r = r0 + tid;
         Span sp{0, 0};
         if (r < p.R) sp = span_of(p, r);
-        int segs = 0, each = 0;  // tokens of one
-        if (sp.count > kFewTokens) {
-            const int chunks = (sp.count + kChunk - 1) / kChunk;
-            segs = (sp.count + plan.seg_tokens - 1) / plan.seg_tokens;
-            const int per = (chunks + segs - 1) / segs;
-            segs = (chunks + per - 1) / per, each = per * kChunk;
+        int e = sp.end();
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, e, o);
+            if (lane >= o) e = max(e, y);
         }
-        int x = segs;
+        if (lane == 31) ends[warp] = e;
+        __syncthreads();
+        int before = __shfl_up_sync(0xffffffffu, e, 1);
+        before = max(end, lane ? before : 0);
+        for (int w = 0; w < kFewThreads / 32; ++w) {
+            if (w < warp) before = max(before, ends[w]);
+            end = max(end, ends[w]);
+        }
+        const Segments sg = segments_of(sp, before, plan.seg_tokens);
+        if (sg.refused) record_status(p.status, kDevBadPosition);
+        int x = sg.count;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -179,19 +176,20 @@ __device__ void make_items(const LinearPool& p, const Plan& plan) {
         }
         if (lane == 31) sums[warp] = x;
         __syncthreads();
-        int at = base + x - segs;
+        int at = base + x - sg.count;
         for (int w = 0; w < kFewThreads / 32; ++w) {
             if (w < warp) at += sums[w];
             base += sums[w];
         }
-        for (int k = 0; k < segs && at + k < plan.most_items; ++k) {
-            const int count = min(each, sp.count - k * each);
-            plan.items[at + k] = Item{r, sp.first + k * each, count, k | segs << 16};
+        const bool fits = at + sg.count <= plan.most_items;  // (always: cut_of)
+        for (int k = 0; k < sg.count && at + k < plan.most_items; ++k) {
+            const int count = fits ? min(sg.tokens, sp.count - k * sg.tokens) : 0;
+            plan.items[at + k] = Item{r, sp.first + k * sg.tokens, count, k | sg.count << 16};
             atomicAdd(&bins[bin_of(count)], 1);
         }
-        if (segs > 1) {  // in any order
-            const int x = atomicAdd(&many, 1);
-            if (x < plan.most_joins) plan.joins[x] = at;
+        if (sg.count > 1 && fits) {  // in any order
+            const int k = atomicAdd(&many, 1);
+            if (k < plan.most_joins) plan.joins[k] = at;
         }
         __syncthreads();
     }
@@ -327,7 +325,7 @@ __global__ void __launch_bounds__(kFewThreads)
 
 // ------------------------------------------------------------------- chunks
 constexpr int kT = kChunk;
-constexpr int kThreads = 256, kBlocksPerSm = 2;
+constexpr int kThreads = 256;
 constexpr float kRange = 100.f;   // log2 of half of what a chunk may lose of a channel
 constexpr int kTile = kT * 128;   // a bf16 tile of 64 x 64
 constexpr int kGp = kDp + 8;      // of a row of sums: eight rows' same columns on different banks
@@ -901,6 +899,7 @@ __global__ void __launch_bounds__(kScanThreads)
     if (at < 0) return;
     const Item it = plan.items[at];
     const int segs = it.seg_segs >> 16, h = blockIdx.y;
+    if (at + segs > plan.most_items) return;  // (never: make_items)
     const int e = blockIdx.z * kScanThreads + threadIdx.x, c = e >> 6, v = e & 63;
     const float* in = state_of(p, __ldg(p.slots_in + it.r), h);
     float C = in != nullptr && c < p.d && v < p.d ? in[(size_t)c * p.d + v] : 0.f;
@@ -925,32 +924,6 @@ __global__ void __launch_bounds__(kScanThreads)
     }
 }
 
-constexpr int kLeastCut = 256, kUncut = 640;
-// How a packed call is cut: requests longer than `seg_tokens` in equal segments of that many at most.
-struct Cut {
-    bool chunked;     // a request may have more than kFewTokens new tokens
-    bool segmented;   // and is worth cutting
-    int seg_tokens, items;
-    int joins;        // requests of more than one segment
-};
-Cut cut_of(int R, int N, int H, int max_fresh, int num_sms) {
-    Cut c{};
-    c.chunked = max_fresh > kFewTokens;
-    if (!c.chunked) return c;
-    // share: a block's equal share of all tokens. A request of up to 1.5 of it, or of up to kUncut tokens, is left whole:
-    // cutting costs the state pass (0.6 of the output pass), the join and two more launches (4 requests, 16 heads
-    // of 64: 512 tokens each 28 us whole and 35 cut, 640: 33 and 35, 768: 39 and 35, 1536: 74 and 48).
-    // One request is cut in equal shares; several in halves of one, kLeastCut at least, as their blocks are evened out by
-    // the order (prompts of up to 2048, 8 heads of 60: 131 us, in whole shares 142, in 512 at least 137, uncut 167).
-    const int64_t share = (int64_t)N * H / (kBlocksPerSm * num_sms);
-    int64_t seg = std::max<int64_t>(kLeastCut, ((R > 1 ? share / 2 : share) + kT - 1) / kT * kT);
-    seg = std::max<int64_t>(seg, ((int64_t)max_fresh / (kMaxSegs - 1) + kT) / kT * kT);
-    c.seg_tokens = (int)std::min<int64_t>(seg, (INT32_MAX - kT) / kT * kT);
-    c.segmented = max_fresh > std::max<int64_t>({kUncut, share + share / 2, c.seg_tokens});
-    c.items = c.segmented ? (int)std::min<int64_t>((int64_t)N / c.seg_tokens + std::min(R, N / (kFewTokens + 1)), INT32_MAX) : R;
-    c.joins = std::min(R, N / (c.seg_tokens + 1));
-    return c;
-}
 // The list of segments, their order, the list of joins.
 size_t items_bytes(const Cut& c) {
     return ((size_t)c.items * (sizeof(Item) + sizeof(int)) + (size_t)c.joins * sizeof(int) + 255) / 256 * 256;
