@@ -461,7 +461,8 @@ __device__ __forceinline__ void row_scalars(ChunkSmem& sm, const ChunkStage& s, 
 // reference would leave bf16's range: sm.g holds G, s.p1 and s.p2 the rows as they came.  Of each 16 queries, keys
 // before them meet the queries at the block's first token, the block's first 8 keys its last 8 queries at the ninth:
 // all factors are retentions.  What is left are pairs inside 8 tokens, a lane a pair.  Warps w and w + 4 share 16
-// queries, 8 keys in turn.  Chunks like this are rare; one costs its block some 9 us (others: 4), most of it code that
+// queries, 8 keys in turn.  Behind n tokens that forget everything the sums keep an exponent to 280 n 2^-24, 2^-10 at
+// most: less than the weights' rounding, 2^-8.  Chunks like this are rare; one costs its block some 9 us (others: 4), most of it code that
 // no other block has fetched.
 __device__ __noinline__ void strong_chunk(ChunkSmem& sm, const ChunkStage& s, int warp, int lane) {
     const int g = lane >> 2, t = lane & 3, rt = warp & 3, half = warp >> 2, i0 = 16 * rt + g;
@@ -625,6 +626,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     }
     const uint32_t own = 8 * warp * 128 + ((c2 & 7) << 1);  // the lane's channels in its tokens' rows, see `at`
     const Gate gate = gate_of<kGate>(p, h, c2);
+    // log2 of the retention of the warp's token i, `left` tokens from the chunk's first one on, from what G holds.
+    auto retention = [&](float2 g, int i, int left) {
+        const float2 e = log2_retention<kGate>(g, gate);
+        return kGate && (8 * warp + i >= left || c2 >= p.d) ? make_float2(0.f, 0.f) : e;  // (a gate opens at zero)
+    };
+    auto retention_of = [&](int n, int i, int left) {
+        float2 g = make_float2(0.f, 0.f);
+        if (c2 < p.d && 8 * warp + i < left)
+            g = __ldg(reinterpret_cast<const float2*>(p.G + row + ((size_t)n * kT + 8 * warp + i) * stride + c2));
+        return retention(g, i, left);
+    };
     float2 lost = make_float2(0.f, 0.f);  // log2 of the segment's retention
     // Operands along a row (K) or across rows (M).
     constexpr uint32_t kKK = ptx::idesc_bf16(64, 64, false, false), kKM = ptx::idesc_bf16(64, 64, false, true),
@@ -663,8 +675,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         float most = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float2 e = log2_retention<kGate>(G[i], gate);
-            if (kGate && (8 * warp + i >= left || c2 >= p.d)) e = make_float2(0.f, 0.f);  // (a gate opens at zero)
+            const float2 e = retention(G[i], i, left);
             if (!kGate) most = ptx::max3(most, e.x, e.y);
             sum = add2(sum, e);
             G[i] = sum;
@@ -684,11 +695,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         if (!kRare && is_strong) return kStop;
         const bool strong = kRare && is_strong;
         lost = add2(lost, all);
-        float2 to_end = sum;
+        float2 later = make_float2(0.f, 0.f);  // (strong) from the warp's tokens to the chunk's end
         if (strong) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-                if (x > warp) to_end = add2(to_end, *reinterpret_cast<const float2*>(&sm.tot[x][c2]));
+                if (x > warp) later = add2(later, *reinterpret_cast<const float2*>(&sm.tot[x][c2]));
             if (kOut) {
                 __syncthreads();  // before the sums are overwritten
 #pragma unroll
@@ -702,12 +713,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         // The operands, in the rows' places: a warp's own tokens, a lane's own channels.  Exponents: of a query
         // G - m and of a key its negative; in a strong chunk from the chunk's start, and to its end.
         const bool third = !kOut || !strong;  // of k~, in the weights' place until those are there
-        const float2 from = strong ? base : make_float2(base.x - half.x, base.y - half.y);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        auto operands = [&](int i, float2 eq, float2 ek) {
             const uint32_t at = own + i * 128 + (((lane >> 2) ^ i) << 4);  // swz(8 warp + i, c2)
-            const float2 f = sm.rs[8 * warp + i], eq = add2(from, G[i]);
-            const float2 ek = strong ? make_float2(to_end.x - G[i].x, to_end.y - G[i].y) : make_float2(-eq.x, -eq.y);
+            const float2 f = sm.rs[8 * warp + i];
             if (kOut) {
                 const uint32_t x = *reinterpret_cast<const uint32_t*>(s.p1 + at);
                 const float2 q = mul2(mul2(make_float2(lo_f(x), hi_f(x)), make_float2(f.x, f.x)),
@@ -725,6 +733,28 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             if (third) {
                 const float2 least = add2(lo, make_float2(-lo_f(l), -hi_f(l)));
                 *reinterpret_cast<uint32_t*>(sm.w + at) = pack2(least.x, least.y);
+            }
+        };
+        if (!strong) {
+            const float2 from = make_float2(base.x - half.x, base.y - half.y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 eq = add2(from, G[i]);
+                operands(i, eq, make_float2(-eq.x, -eq.y));
+            }
+        } else {
+            // A key's retention to the end is summed from the end: as a difference of sums from the start, a token
+            // that forgets everything between takes the fraction of what is left with it (the states of four such tokens
+            // in a row were off by 5e-5 of their sums of magnitudes, so by 7e-6).  What G held is read again: a
+            // loop, one copy of the code in the state pass; unrolled, 2 us of 122 (one request of 32768 tokens).
+#pragma unroll 1
+            for (int i = 7; i >= 0; --i) {
+                float2 prefix = G[0];
+#pragma unroll
+                for (int j = 1; j < 8; ++j)
+                    if (j == i) prefix = G[j];
+                operands(i, add2(base, prefix), later);
+                later = add2(later, retention_of(n, i, left));
             }
         }
         if (warp == 1) {
