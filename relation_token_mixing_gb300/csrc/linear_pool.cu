@@ -23,7 +23,7 @@
 // is the recurrence in four products of 64 x 64 x 64, all from the same two operands.
 // m is half of what the chunk loses, G_end / 2: a chunk may then lose up to 2^(2 kRange) of
 // a channel before a factor leaves the range of bf16.  A chunk that loses more in some
-// channel takes another way to the same sums (strong_chunk below) whose factors
+// channel, or has an |I~| above kLargest, takes another way to the same sums (strong_chunk below) whose factors
 // are all retentions between two of its own tokens.
 //
 // Roundings: q~, the weights and the state as an operand of the output product are
@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(kFewThreads)
 constexpr int kT = kChunk;
 constexpr int kThreads = 256;
 constexpr float kRange = 100.f;   // log2 of half of what a chunk may lose of a channel
+constexpr float kLargest = 0x1p20f;  // of |I~|: 64 terms of 2^(kRange + 20) stay below 2^127
 constexpr int kTile = kT * 128;   // a bf16 tile of 64 x 64
 constexpr int kGp = kDp + 8;      // of a row of sums: eight rows' same columns on different banks
 constexpr int kSegFloats = kDp * kDp + kDp;  // of a segment in the workspace: its state, the log2 of its retention
@@ -429,32 +430,38 @@ struct Loader {
 
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return ptx::add2(a, b); }
 
-// The warp's 8 tokens: |p1|^2, |p2|^2 and p1 . p2 are the diagonals of three 8 x 8 products of the rows with
-// one another (a row's fragment is the same on both sides), then S / |p1| and S / |p2|.  Twelve products and
-// four fetches in place of some 150 multiply-adds and shuffles.
-__device__ __forceinline__ void row_scalars(ChunkSmem& sm, const ChunkStage& s, float zscale, int warp, int lane) {
-    float n1[4] = {}, n2[4] = {}, dt[4] = {};
+// The warp's 8 tokens: |p1|^2, |p2|^2, |I~|^2 and p1 . p2 are the diagonals of 8 x 8 products of the rows with
+// one another (a row's fragment is the same on both sides, and p1's and p2's stand over each other), then S / |p1| and
+// S / |p2|.  Twelve products and six fetches in place of some 200 multiply-adds and shuffles.  Returns whether the lane's
+// |I~| is above kLargest.
+__device__ __forceinline__ bool row_scalars(ChunkSmem& sm, const ChunkStage& s, float zscale, int warp, int lane) {
+    float n1_dt[4] = {}, n2[4] = {}, nv[4] = {};
     const uint32_t at = 8 * warp * 128 + swz(lane & 7, 8 * (lane >> 3)), at2 = 8 * warp * 128 + swz(lane & 7, 32 + 8 * (lane >> 3));
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-        uint32_t x[4], y[4];
+        uint32_t x[4], y[4], v[4];
         ldsm4(x, ptx::smem_u32(s.p1) + (k ? at2 : at));
         ldsm4(y, ptx::smem_u32(s.p2) + (k ? at2 : at));
+        ldsm4(v, ptx::smem_u32(s.v) + (k ? at2 : at));
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const uint32_t ax[4] = {x[2 * h], 0u, x[2 * h + 1], 0u}, ay[4] = {y[2 * h], 0u, y[2 * h + 1], 0u};
-            mma16816(n1, ax, x[2 * h], x[2 * h + 1]);
-            mma16816(dt, ax, y[2 * h], y[2 * h + 1]);
+            const uint32_t axy[4] = {x[2 * h], y[2 * h], x[2 * h + 1], y[2 * h + 1]};
+            const uint32_t ay[4] = {y[2 * h], 0u, y[2 * h + 1], 0u}, av[4] = {v[2 * h], 0u, v[2 * h + 1], 0u};
+            mma16816(n1_dt, axy, x[2 * h], x[2 * h + 1]);
             mma16816(n2, ay, y[2 * h], y[2 * h + 1]);
+            mma16816(nv, av, v[2 * h], v[2 * h + 1]);
         }
     }
     const int g = lane >> 2;
+    bool large = false;
     if ((lane & 3) == g >> 1) {  // the diagonal's entry of row g
-        const float a = g & 1 ? n1[1] : n1[0], b = g & 1 ? n2[1] : n2[0], x = g & 1 ? dt[1] : dt[0];
+        const float a = g & 1 ? n1_dt[1] : n1_dt[0], b = g & 1 ? n2[1] : n2[0], x = g & 1 ? n1_dt[3] : n1_dt[2];
         const float S = 1.f / (1.f + __expf(-x * zscale));
         sm.rs[8 * warp + g] = make_float2(a > 0.f ? S * rsqrtf(a) : 0.f, b > 0.f ? S * rsqrtf(b) : 0.f);
+        large = (g & 1 ? nv[1] : nv[0]) > kLargest * kLargest;
     }
     __syncwarp();
+    return large;
 }
 
 // The weights (in sm.w), q k^T with the retention between the two tokens, for a chunk whose factors from one
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             return kStop;
         }
         if (n + 1 < chunks) load.chunk_into(sm.st[(n + 1) & 1], p, row + (size_t)(n + 1) * kT * stride, left - kT);
-        row_scalars(sm, s, p.zscale, warp, lane);
+        const bool large = row_scalars(sm, s, p.zscale, warp, lane);
         // The running sums inside the warp's 8 tokens.
         float2 sum = make_float2(0.f, 0.f);
         float most = 0.f;
@@ -681,8 +688,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             G[i] = sum;
         }
         *reinterpret_cast<float2*>(&sm.tot[warp][c2]) = sum;
-        // A state that grows may do so at one token and fade at others: the sums say nothing then.
-        const bool grows = kGate ? (__syncthreads(), false) : __syncthreads_or(most > 0.f);
+        // A state that grows may do so at one token and fade at others: the sums say nothing then.  Nor may a large I~
+        // meet k~, which is up to 2^kRange: their sum would pass float32 before 2^m takes that back.
+        const bool grows = __syncthreads_or(large || most > 0.f);
         float2 base = make_float2(0.f, 0.f), all = base;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
