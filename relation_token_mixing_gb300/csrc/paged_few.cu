@@ -576,7 +576,10 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
                     sc[n][mt][e] = r;
                     mt_[n][e & 1] = fmaxf(mt_[n][e & 1], r);
                 }
-            raise |= mt_[n][0] > m[n][0] + kRaise || mt_[n][1] > m[n][1] + kRaise;
+            if constexpr (Q8)  // the difference is exact, where a sum may round up past what float16 holds
+                raise |= mt_[n][0] - m[n][0] > kRaise || mt_[n][1] - m[n][1] > kRaise;
+            else
+                raise |= mt_[n][0] > m[n][0] + kRaise || mt_[n][1] > m[n][1] + kRaise;
         }
         if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
