@@ -629,8 +629,9 @@ relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, 
  *   relation_paged_q8_workspace_bytes, its limits, masks and launches.  P1's rows are
  *   taken to float16 under a power of two of their own where there are few of them
  *   (2^-25 of the row's largest value is lost), and the weights, times the scale of
- *   their I~ row, to float16 or bfloat16; an I~ row whose scale is below 2^-64 counts
- *   for less than that times its weight.
+ *   their I~ row, to float16 (few rows; what is below 2^-32 of the largest such product
+ *   is lost) or bfloat16; an I~ row whose scale is below 2^-64 counts for less than that
+ *   times its weight.
  */
 relation_status_t relation_paged_store_q8(const relation_paged_t* p, const void* X1, const void* X2, const void* I,
                                           const float* theta, int pairing, float rope_base, const int32_t* positions,

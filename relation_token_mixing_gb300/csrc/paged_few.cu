@@ -198,6 +198,11 @@ __device__ __forceinline__ Request few_request(const FwdView& v, int r) {
 // The least power of two of an 8-bit row's scale that the weights' reference follows (below): under it a row's
 // values are below 2^-57 and count for less than f16's least step.
 constexpr float kLeastScale = -64.f;
+// The weights' reference stands this far below the largest score, so the weights are between 2^15 (kRaise above 2^7) and
+// float16's least step: what is 2^-32 of the largest weight still counts (with the largest at 1, 2^-25: a
+// million keys of that weight were 3 % of a row and were lost).
+constexpr float kUpper = 7.f;
+static_assert(kUpper + kRaise <= 15.f, "float16 ends at 2^16");
 
 // A unit has all of a request's packed rows of one cache head.
 //
@@ -207,8 +212,8 @@ constexpr float kLeastScale = -64.f;
 // The bytes of a 16-bit unit are neighbours in a row, so the columns (of P2) or channels (of I~) come in
 // another order, which P1's fragments and the output's columns follow.  P2's scale multiplies
 // the score; P1's rows are f16 under a power of two of their own.  I~'s scale s multiplies the weight
-// before it is rounded (to f16: 2^-12); so that no weight leaves f16's range, the running maximum is that of
-// R + log2 s, while the sum is of the weights themselves.
+// before it is rounded (to f16: 2^-11, or 2^-32 of the largest weight where that is more); so that no weight leaves
+// f16's range, the running maximum is that of R + log2 s, while the sum is of the weights themselves.
 template <int DK, int NT, bool Q8>
 __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
     paged_few_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
                     mt_[n][e & 1] = fmaxf(mt_[n][e & 1], r);
                 }
             if constexpr (Q8)  // the difference is exact, where a sum may round up past what float16 holds
-                raise |= mt_[n][0] - m[n][0] > kRaise || mt_[n][1] - m[n][1] > kRaise;
+                raise |= mt_[n][0] - m[n][0] > kRaise + kUpper || mt_[n][1] - m[n][1] > kRaise + kUpper;
             else
                 raise |= mt_[n][0] > m[n][0] + kRaise || mt_[n][1] > m[n][1] + kRaise;
         }
@@ -590,7 +595,7 @@ __global__ void __launch_bounds__(FewCfg<DK, NT, Q8>::kThreads, 1)
                     float x = mt_[n][e];
 #pragma unroll
                     for (int y = 4; y < 32; y <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, y));
-                    x = fmaxf(x, m[n][e]);
+                    x = fmaxf(Q8 ? x - kUpper : x, m[n][e]);
                     const float f = x == -INFINITY ? 1.f : ptx::ex2_approx(m[n][e] - x);
                     m[n][e] = x;
                     l[n][e] *= f;
