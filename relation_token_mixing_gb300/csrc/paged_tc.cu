@@ -401,8 +401,9 @@ __global__ void __launch_bounds__(TcRoles<Q8>::kAll, 1)
         const int sw_in = D == 128 ? row & 7 : (row >> 1) & 3, sw_out = row & 7;
         auto convert = [&](const uint8_t* src, uint8_t* tile, uint32_t sc) {
             const float f = as_f(sc);
-            // A larger scale's values are made with a 2^16th of it and their exponents raised after (zeros stay).
-            const bool huge = __any_sync(0xffffffffu, f > 0x1p111f);
+            // A larger scale's values are made with a 2^16th of it and their exponents raised after (zeros stay), in
+            // that row alone: a small scale's would lose their last bits.
+            const bool huge = f > 0x1p111f;
             const float g = huge ? f * 0x1p-16f : f;
             const float2 f2 = make_float2(g, g), m2 = make_float2(-32896.f * g, -32896.f * g);
             // The next chunk is on its way while this one is converted.
