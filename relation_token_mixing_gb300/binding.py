@@ -668,8 +668,8 @@ def _on_current_device(*tensors) -> None:
         raise ValueError("Relation tensors must be on the current device")
 
 
-def _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias):
-    _on_current_device(P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias)
+def _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias, *others):
+    _on_current_device(P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias, *others)
     shape, dtype = P1.shape, P1.dtype
     if P2.shape != shape or I.shape != shape or G.shape != shape:
         raise ValueError("P1, P2, I and G are [N, H, d_h]")
@@ -702,7 +702,7 @@ def linear_step(P1, P2, I, G, states, slots_in, slots_out, tau_S: float, A_log=N
     (slots_in, slots_out [R] int32; negative: no state yet, not kept); returns Y.  With A_log and dt_bias [H, d_h] G
     holds the retention gate's input."""
     prob = linear_packed_for(P1, states, slots_in.numel(), tau_S)
-    _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias)
+    _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias, Y)
     Y = _like_on(P1, Y, stream)
     relation_linear_step(prob, P1, P2, I, G, A_log, dt_bias, states, slots_in, slots_out, Y, stream)
     return Y
@@ -714,7 +714,7 @@ def linear_packed_fwd(P1, P2, I, G, starts, states, slots_in, slots_out, max_fre
     returns Y.  max_fresh: a bound of any request's new tokens (0: none known).  Y and workspace are allocated when not
     given, from the stream that the kernels run on."""
     prob = linear_packed_for(P1, states, slots_in.numel(), tau_S)
-    _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias)
+    _linear_packed_check(prob, P1, P2, I, G, states, slots_in, slots_out, A_log, dt_bias, starts, Y, workspace)
     if starts.dtype is not _I32 or starts.numel() != prob.R + 1:
         raise ValueError("starts is [R + 1] of torch.int32")
     Y = _like_on(P1, Y, stream)
