@@ -445,9 +445,13 @@ relation_status_t relation_linear_bwd_gate(const relation_problem_t* p, const vo
  * offsets descend, a later request can have rows of an earlier one: it may be
  * skipped too, and the rows that it shares hold the outputs of either.
  * Outputs must not overlap inputs or each other.
- * A non-finite value of a token makes its request's head non-finite from that token
- * on, the state included, and may reach the up to 63 tokens of the same call before
- * it; other requests and heads are not touched.
+ * A NaN of a token makes its request's head NaN from that token on, the state
+ * included (one of I~: that channel).  Infinities give what the formulas give: a G of
+ * -infinity forgets its channel; a p1 that holds one has no direction, so its token's
+ * output is NaN and the state goes on.  Either may reach the up to 63 tokens of the same
+ * call before it; other requests and heads are not touched.
+ * Norms of p1 and p2 from 2^-63 to 2^63 are formed in float32; beyond, a vector may
+ * count as zero.  exp(A_log) is to be a finite float32.
  *
  * relation_linear_step: one new token a request (row r is request r's; N >= R, rows
  *   from R on are left unwritten); one launch.
@@ -626,7 +630,9 @@ relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, 
  *   the values that the pages hold; rows of negative slots are zero, and so are those of
  *   slots past the last page, which are reported (one launch).
  * relation_paged_fwd_q8: relation_paged_fwd over such pages, with its workspace from
- *   relation_paged_q8_workspace_bytes, its limits, masks and launches.  P1's rows are
+ *   relation_paged_q8_workspace_bytes, its limits, masks and launches.
+ *   As there, a masked key has weight 0 and is still multiplied: a NaN I~ row of a new
+ *   token can reach rows of the same call before it.  P1's rows are
  *   taken to float16 under a power of two of their own where there are few of them
  *   (2^-25 of the row's largest value is lost), and the weights, times the scale of
  *   their I~ row, to float16 (few rows; what is below 2^-32 of the largest such product

@@ -9,9 +9,9 @@
 namespace relation {
 namespace lin {
 
-// Tokens that the recurrence takes one by one. 64 requests, 16 heads of 64, of 16 tokens each: 18.6 us so, 28.8 as a
-// chunk; of 24: 25 and 28.8, but room for 24 tokens' vectors leaves the long requests' kernels beside it less of an
-// SM's memory (prompts of up to 2048 tokens, 8 heads of 60: 139 us against 130).
+// Tokens that the recurrence takes one by one. 64 requests, 16 heads of 64, of 16 tokens each: 18.6 us so, 27.1 as a
+// chunk; of 24: 26.3 and 27.5, but room for 24 tokens' vectors leaves the long requests' kernels beside it less of an
+// SM's memory (prompts of up to 2048 tokens, 8 heads of 60: 134 us against 125).
 constexpr int kFewTokens = 16;
 
 constexpr int kChunk = 64;  // tokens
@@ -58,9 +58,10 @@ inline Cut cut_of(int R, int N, int H, int max_fresh, int num_sms) {
     if (!c.chunked) return c;
     // share: a block's equal share of all tokens. A request of up to 1.5 of it, or of up to kUncut tokens, is left whole:
     // cutting costs the state pass (0.6 of the output pass), the join and two more launches (4 requests, 16 heads
-    // of 64: 512 tokens each 28 us whole and 35 cut, 640: 33 and 35, 768: 39 and 35, 1536: 74 and 48).
+    // of 64: 512 tokens each 25 us whole and 33 cut, 640: 31 and 33, 768: 36 and 35, 1536: 70 and 46).
     // One request is cut in equal shares; several in halves of one, kLeastCut at least, as their blocks are evened out by
-    // the order (prompts of up to 2048, 8 heads of 60: 131 us, in whole shares 142, in 512 at least 137, uncut 167).
+    // the order (prompts of up to 2048, 8 heads of 60: 125 us, in whole shares 134, in 512 at least 131, in 128 at
+    // least 125, but four requests of 1536 46 against 50; uncut 156).
     const int64_t share = (int64_t)N * H / (kBlocksPerSm * num_sms);
     int64_t seg = std::max<int64_t>(kLeastCut, ((R > 1 ? share / 2 : share) + kChunk - 1) / kChunk * kChunk);
     seg = std::max<int64_t>(seg, ((int64_t)max_fresh / (kMaxSegs - 1) + kChunk) / kChunk * kChunk);

@@ -11,8 +11,9 @@
 // (linear_chunk_kernel).  Single tokens are bound by the states' bytes; chunks by the instructions and latencies of
 // forming their operands (a channel of a token: two exponentials, two scales, three roundings), far above the bytes.
 // Measured: one token each of 512 requests, 16 heads of 64: 44 us, 6.2 TB/s; of 16 requests, 8 heads of 60: 3.0 us, one
-// launch's latency; one request of 32768 tokens, 8 heads of 60: 123 us, 1.5 TB/s;
-// 24 prompts of up to 2048, 25198 tokens: 122 us; 60 single tokens and 4 chunks of 250 to 500, 16 heads of 64: 40 us.
+// launch's latency; 16 tokens each of 64 requests, 16 heads of 64: 18.6 us, 23.4 with the gate; one request of 32768
+// tokens, 8 heads of 60: 124 us, 1.5 TB/s; 24 prompts of up to 2048, 25198 tokens: 125 us; 60 single tokens and 4 chunks of
+// 250 to 500, 16 heads of 64: 38 us.
 //
 // A chunk.  With q = S p^1, k = S p^2 and the running sum of the log-retentions
 // G_t (from the chunk's start, in units of log2), the retention between tokens j
@@ -222,7 +223,9 @@ __global__ void __launch_bounds__(kFewThreads)
           (*const sv)[kDp] = sk + most;
     constexpr int kCols = D / 4, kRows = (D + 7) / 8;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    // Beside the chunks' kernel, which waited for what ran before it, only the grid's end has to wait for that kernel's.
+    // Beside the chunks' kernel only the grid's end has to wait for that kernel's: all of its blocks have waited for what
+    // ran before the call when they release this one.  So it may only be launched right behind that kernel, which
+    // must not release before it has waited.
     if (!plan.beside) dependency_wait();
     dependency_release();
     if (plan.beside && blockIdx.x == gridDim.x - 1) {

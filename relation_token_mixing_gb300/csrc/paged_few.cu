@@ -9,9 +9,9 @@
 // every byte serves at most 16 rows (the new tokens times the heads of a group), so
 // memory bandwidth is the limit; what matters is that every SM always has enough
 // loads in flight and that a key costs few instructions.  Hence
-//  - a worker is one warp with a ring of its own: two stages of 32 keys (P2 and I~)
+//  - a worker is one warp with a ring of its own: two or three stages of 32 keys (P2 and I~)
 //    that it refills by TMA itself, one copy a lane, as soon as it has used one; no
-//    worker waits for another, and 192 KB of an SM's shared memory are stages;
+//    worker waits for another, and most of an SM's shared memory is stages (192 KB over bf16 pages);
 //  - the workers cut all requests' key tiles into equal parts (paged_schedule.cuh),
 //    so ragged lengths cost nothing; the pieces of a unit are merged in the block, and
 //    those of different blocks by a second kernel;
@@ -23,7 +23,7 @@
 // Measured: decoding 32 requests of 1000 to 32767, 32 heads over 8 of 128: 0.264 to 0.270 ms,
 // 6.7 to 6.8 TB/s, the copy rate; 8 requests of up to 4095, 16 heads of 64: 22 us, of which 3.3 until the first
 // bytes and 4 for the merge; 48 requests of up to 8192 with 0 to 5 new tokens, 10 heads over 5 of
-// 64: 46 us, 4.5 TB/s.  Over 8-bit pages (below): the 32 requests 179 us, 5.5 TB/s of half the bytes; the 8 requests 18 us;
+// 64: 46 us, 4.5 TB/s.  Over 8-bit pages (below): the 32 requests 180 us, 5.5 TB/s of half the bytes; the 8 requests 18 us;
 // the 48 requests 46 us: at 64 columns a key's instructions, not its bytes, are what a worker spends its time on.
 // The sigmoid is (1 + tanh)/2 by the hardware's tanh (2^-11), below the rounding of
 // the bf16 output; the weights are rounded to bf16 for the second product (as the
@@ -85,11 +85,11 @@ constexpr int kMinTiles = 2;  // a worker's least: below that the merge costs mo
 template <int DK, int NT, bool Q8>
 struct FewCfg {
     static constexpr int kPanels = DK > 4 ? 2 : 1;  // 64-column panels
-    // Workers of a block and stages of each: 192 KB in all.  128 columns and 8 rows: 4 x 3
-    // (decode 32 x 32k: 268 us, 6 x 2: 278 us); 16 rows, more work a key: 6 x 2 (a mixed step
-    // of 80-wide heads: 84 us, 4 x 3: 89 us).  8-bit pages, half the bytes and more work for each, want workers:
-    // 128 columns and 8 rows 11 x 2 (decode 32 x 32k: 180 us, 10 x 2: 195, 8 x 2: 207); 64 columns 12 x 3 (drafted
-    // tokens: 45 us, 8 x 5: 51).
+    // Workers of a block and stages of each.  bf16 pages, 192 KB in all: 128 columns and 8 rows 4 x 3
+    // (decode 32 x 32k: 268 us, 6 x 2: 278 us); 16 rows, more work a key, 6 x 2 (a mixed step
+    // of 80-wide heads: 84 us, 4 x 3: 89 us); 64 columns 12 x 2.  8-bit pages, half the bytes and more work for each,
+    // want workers: 128 columns and 8 rows 11 x 2, 176 KB (decode 32 x 32k: 180 us, 10 x 2: 195, 8 x 2: 207); 16 rows
+    // 8 x 2, 128 KB; 64 columns 12 x 3, 144 KB (drafted tokens: 46 us, 8 x 5: 51).
     static constexpr int kWarps = Q8 ? (kPanels == 1 ? 12 : NT == 1 ? 11 : 8) : kPanels == 1 ? 12 : NT == 1 ? 4 : 6;
     static constexpr int kStages = Q8 ? (kPanels == 1 ? 3 : 2) : kPanels == 2 && NT == 1 ? 3 : 2;
     static constexpr int kThreads = kWarps * 32;

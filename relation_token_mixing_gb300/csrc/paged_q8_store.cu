@@ -16,7 +16,8 @@
 // row (columns c and c + d/2 together, as RoPE turns them) and find its largest value among
 // themselves, so a row never leaves its registers between the prologue and its pages.  Both kernels
 // move bytes.  Measured, 16384 tokens, 32 heads over 8 of 128: the store 70 us (370 MB, 5.3 TB/s), the rows
-// read back right after it 15 us (101 MB, 6.6 TB/s, the pages still in L2); 4999 tokens, 8 heads of 60: 14 and 4.5 us.
+// read back right after it 15 us (101 MB, 6.6 TB/s, the pages still in L2; from memory 18); 4999 tokens, 8 heads of 60: 14 and
+// 4.2 us (6.3).
 #include <math.h>
 
 #include <algorithm>
@@ -29,8 +30,8 @@ namespace relation {
 namespace {
 
 constexpr int kThreads = 256;
-// Tokens of one block (16384 tokens, 32 heads over 8 of 128: 2: 81 us, 4: 77, 8: 75; 4999 tokens, 8 heads of 60: 15.3,
-// 14.7, 16.5).
+// Tokens of one block (16384 tokens, 32 heads over 8 of 128: 2: 70.9 us, 4: 70.0, 8: 66.6; 4999 tokens, 8 heads of 60:
+// 13.4, 14.3, 16.1).
 constexpr int kMaxTokens = 4;
 
 // The scale's bits as a float: of the bits of max |x|, m 2^e, it takes the exponent e - 6, or e - 5

@@ -34,8 +34,8 @@
 // 128) of tensor-core time, so the special-function unit is the limit.  The packed half
 // forms of both functions run at half the rate, so they gain nothing.
 // Measured: nine prompts of 1 to 4096 tokens, 16 heads of 64: 0.344 ms, half of it the special
-// functions' time; two chunks of 1024 tokens over 16k and 31k, 32 heads over 8 of 128: 0.81 ms,
-// 1.0 PFLOP/s, 63% the special functions' time (with a pass for the maximum between the two
+// functions' time; two chunks of 1024 tokens over 16k and 31k, 32 heads over 8 of 128: 0.82 ms,
+// 1.0 PFLOP/s, 62% the special functions' time (with a pass for the maximum between the two
 // functions 0.347 and 0.82).  At d <= 64 the rest is the softmax's own
 // latencies, with two warps to hide them (4.2 thousand cycles a tile of both halves, 3.1 of
 // them special functions), and a unit's beginning and end; at d = 128 the latencies of one
@@ -47,8 +47,8 @@
 // 8-bit pages (Q8).  The copies bring whole numbers, and four more warps (12-15) make bf16 tiles of them, q times the
 // row's scale, exactly, for the products to read.  The softmax goes 32 columns at a time without turns at every width: with
 // half of the registers and 16 warps of code, what it would gain from 128 at once it loses in the instruction caches.
-// Measured: two chunks of 1024 tokens over 16k and 31k, 32 heads over 8 of 128: 0.87 ms (bf16 pages: 0.81; conversion
-// by the loading warps 8.0; with the softmax of 128 columns at once 2.0); mixed step, 20 decoding and 4 chunks of 250 to 500, 8
+// Measured: two chunks of 1024 tokens over 16k and 31k, 32 heads over 8 of 128: 0.87 ms (bf16 pages: 0.82; nine prompts of
+// 1 to 4096 tokens, 16 heads of 64: 0.44, bf16 pages 0.35); mixed step, 20 decoding and 4 chunks of 250 to 500, 8
 // heads of 60: 72 us, 46 of them here.
 #include <cuda_bf16.h>
 
@@ -177,8 +177,9 @@ __device__ __forceinline__ uint2 scaled_bytes(uint32_t w, float2 scale, float2 s
 // with their rows' scales in them, which holds them exactly, where the copies of bf16 tiles would put
 // them; the products are the same.  What bounds it is the size of the code that runs at the same time: with the
 // softmax of 128 columns at once (d 80 and 128) and this conversion unrolled, the roles put one another out of the
-// instruction caches (two chunks over long histories, 32 heads over 8 of 128: 1.98 ms; the conversion in
-// loops 1.20; the softmax in blocks of 32 columns, without turns, 0.89, where bf16 pages take 0.84).
+// instruction caches.  When built, two chunks over long histories, 32 heads over 8 of 128, took 1.98 ms so; with the
+// conversion in loops 1.20; with the softmax in blocks of 32 columns, without turns, 0.89 (conversion by the loading
+// warps: 8.0).
 template <int D, bool Q8>
 __global__ void __launch_bounds__(TcRoles<Q8>::kAll, 1)
     paged_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
