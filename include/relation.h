@@ -634,7 +634,8 @@ relation_status_t relation_paged_fwd(const relation_paged_t* p, const void* P1, 
  *   As there, a masked key has weight 0 and is still multiplied: a NaN I~ row of a new
  *   token can reach rows of the same call before it.  P1's rows are
  *   taken to float16 under a power of two of their own where there are few of them
- *   (2^-25 of the row's largest value is lost), and the weights, times the scale of
+ *   (2^-25 of the row's largest value is lost; a key whose scale is above 2^112 may then
+ *   give an infinite score), and the weights, times the scale of
  *   their I~ row, to float16 (few rows; what is below 2^-32 of the largest such product
  *   is lost) or bfloat16; an I~ row whose scale is below 2^-64 counts for less than that
  *   times its weight.

@@ -24,7 +24,7 @@ def _cut(c, max_fresh=0):
     return Y, rb.relation_check_device_status()
 
 
-@pytest.mark.parametrize("times", [2, 3, 5])
+@pytest.mark.parametrize("times", [2, 3, 5, 100])
 @pytest.mark.parametrize("N,H,d", [(1400, 2, 60), (32768, 2, 48), (9000, 8, 64)])
 def test_rows_that_come_again_are_skipped(N, H, d, times):
     """Offsets 0, N, 0, N, ...: the first request runs; the others, all with its rows, leave their states alone."""
