@@ -452,6 +452,8 @@ relation_status_t relation_linear_bwd_gate(const relation_problem_t* p, const vo
  * call before it; other requests and heads are not touched.
  * Norms of p1 and p2 from 2^-63 to 2^63 are formed in float32; beyond, a vector may
  * count as zero.  exp(A_log) is to be a finite float32.
+ * Requests of more than 16 new tokens: where 64 of them lose up to 2^200 of a channel,
+ * outputs keep the state's share to 2^-31 at least, in absolute terms.
  *
  * relation_linear_step: one new token a request (row r is request r's; N >= R, rows
  *   from R on are left unwritten); one launch.
@@ -661,7 +663,7 @@ relation_status_t relation_paged_fwd_q8(const relation_paged_t* p, const void* P
  * flight expired too, so it returned while they may still have been writing
  * shared memory: discard the outputs and recreate the context),
  * RELATION_ERR_INVALID_ARGUMENT (a decode position outside its cache, or a value
- * that a paged call could not follow) or
+ * that a paged call or one over a pool of states could not follow) or
  * RELATION_ERR_CUDA.
  */
 relation_status_t relation_check_device_status(void);

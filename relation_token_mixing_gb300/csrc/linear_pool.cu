@@ -28,7 +28,8 @@
 // are all retentions between two of its own tokens.
 //
 // Roundings: q~, the weights and the state as an operand of the output product are
-// bf16, as the outputs are; k~ enters the state's product as a sum of three
+// bf16, as the outputs are (2^m C to 2^-134, so an output has its share of the state to 2^-31 in absolute terms);
+// k~ enters the state's product as a sum of three
 // bf16 values (2^-25; of two, 2^-17, in a strongly fading chunk), since the state is kept in float32 from call
 // to call: of two everywhere, the states of 32768 tokens are off by 2e-6 in place of less than 1e-6, 4 % sooner.
 // Sums and the state itself are float32.  Exponents are running sums too: behind a token that takes 2^-190 from a channel

@@ -19,8 +19,8 @@ def rows_of(case, only):
     A weight's relative error: U/2 from products that are exact, summed in float32 in up to 9 steps of 2^-23 of what
     stands there, which with few rows has 1152 |p1| s on it (s: the key's scale, |p1| the sum of absolute values), and
     2^-25 of the row's largest |p1| lost a column; tanh to 2^-10.9 of itself in U/2 (1 + tanh); 6 roundings of the
-    exponents, 2^-24 of the larger of |R| and the row's reference each; the weight's own rounding, 2^-11 (float16) or
-    2^-8 (bfloat16).  All of it counts in the weighted sum, all but the last in the sum of weights too, which multiplies
+    exponents, 2^-24 of the larger of |R| and the row's reference each; the weight's own rounding, 2^-11 (float16, or 2^-32
+    of the largest product of a weight and its state's scale) or 2^-8 (bfloat16).  All of it counts in the weighted sum, all but the last in the sum of weights too, which multiplies
     Y.  The weighted sum adds 2^-23 of itself for each of its steps of 16 keys.  Y is rounded once, 2^-8."""
     d, group = case.d, case.P1.shape[1] // case.q8[0].shape[1 if case.layout == BHTD else 2]
     P1 = case.P1.double().numpy()
@@ -55,6 +55,8 @@ def rows_of(case, only):
             Y = w @ v
             u = 2.0 ** -11 if few else 2.0 ** -8
             bound = 2.0 ** -8 * np.abs(Y) + 1.01 * ((w * (e + u + (i + 1) / 16 * 2.0 ** -23)) @ np.abs(v) + np.abs(Y) * (w @ e))
+            if few:
+                bound = bound + 2.0 ** -32 * (w * s[:, 1]).max() * (np.abs(v) / s[:, 1:]).sum(0)
             yield n, h, Y, bound
 
 
